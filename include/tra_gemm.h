@@ -242,6 +242,122 @@ TRA_API tra_status tra_gemm_describe(int variant, int64_t M, int64_t N, int64_t 
                              char *buf, size_t len);
 
 /*
+ * Fused linear operators: the GEMM with the work around it that a
+ * transformer's dense layers do, in one pass over the result.
+ *
+ *   gated = 0    Y = act(X W + bias) + R
+ *   gated = 1    Y = act(X W) * (X W2)        (element by element)
+ *
+ * X is M x K (M tokens), Y, R are M x N, all row-major with their own leading
+ * dimensions.  The weights are K x N row-major, as the GEMM takes B, or, with
+ * w_trans = 1, N x K row-major; W and W2 share the leading dimension ldw.
+ * Elements are binary32, bfloat16 or binary16, one type per call.
+ *
+ * Numerics: products and sums, bias, activation, gate and residual are
+ * binary32; each element is rounded to its type once, when it is stored.
+ * The order of the sums depends on the sizes, never on timing: a call gives
+ * the same bits every time.
+ *
+ * Z (binary32, M rows of ldz) may be set to keep what the backward pass
+ * needs: X W + bias, or, gated, [X W | X W2], 2 N wide.  It is binary32 so that the gradients carry no rounding
+ * from it.
+ *
+ * tra_linear_backward takes dY = the gradient of Y and writes the gradients
+ * that are asked for (non-NULL):
+ *
+ *   gated = 0    dZ = dY * act'(Z);  dX = dZ W^T;  dW = X^T dZ;
+ *                dbias = column sums of dZ  (that of R is dY itself)
+ *   gated = 1    with Z = [g | u]:  dg = dY * u * act'(g), du = dY * act(g);
+ *                dX = dg W^T + du W2^T;  dW = X^T dg;  dW2 = X^T du
+ *                (both or neither)
+ *
+ * Weight gradients are stored like the weights (K x N, or N x K), both with
+ * leading dimension lddw.  dZ is rounded to the element type, since the
+ * matrix units take it so; dbias sums it unrounded.  Operands that a call
+ * does not need (Z with act NONE, X without dW, W without dX) may be NULL.
+ *
+ * Scratch: the caller's workspace, 256-byte aligned, at least the bytes that
+ * the size query gives for the same arguments (its own workspace fields are
+ * ignored; pointers count, since alignment decides the plan).  Nothing in it
+ * needs to be set, nothing is kept in it between calls, and calls that may run
+ * at the same time each need their own.  No call allocates, so all of them
+ * may be captured into a graph; the graph keeps the pointers.
+ *
+ * Sizes: any of M, N, K may be 0 (an empty sum is 0).  Outputs may share no
+ * element with inputs or each other, but Y may be R itself.  Elements between
+ * a row's end and the next row are neither read nor written.  Errors:
+ * TRA_ERR_INVALID_ARG for a bad type, activation, size, leading dimension,
+ * pointer, overlap or workspace; TRA_ERR_UNSUPPORTED for sizes past 2^30 or
+ * a grid past HIP's limits; nothing is enqueued and no output touched.
+ */
+typedef enum tra_dtype {
+    TRA_DTYPE_F32 = 0,
+    TRA_DTYPE_BF16 = 1,
+    TRA_DTYPE_F16 = 2
+} tra_dtype;
+
+#define TRA_DTYPE_COUNT 3
+
+typedef enum tra_act {
+    TRA_ACT_NONE = 0,
+    TRA_ACT_RELU = 1,        /* max(z, 0); slope 0 at 0 */
+    TRA_ACT_GELU = 2,        /* z Phi(z) */
+    TRA_ACT_GELU_TANH = 3,   /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    TRA_ACT_SILU = 4,        /* z / (1 + exp(-z)) */
+    TRA_ACT_SIGMOID = 5      /* 1 / (1 + exp(-z)) */
+} tra_act;
+
+#define TRA_ACT_COUNT 6
+
+typedef struct tra_linear_args {
+    int32_t dtype, act, w_trans, gated;
+    int64_t M, N, K;
+    const void *X;
+    int64_t ldx;
+    const void *W, *W2;        /* W2: gated only, else NULL */
+    int64_t ldw;
+    const void *bias;          /* N elements or NULL; not gated */
+    const void *R;             /* or NULL; not gated */
+    int64_t ldr;
+    void *Y;
+    int64_t ldy;
+    float *Z;                  /* or NULL */
+    int64_t ldz;
+    void *workspace;
+    uint64_t workspace_bytes;
+} tra_linear_args;
+
+typedef struct tra_linear_grad_args {
+    int32_t dtype, act, w_trans, gated;
+    int64_t M, N, K;
+    const void *dY;
+    int64_t lddy;
+    const float *Z;
+    int64_t ldz;
+    const void *X;
+    int64_t ldx;
+    const void *W, *W2;        /* W2, dW2: gated only */
+    int64_t ldw;
+    void *dX;
+    int64_t lddx;
+    void *dW, *dW2;
+    int64_t lddw;
+    void *dbias;               /* or NULL; not gated */
+    void *workspace;
+    uint64_t workspace_bytes;
+} tra_linear_grad_args;
+
+TRA_API tra_status tra_linear(const tra_linear_args *args, void *stream);
+TRA_API tra_status tra_linear_workspace_size(const tra_linear_args *args, size_t *bytes);
+TRA_API tra_status tra_linear_backward(const tra_linear_grad_args *args, void *stream);
+TRA_API tra_status tra_linear_backward_workspace_size(const tra_linear_grad_args *args,
+                                                      size_t *bytes);
+
+/* Writes what a forward call would launch into buf as
+ * "key=value ..." text; launches nothing. */
+TRA_API tra_status tra_linear_describe(const tra_linear_args *args, char *buf, size_t len);
+
+/*
  * Measurement probes: the two roofs of the roofline model measured on the
  * device (page "Roofline & Tiling notes", legato-user-group.github.io/
  * tensor2silicon-lab/week04/researchers/jaehyeong: performance is bounded

@@ -1,0 +1,206 @@
+"""The fused linear operators' C ABI and binding without a GPU: names, argument
+checks, plans and workspace sizes.  Nothing is launched."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+import tiling_roofline_analysis_amd as tra
+from tiling_roofline_analysis_amd import fused
+
+OK, INVALID, UNSUPPORTED = tra.TRA_OK, tra.TRA_ERR_INVALID_ARG, tra.TRA_ERR_UNSUPPORTED
+FWD = ("dtype act w_trans gated M N K X ldx W W2 ldw bias R ldr Y ldy Z ldz ws ws_bytes").split()
+BWD = ("dtype act w_trans gated M N K dY lddy Z ldz X ldx W W2 ldw dX lddx dW dW2 lddw dbias "
+       "ws ws_bytes").split()
+# addresses that are never read: every call here is answered on the host
+X, W, W2, BIAS, R, Y, Z, DY, DX, DW, DW2, DB, WS = (i << 40 for i in range(1, 14))
+
+
+def fwd(**kw):
+    a = dict(dtype=1, act=0, w_trans=0, gated=0, M=8, N=64, K=32, X=X, ldx=32, W=W, W2=0,
+             ldw=64, bias=0, R=0, ldr=0, Y=Y, ldy=64, Z=0, ldz=0, ws=0, ws_bytes=0)
+    a.update(kw)
+    return fused._ARGS.pack(*(a[k] for k in FWD))
+
+
+def bwd(**kw):
+    a = dict(dtype=1, act=4, w_trans=0, gated=0, M=8, N=64, K=32, dY=DY, lddy=64, Z=Z, ldz=64,
+             X=X, ldx=32, W=W, W2=0, ldw=64, dX=DX, lddx=32, dW=DW, dW2=0, lddw=64, dbias=0, ws=0,
+             ws_bytes=0)
+    a.update(kw)
+    return fused._GRAD_ARGS.pack(*(a[k] for k in BWD))
+
+
+def size(packed, name="tra_linear_workspace_size"):
+    n = ctypes.c_size_t(0)
+    st = getattr(tra.load(), name)(packed, ctypes.byref(n))
+    return st, n.value
+
+
+def bsize(packed):
+    return size(packed, "tra_linear_backward_workspace_size")
+
+
+def test_packed_structs_match_the_header(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src = tmp_path / "s.c"
+    src.write_text('#include "tra_gemm.h"\n#include <stdio.h>\n#include <stddef.h>\n'
+                   "int main(void){printf(\"%zu %zu %zu %zu %zu %zu\\n\","
+                   "sizeof(tra_linear_args),offsetof(tra_linear_args,Y),"
+                   "offsetof(tra_linear_args,workspace),sizeof(tra_linear_grad_args),"
+                   "offsetof(tra_linear_grad_args,dX),"
+                   "offsetof(tra_linear_grad_args,workspace));return 0;}\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "s")
+    subprocess.run([cc, "-I", os.path.join(root, "include"), str(src), "-o", exe], check=True)
+    got = [int(v) for v in subprocess.run([exe], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+
+    def offset(fmt, fields, field):
+        # the offset where a marker in that field lands
+        raw = fmt.pack(*[0x7e if f == field else 0 for f in fields])
+        return raw.index(0x7e)
+
+    assert got == [fused._ARGS.size, offset(fused._ARGS, FWD, "Y"),
+                   offset(fused._ARGS, FWD, "ws"), fused._GRAD_ARGS.size,
+                   offset(fused._GRAD_ARGS, BWD, "dX"), offset(fused._GRAD_ARGS, BWD, "ws")]
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=-1), dict(dtype=3), dict(act=-1), dict(act=6), dict(w_trans=2), dict(gated=2),
+    dict(M=-1), dict(N=-1), dict(K=-1), dict(X=0), dict(W=0), dict(Y=0), dict(ldx=31),
+    dict(ldw=63), dict(ldy=63), dict(w_trans=1, ldw=31), dict(R=R, ldr=63), dict(Z=Z, ldz=63),
+    dict(X=X + 1), dict(Y=Y + 1), dict(Z=Z + 2, ldz=64), dict(bias=BIAS + 1), dict(W2=W2),
+    dict(Y=X), dict(Y=W), dict(Y=X + 16), dict(bias=Y), dict(R=Y + 2, ldr=64),
+    dict(R=Y, ldr=65), dict(Z=Y, ldz=64), dict(Z=X, ldz=64), dict(Y=W + 62 * 2, ldy=64),
+    dict(X=(1 << 64) - 64), dict(ldx=1 << 62),
+], ids=str)
+def test_linear_refuses(bad):
+    assert tra.load().tra_linear(fwd(**bad), None) == INVALID
+    assert size(fwd(**bad))[0] == INVALID
+
+
+@pytest.mark.parametrize("bad", [
+    dict(W2=0), dict(bias=BIAS), dict(R=R, ldr=64), dict(Z=Z, ldz=127), dict(Y=W2),
+    dict(W2=W2 + 1),
+], ids=str)
+def test_gated_linear_refuses(bad):
+    assert tra.load().tra_linear(fwd(**{"gated": 1, "W2": W2, **bad}), None) == INVALID
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=9), dict(act=17), dict(w_trans=-1), dict(gated=-1), dict(K=-5), dict(dY=0),
+    dict(Z=0), dict(X=0), dict(W=0), dict(lddy=63), dict(ldz=63), dict(lddx=31), dict(lddw=63),
+    dict(dX=DY), dict(dX=X), dict(dW=W), dict(dW=DX), dict(dbias=DX), dict(dbias=DB + 1),
+    dict(W2=W2), dict(dW2=DW2), dict(dX=DX + 1),
+], ids=str)
+def test_linear_backward_refuses(bad):
+    assert tra.load().tra_linear_backward(bwd(**bad), None) == INVALID
+
+
+@pytest.mark.parametrize("bad", [
+    dict(W2=0), dict(dW2=0), dict(dW=0), dict(dbias=DB), dict(Z=0), dict(ldz=127), dict(dW2=DW),
+], ids=str)
+def test_gated_backward_refuses(bad):
+    a = dict(gated=1, W2=W2, dW2=DW2, ldz=128)
+    a.update(bad)
+    assert tra.load().tra_linear_backward(bwd(**a), None) == INVALID
+
+
+def test_null_arguments():
+    lib = tra.load()
+    assert lib.tra_linear(None, None) == INVALID
+    assert lib.tra_linear_backward(None, None) == INVALID
+    assert size(None)[0] == INVALID and bsize(None)[0] == INVALID
+    assert lib.tra_linear_workspace_size(fwd(), None) == INVALID
+    assert lib.tra_linear_describe(None, None, 0) == INVALID
+
+
+def test_sizes_past_the_limits_are_unsupported():
+    big = 1 << 31
+    assert tra.load().tra_linear(fwd(M=big), None) == UNSUPPORTED
+    assert tra.load().tra_linear(fwd(M=1 << 29, N=1 << 29, ldw=1 << 29, ldy=1 << 29, W=1 << 58,
+                                     Y=1 << 61), None) == UNSUPPORTED
+    assert tra.load().tra_linear_backward(bwd(K=big, ldx=big, lddx=big), None) == UNSUPPORTED
+
+
+def test_empty_results_need_nothing():
+    assert tra.load().tra_linear(fwd(M=0, X=0, Y=0), None) == OK
+    assert tra.load().tra_linear(fwd(N=0, W=0, Y=0), None) == OK
+    assert tra.load().tra_linear(fwd(M=0, X=0, Y=0, W2=W2, gated=1), None) == OK
+    assert tra.load().tra_linear_backward(bwd(M=0, K=0, dY=0, Z=0), None) == OK
+
+
+def test_column_ranges_of_one_buffer_do_not_overlap():
+    # Y, N = 64 wide, behind X, 32 wide, in rows of 96
+    assert size(fwd(ldx=96, Y=X + 64, ldy=96))[0] == OK
+    assert size(fwd(ldx=96, Y=X + 62, ldy=96))[0] == INVALID
+    # the halves of a packed weight gradient
+    a = dict(gated=1, W2=W2, ldz=128, dW2=DW + 128, lddw=128)
+    assert bsize(bwd(**a))[0] == OK
+    assert bsize(bwd(**{**a, "dW2": DW + 126}))[0] == INVALID
+    # the residual in place
+    assert size(fwd(R=Y, ldr=64))[0] == OK
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1), (5, 7, 9), (16, 4096, 12288), (333, 8192, 2048),
+                                   (37, 5461, 2048), (100, 100, 100000), (4096, 64, 4096)])
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+def test_workspace_is_checked(shape, dtype):
+    M, N, K = shape
+    a = dict(dtype=dtype, M=M, N=N, K=K, ldx=K, ldw=N, ldy=N)
+    st, need = size(fwd(**a))
+    assert st == OK
+    if need:
+        lib = tra.load()
+        assert lib.tra_linear(fwd(**a), None) == INVALID
+        assert lib.tra_linear(fwd(**a, ws=WS, ws_bytes=need - 1), None) == INVALID
+        assert lib.tra_linear(fwd(**a, ws=WS + 16, ws_bytes=need), None) == INVALID
+    b = dict(dtype=dtype, M=M, N=N, K=K, ldx=K, ldw=N, lddy=N, ldz=N, lddx=K, lddw=N, dbias=DB)
+    st, need = bsize(bwd(**b))
+    # dZ itself and the column sums at least
+    assert st == OK and need >= M * N * (4 if dtype == 0 else 2) + 4 * N
+    assert tra.load().tra_linear_backward(bwd(**b, ws=WS, ws_bytes=need - 1), None) == INVALID
+
+
+def describe(packed):
+    buf = ctypes.create_string_buffer(256)
+    assert tra.load().tra_linear_describe(packed, buf, 256) == OK
+    return dict(kv.split("=") for kv in buf.value.decode().split())
+
+
+def test_describe_tells_aligned_from_unaligned():
+    a = dict(M=512, N=512, K=512, ldx=512, ldw=512, ldy=512)
+    assert describe(fwd(**a))["loads"] == "direct"
+    assert describe(fwd(**{**a, "ldx": 513}))["loads"] == "registers"
+    assert describe(fwd(**{**a, "X": X + 2}))["loads"] == "registers"
+    assert describe(fwd(**{**a, "N": 511}))["loads"] == "registers"
+    assert describe(fwd(M=0, X=0, Y=0)) == {"kernel": "none"}
+
+
+def test_binding_refuses_cpu_tensors_and_bad_arguments():
+    x, w = torch.ones(2, 3), torch.ones(3, 4)
+    with pytest.raises(TypeError):
+        tra.linear(x, w)
+    with pytest.raises(TypeError):
+        tra.gated_linear(x, w, w)
+    with pytest.raises(TypeError):
+        tra.linear([1.0], w)
+    with pytest.raises(TypeError):
+        tra.gated_linear(x, w, None)
+    with pytest.raises(ValueError):
+        tra.linear(x, w, act="swish")
+    with pytest.raises(ValueError):
+        tra.linear(x, w, act=None)
+
+
+def test_unknown_names_still_raise():
+    with pytest.raises(AttributeError):
+        tra.no_such_operator

@@ -14,6 +14,10 @@ Low-level calls take raw device addresses (ints) and a hipStream_t handle:
     gemm_f32_variant_noalloc(variant, M, N, K, A, lda, B, ldb, C, ldc,
                              stream) -> status
 
+``linear`` and ``gated_linear`` (see ``fused``) are the GEMM with bias,
+activation, residual or gate fused in, with gradients; they take torch tensors
+and load with torch on first use.
+
 ``matmul(A, B, C=None, variant=AUTO)`` is the torch-tensor convenience
 form: it checks the tensors, passes their device pointers and torch's
 current stream, and raises TraError on a non-OK status.
@@ -50,7 +54,9 @@ ABI_FUNCTIONS = ("gemm_f32", "gemm_f32_variant", "gemm_f32_variant_ws",
                  "tra_gemm_describe", "tra_status_string",
                  "tra_gemm_variant_name", "tra_last_hip_error", "tra_probe_work",
                  "tra_probe_copy_f32", "tra_probe_mfma_f32", "tra_probe_fma_f32",
-                 "tra_probe_launch")
+                 "tra_probe_launch", "tra_linear", "tra_linear_workspace_size",
+                 "tra_linear_backward", "tra_linear_backward_workspace_size",
+                 "tra_linear_describe")
 
 # tra_probe
 PROBE_COPY = 0
@@ -138,6 +144,16 @@ def _open(path: str) -> ctypes.CDLL:
     lib.tra_probe_fma_f32.restype = c_int
     lib.tra_probe_launch.argtypes = [i64, p]
     lib.tra_probe_launch.restype = c_int
+    # the argument structs go as packed bytes
+    args, size = ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)
+    for name in ("tra_linear", "tra_linear_backward"):
+        getattr(lib, name).argtypes = [args, p]
+        getattr(lib, name).restype = c_int
+    for name in ("tra_linear_workspace_size", "tra_linear_backward_workspace_size"):
+        getattr(lib, name).argtypes = [args, size]
+        getattr(lib, name).restype = c_int
+    lib.tra_linear_describe.argtypes = [args, ctypes.c_char_p, ctypes.c_size_t]
+    lib.tra_linear_describe.restype = c_int
     return lib
 
 
@@ -277,3 +293,16 @@ def matmul(A, B, C=None, variant: int = AUTO, stream=None, workspace=None):
     if st != TRA_OK:
         raise TraError(st, "gemm_f32_variant")
     return C
+
+
+# --- fused linear operators (fused.py; imported on first use, since it needs torch) ---
+
+_FUSED = ("linear", "gated_linear", "linear_backward", "gated_linear_backward")
+
+
+def __getattr__(name):
+    if name in _FUSED:
+        from . import fused
+        globals().update({f: getattr(fused, f) for f in _FUSED})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -24,7 +24,7 @@ POISON_LIB = os.path.join(HERE, "libtra_gemm_poison.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["tra_gemm.hip", "gemm_naive.hip", "gemm_lds_tiled.hip", "gemm_regblock.hip",
-           "gemm_mfma.hip", "probes.hip"]
+           "gemm_mfma.hip", "probes.hip", "linear.hip", "linear_bf16.hip", "linear_f16.hip", "linear_f32.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

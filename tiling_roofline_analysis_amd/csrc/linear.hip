@@ -1,0 +1,615 @@
+// linear.hip -- the C-ABI entry points of the fused linear operators (declared
+// in include/tra_gemm.h): argument checks, choice of kernels, launches on the
+// caller's stream; and the small kernels around the products, which join a
+// split's partial sums and take the gradient of the epilogue.  Errors come back as status codes; nothing throws across
+// the ABI and nothing is allocated: scratch is the caller's workspace.
+#include "tra_gemm.h"
+
+#include <algorithm>
+#include <cstdio>
+
+#include "linear_epilogue.h"
+
+namespace tra {
+namespace {
+
+// ---- joining a split, gradients of the epilogue ----------------------------------------------
+
+// One chunk of columns per lane: the partial sums in split order, then the
+// epilogue.
+template <typename T, bool GATED>
+__global__ __launch_bounds__(256) void linear_join(const TileArgs p) {
+    constexpr int V = kChunk<T>;
+    const int64_t vpr = ceil_div(p.N, V);
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (id >= vpr * p.M) return;
+    const int batch = blockIdx.y;
+    const int64_t m = id / vpr, n = (id - m * vpr) * V;
+    const int64_t np = GATED ? 2 * p.N : p.N;
+    float z[V] = {}, u[V] = {};
+    for (int s = 0; s < p.splits; ++s) {
+        const float *in =
+            p.partial + ((static_cast<int64_t>(s) * p.batch + batch) * p.M + m) * np + n;
+        float t[V];
+        load_row<float, V>(in, p.N - n, p.vec_p, t);
+#pragma unroll
+        for (int e = 0; e < V; ++e) z[e] += t[e];
+        if constexpr (GATED) {
+            load_row<float, V>(in + p.N, p.N - n, p.vec_p, t);
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[e] += t[e];
+        }
+    }
+    finish<T, GATED, V>(p.epi, batch, m, n, z, u);
+}
+
+// 64 chunks of columns by rows_per_chunk rows per workgroup; its four waves
+// take every fourth row and add their column sums in wave order.
+template <typename T, bool GATED>
+__global__ __launch_bounds__(256) void linear_slope(const SlopeArgs p) {
+    constexpr int V = kChunk<T>;
+    __shared__ __align__(16) float part[4][64 * V];
+    lds_poison(&part[0][0], 4 * 64 * V);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = (static_cast<int64_t>(blockIdx.x) * 64 + lane) * V;
+    const int64_t first = static_cast<int64_t>(blockIdx.y) * p.rows_per_chunk;
+    const int64_t end = first + p.rows_per_chunk < p.M ? first + p.rows_per_chunk : p.M;
+    const int64_t valid = p.N - n;
+    float sum[V] = {};
+    if (valid > 0) {
+        for (int64_t m = first + wave; m < end; m += 4) {
+            float dy[V], z[V] = {}, y[V], d[V], dz[V];
+            load_row<T, V>(static_cast<const T *>(p.dY) + m * p.lddy + n, valid, p.vec_dy, dy);
+            if (p.Z != nullptr) load_row<float, V>(p.Z + m * p.ldz + n, valid, p.vec_z, z);
+            activate_slope(p.act, z, y, d);
+            if constexpr (GATED) {
+                float u[V];
+                load_row<float, V>(p.Z + m * p.ldz + p.N + n, valid, p.vec_z, u);
+#pragma unroll
+                for (int e = 0; e < V; ++e) dz[e] = dy[e] * u[e] * d[e];
+                T *out = static_cast<T *>(p.dZ) + m * p.lddz + n;
+                store_row<T, V>(out, valid, p.vec_dz, dz);
+#pragma unroll
+                for (int e = 0; e < V; ++e) dz[e] = dy[e] * y[e];
+                store_row<T, V>(out + p.N, valid, p.vec_dz, dz);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) dz[e] = dy[e] * d[e];
+                if (p.dZ != nullptr)
+                    store_row<T, V>(static_cast<T *>(p.dZ) + m * p.lddz + n, valid, p.vec_dz, dz);
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[e] += dz[e];
+            }
+        }
+    }
+    if constexpr (!GATED) {
+        if (p.colsum == nullptr) return;
+#pragma unroll
+        for (int e = 0; e < V; ++e) part[wave][lane * V + e] = sum[e];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 64 * V; i += 256) {
+            const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 * V + i;
+            if (col < p.N)
+                p.colsum[static_cast<int64_t>(blockIdx.y) * p.N + col] =
+                    ((part[0][i] + part[1][i]) + part[2][i]) + part[3][i];
+        }
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void linear_colsum_join(const float *colsum, int64_t chunks,
+                                                          int64_t N, T *out) {
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (n >= N) return;
+    float sum = 0.0f;
+    for (int64_t c = 0; c < chunks; ++c) sum += colsum[c * N + n];
+    out[n] = static_cast<T>(sum);
+}
+
+template <typename T>
+hipError_t launch_join(bool gated, const TileArgs &a, hipStream_t stream) {
+    const int64_t blocks = ceil_div(ceil_div(a.N, kChunk<T>) * a.M, 256);
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(a.batch));
+    if (gated)
+        linear_join<T, true><<<grid, 256, 0, stream>>>(a);
+    else
+        linear_join<T, false><<<grid, 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_slope(bool gated, const SlopeArgs &a, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.N, 64 * kChunk<T>)),
+                    static_cast<unsigned>(ceil_div(a.M, a.rows_per_chunk)));
+    if (gated)
+        linear_slope<T, true><<<grid, 256, 0, stream>>>(a);
+    else
+        linear_slope<T, false><<<grid, 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_colsum(const float *colsum, int64_t chunks, int64_t N, void *out,
+                         hipStream_t stream) {
+    linear_colsum_join<T><<<dim3(static_cast<unsigned>(ceil_div(N, 256))), 256, 0, stream>>>(
+        colsum, chunks, N, static_cast<T *>(out));
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace tra
+
+namespace {
+
+using tra::ceil_div;
+using tra::TileArgs;
+using tra::TileForm;
+using tra::TilePlan;
+
+constexpr int64_t kMaxSize = INT32_MAX;     // M, N, K: tile counts are 32-bit
+constexpr size_t kAlign = 256;              // of the workspace's parts
+
+size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+
+int64_t elem_bytes(int dtype) { return dtype == TRA_DTYPE_F32 ? 4 : 2; }
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Rows of a matrix at p start 16-byte aligned.
+bool rows16(const void *p, int64_t ld, int64_t bytes) {
+    return aligned16(p) && ld * bytes % 16 == 0;
+}
+
+// A row-major view: rows x cols elements of `bytes` bytes.
+struct View {
+    const void *p;
+    int64_t rows, cols, ld, bytes;
+
+    bool empty() const { return rows <= 0 || cols <= 0; }
+    // A view the kernels may touch: aligned to its elements, rows that do not
+    // overlap, extent in the address space.
+    bool valid() const {
+        if (empty()) return true;
+        if (p == nullptr || ld < cols) return false;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        if (lo % static_cast<uintptr_t>(bytes) != 0) return false;
+        const __int128 extent = (static_cast<__int128>(rows - 1) * ld + cols) * bytes;
+        return extent <= static_cast<__int128>(INT64_MAX) &&
+               static_cast<__int128>(lo) + extent <= static_cast<__int128>(UINTPTR_MAX);
+    }
+    uintptr_t lo() const { return reinterpret_cast<uintptr_t>(p); }
+    uintptr_t hi() const {
+        return lo() + static_cast<uintptr_t>(((rows - 1) * ld + cols) * bytes);
+    }
+};
+
+// True if the two (valid) views share an element, or might: column ranges of
+// one row-major buffer (same row pitch) interleave without sharing any.
+bool share(const View &a, const View &b) {
+    if (a.empty() || b.empty() || a.hi() <= b.lo() || b.hi() <= a.lo()) return false;
+    if (a.rows == 1 || b.rows == 1 || a.ld * a.bytes != b.ld * b.bytes) return true;
+    const View &x = a.lo() <= b.lo() ? a : b, &y = a.lo() <= b.lo() ? b : a;
+    const int64_t pitch = x.ld * x.bytes;
+    const int64_t at = static_cast<int64_t>((y.lo() - x.lo()) % static_cast<uintptr_t>(pitch));
+    return at < x.cols * x.bytes || at + y.cols * y.bytes > pitch;
+}
+
+bool same(const View &a, const View &b) { return a.p == b.p && (a.ld == b.ld || a.rows <= 1); }
+
+bool valid_act(int act) { return act >= TRA_ACT_NONE && act < TRA_ACT_COUNT; }
+bool valid_dtype(int d) { return d >= TRA_DTYPE_F32 && d < TRA_DTYPE_COUNT; }
+
+// The weight as stored: N x K when w_trans, else K x N.
+View weight(const void *p, int w_trans, int64_t N, int64_t K, int64_t ld, int64_t bytes) {
+    return w_trans ? View{p, N, K, ld, bytes} : View{p, K, N, ld, bytes};
+}
+
+// Whether an operand can go straight into LDS: every line starts 16-byte
+// aligned and is whole chunks long, and a tile's byte offsets (256 lines) stay
+// below 2^31.
+bool direct_ok(const void *p, int64_t ld, int64_t line, int64_t bytes) {
+    return rows16(p, ld, bytes) && line * bytes % 16 == 0 && ld * bytes < (int64_t{1} << 22);
+}
+
+// The product's plan: tile, staging, split.  `lines_ok`: see direct_ok.
+TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, int64_t K, int segs,
+                   int batch, bool direct) {
+    TilePlan t{};
+    t.form = form;
+    t.gated = gated;
+    t.direct = direct;
+    t.bm = M <= 64 ? 64 : 128;
+    t.bn = 128;
+    const int64_t slice = 128 / elem_bytes(dtype);
+    const int64_t tiles =
+        std::max<int64_t>(1, ceil_div(M, t.bm) * ceil_div(N, gated ? 64 : 128) * batch);
+    const int64_t k_tiles = segs * ceil_div(K, slice);
+    // Fewer tiles than CUs: split K until about one workgroup a CU runs, each
+    // with at least 4 K tiles.
+    int64_t splits = 1;
+    if (tiles < 256) splits = std::max<int64_t>(1, std::min(256 / tiles, k_tiles / 4));
+    splits = std::min<int64_t>(splits, 64);
+    if (splits > 1) splits = ceil_div(k_tiles, ceil_div(k_tiles, splits));
+    t.splits = static_cast<int>(splits);
+    t.partial_bytes =
+        splits > 1 ? static_cast<size_t>(splits) * batch * M * (gated ? 2 : 1) * N * sizeof(float)
+                   : 0;
+    return t;
+}
+
+// Fills in what follows from the plan and checks the launch's size.
+tra_status finish_args(const TilePlan &t, int dtype, TileArgs &a, float *partial) {
+    const int64_t slice = 128 / elem_bytes(dtype);
+    const int64_t tm = ceil_div(a.M, t.bm), tn = ceil_div(a.N, t.gated ? t.bn / 2 : t.bn);
+    // kMaxGridLanes work-items, and tile indices in 32 bits
+    if (static_cast<__int128>(tm) * tn * t.splits * 512 > tra::kMaxGridLanes)
+        return TRA_ERR_UNSUPPORTED;
+    a.tiles_m = static_cast<int>(tm);
+    a.tiles_n = static_cast<int>(tn);
+    a.seg_tiles = static_cast<int>(ceil_div(a.K, slice));
+    a.k_tiles = a.segs * a.seg_tiles;
+    a.splits = t.splits;
+    a.tiles_per_split = static_cast<int>(ceil_div(std::max(a.k_tiles, 1), t.splits));
+    a.partial = t.splits > 1 ? partial : nullptr;
+    a.vec_p = a.N % 4 == 0;
+    a.epi.M = a.M;
+    a.epi.N = a.N;
+    return TRA_OK;
+}
+
+hipError_t run_tile(int dtype, const TilePlan &t, const TileArgs &a, hipStream_t s) {
+    switch (dtype) {
+        case TRA_DTYPE_F32: return tra::LinearKernels<float>::tile(t, a, s);
+        case TRA_DTYPE_BF16: return tra::LinearKernels<__bf16>::tile(t, a, s);
+        default: return tra::LinearKernels<_Float16>::tile(t, a, s);
+    }
+}
+
+hipError_t run_join(int dtype, bool gated, const TileArgs &a, hipStream_t s) {
+    switch (dtype) {
+        case TRA_DTYPE_F32: return tra::launch_join<float>(gated, a, s);
+        case TRA_DTYPE_BF16: return tra::launch_join<__bf16>(gated, a, s);
+        default: return tra::launch_join<_Float16>(gated, a, s);
+    }
+}
+
+hipError_t run_product(int dtype, const TilePlan &t, const TileArgs &a, hipStream_t s) {
+    const hipError_t err = run_tile(dtype, t, a, s);
+    return err == hipSuccess && t.splits > 1 ? run_join(dtype, t.gated, a, s) : err;
+}
+
+tra_status status_of(hipError_t err) {
+    if (err == hipSuccess) return TRA_OK;
+    tra::record_hip_error(err);
+    return TRA_ERR_HIP;
+}
+
+bool workspace_ok(const void *ws, uint64_t have, size_t need) {
+    return need == 0 || (ws != nullptr && have >= need &&
+                         (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) == 0);
+}
+
+// ---- forward ----------------------------------------------------------------------
+
+bool sizes_ok(int64_t M, int64_t N, int64_t K) { return M >= 0 && N >= 0 && K >= 0; }
+
+TilePlan plan_forward(const tra_linear_args &a) {
+    const int64_t b = elem_bytes(a.dtype);
+    const bool direct = direct_ok(a.X, a.ldx, a.K, b) &&
+                        direct_ok(a.W, a.ldw, a.w_trans ? a.K : a.N, b) &&
+                        aligned16(a.W2);
+    return plan_tile(a.w_trans ? tra::kFormKK : tra::kFormKN, a.gated != 0, a.dtype, a.M, a.N,
+                     a.K, 1, 1, direct);
+}
+
+// Host-side checks; launches nothing.
+tra_status check_forward(const tra_linear_args *p) {
+    if (p == nullptr) return TRA_ERR_INVALID_ARG;
+    const tra_linear_args &a = *p;
+    const bool gated = a.gated != 0;
+    if (!valid_dtype(a.dtype) || !valid_act(a.act) || (a.w_trans != 0 && a.w_trans != 1) ||
+        (a.gated != 0 && a.gated != 1) || !sizes_ok(a.M, a.N, a.K))
+        return TRA_ERR_INVALID_ARG;
+    if (gated && (a.bias != nullptr || a.R != nullptr)) return TRA_ERR_INVALID_ARG;
+    if (!gated && a.W2 != nullptr) return TRA_ERR_INVALID_ARG;
+    if (a.M == 0 || a.N == 0) return TRA_OK;
+    if (gated && a.W2 == nullptr && a.K > 0) return TRA_ERR_INVALID_ARG;
+    if (a.M > kMaxSize || a.N > kMaxSize / 2 || a.K > kMaxSize / 2) return TRA_ERR_UNSUPPORTED;
+    const int64_t b = elem_bytes(a.dtype);
+    const View X{a.X, a.M, a.K, a.ldx, b};
+    const View W = weight(a.W, a.w_trans, a.N, a.K, a.ldw, b);
+    const View W2 = gated ? weight(a.W2, a.w_trans, a.N, a.K, a.ldw, b) : View{};
+    const View bias{a.bias, a.bias != nullptr, a.N, a.N, b};
+    const View R{a.R, a.R != nullptr ? a.M : 0, a.N, a.ldr, b};
+    const View Y{a.Y, a.M, a.N, a.ldy, b};
+    const View Z{a.Z, a.Z != nullptr ? a.M : 0, gated ? 2 * a.N : a.N, a.ldz, 4};
+    const View in[] = {X, W, W2, bias, R};
+    for (const View &v : in)
+        if (!v.valid()) return TRA_ERR_INVALID_ARG;
+    if (!Y.valid() || !Z.valid() || share(Y, Z)) return TRA_ERR_INVALID_ARG;
+    for (const View &v : in)
+        if (share(v, Z) || (share(v, Y) && !(v.p == R.p && R.rows > 0 && same(R, Y))))
+            return TRA_ERR_INVALID_ARG;
+    return TRA_OK;
+}
+
+tra_status forward(const tra_linear_args *p, void *stream) {
+    tra_status st = check_forward(p);
+    if (st != TRA_OK || p->M == 0 || p->N == 0) return st;
+    const tra_linear_args &a = *p;
+    const bool gated = a.gated != 0;
+    const int64_t b = elem_bytes(a.dtype);
+    const TilePlan plan = plan_forward(a);
+    if (!workspace_ok(a.workspace, a.workspace_bytes, plan.partial_bytes))
+        return TRA_ERR_INVALID_ARG;
+    TileArgs t{};
+    t.A = a.X;
+    t.lda = a.ldx;
+    t.B[0] = a.W;
+    t.B[1] = gated ? a.W2 : a.W;
+    t.ldb = a.ldw;
+    t.M = a.M;
+    t.N = a.N;
+    t.K = a.K;
+    t.segs = t.batch = 1;
+    t.epi.bias = a.bias;
+    t.epi.R = a.R;
+    t.epi.ldr = a.ldr;
+    t.epi.Y[0] = a.Y;
+    t.epi.ldy = a.ldy;
+    t.epi.Z = a.Z;
+    t.epi.ldz = a.ldz;
+    t.epi.act = a.act;
+    t.epi.vec_bias = aligned16(a.bias);
+    t.epi.vec_r = rows16(a.R, a.ldr, b);
+    t.epi.vec_y = rows16(a.Y, a.ldy, b);
+    t.epi.vec_z = rows16(a.Z, a.ldz, 4) && (!gated || a.N % 4 == 0);
+    st = finish_args(plan, a.dtype, t, static_cast<float *>(a.workspace));
+    if (st != TRA_OK) return st;
+    return status_of(run_product(a.dtype, plan, t, static_cast<hipStream_t>(stream)));
+}
+
+// ---- backward ----------------------------------------------------------------------
+
+// The parts of a backward call and where they live in its workspace.
+struct GradPlan {
+    bool slope;             // dZ differs from dY: an elementwise pass writes it
+    int64_t lddz;           // elements
+    size_t dz_bytes;
+    int64_t chunks;         // row chunks of the column sums
+    int rows_per_chunk;
+    size_t colsum_bytes;
+    TilePlan dx, dw;
+    size_t product_bytes;   // the larger of the two splits' partials
+    size_t total;
+};
+
+// Rows per workgroup of the elementwise pass: about 1024 workgroups, and no
+// more than 64 chunks where their column sums are to be joined.
+void plan_slope(const tra_linear_grad_args &a, GradPlan &g) {
+    const int64_t cols = std::max<int64_t>(1, ceil_div(a.N, 64 * (16 / elem_bytes(a.dtype))));
+    int64_t chunks = std::max<int64_t>(1, 1024 / cols);
+    if (a.dbias != nullptr) chunks = std::min<int64_t>(chunks, 64);
+    const int64_t rows = std::max<int64_t>(4, ceil_div(a.M, chunks));
+    g.rows_per_chunk = static_cast<int>(rows);
+    g.chunks = ceil_div(a.M, rows);
+}
+
+GradPlan plan_backward(const tra_linear_grad_args &a) {
+    GradPlan g{};
+    const bool gated = a.gated != 0;
+    const int64_t b = elem_bytes(a.dtype);
+    const int64_t width = gated ? 2 * a.N : a.N;
+    g.slope = gated || a.act != TRA_ACT_NONE;
+    g.lddz = (width + 7) / 8 * 8;
+    g.dz_bytes = g.slope ? align_up(static_cast<size_t>(a.M * g.lddz * b)) : 0;
+    plan_slope(a, g);
+    g.colsum_bytes =
+        a.dbias != nullptr ? align_up(static_cast<size_t>(g.chunks * a.N) * sizeof(float)) : 0;
+    // dZ as an operand: the workspace's copy is aligned
+    const int64_t ldz = g.slope ? g.lddz : a.lddy;
+    const void *dz = g.slope ? nullptr : a.dY;
+    if (a.dX != nullptr) {
+        const bool direct = direct_ok(dz, ldz, a.N, b) && (!gated || a.N * b % 16 == 0) &&
+                            direct_ok(a.W, a.ldw, a.w_trans ? a.K : a.N, b) &&
+                            (!gated || aligned16(a.W2));
+        g.dx = plan_tile(a.w_trans ? tra::kFormKN : tra::kFormKK, false, a.dtype, a.M, a.K, a.N,
+                         gated ? 2 : 1, 1, direct);
+    }
+    if (a.dW != nullptr) {
+        const bool direct = direct_ok(dz, ldz, a.N, b) && (!gated || a.N * b % 16 == 0) &&
+                            direct_ok(a.X, a.ldx, a.K, b);
+        g.dw = plan_tile(tra::kFormNN, false, a.dtype, a.w_trans ? a.N : a.K,
+                         a.w_trans ? a.K : a.N, a.M, 1, gated ? 2 : 1, direct);
+    }
+    g.product_bytes = align_up(std::max(g.dx.partial_bytes, g.dw.partial_bytes));
+    g.total = g.dz_bytes + g.colsum_bytes + g.product_bytes;
+    return g;
+}
+
+tra_status check_backward(const tra_linear_grad_args *p) {
+    if (p == nullptr) return TRA_ERR_INVALID_ARG;
+    const tra_linear_grad_args &a = *p;
+    const bool gated = a.gated != 0;
+    if (!valid_dtype(a.dtype) || !valid_act(a.act) || (a.w_trans != 0 && a.w_trans != 1) ||
+        (a.gated != 0 && a.gated != 1) || !sizes_ok(a.M, a.N, a.K))
+        return TRA_ERR_INVALID_ARG;
+    if (gated ? a.dbias != nullptr || (a.dW == nullptr) != (a.dW2 == nullptr)
+              : a.W2 != nullptr || a.dW2 != nullptr)
+        return TRA_ERR_INVALID_ARG;
+    if (a.M > kMaxSize || a.N > kMaxSize / 2 || a.K > kMaxSize / 2) return TRA_ERR_UNSUPPORTED;
+    const int64_t b = elem_bytes(a.dtype);
+    const bool slope = gated || a.act != TRA_ACT_NONE;
+    const int64_t wz = gated ? 2 * a.N : a.N;
+    const View dY{a.dY, a.M, a.N, a.lddy, b};
+    const View Z{a.Z, slope ? a.M : 0, wz, a.ldz, 4};
+    const View X{a.X, a.dW != nullptr ? a.M : 0, a.K, a.ldx, b};
+    View W = weight(a.W, a.w_trans, a.N, a.K, a.ldw, b);
+    View W2 = weight(a.W2, a.w_trans, a.N, a.K, a.ldw, b);
+    if (a.dX == nullptr) W.rows = W2.rows = 0;
+    if (!gated) W2.rows = 0;
+    const View in[] = {dY, Z, X, W, W2};
+    for (const View &v : in)
+        if (!v.valid()) return TRA_ERR_INVALID_ARG;
+    const View dX{a.dX, a.dX != nullptr ? a.M : 0, a.K, a.lddx, b};
+    View dW = weight(a.dW, a.w_trans, a.N, a.K, a.lddw, b);
+    View dW2 = weight(a.dW2, a.w_trans, a.N, a.K, a.lddw, b);
+    if (a.dW == nullptr) dW.rows = 0;
+    if (a.dW2 == nullptr) dW2.rows = 0;
+    const View db{a.dbias, a.dbias != nullptr, a.N, a.N, b};
+    const View out[] = {dX, dW, dW2, db};
+    for (int i = 0; i < 4; ++i) {
+        if (!out[i].valid()) return TRA_ERR_INVALID_ARG;
+        for (const View &v : in)
+            if (share(out[i], v)) return TRA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (share(out[i], out[j])) return TRA_ERR_INVALID_ARG;
+    }
+    return TRA_OK;
+}
+
+hipError_t run_slope(int dtype, bool gated, const tra::SlopeArgs &s, hipStream_t st) {
+    switch (dtype) {
+        case TRA_DTYPE_F32: return tra::launch_slope<float>(gated, s, st);
+        case TRA_DTYPE_BF16: return tra::launch_slope<__bf16>(gated, s, st);
+        default: return tra::launch_slope<_Float16>(gated, s, st);
+    }
+}
+
+hipError_t run_colsum(int dtype, const float *colsum, int64_t chunks, int64_t N, void *out,
+                      hipStream_t st) {
+    switch (dtype) {
+        case TRA_DTYPE_F32:
+            return tra::launch_colsum<float>(colsum, chunks, N, out, st);
+        case TRA_DTYPE_BF16:
+            return tra::launch_colsum<__bf16>(colsum, chunks, N, out, st);
+        default: return tra::launch_colsum<_Float16>(colsum, chunks, N, out, st);
+    }
+}
+
+tra_status backward(const tra_linear_grad_args *p, void *stream_) {
+    tra_status st = check_backward(p);
+    if (st != TRA_OK) return st;
+    const tra_linear_grad_args &a = *p;
+    const bool gated = a.gated != 0;
+    const int64_t b = elem_bytes(a.dtype);
+    const hipStream_t stream = static_cast<hipStream_t>(stream_);
+    const GradPlan g = plan_backward(a);
+    if (!workspace_ok(a.workspace, a.workspace_bytes, g.total)) return TRA_ERR_INVALID_ARG;
+    char *ws = static_cast<char *>(a.workspace);
+    void *dz_ws = ws;
+    float *colsum = reinterpret_cast<float *>(ws + g.dz_bytes);
+    float *partial = reinterpret_cast<float *>(ws + g.dz_bytes + g.colsum_bytes);
+    const void *dz = g.slope ? dz_ws : a.dY;
+    const int64_t lddz = g.slope ? g.lddz : a.lddy;
+
+    // Both products are set up, and refused if too large, before anything runs.
+    const bool want_dx = a.dX != nullptr && a.M > 0 && a.K > 0;
+    const bool want_dw = a.dW != nullptr && a.N > 0 && a.K > 0;
+    TileArgs tx{}, tw{};
+    if (want_dx) {
+        tx.A = dz;
+        tx.lda = lddz;
+        tx.a_seg = a.N;
+        tx.B[0] = a.W;
+        tx.B[1] = gated ? a.W2 : a.W;
+        tx.ldb = a.ldw;
+        tx.M = a.M;
+        tx.N = a.K;
+        tx.K = a.N;
+        tx.segs = gated ? 2 : 1;
+        tx.batch = 1;
+        tx.epi.Y[0] = a.dX;
+        tx.epi.ldy = a.lddx;
+        tx.epi.act = TRA_ACT_NONE;
+        tx.epi.vec_y = rows16(a.dX, a.lddx, b);
+        if ((st = finish_args(g.dx, a.dtype, tx, partial)) != TRA_OK) return st;
+    }
+    if (want_dw) {
+        // dW = X^T dZ, stored K x N; or its transpose dZ^T X, stored N x K
+        tw.A = a.w_trans ? dz : a.X;
+        tw.lda = a.w_trans ? lddz : a.ldx;
+        tw.B[0] = tw.B[1] = a.w_trans ? a.X : dz;
+        tw.ldb = a.w_trans ? a.ldx : lddz;
+        tw.a_batch = a.w_trans ? a.N : 0;
+        tw.b_batch = a.w_trans ? 0 : a.N;
+        tw.M = a.w_trans ? a.N : a.K;
+        tw.N = a.w_trans ? a.K : a.N;
+        tw.K = a.M;
+        tw.segs = 1;
+        tw.batch = gated ? 2 : 1;
+        tw.epi.Y[0] = a.dW;
+        tw.epi.Y[1] = a.dW2;
+        tw.epi.ldy = a.lddw;
+        tw.epi.act = TRA_ACT_NONE;
+        tw.epi.vec_y = rows16(a.dW, a.lddw, b) && (!gated || aligned16(a.dW2));
+        if ((st = finish_args(g.dw, a.dtype, tw, partial)) != TRA_OK) return st;
+    }
+
+    hipError_t err = hipSuccess;
+    const bool need_dz = g.slope && ((want_dx && a.N > 0) || (want_dw && a.M > 0));
+    if (a.M > 0 && a.N > 0 && (need_dz || a.dbias != nullptr)) {
+        tra::SlopeArgs s{};
+        s.dY = a.dY;
+        s.lddy = a.lddy;
+        s.Z = g.slope ? a.Z : nullptr;
+        s.ldz = a.ldz;
+        s.dZ = need_dz ? dz_ws : nullptr;
+        s.lddz = lddz;
+        s.colsum = a.dbias != nullptr ? colsum : nullptr;
+        s.M = a.M;
+        s.N = a.N;
+        s.rows_per_chunk = g.rows_per_chunk;
+        s.act = a.act;
+        s.vec_dy = rows16(a.dY, a.lddy, b);
+        s.vec_z = rows16(a.Z, a.ldz, 4) && (!gated || a.N % 4 == 0);
+        s.vec_dz = !gated || a.N * b % 16 == 0;
+        err = run_slope(a.dtype, gated, s, stream);
+    }
+    if (err == hipSuccess && a.dbias != nullptr && a.N > 0)
+        err = run_colsum(a.dtype, colsum, a.M > 0 ? g.chunks : 0, a.N, a.dbias, stream);
+    if (err == hipSuccess && want_dx) err = run_product(a.dtype, g.dx, tx, stream);
+    if (err == hipSuccess && want_dw) err = run_product(a.dtype, g.dw, tw, stream);
+    return status_of(err);
+}
+
+}  // namespace
+
+extern "C" {
+
+tra_status tra_linear(const tra_linear_args *args, void *stream) { return forward(args, stream); }
+
+tra_status tra_linear_workspace_size(const tra_linear_args *args, size_t *bytes) {
+    const tra_status st = check_forward(args);
+    if (st != TRA_OK || bytes == nullptr) return st != TRA_OK ? st : TRA_ERR_INVALID_ARG;
+    *bytes = args->M == 0 || args->N == 0 ? 0 : plan_forward(*args).partial_bytes;
+    return TRA_OK;
+}
+
+tra_status tra_linear_backward(const tra_linear_grad_args *args, void *stream) {
+    return backward(args, stream);
+}
+
+tra_status tra_linear_backward_workspace_size(const tra_linear_grad_args *args, size_t *bytes) {
+    const tra_status st = check_backward(args);
+    if (st != TRA_OK || bytes == nullptr) return st != TRA_OK ? st : TRA_ERR_INVALID_ARG;
+    *bytes = plan_backward(*args).total;
+    return TRA_OK;
+}
+
+tra_status tra_linear_describe(const tra_linear_args *args, char *buf, size_t len) {
+    const tra_status st = check_forward(args);
+    if (st != TRA_OK) return st;
+    if (buf == nullptr) return len == 0 ? TRA_OK : TRA_ERR_INVALID_ARG;
+    if (len == 0) return TRA_OK;
+    if (args->M == 0 || args->N == 0) {
+        std::snprintf(buf, len, "kernel=none");
+        return TRA_OK;
+    }
+    const TilePlan t = plan_forward(*args);
+    std::snprintf(buf, len, "kernel=linear_tile tile=%dx%d loads=%s splits=%d workspace_bytes=%zu",
+                  t.bm, t.bn, t.direct ? "direct" : "registers", t.splits, t.partial_bytes);
+    return TRA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,317 @@
+"""Fused linear operators on torch tensors: ``linear`` and ``gated_linear``.
+
+    linear(x, w, bias, act, residual)   act(x w + bias) + residual
+    gated_linear(x, w_gate, w_up, act)  act(x w_gate) * (x w_up)
+
+Like ``matmul`` these check the tensors, pass their device pointers and torch's
+current stream to the library, and raise TraError on a non-OK status; scratch
+comes from torch's allocator, so calls may be captured into a graph.  With
+gradients enabled and an input that requires one they are differentiable
+(once): the backward pass runs in the library too.  ``linear_backward`` and
+``gated_linear_backward`` are those passes by themselves, for callers that
+keep their own order of work (a captured training step, a pipeline).
+
+x is M x K, the weights K x N: row-major, or the transposed view of a row-major
+N x K tensor (``w.t()`` of a torch.nn.Linear weight).  float32, bfloat16 or
+float16, one type per call.  Every element is summed in float32 and rounded
+once.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import TRA_OK, TraError, _row_major_ld, load
+
+# tra_act
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
+# tra_dtype
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+# tra_linear_args and tra_linear_grad_args, field by field
+_ARGS = struct.Struct("@4i3qPqPPqPPqPqPqPQ")
+_GRAD_ARGS = struct.Struct("@4i3qPqPqPqPPqPqPPqPPQ")
+
+
+def _act(act) -> int:
+    try:
+        return ACTS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"act must be one of {', '.join(ACTS)}; got {act!r}") from None
+
+
+def _matrix(t, name, like=None, dtype=None) -> int:
+    """Checks a row-major 2-D tensor; returns its leading dimension."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 or not t.is_cuda:
+        raise TypeError(f"{name} must be a 2-D tensor on a GPU")
+    if like is None:
+        if t.dtype not in DTYPES:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16")
+    else:
+        if t.dtype != (dtype or like.dtype):
+            raise TypeError(f"{name} must be {dtype or like.dtype}, not {t.dtype}")
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}")
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if s1 == 1 and s0 >= cols > 0:
+        return s0
+    return _row_major_ld((rows, cols), (s0, s1), name)
+
+
+def _weight(w, name, x):
+    """Checks a weight; returns (w_trans, leading dimension)."""
+    if not isinstance(w, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if w.dim() != 2 or not w.is_cuda:
+        raise TypeError(f"{name} must be a 2-D tensor on a GPU")
+    if w.dtype != x.dtype:
+        raise TypeError(f"{name} must be {x.dtype}, not {w.dtype}")
+    if w.device != x.device:
+        raise ValueError(f"{name} must be on {x.device}")
+    K, N = w.shape
+    if K != x.shape[1]:
+        raise ValueError(f"inner dimensions differ: x is {tuple(x.shape)}, {name} is {(K, N)}")
+    s0, s1 = w.stride()
+    if s0 == 1 and (s1 >= K if N > 1 else K > 1):
+        if s1 != 1 or K > 1:
+            return 1, s1 if N > 1 else K
+    try:
+        return 0, _row_major_ld((K, N), (s0, s1), name)
+    except ValueError:
+        if K == 1 and s1 >= 1:
+            return 1, s1
+        raise ValueError(f"{name} must be row-major or the transposed view of a row-major "
+                         "tensor") from None
+
+
+def _vector(b, name, x, N):
+    if not isinstance(b, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if b.dtype != x.dtype or b.dim() != 1 or b.device != x.device:
+        raise TypeError(f"{name} must be a 1-D {x.dtype} tensor on {x.device}")
+    if b.shape[0] != N or (N > 1 and b.stride(0) != 1):
+        raise ValueError(f"{name} must be {N} contiguous elements")
+
+
+def _empty_weight(K, N, trans, like):
+    t = torch.empty((N, K) if trans else (K, N), dtype=like.dtype, device=like.device)
+    return t.t() if trans else t
+
+
+def _call(name, fmt, fields, device):
+    """Packs the arguments, takes the workspace they need and makes the call."""
+    lib = load()
+    packed = fmt.pack(*fields, 0, 0)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(name, fmt, fields, device)
+    need = ctypes.c_size_t(0)
+    st = getattr(lib, name + "_workspace_size")(packed, ctypes.byref(need))
+    if st == TRA_OK:
+        if need.value:
+            # torch's blocks are 512-byte aligned, and 256 are wanted
+            ws = torch.empty(need.value, dtype=torch.uint8, device=device)
+            packed = fmt.pack(*fields, ws.data_ptr(), need.value)
+        st = getattr(lib, name)(packed, torch.cuda.current_stream(device).cuda_stream)
+    if st != TRA_OK:
+        raise TraError(st, name)
+
+
+def _forward(x, w, w2, bias, residual, act, out, z):
+    """One forward call; z (True: allocate it) keeps the pre-activations."""
+    gated = w2 is not None
+    code = _act(act)
+    ldx = _matrix(x, "x")
+    M, K = x.shape
+    trans, ldw = _weight(w, "w_gate" if gated else "w", x)
+    N = w.shape[1]
+    if gated:
+        if _weight(w2, "w_up", x) != (trans, ldw) or w2.shape != w.shape:
+            raise ValueError("w_gate and w_up must have the same shape and strides")
+    if bias is not None:
+        _vector(bias, "bias", x, N)
+    ldr = 0
+    if residual is not None:
+        ldr = _matrix(residual, "residual", x)
+        if residual.shape[0] != M or residual.shape[1] != N:
+            raise ValueError(f"residual must be {M} x {N}")
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        ldy = N
+    else:
+        ldy = _matrix(out, "out", x)
+        if out.shape[0] != M or out.shape[1] != N:
+            raise ValueError(f"out must be {M} x {N}")
+    ldz = 0
+    if z is not None:
+        width = 2 * N if gated else N
+        if z is True:
+            z = torch.empty((M, width), dtype=torch.float32, device=x.device)
+        ldz = _matrix(z, "z", x, torch.float32)
+        if z.shape[0] != M or z.shape[1] != width:
+            raise ValueError(f"z must be {M} x {width}")
+    fields = (DTYPES[x.dtype], code, trans, int(gated), M, N, K, x.data_ptr(), ldx, w.data_ptr(),
+              w2.data_ptr() if gated else 0, ldw, 0 if bias is None else bias.data_ptr(),
+              0 if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy,
+              0 if z is None else z.data_ptr(), ldz)
+    _call("tra_linear", _ARGS, fields, x.device)
+    return out, z
+
+
+def _backward(dy, x, w, w2, z, act, need_dx, need_dw, need_bias):
+    gated = w2 is not None
+    code = _act(act)
+    ldx = _matrix(x, "x")
+    lddy = _matrix(dy, "dy", x)
+    M, K = x.shape
+    trans, ldw = _weight(w, "w_gate" if gated else "w", x)
+    N = w.shape[1]
+    if gated and (_weight(w2, "w_up", x) != (trans, ldw) or w2.shape != w.shape):
+        raise ValueError("w_gate and w_up must have the same shape and strides")
+    if dy.shape[0] != M or dy.shape[1] != N:
+        raise ValueError(f"dy must be {M} x {N}")
+    ldz = 0
+    if gated or code != 0:
+        if z is None:
+            raise ValueError("z, the kept pre-activations, is needed")
+        width = 2 * N if gated else N
+        ldz = _matrix(z, "z", x, torch.float32)
+        if z.shape[0] != M or z.shape[1] != width:
+            raise ValueError(f"z must be {M} x {width}")
+    else:
+        z = None
+    dx = torch.empty((M, K), dtype=x.dtype, device=x.device) if need_dx else None
+    dw = _empty_weight(K, N, trans, x) if need_dw else None
+    dw2 = _empty_weight(K, N, trans, x) if need_dw and gated else None
+    db = torch.empty((N,), dtype=x.dtype, device=x.device) if need_bias else None
+
+    def ptr(t):
+        return 0 if t is None else t.data_ptr()
+
+    fields = (DTYPES[x.dtype], code, trans, int(gated), M, N, K, dy.data_ptr(), lddy, ptr(z), ldz,
+              x.data_ptr(), ldx, w.data_ptr(), ptr(w2), ldw, ptr(dx), K, ptr(dw), ptr(dw2),
+              max(1, K) if trans else max(1, N), ptr(db))
+    _call("tra_linear_backward", _GRAD_ARGS, fields, x.device)
+    return dx, dw, dw2, db
+
+
+def _rows(dy):
+    """dy as the library takes it: autograd may pass an expanded or transposed one."""
+    if dy.stride(1) == 1 and dy.stride(0) >= dy.shape[1]:
+        return dy
+    return dy.contiguous()
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, act):
+        need = any(ctx.needs_input_grad[:3])
+        y, z = _forward(x, w, None, bias, residual, act, None,
+                        True if need and act != "none" else None)
+        ctx.act = act
+        ctx.save_for_backward(x, w, z)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, z = ctx.saved_tensors
+        need_x, need_w, need_b, need_r, _ = ctx.needs_input_grad
+        dx = dw = db = None
+        if need_x or need_w or need_b:
+            dx, dw, _, db = _backward(_rows(dy), x, w, None, z, ctx.act, need_x, need_w, need_b)
+        return dx, dw, db, dy if need_r else None, None
+
+
+class _GatedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, act):
+        h, z = _forward(x, w_gate, w_up, None, None, act, None, True)
+        ctx.act = act
+        ctx.save_for_backward(x, w_gate, w_up, z)
+        return h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh):
+        x, w_gate, w_up, z = ctx.saved_tensors
+        need_x, need_g, need_u, _ = ctx.needs_input_grad
+        dx, dg, du, _ = _backward(_rows(dh), x, w_gate, w_up, z, ctx.act, need_x,
+                                  need_g or need_u, False)
+        return dx, dg if need_g else None, du if need_u else None, None
+
+
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(
+        isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
+
+
+def linear(x, w, bias=None, act="none", residual=None, out=None, z=None, stream=None):
+    """act(x w + bias) + residual, as a new M x N tensor or in ``out``.
+
+    ``bias`` (N elements) and ``residual`` (M x N; ``out`` may be the same
+    tensor) are optional.  ``act``: none, relu, gelu, gelu_tanh, silu or
+    sigmoid.  ``z``, if given, is a float32 M x N tensor that receives
+    x w + bias for ``linear_backward``.  ``stream`` is a torch.cuda.Stream or
+    None for torch's current stream.  ``out`` and ``z`` are refused where
+    autograd records the call.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear(x, w, bias, act, residual, out, z)
+    if _wants_grad(x, w, bias, residual):
+        if out is not None or z is not None:
+            raise ValueError("out and z cannot be given where gradients are recorded")
+        return _Linear.apply(x, w, bias, residual, act)
+    return _forward(x, w, None, bias, residual, act, out, z)[0]
+
+
+def gated_linear(x, w_gate, w_up, act="silu", out=None, z=None, stream=None):
+    """act(x w_gate) * (x w_up), as a new M x N tensor or in ``out``.
+
+    The weights have the same shape and strides (two tensors, or the halves of
+    a packed one).  ``z``, if given, is a float32 M x 2N tensor that receives
+    [x w_gate | x w_up] for ``gated_linear_backward``.  Other arguments as in
+    ``linear``.
+    """
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_linear(x, w_gate, w_up, act, out, z)
+    if w_up is None:
+        raise TypeError("w_up must be a torch.Tensor")
+    if _wants_grad(x, w_gate, w_up):
+        if out is not None or z is not None:
+            raise ValueError("out and z cannot be given where gradients are recorded")
+        return _GatedLinear.apply(x, w_gate, w_up, act)
+    return _forward(x, w_gate, w_up, None, None, act, out, z)[0]
+
+
+def linear_backward(dy, x, w, z=None, act="none", need_dx=True, need_dw=True, need_dbias=False,
+                    stream=None):
+    """(dx, dw, dbias) of ``linear`` for dy, the gradient of its result (that
+    of the residual is dy itself); None for each not asked for.  ``z`` is what
+    ``linear`` kept, needed unless act is "none".  dw has w's layout."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_backward(dy, x, w, z, act, need_dx, need_dw, need_dbias)
+    dx, dw, _, db = _backward(dy, x, w, None, z, act, need_dx, need_dw, need_dbias)
+    return dx, dw, db
+
+
+def gated_linear_backward(dh, x, w_gate, w_up, z, act="silu", need_dx=True, need_dw=True,
+                          stream=None):
+    """(dx, dw_gate, dw_up) of ``gated_linear`` for dh, the gradient of its
+    result; ``z`` is what it kept.  None for what is not asked for."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gated_linear_backward(dh, x, w_gate, w_up, z, act, need_dx, need_dw)
+    if w_up is None:
+        raise TypeError("w_up must be a torch.Tensor")
+    dx, dg, du, _ = _backward(dh, x, w_gate, w_up, z, act, need_dx, need_dw, False)
+    return dx, dg, du
