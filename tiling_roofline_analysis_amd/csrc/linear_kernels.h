@@ -139,24 +139,26 @@ struct Panel {
         return r < rows ? at : OUTSIDE;
     }
 
-    // Loads the panel at `base` (its corner, wave-uniform) into `lds`; `rem`
-    // slices of K are inside.
-    static __device__ __forceinline__ void load_direct(const char *base, const uint32_t (&off)[INS],
-                                                       int64_t rem, char *lds) {
+    // Loads the panel at `base` (its corner, wave-uniform) into `lds`.  `rem`
+    // slices of K are inside (none when rem <= 0: zeros, and no memory is read).
+    // Always INS loads and no branch, so that the number of loads in flight is
+    // the same on every path: where it is not, the compiler waits for all of them
+    // before a fragment read.
+    static __device__ __forceinline__ void load_direct(const char *base, int64_t ld,
+                                                       const uint32_t (&off)[INS], int64_t rem,
+                                                       char *lds) {
+        int length = 0x7fffffff;
+        if constexpr (!KC) {
+            // slices past the last lie past the buffer's end
+            if (rem < kSlice<T>)
+                length = rem > 0 ? static_cast<int>(rem * ld * static_cast<int64_t>(sizeof(T))) : 0;
+        }
         const __amdgpu_buffer_rsrc_t rsrc =
-            __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, 0x7fffffff, 0x00020000);
-        if (rem >= kSlice<T>) {
+            __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, length, 0x00020000);
 #pragma unroll
-            for (int i = 0; i < INS; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, lds + lds_block(i), 16, off[i], 0, 0,
-                                                         0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < INS; ++i) {
-                const int k = KC ? chunk(i) * kChunk<T> : line(i);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, lds + lds_block(i), 16,
-                                                         k < rem ? off[i] : OUTSIDE, 0, 0, 0);
-            }
+        for (int i = 0; i < INS; ++i) {
+            const uint32_t at = KC && chunk(i) * kChunk<T> >= rem ? OUTSIDE : off[i];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, lds + lds_block(i), 16, at, 0, 0, 0);
         }
     }
 
@@ -192,19 +194,25 @@ struct Panel {
             *reinterpret_cast<u32x4 *>(lds + lds_block(i) + (threadIdx.x & 63) * 16) = reg[i];
     }
 
-    // -- fragments: rows row0 .. + 15 (a multiple of 16), MFMA step `step`.
-    static __device__ __forceinline__ u32x4 fragment(const char *lds, int row0, int step) {
+    // -- fragments: rows row0 .. + 15 (a multiple of 16), MFMA step `step`, of the
+    // panel `panel` bytes into the stage `st`.  Each address is one offset from
+    // the stage's array: past a few steps of pointer arithmetic the compiler
+    // forgets which array a read is from, and waits for every direct load in
+    // flight before it.
+    static __device__ __forceinline__ u32x4 fragment(const char *st, int panel, int row0,
+                                                     int step) {
         const int l16 = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
         if constexpr (KC) {
-            return *reinterpret_cast<const u32x4 *>(lds + (row0 + l16) * 128 +
-                                                    (((4 * step + g) ^ (l16 >> 1)) << 4));
+            const int at = panel + (row0 + l16) * 128 + (((4 * step + g) ^ (l16 >> 1)) << 4);
+            return *reinterpret_cast<const u32x4 *>(st + at);
         } else if constexpr (sizeof(T) == 4) {
             u32x4 v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int k = 16 * step + 4 * g + e;
                 const int c = ((row0 + l16) >> 2) ^ (g << 2);
-                v[e] = *reinterpret_cast<const uint32_t *>(lds + k * LINE + c * 16 + (l16 & 3) * 4);
+                const int at = panel + k * LINE + c * 16 + (l16 & 3) * 4;
+                v[e] = *reinterpret_cast<const uint32_t *>(st + at);
             }
             return v;
         } else {
@@ -215,8 +223,9 @@ struct Panel {
             for (int h = 0; h < 2; ++h) {
                 const int k = 32 * step + 8 * g + 4 * h + (l16 >> 2);
                 const int c = ((row0 >> 3) + ((l16 & 3) >> 1)) ^ swizzle(k);
-                const s16x4 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (TRA_LDS(s16x4) *)(lds + k * LINE + c * 16 + (l16 & 1) * 8));
+                const int at = panel + k * LINE + c * 16 + (l16 & 1) * 8;
+                const s16x4 q =
+                    __builtin_amdgcn_ds_read_tr16_b64_v4i16((TRA_LDS(s16x4) *)(st + at));
                 const u32x2 d = __builtin_bit_cast(u32x2, q);
                 v[2 * h] = d[0];
                 v[2 * h + 1] = d[1];
@@ -389,11 +398,11 @@ __global__ __launch_bounds__(256, 2) void linear_tile(const TileArgs p) {
             u32x4 x[TI], w0[2], w1[2];
 #pragma unroll
             for (int i = 0; i < TI; ++i)
-                x[i] = PA::fragment(st, wm * (BM / 2) + i * 16, step);
+                x[i] = PA::fragment(st, 0, wm * (BM / 2) + i * 16, step);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                w0[j] = PB::fragment(st + PA::BYTES, wn * 32 + j * 16, step);
-                w1[j] = PB::fragment(st + PA::BYTES + PB::BYTES, wn * 32 + j * 16, step);
+                w0[j] = PB::fragment(st, PA::BYTES, wn * 32 + j * 16, step);
+                w1[j] = PB::fragment(st, PA::BYTES + PB::BYTES, wn * 32 + j * 16, step);
             }
             mma_step<T, TI, 2>(x, w0, c0);
             mma_step<T, TI, 2>(x, w1, c1);
@@ -409,33 +418,39 @@ __global__ __launch_bounds__(256, 2) void linear_tile(const TileArgs p) {
             ob0[i] = PB::offset(i, rows_b0, p.ldb);
             ob1[i] = PB::offset(i, rows_b1, p.ldb);
         }
+        // Tiles past the last are "loaded" too, as zeros from nowhere, which keeps
+        // the count of loads in flight.
         auto issue = [&](int s, char *st) __attribute__((always_inline)) {
             const KTile<T, AKC, BKC> t(p, at.lda, at.ldb, first + s);
-            PA::load_direct(at.a + t.da, oa, t.rem, st);
-            PB::load_direct(at.b0 + t.db, ob0, t.rem, st + PA::BYTES);
-            PB::load_direct(at.b1 + t.db, ob1, t.rem, st + PA::BYTES + PB::BYTES);
+            const int64_t rem = s < count ? t.rem : 0;
+            PA::load_direct(at.a + t.da, p.lda, oa, rem, st);
+            PB::load_direct(at.b0 + t.db, p.ldb, ob0, rem, st + PA::BYTES);
+            PB::load_direct(at.b1 + t.db, p.ldb, ob1, rem, st + PA::BYTES + PB::BYTES);
         };
-        // Tile s: its loads are the oldest of at most S - 1 tiles in flight.
         auto iteration = [&](int s, const char *st, char *next) __attribute__((always_inline)) {
-            if (s + S - 2 < count)
-                stage_sync<(S - 2) * X::LOADS>();
-            else
-                stage_sync<0>();
-            if (s + S - 1 < count) issue(s + S - 1, next);
+            stage_sync<(S - 2) * X::LOADS>();
+            issue(s + S - 1, next);
+            __builtin_amdgcn_sched_barrier(0);
             compute(st);
         };
-        if (count > 0) issue(0, st0);
-        if constexpr (S > 2)
-            if (count > 1) issue(1, st1);
-        if constexpr (S > 3)
-            if (count > 2) issue(2, st2);
+        // The waits count loads in tile order: none may be moved past another's.
+        issue(0, st0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (S > 2) issue(1, st1);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (S > 3) issue(2, st2);
         for (int s = 0; s < count; s += S) {
             iteration(s, st0, S == 2 ? st1 : S == 3 ? st2 : st3);
-            if (s + 1 < count) iteration(s + 1, st1, st0);
-            if constexpr (S > 2)
-                if (s + 2 < count) iteration(s + 2, st2, st1);
-            if constexpr (S > 3)
-                if (s + 3 < count) iteration(s + 3, st3, st2);
+            if (s + 1 >= count) break;
+            iteration(s + 1, st1, st0);
+            if constexpr (S > 2) {
+                if (s + 2 >= count) break;
+                iteration(s + 2, st2, st1);
+            }
+            if constexpr (S > 3) {
+                if (s + 3 >= count) break;
+                iteration(s + 3, st3, st2);
+            }
         }
     } else {
         u32x4 ra[PA::INS], rb0[PB::INS], rb1[PB::INS];
@@ -468,8 +483,8 @@ __global__ __launch_bounds__(256, 2) void linear_tile(const TileArgs p) {
 
     // Every wave has read its last fragments before the stages are reused: a
     // wave's BM / 2 rows of sums take its share of them, 64 (or 32) rows at a
-    // time in st0 or st1.
-    __syncthreads();
+    // time in st0 or st1.  No load is in flight into them either.
+    stage_sync<0>();
     constexpr int MINE = kEpiBytes * BM / 128;
     char *mine = (wave < 2 ? st0 : st1) + (wave & 1) * MINE;
     epi_put<TI>(mine, c0, 0);
