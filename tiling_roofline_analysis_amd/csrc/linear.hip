@@ -211,30 +211,50 @@ bool direct_ok(const void *p, int64_t ld, int64_t line, int64_t bytes) {
     return rows16(p, ld, bytes) && line * bytes % 16 == 0 && ld * bytes < (int64_t{1} << 22);
 }
 
-// The product's plan: tile, staging, split.  `lines_ok`: see direct_ok.
+// The product's plan: tile, staging, split, by a model of the time.  A CU works
+// off its share of the workgroups (tiles x splits over 256 CUs, rounded up), each
+// its K tiles at the class's measured time per K tile (all of a CU's rate to
+// itself) plus a start and an epilogue; a split adds a launch that reads the
+// partial sums back.  The classes and their times are in `classes`.
 TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, int64_t K, int segs,
                    int batch, bool direct) {
-    TilePlan t{};
-    t.form = form;
-    t.gated = gated;
-    t.direct = direct;
-    t.bm = M <= 64 ? 64 : 128;
-    t.bn = 128;
+    struct Class {
+        int bm, bn;
+        double f32, half;      // microseconds per K tile
+    };
+    static const Class classes[] = {{128, 128, 1.85, 0.36}, {64, 128, 1.0, 0.22}, {64, 64, 0.55, 0.15}};
     const int64_t slice = 128 / elem_bytes(dtype);
-    const int64_t tiles =
-        std::max<int64_t>(1, ceil_div(M, t.bm) * ceil_div(N, gated ? 64 : 128) * batch);
-    const int64_t k_tiles = segs * ceil_div(K, slice);
-    // Fewer tiles than CUs: split K until about one workgroup a CU runs, each
-    // with at least 4 K tiles.
-    int64_t splits = 1;
-    if (tiles < 256) splits = std::max<int64_t>(1, std::min(256 / tiles, k_tiles / 4));
-    splits = std::min<int64_t>(splits, 64);
-    if (splits > 1) splits = ceil_div(k_tiles, ceil_div(k_tiles, splits));
-    t.splits = static_cast<int>(splits);
-    t.partial_bytes =
-        splits > 1 ? static_cast<size_t>(splits) * batch * M * (gated ? 2 : 1) * N * sizeof(float)
-                   : 0;
-    return t;
+    const int64_t k_tiles = std::max<int64_t>(1, segs * ceil_div(K, slice));
+    const double out = static_cast<double>(batch) * M * N * (gated ? 2 : 1);
+    TilePlan best{};
+    double best_us = 0.0;
+    for (const Class &c : classes) {
+        const int64_t tiles = std::max<int64_t>(
+            1, ceil_div(M, c.bm) * ceil_div(N, gated ? c.bn / 2 : c.bn) * batch);
+        for (int64_t want = 1; want <= 32 && want <= k_tiles; ++want) {
+            if (want > 1 && tiles * want > 512) break;
+            const int64_t per = ceil_div(k_tiles, want), splits = ceil_div(k_tiles, per);
+            if (splits != want) continue;
+            const double us =
+                static_cast<double>(ceil_div(tiles * splits, 256)) *
+                    (per * (dtype == TRA_DTYPE_F32 ? c.f32 : c.half) + 2.0) +
+                (splits > 1 ? 4.0 + splits * out * 8.0 / 4e6 : 0.0);
+            if (best_us == 0.0 || us < best_us) {
+                best_us = us;
+                best.bm = c.bm;
+                best.bn = c.bn;
+                best.splits = static_cast<int>(splits);
+                best.deep = direct && tiles * splits <= 256;
+            }
+        }
+    }
+    best.form = form;
+    best.gated = gated;
+    best.direct = direct;
+    best.partial_bytes = best.splits > 1 ? static_cast<size_t>(best.splits) * batch * M *
+                                               (gated ? 2 : 1) * N * sizeof(float)
+                                         : 0;
+    return best;
 }
 
 // Fills in what follows from the plan and checks the launch's size.

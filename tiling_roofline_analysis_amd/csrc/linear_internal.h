@@ -67,6 +67,7 @@ struct TilePlan {
     bool gated;
     int bm, bn;            // tile of P (gated: bn / 2 columns of each of z, u)
     bool direct;           // operands go straight into LDS (16-byte aligned)
+    bool deep;             // direct: one workgroup a CU, with more stages
     int splits;
     size_t partial_bytes;  // workspace of the split
 };

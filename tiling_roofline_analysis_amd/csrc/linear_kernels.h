@@ -11,6 +11,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "linear_epilogue.h"
 
@@ -96,7 +97,8 @@ __device__ __forceinline__ void mma_step(const u32x4 (&x)[TI], const u32x4 (&w)[
 //         chunk ^ (r >> 1);
 //   else  16 bits: 32 lanes of a transposing read take 32 bytes from each of
 //         the 8 slices k = 0..3, 8..11; 32 bits: 64 bytes from each of the
-//         slices k = 0, 4, 8, 12.
+//         slices k = 0, 4, 8, 12 (two of which meet on one bank where a line
+//         is 128 bytes).
 // Which global chunk a lane moves follows from that; a line's bytes still
 // come from consecutive lanes.
 template <typename T, bool KC, int ROWS, int WAVES>
@@ -106,11 +108,13 @@ struct Panel {
     static constexpr int CPL = LINE / 16;             // chunks per line
     static constexpr int LPB = 1024 / LINE;           // lines per block
     static constexpr int INS = BYTES / 1024 / WAVES;  // blocks per wave
-    static_assert(LINE <= 1024 && BYTES % (1024 * WAVES) == 0, "every wave moves whole blocks");
+    static_assert(LINE >= (sizeof(T) == 4 ? 128 : 64) && LINE <= 1024, "swizzle, block");
+    static_assert(BYTES % (1024 * WAVES) == 0, "every wave moves whole blocks");
 
     static __device__ __forceinline__ int swizzle(int line) {
         if constexpr (KC) return (line >> 1) & 7;
-        if constexpr (sizeof(T) == 4) return ((line >> 2) & 3) << 2;
+        if constexpr (sizeof(T) == 4) return ((line >> 2) & (CPL / 4 - 1) & 3) << 2;
+        if constexpr (LINE == 64) return ((line >> 3) & 1) << 1;
         if constexpr (LINE == 128) return (((line >> 1) & 1) | (((line >> 3) & 1) << 1)) << 1;
         return ((line & 3) | (((line >> 3) & 1) << 2)) << 1;
     }
@@ -162,36 +166,97 @@ struct Panel {
         }
     }
 
-    // -- through registers: any alignment.  A panel that lies inside loads
-    // 16 bytes a lane at element alignment; else element by element.
-    static __device__ __forceinline__ void fetch(const char *base, int64_t ld, int64_t rows,
-                                                 int64_t rem, u32x4 (&reg)[INS]) {
-        if (rows >= ROWS && rem >= kSlice<T>) {
+    // -- through registers: any alignment, 16 bytes a lane at element alignment.
+    // Every load is in bounds: a row past the matrix reads the last row (its
+    // results are not stored), a slice past K the last slice, and a chunk that
+    // crosses the end of its line is read where it ends with the line.  Such a
+    // chunk is shifted into place, and what lies past K zeroed, when it is
+    // stored: nothing waits for the loads before that.
+    struct Source {
+        int64_t at[INS];       // bytes from the panel's corner
+        bool edge;             // not KC: the panel crosses the matrix's last column
+    };
+
+    static __device__ __forceinline__ void source(Source &f, int64_t rows, int64_t ld) {
+        constexpr int E = kChunk<T>;
+        f.edge = !KC && rows < ROWS;
 #pragma unroll
-            for (int i = 0; i < INS; ++i)
-                __builtin_memcpy(&reg[i],
-                                 base + line(i) * (ld * static_cast<int64_t>(sizeof(T))) +
-                                     chunk(i) * 16,
-                                 16);
-        } else {
-#pragma unroll
-            for (int i = 0; i < INS; ++i) {
-                const int64_t lines = KC ? rows : rem;
-                const int64_t left = (KC ? rem : rows) - chunk(i) * kChunk<T>;
-                const T *p = reinterpret_cast<const T *>(base) + line(i) * ld +
-                             chunk(i) * kChunk<T>;
-                T t[kChunk<T>];
-#pragma unroll
-                for (int e = 0; e < kChunk<T>; ++e)
-                    t[e] = line(i) < lines && e < left ? p[e] : static_cast<T>(0.0f);
-                __builtin_memcpy(&reg[i], t, 16);
+        for (int i = 0; i < INS; ++i) {
+            if constexpr (KC) {
+                const int64_t r = line(i) < rows ? line(i) : rows - 1;
+                f.at[i] = r * ld * static_cast<int64_t>(sizeof(T)) + chunk(i) * 16;
+            } else {
+                const int64_t c = chunk(i) * E;
+                const int64_t at = c + E <= rows ? c : rows - E;
+                f.at[i] = (line(i) * ld + at) * static_cast<int64_t>(sizeof(T));
             }
         }
     }
-    static __device__ __forceinline__ void store(const u32x4 (&reg)[INS], char *lds) {
+
+    static __device__ __forceinline__ void fetch(const char *base, int64_t ld, int64_t rem,
+                                                 const Source &f, u32x4 (&reg)[INS]) {
+        constexpr int64_t E = kChunk<T>;
+        int64_t at[INS];
 #pragma unroll
-        for (int i = 0; i < INS; ++i)
-            *reinterpret_cast<u32x4 *>(lds + lds_block(i) + (threadIdx.x & 63) * 16) = reg[i];
+        for (int i = 0; i < INS; ++i) at[i] = f.at[i];
+        if (rem < kSlice<T>) {
+#pragma unroll
+            for (int i = 0; i < INS; ++i) {
+                const int64_t over = KC ? chunk(i) * E + E - rem : line(i) + 1 - rem;
+                if (over > 0) at[i] -= over * (KC ? 1 : ld) * static_cast<int64_t>(sizeof(T));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < INS; ++i) __builtin_memcpy(&reg[i], base + at[i], 16);
+    }
+
+    static __device__ __forceinline__ void store(const u32x4 (&reg)[INS], int64_t rows, int64_t rem,
+                                                 const Source &f, char *lds) {
+        constexpr int64_t E = kChunk<T>;
+        if (rem < kSlice<T> || f.edge) {
+#pragma unroll
+            for (int i = 0; i < INS; ++i) {
+                // elements by which the chunk was read too early
+                int64_t over = chunk(i) * E + E - (KC ? rem : rows);
+                if (over < 0) over = 0;
+                if (!KC && line(i) >= rem) over = E;
+                unsigned __int128 x;
+                __builtin_memcpy(&x, &reg[i], 16);
+                x = over < E ? x >> (static_cast<int>(over) * 8 * static_cast<int>(sizeof(T))) : 0;
+                u32x4 v;
+                __builtin_memcpy(&v, &x, 16);
+                put(i, v, lds);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < INS; ++i) put(i, reg[i], lds);
+        }
+    }
+
+    static __device__ __forceinline__ void put(int i, u32x4 v, char *lds) {
+        *reinterpret_cast<u32x4 *>(lds + lds_block(i) + (threadIdx.x & 63) * 16) = v;
+    }
+
+    // -- element by element, at once: for lines shorter than a chunk.
+    static __device__ __forceinline__ void copy_elements(const char *base, int64_t ld, int64_t rows,
+                                                         int64_t rem, char *lds) {
+        constexpr int E = kChunk<T>;
+        const T *p = reinterpret_cast<const T *>(base);
+#pragma unroll
+        for (int i = 0; i < INS; ++i) {
+            T t[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int64_t x = chunk(i) * E + e;
+                const int64_t k = KC ? x : line(i), r = KC ? line(i) : x;
+                const int64_t kk = k < rem ? k : rem - 1, rr = r < rows ? r : rows - 1;
+                const T v = p[KC ? rr * ld + kk : kk * ld + rr];
+                t[e] = k < rem ? v : static_cast<T>(0.0f);
+            }
+            u32x4 v;
+            __builtin_memcpy(&v, t, 16);
+            put(i, v, lds);
+        }
     }
 
     // -- fragments: rows row0 .. + 15 (a multiple of 16), MFMA step `step`, of the
@@ -210,7 +275,7 @@ struct Panel {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int k = 16 * step + 4 * g + e;
-                const int c = ((row0 + l16) >> 2) ^ (g << 2);
+                const int c = ((row0 + l16) >> 2) ^ swizzle(k);
                 const int at = panel + k * LINE + c * 16 + (l16 & 3) * 4;
                 v[e] = *reinterpret_cast<const uint32_t *>(st + at);
             }
@@ -237,47 +302,52 @@ struct Panel {
 
 // ---- epilogue through LDS -------------------------------------------------------------
 //
-// A wave owns 64 rows x (32 columns of half 0, 32 of half 1) of sums at a time.
-// It lays them out in 16 KB of LDS of its own and reads them back a chunk of
-// columns per lane, so that bias, residual and result move 16 bytes a lane and
-// whole lines a row, and the activation's code stands once, in a rolled loop.
-constexpr int kEpiBytes = 64 * 256;
+// A wave lays its sums out in LDS of its own, HC columns of half 0 beside HC of
+// half 1, and reads them back a chunk of columns per lane, so that bias,
+// residual and result move 16 bytes a lane and whole lines a row, and the
+// activation's code stands once, in a rolled loop.  The 16-byte pieces of a row
+// are XORed by the row so that neither side meets bank conflicts.
+template <int HC>
+__device__ __forceinline__ int epi_at(int row, int piece) {
+    static_assert(HC == 32 || HC == 16, "rows of 256 or 128 bytes");
+    return HC == 32 ? row * 256 + ((piece ^ (row & 15)) << 4)
+                    : row * 128 + ((piece ^ ((row >> 1) & 7)) << 4);
+}
 
-template <int TI>
-__device__ __forceinline__ void epi_put(char *lds, const f32x4 (&c)[TI][2], int half) {
+template <int HC, int TI, int TJ>
+__device__ __forceinline__ void epi_put(char *lds, const f32x4 (&c)[TI][TJ], int half) {
     const int l16 = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int row = i * 16 + l16, c16 = half * 8 + j * 4 + g;
-            *reinterpret_cast<f32x4 *>(lds + row * 256 + ((c16 ^ (row & 15)) << 4)) = c[i][j];
-        }
+        for (int j = 0; j < TJ; ++j)
+            *reinterpret_cast<f32x4 *>(
+                lds + epi_at<HC>(i * 16 + l16, half * (HC / 4) + j * 4 + g)) = c[i][j];
 }
 
-// V sums of one row, from column `col` of the wave's 64 on.
-template <int V>
+// V sums of one row, from column `col` of the wave's 2 HC on.
+template <int HC, int V>
 __device__ __forceinline__ void epi_get(const char *lds, int row, int col, float (&v)[V]) {
 #pragma unroll
     for (int q = 0; q < V / 4; ++q) {
-        const f32x4 t =
-            *reinterpret_cast<const f32x4 *>(lds + row * 256 + (((col / 4 + q) ^ (row & 15)) << 4));
+        const f32x4 t = *reinterpret_cast<const f32x4 *>(lds + epi_at<HC>(row, col / 4 + q));
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[4 * q + e] = t[e];
     }
 }
 
-// Rows m0 .. m0 + ROWS - 1; columns n0 .. + 31 (half 0) and n1 .. + 31 (half 1:
+// Rows m0 .. m0 + ROWS - 1; columns n0 .. + HC - 1 (half 0) and n1 .. (half 1:
 // of the same matrix, or, gated, of u, with n1 == n0).
-template <typename T, bool GATED, int ROWS>
+template <typename T, bool GATED, int HC, int ROWS>
 __device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, int split, const char *lds,
                                          int64_t m0, int64_t n0, int64_t n1) {
     constexpr int V = kChunk<T>;
-    constexpr int VPR = (GATED ? 32 : 64) / V;   // chunks per row
-    constexpr int RPI = 64 / VPR;                // rows per iteration
+    constexpr int VPR = (GATED ? HC : 2 * HC) / V;   // chunks per row
+    constexpr int RPI = 64 / VPR;                    // rows per iteration
+    static_assert(ROWS % RPI == 0, "whole iterations");
     const int lane = threadIdx.x & 63;
     const int col = (lane % VPR) * V;
-    const int64_t n = GATED || col < 32 ? n0 + col : n1 + (col - 32);
+    const int64_t n = GATED || col < HC ? n0 + col : n1 + (col - HC);
     if (n >= p.N) return;
 #pragma unroll 2
     for (int t = 0; t < ROWS / RPI; ++t) {
@@ -285,8 +355,8 @@ __device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, int split
         const int64_t m = m0 + row;
         if (m >= p.M) break;
         float z[V], u[V];
-        epi_get(lds, row, col, z);
-        if constexpr (GATED) epi_get(lds, row, 32 + col, u);
+        epi_get<HC>(lds, row, col, z);
+        if constexpr (GATED) epi_get<HC>(lds, row, HC + col, u);
         if (p.partial != nullptr) {
             const int64_t np = GATED ? 2 * p.N : p.N;
             float *out = p.partial +
@@ -301,9 +371,9 @@ __device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, int split
 
 // ---- the tile kernel --------------------------------------------------------------------
 //
-// BM x 128 of P per workgroup of four waves in 2 x 2; a wave computes BM / 2
-// rows by 32 columns of each half of the tile's columns.  Half 1 is the next 64
-// columns, or, gated, the same 64 columns of the second weight: z and u of an
+// BM x BN of P per workgroup of four waves in 2 x 2; a wave computes BM / 2
+// rows by BN / 4 columns of each half of the tile's columns.  Half 1 is the next
+// BN / 2 columns, or, gated, the same columns of the second weight: z and u of an
 // element sit in the same lane and H is finished without a trip to memory.
 //
 // S stages of LDS hold a K tile of both operands each.  DIRECT: iteration s
@@ -312,13 +382,16 @@ __device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, int split
 // computes tile s.  Otherwise (S = 2) tile s + 1 waits in registers while tile s
 // is computed, and is stored behind it.
 
-template <typename T, bool AKC, bool BKC, int BM, bool GATED>
+template <typename T, bool AKC, bool BKC, int BM, int BN>
 struct TileShape {
-    static constexpr int BN = 128, WAVES = 4, TI = BM / 32;
+    static constexpr int WAVES = 4, TI = BM / 32, TJ = BN / 64, HC = BN / 4;
     using PA = Panel<T, AKC, BM, WAVES>;
     using PB = Panel<T, BKC, BN / 2, WAVES>;
     static constexpr int STAGE = PA::BYTES + 2 * PB::BYTES;
     static constexpr int LOADS = PA::INS + 2 * PB::INS;
+    static constexpr int MINE = BM / 2 * HC * 8;     // a wave's sums in the epilogue
+    // Workgroups a CU by LDS: two, where the stages leave room.
+    static constexpr int per_cu(int stages) { return stages * STAGE <= 80 * 1024 ? 2 : 1; }
 };
 
 // Where the operands of this workgroup's tile start.
@@ -355,22 +428,38 @@ struct KTile {
     }
 };
 
-template <typename T, bool AKC, bool BKC, int BM, int S, bool DIRECT, bool GATED>
-__global__ __launch_bounds__(256, 2) void linear_tile(const TileArgs p) {
-    using X = TileShape<T, AKC, BKC, BM, GATED>;
+// f(0), f(1), .. (as constants) until one returns false.
+template <int... U, typename F>
+__device__ __forceinline__ void for_each(std::integer_sequence<int, U...>, F f) {
+    (void)(f(std::integral_constant<int, U>{}) && ...);
+}
+
+template <typename T, bool AKC, bool BKC, int BM, int BN, int S, bool DIRECT, bool GATED>
+__global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) void linear_tile(const TileArgs p) {
+    using X = TileShape<T, AKC, BKC, BM, BN>;
     using PA = typename X::PA;
     using PB = typename X::PB;
-    constexpr int TI = X::TI;
+    constexpr int TI = X::TI, TJ = X::TJ, HC = X::HC;
     static_assert(DIRECT || S == 2, "register staging keeps two stages");
-    static_assert(S >= 2 && S <= 4 && X::STAGE >= 2 * kEpiBytes * BM / 128, "LDS");
+    static_assert(S >= 2 && S <= 6 && X::STAGE >= 2 * X::MINE, "LDS");
     // One array per stage, so that the compiler can tell a fragment read from
     // the direct loads in flight into the other stages.
     __shared__ __align__(1024) char st0[X::STAGE], st1[X::STAGE];
     __shared__ __align__(1024) char st2[S > 2 ? X::STAGE : 16], st3[S > 3 ? X::STAGE : 16];
-    lds_poison(reinterpret_cast<float *>(st0), X::STAGE / 4);
-    lds_poison(reinterpret_cast<float *>(st1), X::STAGE / 4);
-    if constexpr (S > 2) lds_poison(reinterpret_cast<float *>(st2), X::STAGE / 4);
-    if constexpr (S > 3) lds_poison(reinterpret_cast<float *>(st3), X::STAGE / 4);
+    __shared__ __align__(1024) char st4[S > 4 ? X::STAGE : 16], st5[S > 5 ? X::STAGE : 16];
+    auto stage = [&](auto u) __attribute__((always_inline))->char * {
+        constexpr int U = decltype(u)::value % S;
+        if constexpr (U == 0) return st0;
+        if constexpr (U == 1) return st1;
+        if constexpr (U == 2) return st2;
+        if constexpr (U == 3) return st3;
+        if constexpr (U == 4) return st4;
+        return st5;
+    };
+    for_each(std::make_integer_sequence<int, S>{}, [&](auto u) __attribute__((always_inline)) {
+        lds_poison(reinterpret_cast<float *>(stage(u)), X::STAGE / 4);
+        return true;
+    });
 
     const int batch = blockIdx.y;
     const int tiles = p.tiles_m * p.tiles_n;
@@ -378,9 +467,9 @@ __global__ __launch_bounds__(256, 2) void linear_tile(const TileArgs p) {
     const int split = id / tiles;
     int tm, tn;
     grouped_tile32<8>(id - split * tiles, p.tiles_m, p.tiles_n, tm, tn);
-    constexpr int NB = GATED ? 64 : 128;
+    constexpr int NB = GATED ? BN / 2 : BN;
     const int64_t m0 = static_cast<int64_t>(tm) * BM;
-    const int64_t n0 = static_cast<int64_t>(tn) * NB, n1 = GATED ? n0 : n0 + 64;
+    const int64_t n0 = static_cast<int64_t>(tn) * NB, n1 = GATED ? n0 : n0 + BN / 2;
     const Corner<T, AKC, BKC> at(p, batch, m0, n0, n1, GATED);
     const int64_t rows_a = p.M - m0, rows_b0 = p.N - n0, rows_b1 = p.N - n1;
 
@@ -390,22 +479,22 @@ __global__ __launch_bounds__(256, 2) void linear_tile(const TileArgs p) {
 
     const int wave = wave_id();
     const int wm = wave >> 1, wn = wave & 1;
-    f32x4 c0[TI][2] = {}, c1[TI][2] = {};
+    f32x4 c0[TI][TJ] = {}, c1[TI][TJ] = {};
 
     auto compute = [&](const char *st) __attribute__((always_inline)) {
 #pragma unroll
         for (int step = 0; step < 2; ++step) {
-            u32x4 x[TI], w0[2], w1[2];
+            u32x4 x[TI], w0[TJ], w1[TJ];
 #pragma unroll
             for (int i = 0; i < TI; ++i)
                 x[i] = PA::fragment(st, 0, wm * (BM / 2) + i * 16, step);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                w0[j] = PB::fragment(st, PA::BYTES, wn * 32 + j * 16, step);
-                w1[j] = PB::fragment(st, PA::BYTES + PB::BYTES, wn * 32 + j * 16, step);
+            for (int j = 0; j < TJ; ++j) {
+                w0[j] = PB::fragment(st, PA::BYTES, wn * HC + j * 16, step);
+                w1[j] = PB::fragment(st, PA::BYTES + PB::BYTES, wn * HC + j * 16, step);
             }
-            mma_step<T, TI, 2>(x, w0, c0);
-            mma_step<T, TI, 2>(x, w1, c1);
+            mma_step<T, TI, TJ>(x, w0, c0);
+            mma_step<T, TI, TJ>(x, w1, c1);
         }
     };
 
@@ -419,78 +508,88 @@ __global__ __launch_bounds__(256, 2) void linear_tile(const TileArgs p) {
             ob1[i] = PB::offset(i, rows_b1, p.ldb);
         }
         // Tiles past the last are "loaded" too, as zeros from nowhere, which keeps
-        // the count of loads in flight.
+        // the count of loads in flight.  The waits count loads in tile order: none
+        // may be moved past another's.
         auto issue = [&](int s, char *st) __attribute__((always_inline)) {
             const KTile<T, AKC, BKC> t(p, at.lda, at.ldb, first + s);
             const int64_t rem = s < count ? t.rem : 0;
             PA::load_direct(at.a + t.da, p.lda, oa, rem, st);
             PB::load_direct(at.b0 + t.db, p.ldb, ob0, rem, st + PA::BYTES);
             PB::load_direct(at.b1 + t.db, p.ldb, ob1, rem, st + PA::BYTES + PB::BYTES);
-        };
-        auto iteration = [&](int s, const char *st, char *next) __attribute__((always_inline)) {
-            stage_sync<(S - 2) * X::LOADS>();
-            issue(s + S - 1, next);
             __builtin_amdgcn_sched_barrier(0);
-            compute(st);
         };
-        // The waits count loads in tile order: none may be moved past another's.
-        issue(0, st0);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (S > 2) issue(1, st1);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (S > 3) issue(2, st2);
+        for_each(std::make_integer_sequence<int, S - 1>{},
+                   [&](auto u) __attribute__((always_inline)) {
+                       issue(decltype(u)::value, stage(u));
+                       return true;
+                   });
         for (int s = 0; s < count; s += S) {
-            iteration(s, st0, S == 2 ? st1 : S == 3 ? st2 : st3);
-            if (s + 1 >= count) break;
-            iteration(s + 1, st1, st0);
-            if constexpr (S > 2) {
-                if (s + 2 >= count) break;
-                iteration(s + 2, st2, st1);
-            }
-            if constexpr (S > 3) {
-                if (s + 3 >= count) break;
-                iteration(s + 3, st3, st2);
-            }
+            for_each(std::make_integer_sequence<int, S>{},
+                       [&](auto u) __attribute__((always_inline)) {
+                           constexpr int U = decltype(u)::value;
+                           if (s + U >= count) return false;
+                           stage_sync<(S - 2) * X::LOADS>();
+                           issue(s + U + S - 1, stage(std::integral_constant<int, U + S - 1>{}));
+                           compute(stage(u));
+                           return true;
+                       });
         }
     } else {
+        typename PA::Source fa;
+        typename PB::Source fb0, fb1;
+        PA::source(fa, rows_a, p.lda);
+        PB::source(fb0, rows_b0, p.ldb);
+        PB::source(fb1, rows_b1, p.ldb);
         u32x4 ra[PA::INS], rb0[PB::INS], rb1[PB::INS];
         auto fetch = [&](int s) __attribute__((always_inline)) {
             const KTile<T, AKC, BKC> t(p, at.lda, at.ldb, first + s);
-            PA::fetch(at.a + t.da, p.lda, rows_a, t.rem, ra);
-            PB::fetch(at.b0 + t.db, p.ldb, rows_b0, t.rem, rb0);
-            PB::fetch(at.b1 + t.db, p.ldb, rows_b1, t.rem, rb1);
+            PA::fetch(at.a + t.da, p.lda, t.rem, fa, ra);
+            PB::fetch(at.b0 + t.db, p.ldb, t.rem, fb0, rb0);
+            PB::fetch(at.b1 + t.db, p.ldb, t.rem, fb1, rb1);
         };
-        auto store = [&](char *st) __attribute__((always_inline)) {
-            PA::store(ra, st);
-            PB::store(rb0, st + PA::BYTES);
-            PB::store(rb1, st + PA::BYTES + PB::BYTES);
+        auto store = [&](int s, char *st) __attribute__((always_inline)) {
+            const KTile<T, AKC, BKC> t(p, at.lda, at.ldb, first + s);
+            PA::store(ra, rows_a, t.rem, fa, st);
+            PB::store(rb0, rows_b0, t.rem, fb0, st + PA::BYTES);
+            PB::store(rb1, rows_b1, t.rem, fb1, st + PA::BYTES + PB::BYTES);
         };
         auto iteration = [&](int s, const char *st, char *next) __attribute__((always_inline)) {
             __syncthreads();
             if (s + 1 < count) fetch(s + 1);
+            __builtin_amdgcn_sched_barrier(0);
             compute(st);
-            if (s + 1 < count) store(next);
+            __builtin_amdgcn_sched_barrier(0);
+            if (s + 1 < count) store(s + 1, next);
         };
-        if (count > 0) {
+        if ((AKC ? p.K : p.M) < kChunk<T> || (BKC ? p.K : p.N) < kChunk<T>) {
+            for (int s = 0; s < count; ++s) {
+                const KTile<T, AKC, BKC> t(p, at.lda, at.ldb, first + s);
+                __syncthreads();
+                PA::copy_elements(at.a + t.da, p.lda, rows_a, t.rem, st0);
+                PB::copy_elements(at.b0 + t.db, p.ldb, rows_b0, t.rem, st0 + PA::BYTES);
+                PB::copy_elements(at.b1 + t.db, p.ldb, rows_b1, t.rem,
+                                  st0 + PA::BYTES + PB::BYTES);
+                __syncthreads();
+                compute(st0);
+            }
+        } else if (count > 0) {
             fetch(0);
-            store(st0);
-        }
-        for (int s = 0; s < count; s += 2) {
-            iteration(s, st0, st1);
-            if (s + 1 < count) iteration(s + 1, st1, st0);
+            store(0, st0);
+            for (int s = 0; s < count; s += 2) {
+                iteration(s, st0, st1);
+                if (s + 1 < count) iteration(s + 1, st1, st0);
+            }
         }
     }
 
-    // Every wave has read its last fragments before the stages are reused: a
-    // wave's BM / 2 rows of sums take its share of them, 64 (or 32) rows at a
-    // time in st0 or st1.  No load is in flight into them either.
+    // Every wave has read its last fragments, and no load is in flight, before
+    // the stages are reused: a wave's sums take their share of st0 or st1.
     stage_sync<0>();
-    constexpr int MINE = kEpiBytes * BM / 128;
-    char *mine = (wave < 2 ? st0 : st1) + (wave & 1) * MINE;
-    epi_put<TI>(mine, c0, 0);
-    epi_put<TI>(mine, c1, 1);
-    epi_rows<T, GATED, BM / 2>(p, batch, split, mine, m0 + wm * (BM / 2), n0 + wn * 32,
-                               n1 + wn * 32);
+    char *mine = (wave < 2 ? st0 : st1) + (wave & 1) * X::MINE;
+    epi_put<HC>(mine, c0, 0);
+    epi_put<HC>(mine, c1, 1);
+    epi_rows<T, GATED, HC, BM / 2>(p, batch, split, mine, m0 + wm * (BM / 2), n0 + wn * HC,
+                                   n1 + wn * HC);
 }
 
 // ---- launches ----------------------------------------------------------------------------------
@@ -500,16 +599,30 @@ hipError_t launch_tile(const TilePlan &plan, const TileArgs &a, hipStream_t stre
     const dim3 grid(static_cast<unsigned>(a.tiles_m) * static_cast<unsigned>(a.tiles_n) *
                         static_cast<unsigned>(a.splits),
                     static_cast<unsigned>(a.batch));
-    if (plan.bm == 64) {
-        if (plan.direct)
-            linear_tile<T, AKC, BKC, 64, 3, true, GATED><<<grid, 256, 0, stream>>>(a);
+    // Direct loads: two workgroups a CU, or, where the grid gives a CU no more
+    // than one, stages enough that a second does not fit (the dispatcher would put
+    // two on one CU and leave another idle).
+    if (plan.bm == 128) {
+        if (!plan.direct)
+            linear_tile<T, AKC, BKC, 128, 128, 2, false, GATED><<<grid, 256, 0, stream>>>(a);
+        else if (plan.deep)
+            linear_tile<T, AKC, BKC, 128, 128, 4, true, GATED><<<grid, 256, 0, stream>>>(a);
         else
-            linear_tile<T, AKC, BKC, 64, 2, false, GATED><<<grid, 256, 0, stream>>>(a);
+            linear_tile<T, AKC, BKC, 128, 128, 2, true, GATED><<<grid, 256, 0, stream>>>(a);
+    } else if (plan.bn == 128) {
+        if (!plan.direct)
+            linear_tile<T, AKC, BKC, 64, 128, 2, false, GATED><<<grid, 256, 0, stream>>>(a);
+        else if (plan.deep)
+            linear_tile<T, AKC, BKC, 64, 128, 6, true, GATED><<<grid, 256, 0, stream>>>(a);
+        else
+            linear_tile<T, AKC, BKC, 64, 128, 3, true, GATED><<<grid, 256, 0, stream>>>(a);
     } else {
-        if (plan.direct)
-            linear_tile<T, AKC, BKC, 128, 2, true, GATED><<<grid, 256, 0, stream>>>(a);
+        if (!plan.direct)
+            linear_tile<T, AKC, BKC, 64, 64, 2, false, GATED><<<grid, 256, 0, stream>>>(a);
+        else if (plan.deep)
+            linear_tile<T, AKC, BKC, 64, 64, 6, true, GATED><<<grid, 256, 0, stream>>>(a);
         else
-            linear_tile<T, AKC, BKC, 128, 2, false, GATED><<<grid, 256, 0, stream>>>(a);
+            linear_tile<T, AKC, BKC, 64, 64, 3, true, GATED><<<grid, 256, 0, stream>>>(a);
     }
     return hipGetLastError();
 }
