@@ -63,27 +63,35 @@ __device__ __forceinline__ f32x4 mma16(u32x4 w, u32x4 x, f32x4 c) {
                                                       __builtin_bit_cast(f16x8, x), c, 0, 0, 0);
 }
 
-// All tiles of one chunk step: TI row tiles of x times TJ column tiles of w.
-// binary32: four steps of 4; the step is the outer loop, so that consecutive
-// MFMAs add to different tiles.
+// All tiles of one chunk step: TI row tiles of x by the TJ column tiles of each
+// half, into set `SET` of the sums (16 bits) or, binary32 being four steps of 4, into
+// the sets in turn.  A wave needs about 16 MFMAs between two that add to the same
+// registers (one wave a SIMD issuing v_mfma_f32_16x16x4_f32 alone reaches 155
+// TFLOP/s over 16 tiles, 120 over 8 and 104 over 4), so small tiles keep several
+// sets of sums, which are added at the end.
 template <typename T, int TI, int TJ>
-__device__ __forceinline__ void mma_step(const u32x4 (&x)[TI], const u32x4 (&w)[TJ],
-                                         f32x4 (&c)[TI][TJ]) {
-    if constexpr (std::is_same_v<T, float>) {
+constexpr int kSets = 2 * TI * TJ >= 16 ? 1 : 2 * TI * TJ >= 8 ? 2 : sizeof(T) == 4 ? 4 : 2;
+
+template <typename T, int SET, int TI, int TJ, int SETS>
+__device__ __forceinline__ void mma_step(const u32x4 (&x)[TI], const u32x4 (&w)[2][TJ],
+                                         f32x4 (&c)[SETS][2][TI][TJ]) {
+    constexpr int STEPS = std::is_same_v<T, float> ? 4 : 1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < STEPS; ++e)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < TI; ++i)
 #pragma unroll
-                for (int j = 0; j < TJ; ++j)
-                    c[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                        __uint_as_float(w[j][e]), __uint_as_float(x[i][e]), c[i][j], 0, 0, 0);
-    } else {
-#pragma unroll
-        for (int i = 0; i < TI; ++i)
-#pragma unroll
-            for (int j = 0; j < TJ; ++j) c[i][j] = mma16<T>(w[j], x[i], c[i][j]);
-    }
+                for (int j = 0; j < TJ; ++j) {
+                    f32x4 &d = c[(STEPS > 1 ? e : SET) % SETS][h][i][j];
+                    if constexpr (std::is_same_v<T, float>)
+                        d = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[h][j][e]),
+                                                                 __uint_as_float(x[i][e]), d, 0, 0,
+                                                                 0);
+                    else
+                        d = mma16<T>(w[h][j], x[i], d);
+                }
 }
 
 // ---- operands in LDS --------------------------------------------------------------
@@ -119,15 +127,17 @@ struct Panel {
         return ((line & 3) | (((line >> 3) & 1) << 2)) << 1;
     }
 
-    // Line and chunk (inside its line) that this lane moves in its wave's
-    // block i.
-    static __device__ __forceinline__ int line(int i) {
-        return (wave_id() + i * WAVES) * LPB + static_cast<int>(threadIdx.x & 63) / CPL;
+    // Line and chunk (inside its line) that this lane moves in block i of wave
+    // `wave`.
+    static __device__ __forceinline__ int line(int wave, int i) {
+        return (wave + i * WAVES) * LPB + static_cast<int>(threadIdx.x & 63) / CPL;
     }
-    static __device__ __forceinline__ int chunk(int i) {
-        return (static_cast<int>(threadIdx.x & 63) % CPL) ^ swizzle(line(i));
+    static __device__ __forceinline__ int chunk(int wave, int i) {
+        return (static_cast<int>(threadIdx.x & 63) % CPL) ^ swizzle(line(wave, i));
     }
-    static __device__ __forceinline__ int lds_block(int i) { return (wave_id() + i * WAVES) * 1024; }
+    static __device__ __forceinline__ int lds_block(int wave, int i) {
+        return (wave + i * WAVES) * 1024;
+    }
 
     // -- direct loads (buffer_load_dwordx4 .. lds): rows and K tile are whole
     // chunks, bytes outside read as zero because their offset lies past the
@@ -136,33 +146,31 @@ struct Panel {
 
     // Offset of this lane's chunk of block i from the panel's corner, or
     // OUTSIDE where the panel's `rows` rows inside the matrix end before it.
-    static __device__ __forceinline__ uint32_t offset(int i, int64_t rows, int64_t ld) {
-        const int r = KC ? line(i) : chunk(i) * kChunk<T>;
-        const uint32_t at = static_cast<uint32_t>(line(i)) * static_cast<uint32_t>(ld * sizeof(T)) +
-                            static_cast<uint32_t>(chunk(i)) * 16u;
+    static __device__ __forceinline__ uint32_t offset(int wave, int i, int64_t rows, int64_t ld) {
+        const int r = KC ? line(wave, i) : chunk(wave, i) * kChunk<T>;
+        const uint32_t at =
+            static_cast<uint32_t>(line(wave, i)) * static_cast<uint32_t>(ld * sizeof(T)) +
+            static_cast<uint32_t>(chunk(wave, i)) * 16u;
         return r < rows ? at : OUTSIDE;
     }
 
-    // Loads the panel at `base` (its corner, wave-uniform) into `lds`.  `rem`
-    // slices of K are inside (none when rem <= 0: zeros, and no memory is read).
-    // Always INS loads and no branch, so that the number of loads in flight is
-    // the same on every path: where it is not, the compiler waits for all of them
-    // before a fragment read.
-    static __device__ __forceinline__ void load_direct(const char *base, int64_t ld,
-                                                       const uint32_t (&off)[INS], int64_t rem,
+    // Loads the panel at `base` (its corner, wave-uniform) into `lds`; lines are
+    // `pitch` bytes apart.  `rem` slices of K are inside (none when rem <= 0:
+    // zeros, and no memory is read).  Always INS loads and no branch, so that the
+    // number of loads in flight is the same on every path: where it is not, the
+    // compiler waits for all of them before a fragment read.
+    static __device__ __forceinline__ void load_direct(int wave, const char *base, int pitch,
+                                                       const uint32_t (&off)[INS], int rem,
                                                        char *lds) {
-        int length = 0x7fffffff;
-        if constexpr (!KC) {
-            // slices past the last lie past the buffer's end
-            if (rem < kSlice<T>)
-                length = rem > 0 ? static_cast<int>(rem * ld * static_cast<int64_t>(sizeof(T))) : 0;
-        }
+        // not KC: slices past the last lie past the buffer's end
+        const int length = KC || rem >= kSlice<T> ? 0x7fffffff : (rem > 0 ? rem : 0) * pitch;
         const __amdgpu_buffer_rsrc_t rsrc =
             __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, length, 0x00020000);
 #pragma unroll
         for (int i = 0; i < INS; ++i) {
-            const uint32_t at = KC && chunk(i) * kChunk<T> >= rem ? OUTSIDE : off[i];
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, lds + lds_block(i), 16, at, 0, 0, 0);
+            const uint32_t at = KC && chunk(wave, i) * kChunk<T> >= rem ? OUTSIDE : off[i];
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, lds + lds_block(wave, i), 16, at, 0, 0,
+                                                     0);
         }
     }
 
@@ -177,32 +185,29 @@ struct Panel {
         bool edge;             // not KC: the panel crosses the matrix's last column
     };
 
-    static __device__ __forceinline__ void source(Source &f, int64_t rows, int64_t ld) {
+    static __device__ __forceinline__ void source(Source &f, int wave, int64_t rows, int64_t ld) {
         constexpr int E = kChunk<T>;
         f.edge = !KC && rows < ROWS;
 #pragma unroll
         for (int i = 0; i < INS; ++i) {
-            if constexpr (KC) {
-                const int64_t r = line(i) < rows ? line(i) : rows - 1;
-                f.at[i] = r * ld * static_cast<int64_t>(sizeof(T)) + chunk(i) * 16;
-            } else {
-                const int64_t c = chunk(i) * E;
-                const int64_t at = c + E <= rows ? c : rows - E;
-                f.at[i] = (line(i) * ld + at) * static_cast<int64_t>(sizeof(T));
-            }
+            const int64_t n = line(wave, i), c = chunk(wave, i) * E;
+            if constexpr (KC)
+                f.at[i] = ((n < rows ? n : rows - 1) * ld + c) * static_cast<int64_t>(sizeof(T));
+            else
+                f.at[i] = (n * ld + (c + E <= rows ? c : rows - E)) * static_cast<int64_t>(sizeof(T));
         }
     }
 
-    static __device__ __forceinline__ void fetch(const char *base, int64_t ld, int64_t rem,
+    static __device__ __forceinline__ void fetch(int wave, const char *base, int64_t ld, int rem,
                                                  const Source &f, u32x4 (&reg)[INS]) {
-        constexpr int64_t E = kChunk<T>;
+        constexpr int E = kChunk<T>;
         int64_t at[INS];
 #pragma unroll
         for (int i = 0; i < INS; ++i) at[i] = f.at[i];
         if (rem < kSlice<T>) {
 #pragma unroll
             for (int i = 0; i < INS; ++i) {
-                const int64_t over = KC ? chunk(i) * E + E - rem : line(i) + 1 - rem;
+                const int over = (KC ? chunk(wave, i) * E + E : line(wave, i) + 1) - rem;
                 if (over > 0) at[i] -= over * (KC ? 1 : ld) * static_cast<int64_t>(sizeof(T));
             }
         }
@@ -210,36 +215,36 @@ struct Panel {
         for (int i = 0; i < INS; ++i) __builtin_memcpy(&reg[i], base + at[i], 16);
     }
 
-    static __device__ __forceinline__ void store(const u32x4 (&reg)[INS], int64_t rows, int64_t rem,
-                                                 const Source &f, char *lds) {
+    static __device__ __forceinline__ void store(int wave, const u32x4 (&reg)[INS], int64_t rows,
+                                                 int rem, const Source &f, char *lds) {
         constexpr int64_t E = kChunk<T>;
         if (rem < kSlice<T> || f.edge) {
 #pragma unroll
             for (int i = 0; i < INS; ++i) {
                 // elements by which the chunk was read too early
-                int64_t over = chunk(i) * E + E - (KC ? rem : rows);
+                int64_t over = chunk(wave, i) * E + E - (KC ? rem : rows);
                 if (over < 0) over = 0;
-                if (!KC && line(i) >= rem) over = E;
+                if (!KC && line(wave, i) >= rem) over = E;
                 unsigned __int128 x;
                 __builtin_memcpy(&x, &reg[i], 16);
                 x = over < E ? x >> (static_cast<int>(over) * 8 * static_cast<int>(sizeof(T))) : 0;
                 u32x4 v;
                 __builtin_memcpy(&v, &x, 16);
-                put(i, v, lds);
+                put(wave, i, v, lds);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < INS; ++i) put(i, reg[i], lds);
+            for (int i = 0; i < INS; ++i) put(wave, i, reg[i], lds);
         }
     }
 
-    static __device__ __forceinline__ void put(int i, u32x4 v, char *lds) {
-        *reinterpret_cast<u32x4 *>(lds + lds_block(i) + (threadIdx.x & 63) * 16) = v;
+    static __device__ __forceinline__ void put(int wave, int i, u32x4 v, char *lds) {
+        *reinterpret_cast<u32x4 *>(lds + lds_block(wave, i) + (threadIdx.x & 63) * 16) = v;
     }
 
     // -- element by element, at once: for lines shorter than a chunk.
-    static __device__ __forceinline__ void copy_elements(const char *base, int64_t ld, int64_t rows,
-                                                         int64_t rem, char *lds) {
+    static __device__ __forceinline__ void copy_elements(int wave, const char *base, int64_t ld,
+                                                         int64_t rows, int rem, char *lds) {
         constexpr int E = kChunk<T>;
         const T *p = reinterpret_cast<const T *>(base);
 #pragma unroll
@@ -247,15 +252,15 @@ struct Panel {
             T t[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int64_t x = chunk(i) * E + e;
-                const int64_t k = KC ? x : line(i), r = KC ? line(i) : x;
+                const int64_t x = chunk(wave, i) * E + e;
+                const int64_t k = KC ? x : line(wave, i), r = KC ? line(wave, i) : x;
                 const int64_t kk = k < rem ? k : rem - 1, rr = r < rows ? r : rows - 1;
                 const T v = p[KC ? rr * ld + kk : kk * ld + rr];
                 t[e] = k < rem ? v : static_cast<T>(0.0f);
             }
             u32x4 v;
             __builtin_memcpy(&v, t, 16);
-            put(i, v, lds);
+            put(wave, i, v, lds);
         }
     }
 
@@ -376,11 +381,17 @@ __device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, int split
 // BN / 2 columns, or, gated, the same columns of the second weight: z and u of an
 // element sit in the same lane and H is finished without a trip to memory.
 //
-// S stages of LDS hold a K tile of both operands each.  DIRECT: iteration s
-// waits for its own loads of tile s, meets the other waves, issues the loads of
-// tile s + S - 1 into the stage whose tile s - 1 every wave has finished, and
-// computes tile s.  Otherwise (S = 2) tile s + 1 waits in registers while tile s
-// is computed, and is stored behind it.
+// S stages of LDS hold a K tile of both operands each.  A K tile is two MFMA
+// steps, and the fragments of a step are read while the step before it is
+// computed, so that one wave a SIMD keeps its matrix unit busy.  Iteration s:
+//   read step 1 of tile s; compute step 0;
+//   wait for this wave's loads of tile s + 1, meet the other waves: tile s + 1 is
+//   in LDS, and every wave has read tile s;
+//   DIRECT: load tile s + S into the stage of tile s;
+//   read step 0 of tile s + 1; compute step 1.
+// Without DIRECT (S = 2) tile s + 1 waits in registers until it is stored,
+// before the meeting, into the stage of tile s - 1.
+// (Reading both steps of tile s after the meeting: 1024^3 in binary32 31.9 us.)
 
 template <typename T, bool AKC, bool BKC, int BM, int BN>
 struct TileShape {
@@ -394,44 +405,75 @@ struct TileShape {
     static constexpr int per_cu(int stages) { return stages * STAGE <= 80 * 1024 ? 2 : 1; }
 };
 
-// Where the operands of this workgroup's tile start.
+// A workgroup's way along K: the corners of its panels at the current K tile, and
+// the slices left.  The steps are few scalar instructions, since with one wave a
+// SIMD every one of them delays the MFMAs (addresses worked out anew for each tile
+// took half the time of a 64 x 64 tile in binary32).
 template <typename T, bool AKC, bool BKC>
-struct Corner {
+struct Walk {
     const char *a, *b0, *b1;
-    int64_t lda, ldb;      // bytes
+    int64_t step_a, step_b;    // bytes per K tile
+    int rem;                   // slices left in this segment; then none
+    int then;                  // slices of the second segment that follow
 
-    __device__ __forceinline__ Corner(const TileArgs &p, int batch, int64_t m0, int64_t n0,
-                                      int64_t n1, bool gated) {
+    // K tiles first .. first + count - 1 of the concatenated segments.
+    __device__ __forceinline__ Walk(const TileArgs &p, int batch, int64_t m0, int64_t n0,
+                                    int64_t n1, bool gated, int first, int count) {
         constexpr int64_t E = sizeof(T);
-        lda = p.lda * E;
-        ldb = p.ldb * E;
-        a = static_cast<const char *>(p.A) + (batch ? p.a_batch * E : 0) + m0 * (AKC ? lda : E);
+        constexpr int L = kSlice<T>;
+        a = static_cast<const char *>(p.A) + (batch ? p.a_batch * E : 0) +
+            m0 * (AKC ? p.lda * E : E);
         const char *b = static_cast<const char *>(p.B[0]) + (batch ? p.b_batch * E : 0);
-        b0 = b + n0 * (BKC ? ldb : E);
-        b1 = (gated ? static_cast<const char *>(p.B[1]) : b) + n1 * (BKC ? ldb : E);
+        b0 = b + n0 * (BKC ? p.ldb * E : E);
+        b1 = (gated ? static_cast<const char *>(p.B[1]) : b) + n1 * (BKC ? p.ldb * E : E);
+        step_a = L * (AKC ? E : p.lda * E);
+        step_b = L * (BKC ? E : p.ldb * E);
+        const int K = static_cast<int>(p.K);
+        int in = p.seg_tiles - first;          // tiles in the first segment
+        int at = first;
+        if (in <= 0 && count > 0) {            // none: this part lies in the second
+            second(p);
+            at = -in;
+            in = count;
+            then = 0;
+        } else {
+            const int more = count - in;
+            then = more <= 0 ? 0 : more * L < K ? more * L : K;
+            in = more <= 0 ? count : in;
+        }
+        a += at * step_a;
+        b0 += at * step_b;
+        b1 += at * step_b;
+        rem = K - at * L < in * L ? K - at * L : in * L;
+    }
+
+    __device__ __forceinline__ void second(const TileArgs &p) {
+        const int64_t d = static_cast<const char *>(p.B[1]) - static_cast<const char *>(p.B[0]);
+        a += p.a_seg * static_cast<int64_t>(sizeof(T));
+        b0 += d;
+        b1 += d;
+    }
+
+    __device__ __forceinline__ void next(const TileArgs &p) {
+        a += step_a;
+        b0 += step_b;
+        b1 += step_b;
+        rem -= kSlice<T>;
+        if (then > 0 && rem <= 0) {
+            a -= p.seg_tiles * step_a;
+            b0 -= p.seg_tiles * step_b;
+            b1 -= p.seg_tiles * step_b;
+            second(p);
+            rem = then;
+            then = 0;
+        }
     }
 };
 
-// The K tile s: slices left in its segment, and its byte distance from the
-// corner of each operand.
-template <typename T, bool AKC, bool BKC>
-struct KTile {
-    int64_t rem, da, db;
-    __device__ __forceinline__ KTile(const TileArgs &p, int64_t lda, int64_t ldb, int s) {
-        constexpr int64_t E = sizeof(T);
-        const bool second = s >= p.seg_tiles;
-        const int64_t k0 = static_cast<int64_t>(second ? s - p.seg_tiles : s) * kSlice<T>;
-        rem = p.K - k0;
-        da = k0 * (AKC ? E : lda) + (second ? p.a_seg * E : 0);
-        db = k0 * (BKC ? E : ldb);
-        if (second) db += static_cast<const char *>(p.B[1]) - static_cast<const char *>(p.B[0]);
-    }
-};
-
-// f(0), f(1), .. (as constants) until one returns false.
+// f(0), f(1), .. (as constants) until one returns false; whether none did.
 template <int... U, typename F>
-__device__ __forceinline__ void for_each(std::integer_sequence<int, U...>, F f) {
-    (void)(f(std::integral_constant<int, U>{}) && ...);
+__device__ __forceinline__ bool for_each(std::integer_sequence<int, U...>, F f) {
+    return (f(std::integral_constant<int, U>{}) && ...);
 }
 
 template <typename T, bool AKC, bool BKC, int BM, int BN, int S, bool DIRECT, bool GATED>
@@ -470,114 +512,142 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
     constexpr int NB = GATED ? BN / 2 : BN;
     const int64_t m0 = static_cast<int64_t>(tm) * BM;
     const int64_t n0 = static_cast<int64_t>(tn) * NB, n1 = GATED ? n0 : n0 + BN / 2;
-    const Corner<T, AKC, BKC> at(p, batch, m0, n0, n1, GATED);
     const int64_t rows_a = p.M - m0, rows_b0 = p.N - n0, rows_b1 = p.N - n1;
 
     const int first = split * p.tiles_per_split;
     const int left = p.k_tiles - first;
     const int count = left < p.tiles_per_split ? left : p.tiles_per_split;
 
+    Walk<T, AKC, BKC> walk(p, batch, m0, n0, n1, GATED, first, count);
+
     const int wave = wave_id();
     const int wm = wave >> 1, wn = wave & 1;
-    f32x4 c0[TI][TJ] = {}, c1[TI][TJ] = {};
+    constexpr int SETS = kSets<T, TI, TJ>;
+    f32x4 c[SETS][2][TI][TJ] = {};
 
-    auto compute = [&](const char *st) __attribute__((always_inline)) {
+    u32x4 x[2][TI], w[2][2][TJ];
+    auto read = [&](auto step, const char *st) __attribute__((always_inline)) {
+        constexpr int P = decltype(step)::value;
 #pragma unroll
-        for (int step = 0; step < 2; ++step) {
-            u32x4 x[TI], w0[TJ], w1[TJ];
+        for (int i = 0; i < TI; ++i)
+            x[P][i] = PA::fragment(st, 0, wm * (BM / 2) + i * 16, P);
 #pragma unroll
-            for (int i = 0; i < TI; ++i)
-                x[i] = PA::fragment(st, 0, wm * (BM / 2) + i * 16, step);
-#pragma unroll
-            for (int j = 0; j < TJ; ++j) {
-                w0[j] = PB::fragment(st, PA::BYTES, wn * HC + j * 16, step);
-                w1[j] = PB::fragment(st, PA::BYTES + PB::BYTES, wn * HC + j * 16, step);
-            }
-            mma_step<T, TI, TJ>(x, w0, c0);
-            mma_step<T, TI, TJ>(x, w1, c1);
+        for (int j = 0; j < TJ; ++j) {
+            w[P][0][j] = PB::fragment(st, PA::BYTES, wn * HC + j * 16, P);
+            w[P][1][j] = PB::fragment(st, PA::BYTES + PB::BYTES, wn * HC + j * 16, P);
         }
+        // reads first: the compiler would sink them below the MFMAs
+        __builtin_amdgcn_sched_barrier(0);
     };
+    constexpr std::integral_constant<int, 0> step0;
+    constexpr std::integral_constant<int, 1> step1;
 
     if constexpr (DIRECT) {
         uint32_t oa[PA::INS], ob0[PB::INS], ob1[PB::INS];
 #pragma unroll
-        for (int i = 0; i < PA::INS; ++i) oa[i] = PA::offset(i, rows_a, p.lda);
+        for (int i = 0; i < PA::INS; ++i) oa[i] = PA::offset(wave, i, rows_a, p.lda);
 #pragma unroll
         for (int i = 0; i < PB::INS; ++i) {
-            ob0[i] = PB::offset(i, rows_b0, p.ldb);
-            ob1[i] = PB::offset(i, rows_b1, p.ldb);
+            ob0[i] = PB::offset(wave, i, rows_b0, p.ldb);
+            ob1[i] = PB::offset(wave, i, rows_b1, p.ldb);
         }
+        const int pitch_a = static_cast<int>(p.lda * static_cast<int64_t>(sizeof(T)));
+        const int pitch_b = static_cast<int>(p.ldb * static_cast<int64_t>(sizeof(T)));
         // Tiles past the last are "loaded" too, as zeros from nowhere, which keeps
         // the count of loads in flight.  The waits count loads in tile order: none
         // may be moved past another's.
-        auto issue = [&](int s, char *st) __attribute__((always_inline)) {
-            const KTile<T, AKC, BKC> t(p, at.lda, at.ldb, first + s);
-            const int64_t rem = s < count ? t.rem : 0;
-            PA::load_direct(at.a + t.da, p.lda, oa, rem, st);
-            PB::load_direct(at.b0 + t.db, p.ldb, ob0, rem, st + PA::BYTES);
-            PB::load_direct(at.b1 + t.db, p.ldb, ob1, rem, st + PA::BYTES + PB::BYTES);
+        auto issue = [&](char *st) __attribute__((always_inline)) {
+            PA::load_direct(wave, walk.a, pitch_a, oa, walk.rem, st);
+            PB::load_direct(wave, walk.b0, pitch_b, ob0, walk.rem, st + PA::BYTES);
+            PB::load_direct(wave, walk.b1, pitch_b, ob1, walk.rem, st + PA::BYTES + PB::BYTES);
+            walk.next(p);
             __builtin_amdgcn_sched_barrier(0);
         };
-        for_each(std::make_integer_sequence<int, S - 1>{},
-                   [&](auto u) __attribute__((always_inline)) {
-                       issue(decltype(u)::value, stage(u));
-                       return true;
-                   });
-        for (int s = 0; s < count; s += S) {
+        for_each(std::make_integer_sequence<int, S>{}, [&](auto u) __attribute__((always_inline)) {
+            issue(stage(u));
+            return true;
+        });
+        stage_sync<(S - 1) * X::LOADS>();
+        read(step0, st0);
+        auto iteration = [&](auto u) __attribute__((always_inline)) {
+            constexpr int U = decltype(u)::value;
+            read(step1, stage(u));
+            mma_step<T, 0>(x[0], w[0], c);
+            stage_sync<(S - 2) * X::LOADS>();
+            issue(stage(u));
+            read(step0, stage(std::integral_constant<int, U + 1>{}));
+            mma_step<T, 1>(x[1], w[1], c);
+        };
+        // Whole rounds of the ring, then what is left: a way out of the middle of
+        // the loop, which the compiler might join to its head, would make it wait
+        // for every load there.
+        int s = 0;
+        for (; s + S <= count; s += S)
             for_each(std::make_integer_sequence<int, S>{},
-                       [&](auto u) __attribute__((always_inline)) {
-                           constexpr int U = decltype(u)::value;
-                           if (s + U >= count) return false;
-                           stage_sync<(S - 2) * X::LOADS>();
-                           issue(s + U + S - 1, stage(std::integral_constant<int, U + S - 1>{}));
-                           compute(stage(u));
-                           return true;
-                       });
-        }
+                     [&](auto u) __attribute__((always_inline)) {
+                         iteration(u);
+                         return true;
+                     });
+        for_each(std::make_integer_sequence<int, S - 1>{},
+                 [&](auto u) __attribute__((always_inline)) {
+                     if (s + decltype(u)::value >= count) return false;
+                     iteration(u);
+                     return true;
+                 });
     } else {
         typename PA::Source fa;
         typename PB::Source fb0, fb1;
-        PA::source(fa, rows_a, p.lda);
-        PB::source(fb0, rows_b0, p.ldb);
-        PB::source(fb1, rows_b1, p.ldb);
+        PA::source(fa, wave, rows_a, p.lda);
+        PB::source(fb0, wave, rows_b0, p.ldb);
+        PB::source(fb1, wave, rows_b1, p.ldb);
         u32x4 ra[PA::INS], rb0[PB::INS], rb1[PB::INS];
-        auto fetch = [&](int s) __attribute__((always_inline)) {
-            const KTile<T, AKC, BKC> t(p, at.lda, at.ldb, first + s);
-            PA::fetch(at.a + t.da, p.lda, t.rem, fa, ra);
-            PB::fetch(at.b0 + t.db, p.ldb, t.rem, fb0, rb0);
-            PB::fetch(at.b1 + t.db, p.ldb, t.rem, fb1, rb1);
-        };
-        auto store = [&](int s, char *st) __attribute__((always_inline)) {
-            const KTile<T, AKC, BKC> t(p, at.lda, at.ldb, first + s);
-            PA::store(ra, rows_a, t.rem, fa, st);
-            PB::store(rb0, rows_b0, t.rem, fb0, st + PA::BYTES);
-            PB::store(rb1, rows_b1, t.rem, fb1, st + PA::BYTES + PB::BYTES);
-        };
-        auto iteration = [&](int s, const char *st, char *next) __attribute__((always_inline)) {
-            __syncthreads();
-            if (s + 1 < count) fetch(s + 1);
+        int rem = 0;       // slices of the tile in registers
+        auto fetch = [&]() __attribute__((always_inline)) {
+            rem = walk.rem;
+            PA::fetch(wave, walk.a, p.lda, rem, fa, ra);
+            PB::fetch(wave, walk.b0, p.ldb, rem, fb0, rb0);
+            PB::fetch(wave, walk.b1, p.ldb, rem, fb1, rb1);
+            walk.next(p);
             __builtin_amdgcn_sched_barrier(0);
-            compute(st);
+        };
+        auto store = [&](char *st) __attribute__((always_inline)) {
+            PA::store(wave, ra, rows_a, rem, fa, st);
+            PB::store(wave, rb0, rows_b0, rem, fb0, st + PA::BYTES);
+            PB::store(wave, rb1, rows_b1, rem, fb1, st + PA::BYTES + PB::BYTES);
+        };
+        auto iteration = [&](const char *st, char *next) __attribute__((always_inline)) {
+            read(step1, st);
+            mma_step<T, 0>(x[0], w[0], c);
             __builtin_amdgcn_sched_barrier(0);
-            if (s + 1 < count) store(s + 1, next);
+            store(next);
+            stage_sync<0>();
+            fetch();
+            read(step0, next);
+            mma_step<T, 1>(x[1], w[1], c);
         };
         if ((AKC ? p.K : p.M) < kChunk<T> || (BKC ? p.K : p.N) < kChunk<T>) {
             for (int s = 0; s < count; ++s) {
-                const KTile<T, AKC, BKC> t(p, at.lda, at.ldb, first + s);
                 __syncthreads();
-                PA::copy_elements(at.a + t.da, p.lda, rows_a, t.rem, st0);
-                PB::copy_elements(at.b0 + t.db, p.ldb, rows_b0, t.rem, st0 + PA::BYTES);
-                PB::copy_elements(at.b1 + t.db, p.ldb, rows_b1, t.rem,
+                PA::copy_elements(wave, walk.a, p.lda, rows_a, walk.rem, st0);
+                PB::copy_elements(wave, walk.b0, p.ldb, rows_b0, walk.rem, st0 + PA::BYTES);
+                PB::copy_elements(wave, walk.b1, p.ldb, rows_b1, walk.rem,
                                   st0 + PA::BYTES + PB::BYTES);
+                walk.next(p);
                 __syncthreads();
-                compute(st0);
+                read(step0, st0);
+                read(step1, st0);
+                mma_step<T, 0>(x[0], w[0], c);
+                mma_step<T, 1>(x[1], w[1], c);
             }
         } else if (count > 0) {
-            fetch(0);
-            store(0, st0);
+            fetch();
+            store(st0);
+            fetch();
+            stage_sync<0>();
+            read(step0, st0);
             for (int s = 0; s < count; s += 2) {
-                iteration(s, st0, st1);
-                if (s + 1 < count) iteration(s + 1, st1, st0);
+                iteration(st0, st1);
+                if (s + 1 < count) iteration(st1, st0);
             }
         }
     }
@@ -586,8 +656,16 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
     // the stages are reused: a wave's sums take their share of st0 or st1.
     stage_sync<0>();
     char *mine = (wave < 2 ? st0 : st1) + (wave & 1) * X::MINE;
-    epi_put<HC>(mine, c0, 0);
-    epi_put<HC>(mine, c1, 1);
+#pragma unroll
+    for (int a = 1; a < SETS; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) c[0][h][i][j] += c[a][h][i][j];
+    epi_put<HC>(mine, c[0][0], 0);
+    epi_put<HC>(mine, c[0][1], 1);
     epi_rows<T, GATED, HC, BM / 2>(p, batch, split, mine, m0 + wm * (BM / 2), n0 + wn * HC,
                                    n1 + wn * HC);
 }
