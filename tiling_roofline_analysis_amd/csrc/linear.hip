@@ -229,6 +229,7 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
     TilePlan best{};
     double best_us = 0.0;
     for (const Class &c : classes) {
+        if (c.bm == 128 && !direct && dtype == TRA_DTYPE_F32) continue;   // not built
         const int64_t tiles = std::max<int64_t>(
             1, ceil_div(M, c.bm) * ceil_div(N, gated ? c.bn / 2 : c.bn) * batch);
         for (int64_t want = 1; want <= 32 && want <= k_tiles; ++want) {

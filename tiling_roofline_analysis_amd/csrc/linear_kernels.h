@@ -38,11 +38,12 @@ __device__ __forceinline__ int wave_id() {
 // would wait for every load in flight.)  s_waitcnt's gfx9 encoding: vmcnt in
 // bits 3:0 and 15:14, expcnt 6:4 (not waited for), lgkmcnt 11:8.  The empty asm
 // keeps the compiler from moving memory accesses across it.
-template <int VM>
+template <int VM, bool LOADS = true>
 __device__ __forceinline__ void stage_sync() {
     static_assert(VM >= 0 && VM < 64, "vmcnt range");
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4));
+    // (not LOADS: vmcnt is not waited for)
+    __builtin_amdgcn_s_waitcnt(LOADS ? (VM & 15) | ((VM >> 4) << 14) | (7 << 4) : 0xc07f);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -264,6 +265,9 @@ struct Panel {
         }
     }
 
+    // LDS reads of a fragment (of 32-bit words the compiler pairs two)
+    static constexpr int READS = KC ? 1 : 2;
+
     // -- fragments: rows row0 .. + 15 (a multiple of 16), MFMA step `step`, of the
     // panel `panel` bytes into the stage `st`.  Each address is one offset from
     // the stage's array: past a few steps of pointer arithmetic the compiler
@@ -413,6 +417,7 @@ template <typename T, bool AKC, bool BKC>
 struct Walk {
     const char *a, *b0, *b1;
     int64_t step_a, step_b;    // bytes per K tile
+    int64_t jump_a, jump_b;    // from the first segment's last tile to the second
     int rem;                   // slices left in this segment; then none
     int then;                  // slices of the second segment that follow
 
@@ -428,11 +433,18 @@ struct Walk {
         b1 = (gated ? static_cast<const char *>(p.B[1]) : b) + n1 * (BKC ? p.ldb * E : E);
         step_a = L * (AKC ? E : p.lda * E);
         step_b = L * (BKC ? E : p.ldb * E);
+        const int64_t to_a = p.a_seg * E;
+        const int64_t to_b =
+            static_cast<const char *>(p.B[1]) - static_cast<const char *>(p.B[0]);
+        jump_a = to_a - (p.seg_tiles - 1) * step_a;
+        jump_b = to_b - (p.seg_tiles - 1) * step_b;
         const int K = static_cast<int>(p.K);
         int in = p.seg_tiles - first;          // tiles in the first segment
         int at = first;
         if (in <= 0 && count > 0) {            // none: this part lies in the second
-            second(p);
+            a += to_a;
+            b0 += to_b;
+            b1 += to_b;
             at = -in;
             in = count;
             then = 0;
@@ -447,28 +459,34 @@ struct Walk {
         rem = K - at * L < in * L ? K - at * L : in * L;
     }
 
-    __device__ __forceinline__ void second(const TileArgs &p) {
-        const int64_t d = static_cast<const char *>(p.B[1]) - static_cast<const char *>(p.B[0]);
-        a += p.a_seg * static_cast<int64_t>(sizeof(T));
-        b0 += d;
-        b1 += d;
-    }
-
-    __device__ __forceinline__ void next(const TileArgs &p) {
-        a += step_a;
-        b0 += step_b;
-        b1 += step_b;
+    __device__ __forceinline__ void next() {
         rem -= kSlice<T>;
-        if (then > 0 && rem <= 0) {
-            a -= p.seg_tiles * step_a;
-            b0 -= p.seg_tiles * step_b;
-            b1 -= p.seg_tiles * step_b;
-            second(p);
-            rem = then;
-            then = 0;
-        }
+        // no branch: the tile's loads are to mix with its MFMAs
+        const bool jump = (rem <= 0) & (then > 0);
+        a += jump ? jump_a : step_a;
+        b0 += jump ? jump_b : step_b;
+        b1 += jump ? jump_b : step_b;
+        rem = jump ? then : rem;
+        then = jump ? 0 : then;
     }
 };
+
+// Orders what stands since the last scheduling barrier: after each MFMA a share
+// of the LDS reads (all within the first half of the MFMAs, so that they are done
+// by the end) and of the loads.  A wave issues them while its MFMA runs; in a
+// block of their own they would leave the matrix unit idle, and left alone the
+// compiler sinks the reads below the MFMAs, to where their results are waited for.
+template <int MFMAS, int READS, int LOADS>
+__device__ __forceinline__ void interleave() {
+    constexpr int HALF = MFMAS / 2 > 0 ? MFMAS / 2 : 1;
+#pragma unroll
+    for (int i = 0; i < MFMAS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        constexpr int R = (READS + HALF - 1) / HALF, L = (LOADS + MFMAS - 1) / MFMAS;
+        if (i * R < READS) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+        if (i * L < LOADS) __builtin_amdgcn_sched_group_barrier(0x010, L, 0);
+    }
+}
 
 // f(0), f(1), .. (as constants) until one returns false; whether none did.
 template <int... U, typename F>
@@ -536,9 +554,10 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
             w[P][0][j] = PB::fragment(st, PA::BYTES, wn * HC + j * 16, P);
             w[P][1][j] = PB::fragment(st, PA::BYTES + PB::BYTES, wn * HC + j * 16, P);
         }
-        // reads first: the compiler would sink them below the MFMAs
-        __builtin_amdgcn_sched_barrier(0);
     };
+    // LDS instructions of one step's fragments, MFMAs of a step
+    constexpr int READS = PA::READS * TI + 2 * PB::READS * TJ;
+    constexpr int MFMAS = 2 * TI * TJ * (sizeof(T) == 4 ? 4 : 1);
     constexpr std::integral_constant<int, 0> step0;
     constexpr std::integral_constant<int, 1> step1;
 
@@ -560,11 +579,11 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
             PA::load_direct(wave, walk.a, pitch_a, oa, walk.rem, st);
             PB::load_direct(wave, walk.b0, pitch_b, ob0, walk.rem, st + PA::BYTES);
             PB::load_direct(wave, walk.b1, pitch_b, ob1, walk.rem, st + PA::BYTES + PB::BYTES);
-            walk.next(p);
-            __builtin_amdgcn_sched_barrier(0);
+            walk.next();
         };
         for_each(std::make_integer_sequence<int, S>{}, [&](auto u) __attribute__((always_inline)) {
             issue(stage(u));
+            __builtin_amdgcn_sched_barrier(0);
             return true;
         });
         stage_sync<(S - 1) * X::LOADS>();
@@ -573,10 +592,13 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
             constexpr int U = decltype(u)::value;
             read(step1, stage(u));
             mma_step<T, 0>(x[0], w[0], c);
+            interleave<MFMAS, READS, 0>();
             stage_sync<(S - 2) * X::LOADS>();
             issue(stage(u));
             read(step0, stage(std::integral_constant<int, U + 1>{}));
             mma_step<T, 1>(x[1], w[1], c);
+            interleave<MFMAS, READS, X::LOADS>();
+            __builtin_amdgcn_sched_barrier(0);
         };
         // Whole rounds of the ring, then what is left: a way out of the middle of
         // the loop, which the compiler might join to its head, would make it wait
@@ -607,8 +629,7 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
             PA::fetch(wave, walk.a, p.lda, rem, fa, ra);
             PB::fetch(wave, walk.b0, p.ldb, rem, fb0, rb0);
             PB::fetch(wave, walk.b1, p.ldb, rem, fb1, rb1);
-            walk.next(p);
-            __builtin_amdgcn_sched_barrier(0);
+            walk.next();
         };
         auto store = [&](char *st) __attribute__((always_inline)) {
             PA::store(wave, ra, rows_a, rem, fa, st);
@@ -618,12 +639,16 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
         auto iteration = [&](const char *st, char *next) __attribute__((always_inline)) {
             read(step1, st);
             mma_step<T, 0>(x[0], w[0], c);
+            interleave<MFMAS, READS, 0>();
             __builtin_amdgcn_sched_barrier(0);
             store(next);
-            stage_sync<0>();
+            stage_sync<0, false>();
             fetch();
+            __builtin_amdgcn_sched_barrier(0);
             read(step0, next);
             mma_step<T, 1>(x[1], w[1], c);
+            interleave<MFMAS, READS, 0>();
+            __builtin_amdgcn_sched_barrier(0);
         };
         if ((AKC ? p.K : p.M) < kChunk<T> || (BKC ? p.K : p.N) < kChunk<T>) {
             for (int s = 0; s < count; ++s) {
@@ -632,7 +657,7 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
                 PB::copy_elements(wave, walk.b0, p.ldb, rows_b0, walk.rem, st0 + PA::BYTES);
                 PB::copy_elements(wave, walk.b1, p.ldb, rows_b1, walk.rem,
                                   st0 + PA::BYTES + PB::BYTES);
-                walk.next(p);
+                walk.next();
                 __syncthreads();
                 read(step0, st0);
                 read(step1, st0);
@@ -680,10 +705,12 @@ hipError_t launch_tile(const TilePlan &plan, const TileArgs &a, hipStream_t stre
     // Direct loads: two workgroups a CU, or, where the grid gives a CU no more
     // than one, stages enough that a second does not fit (the dispatcher would put
     // two on one CU and leave another idle).
+    // Binary32 through registers has no 128 x 128 tile: it needs more than 256 VGPRs.
     if (plan.bm == 128) {
-        if (!plan.direct)
-            linear_tile<T, AKC, BKC, 128, 128, 2, false, GATED><<<grid, 256, 0, stream>>>(a);
-        else if (plan.deep)
+        if (!plan.direct) {
+            if constexpr (sizeof(T) == 4) return hipErrorInvalidValue;
+            else linear_tile<T, AKC, BKC, 128, 128, 2, false, GATED><<<grid, 256, 0, stream>>>(a);
+        } else if (plan.deep)
             linear_tile<T, AKC, BKC, 128, 128, 4, true, GATED><<<grid, 256, 0, stream>>>(a);
         else
             linear_tile<T, AKC, BKC, 128, 128, 2, true, GATED><<<grid, 256, 0, stream>>>(a);
