@@ -249,6 +249,22 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
             }
         }
     }
+    // Few rows: the weights' bytes at about 4.8 TB/s, or 25 GB/s a CU where there
+    // are fewer strips than CUs can saturate memory from, plus a start.
+    const int64_t b = elem_bytes(dtype);
+    const int64_t cols = form == tra::kFormKK ? 16 : 64 / b;
+    if (form != tra::kFormNN && M <= 16 && K >= 16 / b && N >= 4 / b) {
+        const double strips = static_cast<double>(ceil_div(N, cols));
+        const double bytes = static_cast<double>(segs) * K * N * b * (gated ? 2 : 1);
+        const double us = 2.0 + bytes / std::min(4.8e6, strips * 2.5e4);
+        if (us < best_us) {
+            best = TilePlan{};
+            best.few = true;
+            best.bm = 16;
+            best.bn = static_cast<int>(gated ? 2 * cols : cols);
+            best.splits = 1;
+        }
+    }
     best.form = form;
     best.gated = gated;
     best.direct = direct;
@@ -628,8 +644,9 @@ tra_status tra_linear_describe(const tra_linear_args *args, char *buf, size_t le
         return TRA_OK;
     }
     const TilePlan t = plan_forward(*args);
-    std::snprintf(buf, len, "kernel=linear_tile tile=%dx%d loads=%s splits=%d workspace_bytes=%zu",
-                  t.bm, t.bn, t.direct ? "direct" : "registers", t.splits, t.partial_bytes);
+    std::snprintf(buf, len, "kernel=%s tile=%dx%d loads=%s splits=%d workspace_bytes=%zu",
+                  t.few ? "linear_few" : "linear_tile", t.bm, t.bn,
+                  t.few || !t.direct ? "registers" : "direct", t.splits, t.partial_bytes);
     return TRA_OK;
 }
 

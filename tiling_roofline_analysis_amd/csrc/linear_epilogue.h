@@ -121,8 +121,8 @@ __device__ __forceinline__ void activate_slope(int act, const float (&z)[V], flo
 template <typename T, int V>
 __device__ __forceinline__ void load_row(const T *p, int64_t valid, bool vec, float (&v)[V]) {
     constexpr int C = kChunk<T>;
-    static_assert(V % C == 0, "whole chunks");
-    if (vec && valid >= V) {
+    static_assert(V == 1 || V % C == 0, "one element or whole chunks");
+    if (V > 1 && vec && valid >= V) {
 #pragma unroll
         for (int c = 0; c < V / C; ++c) {
             T t[C];
@@ -140,8 +140,8 @@ __device__ __forceinline__ void load_row(const T *p, int64_t valid, bool vec, fl
 template <typename T, int V>
 __device__ __forceinline__ void store_row(T *p, int64_t valid, bool vec, const float (&v)[V]) {
     constexpr int C = kChunk<T>;
-    static_assert(V % C == 0, "whole chunks");
-    if (vec && valid >= V) {
+    static_assert(V == 1 || V % C == 0, "one element or whole chunks");
+    if (V > 1 && vec && valid >= V) {
 #pragma unroll
         for (int c = 0; c < V / C; ++c) {
             T t[C];
@@ -158,7 +158,7 @@ __device__ __forceinline__ void store_row(T *p, int64_t valid, bool vec, const f
     }
 }
 
-// Finishes V = one chunk of elements of row m from column n on: z (and u)
+// Finishes V (one, or a chunk of) elements of row m from column n on: z (and u)
 // are the whole sums.  The one rounding to T is at the store; bias, activation
 // and residual are binary32.
 template <typename T, bool GATED, int V>

@@ -65,6 +65,7 @@ enum TileForm {
 struct TilePlan {
     TileForm form;
     bool gated;
+    bool few;              // the kernel for few rows; bn: columns per workgroup
     int bm, bn;            // tile of P (gated: bn / 2 columns of each of z, u)
     bool direct;           // operands go straight into LDS (16-byte aligned)
     bool deep;             // direct: one workgroup a CU, with more stages

@@ -695,6 +695,158 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
                                    n1 + wn * HC);
 }
 
+// ---- the kernel for few rows --------------------------------------------------------------
+//
+// M <= 16 (tokens being decoded): the weights are read once and nothing else
+// counts, so they go from memory straight into the MFMA's registers, with no LDS
+// and no second launch.  A workgroup of eight waves owns a strip of columns as
+// wide as 64 bytes of a weight row (16 columns where the weights are
+// k-contiguous) and shares K out over its waves; the sums meet in LDS.
+//   k-contiguous   lane l loads chunk l / 16 of column l % 16: an operand as it
+//                  stands;
+//   else           lane l loads 4 bytes (two columns, or one in binary32) of each
+//                  of 8 (4) slices, and v_perm makes two operands of them.
+// Loads take any alignment, in bounds: columns past the last read the last, and
+// what lies past K is zeroed.
+template <typename T, bool BKC>
+struct FewShape {
+    static constexpr int WAVES = 8;
+    static constexpr int V = BKC ? 1 : 4 / static_cast<int>(sizeof(T));   // columns per lane
+    static constexpr int COLS = 16 * V;
+    static constexpr int STEP = 4 * kChunk<T>;     // slices per MFMA step
+    static constexpr int U = 4;                    // steps loaded at a time
+    static constexpr int ROUND = U * STEP;         // slices per wave and round
+};
+
+// The chunk at slices k .. of a line of K >= one chunk of elements, zero past
+// its end.
+template <typename T>
+__device__ __forceinline__ u32x4 chunk_to_end(const T *line, int k, int K) {
+    constexpr int E = kChunk<T>;
+    const int over = k + E - K;
+    u32x4 v;
+    __builtin_memcpy(&v, line + (over > 0 ? K - E : k), 16);
+    unsigned __int128 x;
+    __builtin_memcpy(&x, &v, 16);
+    x = over <= 0 ? x : over < E ? x >> (over * 8 * static_cast<int>(sizeof(T))) : 0;
+    __builtin_memcpy(&v, &x, 16);
+    return v;
+}
+
+template <typename T, bool BKC, bool GATED>
+__global__ __launch_bounds__(512) void linear_few(const TileArgs p) {
+    using F = FewShape<T, BKC>;
+    constexpr int E = kChunk<T>, V = F::V, U = F::U, W = GATED ? 2 : 1;
+    __shared__ __align__(16) float sums[F::WAVES][W * V][256];
+    lds_poison(&sums[0][0][0], F::WAVES * W * V * 256);
+    const int wave = wave_id(), l16 = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+    const int M = static_cast<int>(p.M), N = static_cast<int>(p.N), K = static_cast<int>(p.K);
+    const int n0 = xcd_remap32(blockIdx.x, gridDim.x) * F::COLS;
+    const T *xrow = static_cast<const T *>(p.A) + (l16 < M ? l16 : M - 1) * p.lda;
+    // k-contiguous: this lane's column; else its first, moved back by one where
+    // two columns would cross the last
+    const int want = n0 + l16 * V, col = want + V <= N ? want : N - V;
+    f32x4 c[W][V] = {};
+
+    for (int seg = 0; seg < p.segs; ++seg) {
+        const T *x = xrow + seg * p.a_seg;
+        const T *w[W];
+        for (int h = 0; h < W; ++h)
+            w[h] = static_cast<const T *>(p.B[GATED ? h : seg]) + (BKC ? col * p.ldb : col);
+
+        // Rounds of U steps: `whole` where all of them lie inside K.
+        auto round = [&](int k0, auto whole) __attribute__((always_inline)) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            u32x4 a[U], b[W][V][U];
+#pragma unroll
+            for (int h = 0; h < W; ++h)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int k = k0 + u * F::STEP + g * E;
+                    if constexpr (BKC) {
+                        if constexpr (WHOLE)
+                            __builtin_memcpy(&b[h][0][u], w[h] + k, 16);
+                        else
+                            b[h][0][u] = chunk_to_end(w[h], k, K);
+                    } else {
+                        uint32_t t[E];
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            const int kk = WHOLE || k + e < K ? k + e : K - 1;
+                            __builtin_memcpy(&t[e], w[h] + kk * p.ldb, 4);
+                        }
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            if (V == 2 && want > col) t[e] >>= 16;
+                            if (!WHOLE && k + e >= K) t[e] = 0;
+                        }
+                        if constexpr (V == 1) {
+                            b[h][0][u] = u32x4{t[0], t[1], t[2], t[3]};
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                // low halves, then high halves, of slices 2q, 2q + 1
+                                b[h][0][u][q] = __builtin_amdgcn_perm(t[2 * q + 1], t[2 * q],
+                                                                      0x05040100);
+                                b[h][V - 1][u][q] = __builtin_amdgcn_perm(t[2 * q + 1], t[2 * q],
+                                                                          0x07060302);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * F::STEP + g * E;
+                if constexpr (WHOLE)
+                    __builtin_memcpy(&a[u], x + k, 16);
+                else
+                    a[u] = chunk_to_end(x, k, K);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int h = 0; h < W; ++h)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if constexpr (std::is_same_v<T, float>) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                c[h][v] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                    __uint_as_float(b[h][v][u][e]), __uint_as_float(a[u][e]),
+                                    c[h][v], 0, 0, 0);
+                        } else {
+                            c[h][v] = mma16<T>(b[h][v][u], a[u], c[h][v]);
+                        }
+                    }
+        };
+        int k0 = wave * F::ROUND;
+        for (; k0 + F::ROUND <= K; k0 += F::WAVES * F::ROUND)
+            round(k0, std::integral_constant<bool, true>{});
+        if (k0 < K) round(k0, std::integral_constant<bool, false>{});
+    }
+
+    // Lane l holds token l % 16 of strip rows 4 (l / 16) .. + 3.
+#pragma unroll
+    for (int h = 0; h < W; ++h)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                sums[wave][h * V + v][l16 * 16 + 4 * g + r] = c[h][v][r];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 256 * V; i += 512) {
+        const int m = i / F::COLS, j = i - m * F::COLS, n = n0 + j;
+        if (m >= M || n >= N) continue;
+        float z[1] = {}, u[1] = {};
+#pragma unroll
+        for (int s = 0; s < F::WAVES; ++s) {
+            z[0] += sums[s][j % V][m * 16 + j / V];
+            if constexpr (GATED) u[0] += sums[s][V + j % V][m * 16 + j / V];
+        }
+        finish<T, GATED, 1>(p.epi, 0, m, n, z, u);
+    }
+}
+
 // ---- launches ----------------------------------------------------------------------------------
 
 template <typename T, bool AKC, bool BKC, bool GATED>
@@ -702,6 +854,13 @@ hipError_t launch_tile(const TilePlan &plan, const TileArgs &a, hipStream_t stre
     const dim3 grid(static_cast<unsigned>(a.tiles_m) * static_cast<unsigned>(a.tiles_n) *
                         static_cast<unsigned>(a.splits),
                     static_cast<unsigned>(a.batch));
+    if constexpr (AKC) {
+        if (plan.few) {
+            linear_few<T, BKC, GATED>
+                <<<dim3(static_cast<unsigned>(a.tiles_n)), 512, 0, stream>>>(a);
+            return hipGetLastError();
+        }
+    }
     // Direct loads: two workgroups a CU, or, where the grid gives a CU no more
     // than one, stages enough that a second does not fit (the dispatcher would put
     // two on one CU and leave another idle).
