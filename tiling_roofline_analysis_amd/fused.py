@@ -24,7 +24,7 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import TRA_OK, TraError, _row_major_ld, load
+from . import TRA_ERR_INVALID_ARG, TRA_OK, TraError, _row_major_ld, load
 
 # tra_act
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
@@ -45,6 +45,11 @@ def _act(act) -> int:
 
 def _matrix(t, name, like=None, dtype=None) -> int:
     """Checks a row-major 2-D tensor; returns its leading dimension."""
+    if (like is not None and isinstance(t, torch.Tensor) and t.dim() == 2
+            and t.dtype is (dtype or like.dtype) and t.device == like.device):
+        rows, cols = t.shape
+        s0, s1 = t.stride()
+        return s0 if s1 == 1 and s0 >= cols > 0 else _row_major_ld((rows, cols), (s0, s1), name)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 2 or not t.is_cuda:
@@ -105,20 +110,24 @@ def _empty_weight(K, N, trans, like):
 
 
 def _call(name, fmt, fields, device):
-    """Packs the arguments, takes the workspace they need and makes the call."""
-    lib = load()
-    packed = fmt.pack(*fields, 0, 0)
-    if torch.cuda.current_device() != device.index:
+    """Packs the arguments and makes the call; where it needs a workspace (it
+    is refused without one, before anything is enqueued), takes that from
+    torch's allocator and calls again."""
+    index = device.index
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
             return _call(name, fmt, fields, device)
-    need = ctypes.c_size_t(0)
-    st = getattr(lib, name + "_workspace_size")(packed, ctypes.byref(need))
-    if st == TRA_OK:
-        if need.value:
+    lib = load()
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    call = getattr(lib, name)
+    st = call(fmt.pack(*fields, 0, 0), stream)
+    if st == TRA_ERR_INVALID_ARG:
+        need = ctypes.c_size_t(0)
+        size = getattr(lib, name + "_workspace_size")(fmt.pack(*fields, 0, 0), ctypes.byref(need))
+        if size == TRA_OK and need.value:
             # torch's blocks are 512-byte aligned, and 256 are wanted
             ws = torch.empty(need.value, dtype=torch.uint8, device=device)
-            packed = fmt.pack(*fields, ws.data_ptr(), need.value)
-        st = getattr(lib, name)(packed, torch.cuda.current_stream(device).cuda_stream)
+            st = call(fmt.pack(*fields, ws.data_ptr(), need.value), stream)
     if st != TRA_OK:
         raise TraError(st, name)
 
@@ -142,7 +151,7 @@ def _forward(x, w, w2, bias, residual, act, out, z):
         if residual.shape[0] != M or residual.shape[1] != N:
             raise ValueError(f"residual must be {M} x {N}")
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+        out = x.new_empty(M, N)
         ldy = N
     else:
         ldy = _matrix(out, "out", x)
@@ -248,8 +257,11 @@ class _GatedLinear(torch.autograd.Function):
 
 
 def _wants_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(
-        isinstance(t, torch.Tensor) and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                return True
+    return False
 
 
 def linear(x, w, bias=None, act="none", residual=None, out=None, z=None, stream=None):
