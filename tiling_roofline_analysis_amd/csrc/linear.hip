@@ -222,14 +222,20 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
         int bm, bn;
         double f32, half;      // microseconds per K tile
     };
-    static const Class classes[] = {{128, 128, 1.85, 0.36}, {64, 128, 1.0, 0.22}, {64, 64, 0.55, 0.15}};
+    static const Class classes[] = {{256, 256, 0.0, 1.0},
+                                    {128, 128, 1.85, 0.36},
+                                    {64, 128, 1.0, 0.22},
+                                    {64, 64, 0.55, 0.15}};
     const int64_t slice = 128 / elem_bytes(dtype);
     const int64_t k_tiles = std::max<int64_t>(1, segs * ceil_div(K, slice));
     const double out = static_cast<double>(batch) * M * N * (gated ? 2 : 1);
     TilePlan best{};
     double best_us = 0.0;
     for (const Class &c : classes) {
-        if (c.bm == 128 && !direct && dtype == TRA_DTYPE_F32) continue;   // not built
+        // not built: 256 x 256 but for direct 16-bit loads, 128 x 128 for binary32
+        // through registers
+        if (c.bm == 256 && (!direct || dtype == TRA_DTYPE_F32)) continue;
+        if (c.bm == 128 && !direct && dtype == TRA_DTYPE_F32) continue;
         const int64_t tiles = std::max<int64_t>(
             1, ceil_div(M, c.bm) * ceil_div(N, gated ? c.bn / 2 : c.bn) * batch);
         for (int64_t want = 1; want <= 32 && want <= k_tiles; ++want) {

@@ -847,6 +847,183 @@ __global__ __launch_bounds__(512) void linear_few(const TileArgs p) {
     }
 }
 
+// ---- the wide kernel -----------------------------------------------------------------------
+//
+// 256 x 256 of P per workgroup of eight waves, for 16-bit products of many tiles,
+// which the matrix units bound.  A K tile is four panels of 128 rows or columns:
+// A0, A1, B0, B1 (gated: B0 of the one weight, B1 of the other); a wave computes 64
+// rows of each A panel by 32 columns of each B panel, as four quadrants of 16
+// MFMAs.  Two stages of each panel, an array each, take 128 KB of LDS.
+//
+// The waves of the lower rows run half a phase behind those of the upper: there is
+// one of each on every SIMD, and while the one computes a quadrant the other
+// reads the fragments of its next.  A phase is
+//   read this quadrant's fragments and load one panel of a later tile; barrier;
+//   16 MFMAs; barrier.
+// Phases of tile s, with the panels loaded ("> s + 2": of tile s + 2):
+//   0  reads B0, A0, loads A1 > s + 1;  A0 B0      2  reads A1, loads B0 > s + 2;  A1 B1
+//   1  reads B1,     loads A0 > s + 2;  A0 B1      3  loads B1 > s + 2;            A1 B0
+// A panel is loaded into the stage that held it two tiles before, one phase or
+// more after both groups of waves have read it: reads are waited for before the
+// barrier that follows them, and the group behind reads one barrier later.  In
+// phase 3 a wave waits until only its last three panels are in flight: all of tile
+// s + 1 is then in LDS two barriers on, when the first group reads it.
+template <typename T, bool AKC, bool BKC, bool GATED>
+__global__ __launch_bounds__(512, 2) void linear_wide(const TileArgs p) {
+    using PA = Panel<T, AKC, 128, 8>;
+    using PB = Panel<T, BKC, 128, 8>;
+    constexpr int L = PA::INS;
+    static_assert(sizeof(T) == 2 && L == 2 && PB::INS == 2 && PA::BYTES == 64 * 64 * 4,
+                  "panels of two loads a wave; a wave's sums fill one");
+    __shared__ __align__(1024) char a00[PA::BYTES], a01[PA::BYTES], a10[PA::BYTES], a11[PA::BYTES];
+    __shared__ __align__(1024) char b00[PB::BYTES], b01[PB::BYTES], b10[PB::BYTES], b11[PB::BYTES];
+    lds_poison(reinterpret_cast<float *>(a00), PA::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(a01), PA::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(a10), PA::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(a11), PA::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(b00), PB::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(b01), PB::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(b10), PB::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(b11), PB::BYTES / 4);
+
+    const int batch = blockIdx.y;
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int id = xcd_remap32(blockIdx.x, gridDim.x);
+    const int split = id / tiles;
+    int tm, tn;
+    grouped_tile32<4>(id - split * tiles, p.tiles_m, p.tiles_n, tm, tn);
+    const int64_t m0 = static_cast<int64_t>(tm) * 256;
+    const int64_t n0 = static_cast<int64_t>(tn) * (GATED ? 128 : 256), n1 = GATED ? n0 : n0 + 128;
+    const int first = split * p.tiles_per_split;
+    const int left = p.k_tiles - first;
+    const int count = left < p.tiles_per_split ? left : p.tiles_per_split;
+    Walk<T, AKC, BKC> walk(p, batch, m0, n0, n1, GATED, first, count);
+    const int64_t lower = 128 * (AKC ? p.lda : 1) * static_cast<int64_t>(sizeof(T));
+
+    const int wave = wave_id();
+    const int wm = wave >> 2, wn = wave & 3;
+    uint32_t oa0[L], oa1[L], ob0[L], ob1[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        oa0[i] = PA::offset(wave, i, p.M - m0, p.lda);
+        oa1[i] = PA::offset(wave, i, p.M - m0 - 128, p.lda);
+        ob0[i] = PB::offset(wave, i, p.N - n0, p.ldb);
+        ob1[i] = PB::offset(wave, i, p.N - n1, p.ldb);
+    }
+    const int pitch_a = static_cast<int>(p.lda * static_cast<int64_t>(sizeof(T)));
+    const int pitch_b = static_cast<int>(p.ldb * static_cast<int64_t>(sizeof(T)));
+
+    // A1 is loaded one tile behind the others: where its tile starts
+    const char *late = nullptr;
+    int late_rem = 0;
+    auto load_a0 = [&](char *st) __attribute__((always_inline)) {
+        PA::load_direct(wave, walk.a, pitch_a, oa0, walk.rem, st);
+    };
+    auto load_b0 = [&](char *st) __attribute__((always_inline)) {
+        PB::load_direct(wave, walk.b0, pitch_b, ob0, walk.rem, st);
+    };
+    auto load_b1 = [&](char *st) __attribute__((always_inline)) {
+        PB::load_direct(wave, walk.b1, pitch_b, ob1, walk.rem, st);
+        late = walk.a + lower;
+        late_rem = walk.rem;
+        walk.next();
+    };
+    auto load_a1 = [&](char *st) __attribute__((always_inline)) {
+        PA::load_direct(wave, late, pitch_a, oa1, late_rem, st);
+    };
+
+    f32x4 c[2][2][4][2] = {};      // [A panel][B panel]
+    u32x4 x[2][4], w[2][2][2];     // [step][row tile]; [B panel][step][column tile]
+    auto read_a = [&](const char *st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int step = 0; step < 2; ++step)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[step][i] = PA::fragment(st, 0, wm * 64 + i * 16, step);
+    };
+    auto read_b = [&](auto half, const char *st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int step = 0; step < 2; ++step)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                w[decltype(half)::value][step][j] = PB::fragment(st, 0, wn * 32 + j * 16, step);
+    };
+    // The barrier behind the reads and loads, the MFMAs, the barrier behind them.
+    // VM: loads that may still be in flight (63: any).
+    auto compute = [&](auto vm, auto ha, auto hb) __attribute__((always_inline)) {
+        constexpr int HA = decltype(ha)::value, HB = decltype(hb)::value;
+        stage_sync<decltype(vm)::value>();
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int step = 0; step < 2; ++step)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    c[HA][HB][i][j] = mma16<T>(w[HB][step][j], x[step][i], c[HA][HB][i][j]);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr std::integral_constant<int, 0> zero;
+    constexpr std::integral_constant<int, 1> one;
+    constexpr std::integral_constant<int, 3 * L> three_panels;
+    constexpr std::integral_constant<int, 63> any;
+    // Tile s, in the stages a0, a1, b0, b1; `a1_next` is the other A1.
+    auto tile = [&](char *a0, char *a1, char *b0, char *b1, char *a1_next)
+                    __attribute__((always_inline)) {
+        read_b(zero, b0);
+        read_a(a0);
+        load_a1(a1_next);
+        compute(any, zero, zero);
+        read_b(one, b1);
+        load_a0(a0);
+        compute(any, zero, one);
+        read_a(a1);
+        load_b0(b0);
+        compute(any, one, one);
+        load_b1(b1);
+        compute(three_panels, one, zero);
+    };
+
+    load_a0(a00);
+    __builtin_amdgcn_sched_barrier(0);
+    load_b0(b00);
+    __builtin_amdgcn_sched_barrier(0);
+    load_b1(b10);
+    __builtin_amdgcn_sched_barrier(0);
+    load_a1(a10);
+    __builtin_amdgcn_sched_barrier(0);
+    load_a0(a01);
+    __builtin_amdgcn_sched_barrier(0);
+    load_b0(b01);
+    __builtin_amdgcn_sched_barrier(0);
+    load_b1(b11);
+    stage_sync<3 * L>();
+    if (wm != 0) __builtin_amdgcn_s_barrier();
+    int s = 0;
+    for (; s + 2 <= count; s += 2) {
+        tile(a00, a10, b00, b10, a11);
+        tile(a01, a11, b01, b11, a10);
+    }
+    if (s < count) tile(a00, a10, b00, b10, a11);
+    if (wm == 0) __builtin_amdgcn_s_barrier();
+    stage_sync<0>();
+
+    // One array takes a wave's sums of one A panel.
+    char *mine = wave < 4 ? (wave < 2 ? (wave < 1 ? a00 : a01) : (wave < 3 ? a10 : a11))
+                          : (wave < 6 ? (wave < 5 ? b00 : b01) : (wave < 7 ? b10 : b11));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        epi_put<32>(mine, c[h][0], 0);
+        epi_put<32>(mine, c[h][1], 1);
+        epi_rows<T, GATED, 32, 64>(p, batch, split, mine, m0 + h * 128 + wm * 64, n0 + wn * 32,
+                                   n1 + wn * 32);
+    }
+}
+
 // ---- launches ----------------------------------------------------------------------------------
 
 template <typename T, bool AKC, bool BKC, bool GATED>
@@ -858,6 +1035,12 @@ hipError_t launch_tile(const TilePlan &plan, const TileArgs &a, hipStream_t stre
         if (plan.few) {
             linear_few<T, BKC, GATED>
                 <<<dim3(static_cast<unsigned>(a.tiles_n)), 512, 0, stream>>>(a);
+            return hipGetLastError();
+        }
+    }
+    if constexpr (sizeof(T) == 2) {
+        if (plan.bm == 256) {
+            linear_wide<T, AKC, BKC, GATED><<<grid, 512, 0, stream>>>(a);
             return hipGetLastError();
         }
     }
