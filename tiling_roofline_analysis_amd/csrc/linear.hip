@@ -27,20 +27,23 @@ __global__ __launch_bounds__(256) void linear_join(const TileArgs p) {
     const int64_t m = id / vpr, n = (id - m * vpr) * V;
     const int64_t np = GATED ? 2 * p.N : p.N;
     float z[V] = {}, u[V] = {};
-    for (int s = 0; s < p.splits; ++s) {
-        const float *in =
-            p.partial + ((static_cast<int64_t>(s) * p.batch + batch) * p.M + m) * np + n;
+    const int64_t next = static_cast<int64_t>(p.batch) * p.M * np;
+    const float *in = p.partial + (static_cast<int64_t>(batch) * p.M + m) * np + n;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s, in += next) {
         float t[V];
-        load_row<float, V>(in, p.N - n, p.vec_p, t);
+        load_part<float, V>(in, p.N - n, t);
 #pragma unroll
         for (int e = 0; e < V; ++e) z[e] += t[e];
         if constexpr (GATED) {
-            load_row<float, V>(in + p.N, p.N - n, p.vec_p, t);
+            load_part<float, V>(in + p.N, p.N - n, t);
 #pragma unroll
             for (int e = 0; e < V; ++e) u[e] += t[e];
         }
     }
-    finish<T, GATED, V>(p.epi, batch, m, n, z, u);
+    with_act(p.epi.act, [&](auto act) __attribute__((always_inline)) {
+        finish<T, GATED, decltype(act)::value, V>(p.epi, batch, m, n, z, u);
+    });
 }
 
 // 64 chunks of columns by rows_per_chunk rows per workgroup; its four waves
@@ -57,30 +60,28 @@ __global__ __launch_bounds__(256) void linear_slope(const SlopeArgs p) {
     const int64_t valid = p.N - n;
     float sum[V] = {};
     if (valid > 0) {
-        for (int64_t m = first + wave; m < end; m += 4) {
-            float dy[V], z[V] = {}, y[V], d[V], dz[V];
-            load_row<T, V>(static_cast<const T *>(p.dY) + m * p.lddy + n, valid, p.vec_dy, dy);
-            if (p.Z != nullptr) load_row<float, V>(p.Z + m * p.ldz + n, valid, p.vec_z, z);
-            activate_slope(p.act, z, y, d);
-            if constexpr (GATED) {
-                float u[V];
-                load_row<float, V>(p.Z + m * p.ldz + p.N + n, valid, p.vec_z, u);
-#pragma unroll
-                for (int e = 0; e < V; ++e) dz[e] = dy[e] * u[e] * d[e];
+        with_act(p.act, [&](auto act) __attribute__((always_inline)) {
+            constexpr int ACT = decltype(act)::value;
+#pragma unroll 2
+            for (int64_t m = first + wave; m < end; m += 4) {
+                float dy[V], z[V], u[V], dz[V];
+                load_part<T, V>(static_cast<const T *>(p.dY) + m * p.lddy + n, valid, dy);
+                if (GATED || ACT != TRA_ACT_NONE)
+                    load_part<float, V>(p.Z + m * p.ldz + n, valid, z);
+                if constexpr (GATED) load_part<float, V>(p.Z + m * p.ldz + p.N + n, valid, u);
                 T *out = static_cast<T *>(p.dZ) + m * p.lddz + n;
-                store_row<T, V>(out, valid, p.vec_dz, dz);
 #pragma unroll
-                for (int e = 0; e < V; ++e) dz[e] = dy[e] * y[e];
-                store_row<T, V>(out + p.N, valid, p.vec_dz, dz);
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) dz[e] = dy[e] * d[e];
-                if (p.dZ != nullptr)
-                    store_row<T, V>(static_cast<T *>(p.dZ) + m * p.lddz + n, valid, p.vec_dz, dz);
-#pragma unroll
-                for (int e = 0; e < V; ++e) sum[e] += dz[e];
+                for (int e = 0; e < V; ++e) {
+                    float y;
+                    const float d = GATED || ACT != TRA_ACT_NONE ? activate_slope<ACT>(z[e], y) : 1.0f;
+                    dz[e] = GATED ? dy[e] * u[e] * d : dy[e] * d;
+                    if constexpr (GATED) u[e] = dy[e] * y;
+                    sum[e] += dz[e];
+                }
+                if (GATED || p.dZ != nullptr) store_part<T, V>(out, valid, dz);
+                if constexpr (GATED) store_part<T, V>(out + p.N, valid, u);
             }
-        }
+        });
     }
     if constexpr (!GATED) {
         if (p.colsum == nullptr) return;
@@ -96,14 +97,26 @@ __global__ __launch_bounds__(256) void linear_slope(const SlopeArgs p) {
     }
 }
 
+// Sums the chunks in order: 16 columns per workgroup, whose 16 groups of lanes
+// take every 16th chunk and are added in order.
 template <typename T>
 __global__ __launch_bounds__(256) void linear_colsum_join(const float *colsum, int64_t chunks,
                                                           int64_t N, T *out) {
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (n >= N) return;
+    __shared__ float part[16][16];
+    lds_poison(&part[0][0], 256);
+    const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * 16 + j;
     float sum = 0.0f;
-    for (int64_t c = 0; c < chunks; ++c) sum += colsum[c * N + n];
-    out[n] = static_cast<T>(sum);
+    if (n < N) {
+#pragma unroll 4
+        for (int64_t c = group; c < chunks; c += 16) sum += colsum[c * N + n];
+    }
+    part[group][j] = sum;
+    __syncthreads();
+    if (group == 0 && n < N) {
+        for (int i = 1; i < 16; ++i) sum += part[i][j];
+        out[n] = static_cast<T>(sum);
+    }
 }
 
 template <typename T>
@@ -131,7 +144,7 @@ hipError_t launch_slope(bool gated, const SlopeArgs &a, hipStream_t stream) {
 template <typename T>
 hipError_t launch_colsum(const float *colsum, int64_t chunks, int64_t N, void *out,
                          hipStream_t stream) {
-    linear_colsum_join<T><<<dim3(static_cast<unsigned>(ceil_div(N, 256))), 256, 0, stream>>>(
+    linear_colsum_join<T><<<dim3(static_cast<unsigned>(ceil_div(N, 16))), 256, 0, stream>>>(
         colsum, chunks, N, static_cast<T *>(out));
     return hipGetLastError();
 }
@@ -294,7 +307,6 @@ tra_status finish_args(const TilePlan &t, int dtype, TileArgs &a, float *partial
     a.splits = t.splits;
     a.tiles_per_split = static_cast<int>(ceil_div(std::max(a.k_tiles, 1), t.splits));
     a.partial = t.splits > 1 ? partial : nullptr;
-    a.vec_p = a.N % 4 == 0;
     a.epi.M = a.M;
     a.epi.N = a.N;
     return TRA_OK;
@@ -403,10 +415,6 @@ tra_status forward(const tra_linear_args *p, void *stream) {
     t.epi.Z = a.Z;
     t.epi.ldz = a.ldz;
     t.epi.act = a.act;
-    t.epi.vec_bias = aligned16(a.bias);
-    t.epi.vec_r = rows16(a.R, a.ldr, b);
-    t.epi.vec_y = rows16(a.Y, a.ldy, b);
-    t.epi.vec_z = rows16(a.Z, a.ldz, 4) && (!gated || a.N % 4 == 0);
     st = finish_args(plan, a.dtype, t, static_cast<float *>(a.workspace));
     if (st != TRA_OK) return st;
     return status_of(run_product(a.dtype, plan, t, static_cast<hipStream_t>(stream)));
@@ -565,7 +573,6 @@ tra_status backward(const tra_linear_grad_args *p, void *stream_) {
         tx.epi.Y[0] = a.dX;
         tx.epi.ldy = a.lddx;
         tx.epi.act = TRA_ACT_NONE;
-        tx.epi.vec_y = rows16(a.dX, a.lddx, b);
         if ((st = finish_args(g.dx, a.dtype, tx, partial)) != TRA_OK) return st;
     }
     if (want_dw) {
@@ -585,7 +592,6 @@ tra_status backward(const tra_linear_grad_args *p, void *stream_) {
         tw.epi.Y[1] = a.dW2;
         tw.epi.ldy = a.lddw;
         tw.epi.act = TRA_ACT_NONE;
-        tw.epi.vec_y = rows16(a.dW, a.lddw, b) && (!gated || aligned16(a.dW2));
         if ((st = finish_args(g.dw, a.dtype, tw, partial)) != TRA_OK) return st;
     }
 
@@ -604,9 +610,6 @@ tra_status backward(const tra_linear_grad_args *p, void *stream_) {
         s.N = a.N;
         s.rows_per_chunk = g.rows_per_chunk;
         s.act = a.act;
-        s.vec_dy = rows16(a.dY, a.lddy, b);
-        s.vec_z = rows16(a.Z, a.ldz, 4) && (!gated || a.N % 4 == 0);
-        s.vec_dz = !gated || a.N * b % 16 == 0;
         err = run_slope(a.dtype, gated, s, stream);
     }
     if (err == hipSuccess && a.dbias != nullptr && a.N > 0)

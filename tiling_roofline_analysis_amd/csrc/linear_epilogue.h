@@ -3,6 +3,8 @@
 // split or compute gradients.
 #pragma once
 
+#include <type_traits>
+
 #include "gemm_internal.h"
 #include "linear_internal.h"
 
@@ -17,7 +19,11 @@ constexpr int kChunk = 16 / sizeof(T);     // elements of a 16-byte chunk
 // ---- activations -------------------------------------------------------------
 //
 // In binary32, with the formulas of the definitions:
-//   gelu       z Phi(z);  slope Phi(z) + z phi(z)
+//   gelu       z Phi(z);  slope Phi(z) + z phi(z), with Phi(-|z|) = erfc(|z| /
+//              sqrt(2)) / 2 by the rational approximation 7.1.26 of Abramowitz and
+//              Stegun, "Handbook of Mathematical Functions" (error of erfc at most
+//              1.5e-7, near binary32's own): no branches, and phi's exponential
+//              comes with it
 //   gelu_tanh  z s,  s = sigmoid(2 sqrt(2/pi) (z + 0.044715 z^3)), the tanh form
 //              rewritten with 1 + tanh(a) = 2 sigmoid(2a)
 //   silu       z sigmoid(z);  slope s (1 + z (1 - s))
@@ -29,108 +35,116 @@ __device__ __forceinline__ float sigmoid(float z) {
 constexpr float kGeluA = 1.5957691216057308f;              // 2 sqrt(2 / pi)
 constexpr float kGeluB = 1.5957691216057308f * 0.044715f;
 
-// NaN stays NaN, as in max(z, 0) of the array libraries.
-__device__ __forceinline__ float relu(float z) { return z < 0.0f ? 0.0f : z; }
-
-template <int V>
-__device__ __forceinline__ void activate(int act, const float (&z)[V], float (&y)[V]) {
-    switch (act) {
-        case TRA_ACT_RELU:
-#pragma unroll
-            for (int e = 0; e < V; ++e) y[e] = relu(z[e]);
-            break;
-        case TRA_ACT_GELU:
-#pragma unroll
-            for (int e = 0; e < V; ++e) y[e] = 0.5f * z[e] * (1.0f + erff(z[e] * 0.70710678f));
-            break;
-        case TRA_ACT_GELU_TANH:
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                y[e] = z[e] * sigmoid(z[e] * (kGeluA + kGeluB * z[e] * z[e]));
-            break;
-        case TRA_ACT_SILU:
-#pragma unroll
-            for (int e = 0; e < V; ++e) y[e] = z[e] * sigmoid(z[e]);
-            break;
-        case TRA_ACT_SIGMOID:
-#pragma unroll
-            for (int e = 0; e < V; ++e) y[e] = sigmoid(z[e]);
-            break;
-        default:
-#pragma unroll
-            for (int e = 0; e < V; ++e) y[e] = z[e];
-    }
+// Phi(z); e = exp(-z^2 / 2).
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+    const float x = fabsf(z) * 0.70710678f;
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+    float q = 1.061405429f;
+    q = q * t - 1.453152027f;
+    q = q * t + 1.421413741f;
+    q = q * t - 0.284496736f;
+    q = q * t + 0.254829592f;
+    e = __expf(-x * x);
+    q = 0.5f * q * t * e;
+    return z > 0.0f ? 1.0f - q : q;
 }
 
-// y = act(z) and d = act'(z).
-template <int V>
-__device__ __forceinline__ void activate_slope(int act, const float (&z)[V], float (&y)[V],
-                                               float (&d)[V]) {
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+    // NaN stays NaN, as in max(z, 0) of the array libraries
+    if constexpr (ACT == TRA_ACT_RELU) return z < 0.0f ? 0.0f : z;
+    if constexpr (ACT == TRA_ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, e);
+    }
+    if constexpr (ACT == TRA_ACT_GELU_TANH) return z * sigmoid(z * (kGeluA + kGeluB * z * z));
+    if constexpr (ACT == TRA_ACT_SILU) return z * sigmoid(z);
+    if constexpr (ACT == TRA_ACT_SIGMOID) return sigmoid(z);
+    return z;
+}
+
+// y = act(z); returns act'(z).
+template <int ACT>
+__device__ __forceinline__ float activate_slope(float z, float &y) {
+    if constexpr (ACT == TRA_ACT_RELU) {
+        y = activate<ACT>(z);
+        return z > 0.0f ? 1.0f : 0.0f;
+    }
+    if constexpr (ACT == TRA_ACT_GELU) {
+        float e;
+        const float cdf = normal_cdf(z, e);
+        y = z * cdf;
+        return cdf + z * 0.39894228f * e;
+    }
+    if constexpr (ACT == TRA_ACT_GELU_TANH) {
+        const float s = sigmoid(z * (kGeluA + kGeluB * z * z));
+        y = z * s;
+        return s + y * (1.0f - s) * (kGeluA + 3.0f * kGeluB * z * z);
+    }
+    if constexpr (ACT == TRA_ACT_SILU) {
+        const float s = sigmoid(z);
+        y = z * s;
+        return s + y * (1.0f - s);
+    }
+    if constexpr (ACT == TRA_ACT_SIGMOID) {
+        y = sigmoid(z);
+        return y * (1.0f - y);
+    }
+    y = z;
+    return 1.0f;
+}
+
+// f(std::integral_constant<int, act>{}): the activation is chosen once for many
+// elements.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
     switch (act) {
-        case TRA_ACT_RELU:
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                y[e] = relu(z[e]);
-                d[e] = z[e] > 0.0f ? 1.0f : 0.0f;
-            }
-            break;
-        case TRA_ACT_GELU:
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float cdf = 0.5f * (1.0f + erff(z[e] * 0.70710678f));
-                y[e] = z[e] * cdf;
-                d[e] = cdf + z[e] * 0.39894228f * __expf(-0.5f * z[e] * z[e]);
-            }
-            break;
-        case TRA_ACT_GELU_TANH:
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float s = sigmoid(z[e] * (kGeluA + kGeluB * z[e] * z[e]));
-                y[e] = z[e] * s;
-                d[e] = s + y[e] * (1.0f - s) * (kGeluA + 3.0f * kGeluB * z[e] * z[e]);
-            }
-            break;
-        case TRA_ACT_SILU:
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float s = sigmoid(z[e]);
-                y[e] = z[e] * s;
-                d[e] = s + y[e] * (1.0f - s);
-            }
-            break;
-        case TRA_ACT_SIGMOID:
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                y[e] = sigmoid(z[e]);
-                d[e] = y[e] * (1.0f - y[e]);
-            }
-            break;
-        default:
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                y[e] = z[e];
-                d[e] = 1.0f;
-            }
+        case TRA_ACT_RELU: f(std::integral_constant<int, TRA_ACT_RELU>{}); break;
+        case TRA_ACT_GELU: f(std::integral_constant<int, TRA_ACT_GELU>{}); break;
+        case TRA_ACT_GELU_TANH: f(std::integral_constant<int, TRA_ACT_GELU_TANH>{}); break;
+        case TRA_ACT_SILU: f(std::integral_constant<int, TRA_ACT_SILU>{}); break;
+        case TRA_ACT_SIGMOID: f(std::integral_constant<int, TRA_ACT_SIGMOID>{}); break;
+        default: f(std::integral_constant<int, TRA_ACT_NONE>{});
     }
 }
 
 // ---- rows of V consecutive elements --------------------------------------------
+//
+// V is one element or whole 16-byte chunks.  Vector loads and stores take any
+// alignment of whole elements (gfx950 global memory instructions do).
 
-// V elements from p, `valid` of them inside (the others read as zero);
-// `vec`: p is 16-byte aligned.
 template <typename T, int V>
-__device__ __forceinline__ void load_row(const T *p, int64_t valid, bool vec, float (&v)[V]) {
-    constexpr int C = kChunk<T>;
-    static_assert(V == 1 || V % C == 0, "one element or whole chunks");
-    if (V > 1 && vec && valid >= V) {
+__device__ __forceinline__ void load_row(const T *p, float (&v)[V]) {
+    constexpr int C = V == 1 ? 1 : kChunk<T>;
+    static_assert(V % C == 0, "whole chunks");
 #pragma unroll
-        for (int c = 0; c < V / C; ++c) {
-            T t[C];
-            const u32x4 q = reinterpret_cast<const u32x4 *>(p)[c];
-            __builtin_memcpy(t, &q, 16);
+    for (int c = 0; c < V / C; ++c) {
+        T t[C];
+        __builtin_memcpy(t, p + c * C, C * sizeof(T));
 #pragma unroll
-            for (int e = 0; e < C; ++e) v[c * C + e] = static_cast<float>(t[e]);
-        }
+        for (int e = 0; e < C; ++e) v[c * C + e] = static_cast<float>(t[e]);
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_row(T *p, const float (&v)[V]) {
+    constexpr int C = V == 1 ? 1 : kChunk<T>;
+    static_assert(V % C == 0, "whole chunks");
+#pragma unroll
+    for (int c = 0; c < V / C; ++c) {
+        T t[C];
+#pragma unroll
+        for (int e = 0; e < C; ++e) t[e] = static_cast<T>(v[c * C + e]);
+        __builtin_memcpy(p + c * C, t, C * sizeof(T));
+    }
+}
+
+// The same for a row that ends after `valid` of the V elements (the others
+// read as zero).
+template <typename T, int V>
+__device__ __forceinline__ void load_part(const T *p, int64_t valid, float (&v)[V]) {
+    if (valid >= V) {
+        load_row<T, V>(p, v);
     } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = e < valid ? static_cast<float>(p[e]) : 0.0f;
@@ -138,19 +152,9 @@ __device__ __forceinline__ void load_row(const T *p, int64_t valid, bool vec, fl
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void store_row(T *p, int64_t valid, bool vec, const float (&v)[V]) {
-    constexpr int C = kChunk<T>;
-    static_assert(V == 1 || V % C == 0, "one element or whole chunks");
-    if (V > 1 && vec && valid >= V) {
-#pragma unroll
-        for (int c = 0; c < V / C; ++c) {
-            T t[C];
-#pragma unroll
-            for (int e = 0; e < C; ++e) t[e] = static_cast<T>(v[c * C + e]);
-            u32x4 q;
-            __builtin_memcpy(&q, t, 16);
-            reinterpret_cast<u32x4 *>(p)[c] = q;
-        }
+__device__ __forceinline__ void store_part(T *p, int64_t valid, const float (&v)[V]) {
+    if (valid >= V) {
+        store_row<T, V>(p, v);
     } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -158,40 +162,33 @@ __device__ __forceinline__ void store_row(T *p, int64_t valid, bool vec, const f
     }
 }
 
-// Finishes V (one, or a chunk of) elements of row m from column n on: z (and u)
-// are the whole sums.  The one rounding to T is at the store; bias, activation
-// and residual are binary32.
-template <typename T, bool GATED, int V>
+// Finishes V elements of row m from column n on, of which `valid` = N - n are
+// inside: z (and u) are the whole sums.  The one rounding to T is at the store;
+// bias, activation and residual are binary32.
+template <typename T, bool GATED, int ACT, int V>
 __device__ __forceinline__ void finish(const EpiArgs &e, int batch, int64_t m, int64_t n,
                                        float (&z)[V], float (&u)[V]) {
     const int64_t valid = e.N - n;
-    float y[V];
-    if constexpr (GATED) {
-        if (e.Z != nullptr) {
-            store_row<float, V>(e.Z + m * e.ldz + n, valid, e.vec_z, z);
-            store_row<float, V>(e.Z + m * e.ldz + e.N + n, valid, e.vec_z, u);
-        }
-        activate(e.act, z, y);
+    if (!GATED && e.bias != nullptr) {
+        float b[V];
+        load_part<T, V>(static_cast<const T *>(e.bias) + n, valid, b);
 #pragma unroll
-        for (int i = 0; i < V; ++i) y[i] *= u[i];
-    } else {
-        if (e.bias != nullptr) {
-            float b[V];
-            load_row<T, V>(static_cast<const T *>(e.bias) + n, valid, e.vec_bias, b);
+        for (int i = 0; i < V; ++i) z[i] += b[i];
+    }
+    if (e.Z != nullptr) {
+        store_part<float, V>(e.Z + m * e.ldz + n, valid, z);
+        if constexpr (GATED) store_part<float, V>(e.Z + m * e.ldz + e.N + n, valid, u);
+    }
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[i] += b[i];
-        }
-        if (e.Z != nullptr) store_row<float, V>(e.Z + m * e.ldz + n, valid, e.vec_z, z);
-        activate(e.act, z, y);
-        if (e.R != nullptr) {
-            float r[V];
-            load_row<T, V>(static_cast<const T *>(e.R) + m * e.ldr + n, valid, e.vec_r, r);
+    for (int i = 0; i < V; ++i) z[i] = GATED ? activate<ACT>(z[i]) * u[i] : activate<ACT>(z[i]);
+    if (!GATED && e.R != nullptr) {
+        float r[V];
+        load_part<T, V>(static_cast<const T *>(e.R) + m * e.ldr + n, valid, r);
 #pragma unroll
-            for (int i = 0; i < V; ++i) y[i] += r[i];
-        }
+        for (int i = 0; i < V; ++i) z[i] += r[i];
     }
     T *out = static_cast<T *>(batch == 0 ? e.Y[0] : e.Y[1]);
-    store_row<T, V>(out + m * e.ldy + n, valid, e.vec_y, y);
+    store_part<T, V>(out + m * e.ldy + n, valid, z);
 }
 
 }  // namespace

@@ -27,7 +27,6 @@ struct EpiArgs {
     int64_t ldz;
     int64_t M, N;
     int act;
-    bool vec_bias, vec_r, vec_y, vec_z;   // 16-byte aligned rows
 };
 
 // One product  P = op(A) x op(B)  on tiles, A's rows and B's columns being
@@ -50,7 +49,6 @@ struct TileArgs {
     int k_tiles;                        // K tiles in all
     int splits, tiles_per_split;        // of the K tiles
     float *partial;                     // splits > 1: [split][batch][M][N or 2N]
-    bool vec_p;
     EpiArgs epi;
 };
 
@@ -87,7 +85,6 @@ struct SlopeArgs {
     int64_t M, N;
     int rows_per_chunk;
     int act;
-    bool vec_dy, vec_z, vec_dz;
 };
 
 template <typename T>
