@@ -224,63 +224,100 @@ bool direct_ok(const void *p, int64_t ld, int64_t line, int64_t bytes) {
     return rows16(p, ld, bytes) && line * bytes % 16 == 0 && ld * bytes < (int64_t{1} << 22);
 }
 
-// The product's plan: tile, staging, split, by a model of the time.  A CU works
-// off its share of the workgroups (tiles x splits over 256 CUs, rounded up), each
-// its K tiles at the class's measured time per K tile (all of a CU's rate to
-// itself) plus a start and an epilogue; a split adds a launch that reads the
-// partial sums back.  The classes and their times are in `classes`.
+// How a kernel of one tile size goes, in microseconds, as measured on MI355X with
+// 1 to 12 workgroups a CU and 16 to 64 K tiles (a K tile is 128 bytes of a row).
+struct TileClass {
+    int bm, bn;
+    int resident;     // workgroups a CU holds
+    double alone;     // per K tile, one workgroup on a CU
+    double shared;    // per K tile and workgroup, CU full
+    double base;      // launch, first loads, epilogue without its stores
+};
+
+constexpr double kBytesPerUs = 4.8e6;     // memory, as a large copy reaches
+constexpr double kBytesPerUsWg = 3.0e4;   // what one workgroup's loads in flight can ask for
+
+// direct loads, 16-bit and binary32; through registers, the same.  The 256 x 256
+// kernel is built for direct 16-bit loads only; 128 x 128 through registers in
+// binary32 needs more VGPRs than there are.
+constexpr TileClass kClasses[2][2][4] = {
+    {{{256, 256, 1, 1.28, 1.42, 5.7},
+      {128, 128, 2, 0.50, 0.47, 5.2},
+      {64, 128, 2, 0.30, 0.27, 4.5},
+      {64, 64, 3, 0.21, 0.185, 4.0}},
+     {{128, 128, 2, 1.77, 1.77, 5.6},
+      {64, 128, 2, 0.93, 0.90, 4.5},
+      {64, 64, 3, 0.505, 0.46, 4.0},
+      {0, 0, 0, 0.0, 0.0, 0.0}}},
+    {{{128, 128, 2, 0.97, 0.68, 5.2},
+      {64, 128, 3, 0.85, 0.455, 4.5},
+      {64, 64, 4, 0.70, 0.32, 4.0},
+      {0, 0, 0, 0.0, 0.0, 0.0}},
+     {{64, 128, 2, 1.22, 1.04, 4.5},
+      {64, 64, 4, 0.74, 0.545, 4.0},
+      {0, 0, 0, 0.0, 0.0, 0.0},
+      {0, 0, 0, 0.0, 0.0, 0.0}}}};
+
+// The product's plan: the kernel, tile and split with the least predicted time.
+//   Tiles: a CU runs its share of the workgroups (tiles x splits), `resident` at a
+//   time; the K loop is bounded by the operands' bytes too; the results' stores
+//   add to it.  A split stores binary32 sums and adds a launch that reads them.
+//   Few rows: the weights' bytes at the rate that their strips can ask for (one
+//   strip, of 512 lanes, about 25 GB/s; 64-byte pieces of rows K apart reach about
+//   half of the memory's rate in 16 bits; unaligned rows three quarters).
+// `kept`: binary32 values stored besides each result (the pre-activations).
 TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, int64_t K, int segs,
-                   int batch, bool direct) {
-    struct Class {
-        int bm, bn;
-        double f32, half;      // microseconds per K tile
-    };
-    static const Class classes[] = {{256, 256, 0.0, 1.0},
-                                    {128, 128, 1.85, 0.36},
-                                    {64, 128, 1.0, 0.22},
-                                    {64, 64, 0.55, 0.15}};
-    const int64_t slice = 128 / elem_bytes(dtype);
+                   int batch, bool direct, bool kept) {
+    const int64_t b = elem_bytes(dtype), slice = 128 / b;
+    const bool f32 = dtype == TRA_DTYPE_F32;
     const int64_t k_tiles = std::max<int64_t>(1, segs * ceil_div(K, slice));
-    const double out = static_cast<double>(batch) * M * N * (gated ? 2 : 1);
+    const double columns = static_cast<double>(N) * (gated ? 2 : 1);      // of z and u
+    const double in = static_cast<double>(batch) * segs * K * (static_cast<double>(M) + columns) * b;
     TilePlan best{};
     double best_us = 0.0;
-    for (const Class &c : classes) {
-        // not built: 256 x 256 but for direct 16-bit loads, 128 x 128 for binary32
-        // through registers
-        if (c.bm == 256 && (!direct || dtype == TRA_DTYPE_F32)) continue;
-        if (c.bm == 128 && !direct && dtype == TRA_DTYPE_F32) continue;
+    for (const TileClass &c : kClasses[direct ? 0 : 1][f32 ? 1 : 0]) {
+        if (c.bm == 0) break;
         const int64_t tiles = std::max<int64_t>(
             1, ceil_div(M, c.bm) * ceil_div(N, gated ? c.bn / 2 : c.bn) * batch);
         for (int64_t want = 1; want <= 32 && want <= k_tiles; ++want) {
-            if (want > 1 && tiles * want > 512) break;
+            if (want > 1 && tiles * want > 1024) break;
             const int64_t per = ceil_div(k_tiles, want), splits = ceil_div(k_tiles, per);
             if (splits != want) continue;
-            const double us =
-                static_cast<double>(ceil_div(tiles * splits, 256)) *
-                    (per * (dtype == TRA_DTYPE_F32 ? c.f32 : c.half) + 2.0) +
-                (splits > 1 ? 4.0 + splits * out * 8.0 / 4e6 : 0.0);
+            const int64_t n = tiles * splits, wave = 256 * c.resident;
+            const int64_t full = n / wave, rest = ceil_div(n % wave, 256);
+            double loop = per * (full * std::max(c.alone, c.resident * c.shared) +
+                                 (rest > 0 ? std::max(c.alone, rest * c.shared) : 0.0));
+            // 64-byte lines (16-bit weights, 64 x 64 tiles, not k-contiguous)
+            const double most =
+                kBytesPerUs * (form == tra::kFormKN && !f32 && c.bn == 64 ? 0.7 : 1.0);
+            loop = std::max(loop, in / std::min(most, n * kBytesPerUsWg));
+            // bytes stored per column of z or u
+            const double out = splits > 1 ? 4.0 : (kept ? 4.0 : 0.0) + (gated ? 0.5 : 1.0) * b;
+            const double stored = splits * static_cast<double>(batch) * M * columns * out;
+            double us = c.base + loop + stored / kBytesPerUs;
+            if (splits > 1) us += 2.7 + stored / kBytesPerUs;
             if (best_us == 0.0 || us < best_us) {
                 best_us = us;
                 best.bm = c.bm;
                 best.bn = c.bn;
                 best.splits = static_cast<int>(splits);
-                best.deep = direct && tiles * splits <= 256;
+                best.deep = direct && n <= 256;
             }
         }
     }
-    // Few rows: the weights' bytes at about 4.8 TB/s, or 25 GB/s a CU where there
-    // are fewer strips than CUs can saturate memory from, plus a start.
-    const int64_t b = elem_bytes(dtype);
-    const int64_t cols = form == tra::kFormKK ? 16 : 64 / b;
+    const int64_t strip = form == tra::kFormKK ? 16 : 64 / b;
     if (form != tra::kFormNN && M <= 16 && K >= 16 / b && N >= 4 / b) {
-        const double strips = static_cast<double>(ceil_div(N, cols));
-        const double bytes = static_cast<double>(segs) * K * N * b * (gated ? 2 : 1);
-        const double us = 2.0 + bytes / std::min(4.8e6, strips * 2.5e4);
+        const double strips = static_cast<double>(ceil_div(N, strip));
+        const double most = form == tra::kFormKK ? (strips < 512 ? 3.9e6 : 4.9e6)
+                                                 : (f32 ? 3.8e6 : 2.4e6);
+        const double each = form == tra::kFormKK ? 2.6e4 : f32 ? 1.8e4 : 3.0e4;
+        const double us = 2.8 + segs * static_cast<double>(K) * columns * b * (1.0 + M / 80.0) /
+                                    std::min(most, strips * each) / (direct ? 1.0 : 0.75);
         if (us < best_us) {
             best = TilePlan{};
             best.few = true;
             best.bm = 16;
-            best.bn = static_cast<int>(gated ? 2 * cols : cols);
+            best.bn = static_cast<int>(gated ? 2 * strip : strip);
             best.splits = 1;
         }
     }
@@ -354,7 +391,7 @@ TilePlan plan_forward(const tra_linear_args &a) {
                         direct_ok(a.W, a.ldw, a.w_trans ? a.K : a.N, b) &&
                         aligned16(a.W2);
     return plan_tile(a.w_trans ? tra::kFormKK : tra::kFormKN, a.gated != 0, a.dtype, a.M, a.N,
-                     a.K, 1, 1, direct);
+                     a.K, 1, 1, direct, a.Z != nullptr);
 }
 
 // Host-side checks; launches nothing.
@@ -465,13 +502,13 @@ GradPlan plan_backward(const tra_linear_grad_args &a) {
                             direct_ok(a.W, a.ldw, a.w_trans ? a.K : a.N, b) &&
                             (!gated || aligned16(a.W2));
         g.dx = plan_tile(a.w_trans ? tra::kFormKN : tra::kFormKK, false, a.dtype, a.M, a.K, a.N,
-                         gated ? 2 : 1, 1, direct);
+                         gated ? 2 : 1, 1, direct, false);
     }
     if (a.dW != nullptr) {
         const bool direct = direct_ok(dz, ldz, a.N, b) && (!gated || a.N * b % 16 == 0) &&
                             direct_ok(a.X, a.ldx, a.K, b);
         g.dw = plan_tile(tra::kFormNN, false, a.dtype, a.w_trans ? a.N : a.K,
-                         a.w_trans ? a.K : a.N, a.M, 1, gated ? 2 : 1, direct);
+                         a.w_trans ? a.K : a.N, a.M, 1, gated ? 2 : 1, direct, false);
     }
     g.product_bytes = align_up(std::max(g.dx.partial_bytes, g.dw.partial_bytes));
     g.total = g.dz_bytes + g.colsum_bytes + g.product_bytes;

@@ -105,14 +105,19 @@ def _vector(b, name, x, N):
 
 
 def _empty_weight(K, N, trans, like):
-    t = torch.empty((N, K) if trans else (K, N), dtype=like.dtype, device=like.device)
-    return t.t() if trans else t
+    return like.new_empty(N, K).t() if trans else like.new_empty(K, N)
+
+
+# Workspace bytes of the calls seen so far, by name, type, layout and sizes: what
+# to allocate before a call.  Alignment and which gradients are asked for count
+# too, so a call may need more; the library then refuses it, before anything is
+# enqueued, and says how much.
+_seen: dict = {}
 
 
 def _call(name, fmt, fields, device):
-    """Packs the arguments and makes the call; where it needs a workspace (it
-    is refused without one, before anything is enqueued), takes that from
-    torch's allocator and calls again."""
+    """Takes a workspace from torch's allocator, packs the arguments and makes
+    the call."""
     index = device.index
     if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
@@ -120,14 +125,20 @@ def _call(name, fmt, fields, device):
     lib = load()
     stream = torch._C._cuda_getCurrentRawStream(index)
     call = getattr(lib, name)
-    st = call(fmt.pack(*fields, 0, 0), stream)
+    key = (name, fields[:7])
+    need = _seen.get(key, 0)
+    # torch's blocks are 512-byte aligned, and 256 are wanted
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    st = call(fmt.pack(*fields, ws.data_ptr() if need else 0, need), stream)
     if st == TRA_ERR_INVALID_ARG:
-        need = ctypes.c_size_t(0)
-        size = getattr(lib, name + "_workspace_size")(fmt.pack(*fields, 0, 0), ctypes.byref(need))
-        if size == TRA_OK and need.value:
-            # torch's blocks are 512-byte aligned, and 256 are wanted
-            ws = torch.empty(need.value, dtype=torch.uint8, device=device)
-            st = call(fmt.pack(*fields, ws.data_ptr(), need.value), stream)
+        size = ctypes.c_size_t(0)
+        ok = getattr(lib, name + "_workspace_size")(fmt.pack(*fields, 0, 0), ctypes.byref(size))
+        if ok == TRA_OK and size.value > need:
+            if len(_seen) >= 4096:
+                _seen.clear()
+            need = _seen[key] = size.value
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+            st = call(fmt.pack(*fields, ws.data_ptr(), need), stream)
     if st != TRA_OK:
         raise TraError(st, name)
 
@@ -195,10 +206,10 @@ def _backward(dy, x, w, w2, z, act, need_dx, need_dw, need_bias):
             raise ValueError(f"z must be {M} x {width}")
     else:
         z = None
-    dx = torch.empty((M, K), dtype=x.dtype, device=x.device) if need_dx else None
+    dx = x.new_empty(M, K) if need_dx else None
     dw = _empty_weight(K, N, trans, x) if need_dw else None
     dw2 = _empty_weight(K, N, trans, x) if need_dw and gated else None
-    db = torch.empty((N,), dtype=x.dtype, device=x.device) if need_bias else None
+    db = x.new_empty(N) if need_bias else None
 
     def ptr(t):
         return 0 if t is None else t.data_ptr()
