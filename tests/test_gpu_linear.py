@@ -291,6 +291,10 @@ EXACT = [(1, 520, 4104), (5, 264, 96), (16, 1000, 264), (48, 200, 8), (64, 4096,
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("shape", EXACT, ids=str)
 def test_integers_are_exact(shape, dtype, layout, lib, monkeypatch):
+    check_integers(shape, dtype, layout, lib, monkeypatch)
+
+
+def check_integers(shape, dtype, layout, lib, monkeypatch):
     if lib == "poison":
         # every kernel fills its LDS with NaN first
         poisoned = tra.load_poisoned()
@@ -326,6 +330,19 @@ def test_integers_are_exact(shape, dtype, layout, lib, monkeypatch):
     assert torch.equal(dx, (zg @ vs[0].double().t() + zu @ vs[1].double().t()).to(dt))
     assert torch.equal(dg, (x.double().t() @ zg).to(dt))
     assert torch.equal(du, (x.double().t() @ zu).to(dt))
+
+
+# products that the 256 x 256 kernel takes (16 bits): forward, dX and dW each,
+# with ragged rows and a K tile that ends early
+WIDE = [(4090, 4104, 520), (4090, 520, 4104), (515, 4104, 4088)]
+
+
+@pytest.mark.parametrize("lib", ["product", "poison"])
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", WIDE, ids=str)
+def test_wide_integers_are_exact(shape, dtype, layout, lib, monkeypatch):
+    check_integers(shape, dtype, layout, lib, monkeypatch)
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
@@ -369,6 +386,55 @@ def test_packed_gate_and_up_weights():
         _, dg, du = tra.gated_linear_backward(torch.ones_like(h), x, wg, wu, z)
         want = torch.cat([dg, du], 1)
         assert torch.equal(dp if packed is kn else dp.t(), want)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_rows_past_32_bit_offsets(dtype):
+    # rows 5 GB (and more) into a buffer, for every operand that has rows
+    dt = DTYPES[dtype]
+    M, N, K, ld = 70000, 72, 64, 40000
+    big = torch.empty(M, ld, device="cuda", dtype=dt)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x, y = big[:, :K], big[:, 1024:1024 + N]
+    x.copy_(ints((M, K), -3, 3, gen, dt))
+    w = ints((K, N), -3, 3, gen, dt)
+    tra.linear(x, w, out=y)
+    want = (x.double() @ w.double()).to(dt)
+    assert torch.equal(y, want)
+    dx, dw, db = tra.linear_backward(y, x, w, need_dbias=True)
+    assert torch.equal(dx, (want.double() @ w.double().t()).to(dt))
+    del big, x, y
+
+
+def test_long_k():
+    # long enough that no summation order keeps 16-bit products exact: the bound
+    for dtype in DTYPES:
+        x, (w,), b, r, dy = make(20, 24, 150000, DTYPES[dtype], "nk")
+        check_linear(x, w, b, r, "silu", tra.linear(x, w, b, "silu", r))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("shape", [(5, 96, 128), (90, 136, 264), (300, 512, 520)], ids=str)
+def test_operands_off_alignment(shape, dtype):
+    # every pointer one element past a 16-byte boundary, row lengths aligned
+    M, N, K = shape
+    dt = DTYPES[dtype]
+    gen = torch.Generator(device="cuda").manual_seed(6)
+
+    def off(rows, cols):
+        t = torch.randn(rows, cols + 16, generator=gen, device="cuda").to(dt)
+        return t[:, 1:cols + 1]
+
+    for layout in ("kn", "nk"):
+        x, r = off(M, K), off(M, N)
+        w = off(K, N) if layout == "kn" else off(N, K).t()
+        b = torch.randn(N + 1, generator=gen, device="cuda").to(dt)[1:]
+        out = off(M, N)
+        check_linear(x, w, b, r, "gelu", tra.linear(x, w, b, "gelu", r, out=out))
+        dy = off(M, N)
+        dx, dw, db = tra.linear_backward(dy, x, w, need_dbias=True)
+        zero = torch.zeros(M, N, device="cuda", dtype=torch.float64)
+        check_grads(x, w, dy.double(), zero, dt, dx, dw, db)
 
 
 def test_residual_in_place():
@@ -479,6 +545,48 @@ def test_captured_step_replays():
         got = [t.clone() for t in out]
         want = step()
         assert all(torch.equal(a, w) for a, w in zip(got, want)), i
+
+
+def test_graphs_and_streams_side_by_side():
+    # two captured graphs and an eager call, all with a split, on three streams at
+    # once: each has its own workspace
+    M, N, K = 24, 512, 8192
+    x, ws, b, r, dy = make(M, N, K, torch.bfloat16, "kn", gated=True)
+    xs = [x, x.flip(0).contiguous(), -x]
+    want = [tra.gated_linear(t, *ws) for t in xs]
+    assert want[0].isfinite().all() and not torch.equal(want[0], want[1])
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for t in xs[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append([tra.gated_linear(t, *ws) for _ in range(8)])
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = [tra.gated_linear(xs[2], *ws) for _ in range(8)]
+        torch.cuda.synchronize()
+        for got, w in zip([*outs, eager], want):
+            assert all(torch.equal(y, w) for y in got)
+
+
+def test_autograd_is_refused_in_a_capture():
+    # (a stand-in for the capture: nothing is recorded on the GPU)
+    x, (w,), b, _, _ = make(4, 8, 16, torch.float32, "kn")
+    real = torch.cuda.is_current_stream_capturing
+    torch.cuda.is_current_stream_capturing = lambda: True
+    try:
+        with pytest.raises(RuntimeError, match="captured"):
+            tra.linear(x.detach().requires_grad_(), w)
+        with pytest.raises(RuntimeError, match="captured"):
+            tra.gated_linear(x, w, w.detach().clone().requires_grad_())
+        tra.linear(x, w)
+    finally:
+        torch.cuda.is_current_stream_capturing = real
 
 
 def test_block_of_both():

@@ -185,6 +185,45 @@ def test_describe_tells_aligned_from_unaligned():
     assert describe(fwd(M=0, X=0, Y=0)) == {"kernel": "none"}
 
 
+def plan(M, N, K, dtype, layout, gated=0, pad=0):
+    kn = layout == "kn"
+    return describe(fwd(M=M, N=N, K=K, dtype=dtype, w_trans=0 if kn else 1, gated=gated,
+                        W2=W2 if gated else 0, ldx=K + pad, ldw=(N if kn else K) + pad, ldy=N))
+
+
+@pytest.mark.parametrize("args, want", [
+    # one token: straight from memory; few strips and a long K: a split instead
+    ((1, 2048, 2048, 1, "nk"), dict(kernel="linear_few", splits="1")),
+    ((16, 1024, 1024, 0, "kn"), dict(kernel="linear_few", tile="16x16")),
+    ((1, 12288, 4096, 1, "nk", 1), dict(kernel="linear_few", tile="16x32")),
+    ((2, 512, 8192, 1, "kn"), dict(kernel="linear_tile")),
+    # many 16-bit tiles
+    ((8192, 12288, 4096, 1, "nk", 1), dict(tile="256x256", loads="direct")),
+    ((4096, 4096, 4096, 2, "kn"), dict(tile="256x256")),
+    # ... not in binary32, nor unaligned
+    ((4096, 4096, 4096, 0, "kn"), dict(tile="128x128", loads="direct")),
+    ((4096, 4096, 4096, 1, "kn", 0, 1), dict(tile="128x128", loads="registers")),
+    ((4096, 4096, 4096, 0, "nk", 0, 1), dict(loads="registers")),
+    # a tile a CU
+    ((1024, 1024, 1024, 0, "kn"), dict(tile="64x64", splits="1")),
+    ((333, 8192, 2048, 1, "nk"), dict(tile="128x128", splits="1")),
+], ids=str)
+def test_plans(args, want):
+    got = plan(*args)
+    assert {k: got[k] for k in want} == want, got
+
+
+def test_splits_cover_every_k_tile_once():
+    for M, N, K, dtype in ((20, 200, 100000, 1), (100, 500, 7777, 0), (64, 64, 64, 2),
+                           (17, 1000, 12345, 2), (300, 300, 30000, 0)):
+        d = plan(M, N, K, dtype, "nk")
+        tiles = -(-K // (32 if dtype == 0 else 64))
+        splits = int(d["splits"])
+        per = -(-tiles // splits)
+        assert (splits - 1) * per < tiles <= splits * per
+        assert int(d["workspace_bytes"]) == (0 if splits == 1 else splits * M * N * 4)
+
+
 def test_binding_refuses_cpu_tensors_and_bad_arguments():
     x, w = torch.ones(2, 3), torch.ones(3, 4)
     with pytest.raises(TypeError):

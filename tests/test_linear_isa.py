@@ -1,0 +1,65 @@
+"""Static properties of the fused linear kernels' gfx950 code (host only).
+
+The direct-load kernels wait for their loads by explicit counts.  A
+vector-memory wait that the compiler puts right before an LDS read waits for
+loads still in flight into other stages; none may stand among the MFMAs.  And
+every direct load writes LDS at M0, which must be set.
+"""
+from __future__ import annotations
+
+import os
+import re
+import subprocess
+
+import pytest
+
+from tiling_roofline_analysis_amd import build
+
+
+@pytest.fixture(scope="module", params=["linear_bf16.hip", "linear_f32.hip"])
+def kernels(request, tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("isa") / "k.s")
+    cmd = [build.hipcc(), *build.FLAGS, "--cuda-device-only", "-S",
+           os.path.join(build.CSRC, request.param), "-o", out]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    with open(out) as fh:
+        text = fh.read()
+    found = {}
+    for m in re.finditer(r"^(_Z\S+):\s*;\s*@\1\n(.*?)^\.Lfunc_end", text, re.M | re.S):
+        lines = [x.split(";")[0].strip() for x in m.group(2).splitlines()]
+        found[m.group(1)] = [x for x in lines if x and not x.startswith(".")]
+    return request.param, found
+
+
+def direct(found):
+    dma = re.compile(r"^buffer_load_dwordx4 .* lds$")
+    return {n: b for n, b in found.items() if any(dma.match(x) for x in b)}
+
+
+def test_the_direct_kernels_are_there(kernels):
+    src, found = kernels
+    got = direct(found)
+    tiles = [n for n in got if "linear_tile" in n]
+    wide = [n for n in got if "linear_wide" in n]
+    # three tile sizes, shallow and deep, by three forms plain and two gated
+    assert len(tiles) == 30
+    # the 256 x 256 kernel: 16 bits only
+    assert len(wide) == (0 if src == "linear_f32.hip" else 5)
+
+
+def test_fragment_reads_wait_for_no_other_stage(kernels):
+    _, found = kernels
+    memory = re.compile(r"(ds_|global_|buffer_|s_barrier|s_endpgm)")
+    for name, body in direct(found).items():
+        last = max(i for i, x in enumerate(body) if x.startswith("v_mfma"))
+        for i, x in enumerate(body[:last]):
+            if x.startswith("s_waitcnt") and "vmcnt" in x:
+                after = next(y for y in body[i + 1:] if memory.match(y))
+                assert not after.startswith("ds_read"), f"{name}: '{x}' before '{after}'"
+
+
+def test_m0_is_set(kernels):
+    _, found = kernels
+    for name, body in direct(found).items():
+        assert any(re.match(r"s_\w+ m0,", x) for x in body), name

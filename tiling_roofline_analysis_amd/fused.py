@@ -9,7 +9,8 @@ comes from torch's allocator, so calls may be captured into a graph.  With
 gradients enabled and an input that requires one they are differentiable
 (once): the backward pass runs in the library too.  ``linear_backward`` and
 ``gated_linear_backward`` are those passes by themselves, for callers that
-keep their own order of work (a captured training step, a pipeline).
+keep their own order of work (a pipeline, a captured training step: autograd
+itself is refused inside a capture).
 
 x is M x K, the weights K x N: row-major, or the transposed view of a row-major
 N x K tensor (``w.t()`` of a torch.nn.Linear weight).  float32, bfloat16 or
@@ -241,6 +242,7 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
+        _no_capture()
         x, w, z = ctx.saved_tensors
         need_x, need_w, need_b, need_r, _ = ctx.needs_input_grad
         dx = dw = db = None
@@ -260,6 +262,7 @@ class _GatedLinear(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dh):
+        _no_capture()
         x, w_gate, w_up, z = ctx.saved_tensors
         need_x, need_g, need_u, _ = ctx.needs_input_grad
         dx, dg, du, _ = _backward(_rows(dh), x, w_gate, w_up, z, ctx.act, need_x,
@@ -271,8 +274,19 @@ def _wants_grad(*tensors) -> bool:
     if torch.is_grad_enabled():
         for t in tensors:
             if isinstance(t, torch.Tensor) and t.requires_grad:
+                _no_capture()
                 return True
     return False
+
+
+def _no_capture():
+    # Autograd's engine orders a leaf's gradient behind the stream that the leaf
+    # was first used on.  Inside a capture, with an eager graph of the same leaf
+    # alive, that stream is outside the capture, and the process ends.
+    if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("gradients cannot be recorded into a captured graph: capture the call "
+                           "without gradients (z=...) and linear_backward or "
+                           "gated_linear_backward")
 
 
 def linear(x, w, bias=None, act="none", residual=None, out=None, z=None, stream=None):
