@@ -215,13 +215,17 @@ def test_plans(args, want):
 
 def test_splits_cover_every_k_tile_once():
     for M, N, K, dtype in ((20, 200, 100000, 1), (100, 500, 7777, 0), (64, 64, 64, 2),
-                           (17, 1000, 12345, 2), (300, 300, 30000, 0)):
+                           (17, 1000, 12345, 2), (300, 300, 30000, 0), (3000, 2049, 1531, 0),
+                           (4200, 4200, 4096, 1), (4608, 4608, 4096, 2)):
         d = plan(M, N, K, dtype, "nk")
         tiles = -(-K // (32 if dtype == 0 else 64))
         splits = int(d["splits"])
         per = -(-tiles // splits)
         assert (splits - 1) * per < tiles <= splits * per
-        assert int(d["workspace_bytes"]) == (0 if splits == 1 else splits * M * N * 4)
+        bm, bn = (int(v) for v in d["tile"].split("x"))
+        split_tiles = -(-M // bm) * -(-N // bn) - int(d["whole"])
+        assert (split_tiles > 0) == (splits > 1)
+        assert int(d["workspace_bytes"]) == (splits > 1) * split_tiles * splits * bm * bn * 4
 
 
 def test_binding_refuses_cpu_tensors_and_bad_arguments():

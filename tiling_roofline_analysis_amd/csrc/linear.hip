@@ -15,28 +15,36 @@ namespace {
 
 // ---- joining a split, gradients of the epilogue ----------------------------------------------
 
-// One chunk of columns per lane: the partial sums in split order, then the
-// epilogue.
+// One chunk of columns of a split tile per lane: the partial sums in split order,
+// then the epilogue.
 template <typename T, bool GATED>
-__global__ __launch_bounds__(256) void linear_join(const TileArgs p) {
+__global__ __launch_bounds__(256) void linear_join(const TileArgs p, int bm, int bn, int blocks) {
     constexpr int V = kChunk<T>;
-    const int64_t vpr = ceil_div(p.N, V);
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (id >= vpr * p.M) return;
+    const int cols = GATED ? bn / 2 : bn, per_row = cols / V;
+    const int at = static_cast<int>(blockIdx.x) / blocks;
+    const int item = (static_cast<int>(blockIdx.x) - at * blocks) * 256 + threadIdx.x;
+    const int row = item / per_row, col = (item - row * per_row) * V;
     const int batch = blockIdx.y;
-    const int64_t m = id / vpr, n = (id - m * vpr) * V;
-    const int64_t np = GATED ? 2 * p.N : p.N;
+    int tm, tn;
+    if (bm == 256)
+        grouped_tile32<kGroupWide>(p.whole + at, p.tiles_m, p.tiles_n, tm, tn);
+    else
+        grouped_tile32<kGroupTile>(p.whole + at, p.tiles_m, p.tiles_n, tm, tn);
+    const int64_t m = static_cast<int64_t>(tm) * bm + row, n = static_cast<int64_t>(tn) * cols + col;
+    if (row >= bm || m >= p.M || n >= p.N) return;
+    const int split_tiles = p.tiles_m * p.tiles_n - p.whole, area = bm * bn;
+    const float *in = p.partial +
+                      (static_cast<int64_t>(batch) * split_tiles + at) * p.splits * area +
+                      row * bn + col;
     float z[V] = {}, u[V] = {};
-    const int64_t next = static_cast<int64_t>(p.batch) * p.M * np;
-    const float *in = p.partial + (static_cast<int64_t>(batch) * p.M + m) * np + n;
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s, in += next) {
+    for (int s = 0; s < p.splits; ++s, in += area) {
         float t[V];
-        load_part<float, V>(in, p.N - n, t);
+        load_row<float, V>(in, t);
 #pragma unroll
         for (int e = 0; e < V; ++e) z[e] += t[e];
         if constexpr (GATED) {
-            load_part<float, V>(in + p.N, p.N - n, t);
+            load_row<float, V>(in + cols, t);
 #pragma unroll
             for (int e = 0; e < V; ++e) u[e] += t[e];
         }
@@ -120,13 +128,16 @@ __global__ __launch_bounds__(256) void linear_colsum_join(const float *colsum, i
 }
 
 template <typename T>
-hipError_t launch_join(bool gated, const TileArgs &a, hipStream_t stream) {
-    const int64_t blocks = ceil_div(ceil_div(a.N, kChunk<T>) * a.M, 256);
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(a.batch));
-    if (gated)
-        linear_join<T, true><<<grid, 256, 0, stream>>>(a);
+hipError_t launch_join(const TilePlan &t, const TileArgs &a, hipStream_t stream) {
+    const int64_t rows = a.M < t.bm ? a.M : t.bm;
+    const int blocks =
+        static_cast<int>(ceil_div(rows * (t.gated ? t.bn / 2 : t.bn) / kChunk<T>, 256));
+    const dim3 grid(static_cast<unsigned>((a.tiles_m * a.tiles_n - a.whole) * blocks),
+                    static_cast<unsigned>(a.batch));
+    if (t.gated)
+        linear_join<T, true><<<grid, 256, 0, stream>>>(a, t.bm, t.bn, blocks);
     else
-        linear_join<T, false><<<grid, 256, 0, stream>>>(a);
+        linear_join<T, false><<<grid, 256, 0, stream>>>(a, t.bm, t.bn, blocks);
     return hipGetLastError();
 }
 
@@ -234,8 +245,9 @@ struct TileClass {
     double base;      // launch, first loads, epilogue without its stores
 };
 
+constexpr int64_t kCUs = 256;
 constexpr double kBytesPerUs = 4.8e6;     // memory, as a large copy reaches
-constexpr double kBytesPerUsWg = 3.0e4;   // what one workgroup's loads in flight can ask for
+constexpr double kBytesPerUsWg = 2.2e4;   // what one workgroup's loads in flight can ask for
 
 // direct loads, 16-bit and binary32; through registers, the same.  The 256 x 256
 // kernel is built for direct 16-bit loads only; 128 x 128 through registers in
@@ -262,6 +274,8 @@ constexpr TileClass kClasses[2][2][4] = {
 //   Tiles: a CU runs its share of the workgroups (tiles x splits), `resident` at a
 //   time; the K loop is bounded by the operands' bytes too; the results' stores
 //   add to it.  A split stores binary32 sums and adds a launch that reads them.
+//   Split are all tiles, where they are few, or those of the last, partial round
+//   over the CUs, whose K loops would leave most CUs idle.
 //   Few rows: the weights' bytes at the rate that their strips can ask for (one
 //   strip, of 512 lanes, about 25 GB/s; 64-byte pieces of rows K apart reach about
 //   half of the memory's rate in 16 bits; unaligned rows three quarters).
@@ -278,32 +292,47 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
     for (const TileClass &c : kClasses[direct ? 0 : 1][f32 ? 1 : 0]) {
         if (c.bm == 0) break;
         const int64_t tiles = std::max<int64_t>(
-            1, ceil_div(M, c.bm) * ceil_div(N, gated ? c.bn / 2 : c.bn) * batch);
-        for (int64_t want = 1; want <= 32 && want <= k_tiles; ++want) {
-            if (want > 1 && tiles * want > 1024) break;
+            1, ceil_div(M, c.bm) * ceil_div(N, gated ? c.bn / 2 : c.bn));     // of a batch
+        // 64-byte lines (16-bit weights, 64 x 64 tiles, not k-contiguous)
+        const double most = kBytesPerUs * (form == tra::kFormKN && !f32 && c.bn == 64 ? 0.7 : 1.0);
+        const double area = std::min<double>(M, c.bm) * std::min<double>(columns, c.bn);
+        const double out = (kept ? 4.0 : 0.0) + (gated ? 0.5 : 1.0) * b;     // per column of z or u
+        // K loops of n workgroups of `per` K tiles
+        auto loops = [&](int64_t n, int64_t per) {
+            const int64_t wave = kCUs * c.resident;
+            const int64_t full = n / wave, rest = ceil_div(n % wave, kCUs);
+            return per * (full * std::max(c.alone, c.resident * c.shared) +
+                          (rest > 0 ? std::max(c.alone, rest * c.shared) : 0.0));
+        };
+        auto consider = [&](int64_t whole, int64_t want) {
             const int64_t per = ceil_div(k_tiles, want), splits = ceil_div(k_tiles, per);
-            if (splits != want) continue;
-            const int64_t n = tiles * splits, wave = 256 * c.resident;
-            const int64_t full = n / wave, rest = ceil_div(n % wave, 256);
-            double loop = per * (full * std::max(c.alone, c.resident * c.shared) +
-                                 (rest > 0 ? std::max(c.alone, rest * c.shared) : 0.0));
-            // 64-byte lines (16-bit weights, 64 x 64 tiles, not k-contiguous)
-            const double most =
-                kBytesPerUs * (form == tra::kFormKN && !f32 && c.bn == 64 ? 0.7 : 1.0);
+            if (splits != want || want > k_tiles) return;
+            const int64_t parts = batch * (tiles - whole) * splits, n = batch * whole + parts;
+            double loop = (whole > 0 ? loops(batch * whole, k_tiles) : 0.0) +
+                          (parts > 0 ? loops(parts, per) : 0.0);
             loop = std::max(loop, in / std::min(most, n * kBytesPerUsWg));
-            // bytes stored per column of z or u
-            const double out = splits > 1 ? 4.0 : (kept ? 4.0 : 0.0) + (gated ? 0.5 : 1.0) * b;
-            const double stored = splits * static_cast<double>(batch) * M * columns * out;
+            const double sums = splits > 1 ? parts * area * 4.0 : 0.0;
+            const double stored = sums + batch * (splits > 1 ? whole : tiles) * area * out;
             double us = c.base + loop + stored / kBytesPerUs;
-            if (splits > 1) us += 2.7 + stored / kBytesPerUs;
+            if (splits > 1) us += 2.7 + sums / kBytesPerUs;
             if (best_us == 0.0 || us < best_us) {
                 best_us = us;
                 best.bm = c.bm;
                 best.bn = c.bn;
+                best.whole = static_cast<int>(splits > 1 ? whole : tiles);
                 best.splits = static_cast<int>(splits);
-                best.deep = direct && n <= 256;
+                best.deep = direct && n <= kCUs;
+                best.partial_bytes =
+                    splits > 1 ? static_cast<size_t>(parts) * c.bm * c.bn * sizeof(float) : 0;
             }
-        }
+        };
+        // none split; all split; those past the last whole round over the CUs split
+        consider(tiles, 1);
+        for (int64_t want = 2; want <= 32 && tiles * batch * want <= 1024; ++want)
+            consider(0, want);
+        const int64_t rounds = tiles * batch / kCUs * kCUs / batch;
+        if (rounds > 0 && rounds < tiles && kCUs % batch == 0)
+            for (int64_t want = 2; want <= 16; ++want) consider(rounds, want);
     }
     const int64_t strip = form == tra::kFormKK ? 16 : 64 / b;
     if (form != tra::kFormNN && M <= 16 && K >= 16 / b && N >= 4 / b) {
@@ -316,6 +345,7 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
         if (us < best_us) {
             best = TilePlan{};
             best.few = true;
+            best.whole = static_cast<int>(ceil_div(N, strip));
             best.bm = 16;
             best.bn = static_cast<int>(gated ? 2 * strip : strip);
             best.splits = 1;
@@ -324,9 +354,6 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
     best.form = form;
     best.gated = gated;
     best.direct = direct;
-    best.partial_bytes = best.splits > 1 ? static_cast<size_t>(best.splits) * batch * M *
-                                               (gated ? 2 : 1) * N * sizeof(float)
-                                         : 0;
     return best;
 }
 
@@ -341,6 +368,7 @@ tra_status finish_args(const TilePlan &t, int dtype, TileArgs &a, float *partial
     a.tiles_n = static_cast<int>(tn);
     a.seg_tiles = static_cast<int>(ceil_div(a.K, slice));
     a.k_tiles = a.segs * a.seg_tiles;
+    a.whole = t.splits > 1 ? t.whole : a.tiles_m * a.tiles_n;
     a.splits = t.splits;
     a.tiles_per_split = static_cast<int>(ceil_div(std::max(a.k_tiles, 1), t.splits));
     a.partial = t.splits > 1 ? partial : nullptr;
@@ -357,17 +385,17 @@ hipError_t run_tile(int dtype, const TilePlan &t, const TileArgs &a, hipStream_t
     }
 }
 
-hipError_t run_join(int dtype, bool gated, const TileArgs &a, hipStream_t s) {
+hipError_t run_join(int dtype, const TilePlan &t, const TileArgs &a, hipStream_t s) {
     switch (dtype) {
-        case TRA_DTYPE_F32: return tra::launch_join<float>(gated, a, s);
-        case TRA_DTYPE_BF16: return tra::launch_join<__bf16>(gated, a, s);
-        default: return tra::launch_join<_Float16>(gated, a, s);
+        case TRA_DTYPE_F32: return tra::launch_join<float>(t, a, s);
+        case TRA_DTYPE_BF16: return tra::launch_join<__bf16>(t, a, s);
+        default: return tra::launch_join<_Float16>(t, a, s);
     }
 }
 
 hipError_t run_product(int dtype, const TilePlan &t, const TileArgs &a, hipStream_t s) {
     const hipError_t err = run_tile(dtype, t, a, s);
-    return err == hipSuccess && t.splits > 1 ? run_join(dtype, t.gated, a, s) : err;
+    return err == hipSuccess && t.splits > 1 ? run_join(dtype, t, a, s) : err;
 }
 
 tra_status status_of(hipError_t err) {
@@ -690,9 +718,10 @@ tra_status tra_linear_describe(const tra_linear_args *args, char *buf, size_t le
         return TRA_OK;
     }
     const TilePlan t = plan_forward(*args);
-    std::snprintf(buf, len, "kernel=%s tile=%dx%d loads=%s splits=%d workspace_bytes=%zu",
+    std::snprintf(buf, len, "kernel=%s tile=%dx%d loads=%s whole=%d splits=%d workspace_bytes=%zu",
                   t.few ? "linear_few" : "linear_tile", t.bm, t.bn,
-                  t.few || !t.direct ? "registers" : "direct", t.splits, t.partial_bytes);
+                  t.few || !t.direct ? "registers" : "direct", t.whole, t.splits,
+                  t.partial_bytes);
     return TRA_OK;
 }
 

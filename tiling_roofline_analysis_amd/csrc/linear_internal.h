@@ -47,8 +47,12 @@ struct TileArgs {
     int tiles_m, tiles_n;
     int seg_tiles;                      // K tiles of one segment
     int k_tiles;                        // K tiles in all
-    int splits, tiles_per_split;        // of the K tiles
-    float *partial;                     // splits > 1: [split][batch][M][N or 2N]
+    // Tiles 0 .. whole - 1 of each batch are computed whole.  Each of the others is
+    // split along K into `splits` parts of tiles_per_split K tiles, whose sums go to
+    // partial: [batch][tile - whole][split][bm][bn] (gated: bn / 2 of z, then of u).
+    int whole;
+    int splits, tiles_per_split;
+    float *partial;
     EpiArgs epi;
 };
 
@@ -67,9 +71,13 @@ struct TilePlan {
     int bm, bn;            // tile of P (gated: bn / 2 columns of each of z, u)
     bool direct;           // operands go straight into LDS (16-byte aligned)
     bool deep;             // direct: one workgroup a CU, with more stages
+    int whole;             // tiles of a batch not split along K (all when splits is 1)
     int splits;
     size_t partial_bytes;  // workspace of the split
 };
+
+// Tile rows swept together by the tile kernels (grouped_tile32), by tile height.
+constexpr int kGroupTile = 8, kGroupWide = 4;
 
 // Gradient of the epilogue, element by element: dZ = dY * act'(Z), or, gated,
 // dG | dU = dH * u * act'(g) | dH * act(g) from the kept [g | u]; and the

@@ -350,9 +350,11 @@ __device__ __forceinline__ void epi_get(const char *lds, int row, int col, float
 // is inside or outside as a whole, several rows are in hand at a time, with no
 // branch between a row's read and its store but those of the row's end: branches
 // and waits row by row took 8 us of a 128 x 128 tile in binary32.
+// Not a whole tile: the sums go to `sums` (this wave's rows and columns; rows
+// `pitch` long, half 1 half a row on) as they are.
 template <typename T, bool GATED, int HC, int ROWS>
-__device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, int split, const char *lds,
-                                         int64_t m0, int64_t n0, int64_t n1) {
+__device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, float *sums, int pitch,
+                                         const char *lds, int64_t m0, int64_t n0, int64_t n1) {
     constexpr int V = kChunk<T>;
     constexpr int VPR = (GATED ? HC : 2 * HC) / V;   // chunks per row
     constexpr int RPI = 64 / VPR;                    // rows per step
@@ -367,22 +369,20 @@ __device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, int split
     const int first = lane / VPR;
     const int rows = static_cast<int>(p.M - m0 < ROWS ? p.M - m0 : ROWS);
 
-    if (p.partial != nullptr) {
-        const int64_t np = GATED ? 2 * p.N : p.N;
-        float *out = p.partial +
-                     ((static_cast<int64_t>(split) * p.batch + batch) * p.M + m0 + first) * np + n;
+    if (sums != nullptr) {
+        float *out = sums + first * pitch + (GATED || col < HC ? col : pitch / 2 + (col - HC));
 #pragma unroll 4
         for (int t = 0; t < STEPS; ++t) {
             const int row = t * RPI + first;
             if (row >= rows) break;
             float z[V];
             epi_get<HC>(lds, row, col, z);
-            store_part<float, V>(out, p.N - n, z);
+            store_row<float, V>(out, z);
             if constexpr (GATED) {
                 epi_get<HC>(lds, row, HC + col, z);
-                store_part<float, V>(out + p.N, p.N - n, z);
+                store_row<float, V>(out + pitch / 2, z);
             }
-            out += RPI * np;
+            out += RPI * pitch;
         }
         return;
     }
@@ -542,6 +542,33 @@ struct Walk {
     }
 };
 
+// What a workgroup computes: a whole tile, or one part of a split one.
+struct Part {
+    int tile;
+    int first, count;      // K tiles
+    float *sums;           // of a part: bm x bn, else null
+
+    __device__ __forceinline__ Part(const TileArgs &p, int batch, int area) {
+        const int tiles = p.tiles_m * p.tiles_n, bid = static_cast<int>(blockIdx.x);
+        if (bid < p.whole) {
+            tile = xcd_remap32(bid, p.whole);
+            first = 0;
+            count = p.k_tiles;
+            sums = nullptr;
+        } else {
+            const int split_tiles = tiles - p.whole;
+            const int id = xcd_remap32(bid - p.whole, static_cast<int>(gridDim.x) - p.whole);
+            const int split = id / split_tiles, at = id - split * split_tiles;
+            tile = p.whole + at;
+            first = split * p.tiles_per_split;
+            const int left = p.k_tiles - first;
+            count = left < p.tiles_per_split ? left : p.tiles_per_split;
+            sums = p.partial +
+                   ((static_cast<int64_t>(batch) * split_tiles + at) * p.splits + split) * area;
+        }
+    }
+};
+
 // Orders what stands since the last scheduling barrier: after each MFMA a share
 // of the LDS reads (all within the first half of the MFMAs, so that they are done
 // by the end) and of the loads.  A wave issues them while its MFMA runs; in a
@@ -593,19 +620,15 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
     });
 
     const int batch = blockIdx.y;
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int id = xcd_remap32(blockIdx.x, gridDim.x);
-    const int split = id / tiles;
+    const Part part(p, batch, BM * BN);
     int tm, tn;
-    grouped_tile32<8>(id - split * tiles, p.tiles_m, p.tiles_n, tm, tn);
+    grouped_tile32<kGroupTile>(part.tile, p.tiles_m, p.tiles_n, tm, tn);
     constexpr int NB = GATED ? BN / 2 : BN;
     const int64_t m0 = static_cast<int64_t>(tm) * BM;
     const int64_t n0 = static_cast<int64_t>(tn) * NB, n1 = GATED ? n0 : n0 + BN / 2;
     const int64_t rows_a = p.M - m0, rows_b0 = p.N - n0, rows_b1 = p.N - n1;
 
-    const int first = split * p.tiles_per_split;
-    const int left = p.k_tiles - first;
-    const int count = left < p.tiles_per_split ? left : p.tiles_per_split;
+    const int first = part.first, count = part.count;
 
     Walk<T, AKC, BKC> walk(p, batch, m0, n0, n1, GATED, first, count);
 
@@ -762,8 +785,9 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
                 for (int j = 0; j < TJ; ++j) c[0][h][i][j] += c[a][h][i][j];
     epi_put<HC>(mine, c[0][0], 0);
     epi_put<HC>(mine, c[0][1], 1);
-    epi_rows<T, GATED, HC, BM / 2>(p, batch, split, mine, m0 + wm * (BM / 2), n0 + wn * HC,
-                                   n1 + wn * HC);
+    epi_rows<T, GATED, HC, BM / 2>(
+        p, batch, part.sums == nullptr ? nullptr : part.sums + wm * (BM / 2) * BN + wn * HC, BN,
+        mine, m0 + wm * (BM / 2), n0 + wn * HC, n1 + wn * HC);
 }
 
 // ---- the kernel for few rows --------------------------------------------------------------
@@ -960,16 +984,12 @@ __global__ __launch_bounds__(512, 2) void linear_wide(const TileArgs p) {
     lds_poison(reinterpret_cast<float *>(b11), PB::BYTES / 4);
 
     const int batch = blockIdx.y;
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int id = xcd_remap32(blockIdx.x, gridDim.x);
-    const int split = id / tiles;
+    const Part part(p, batch, 256 * 256);
     int tm, tn;
-    grouped_tile32<4>(id - split * tiles, p.tiles_m, p.tiles_n, tm, tn);
+    grouped_tile32<kGroupWide>(part.tile, p.tiles_m, p.tiles_n, tm, tn);
     const int64_t m0 = static_cast<int64_t>(tm) * 256;
     const int64_t n0 = static_cast<int64_t>(tn) * (GATED ? 128 : 256), n1 = GATED ? n0 : n0 + 128;
-    const int first = split * p.tiles_per_split;
-    const int left = p.k_tiles - first;
-    const int count = left < p.tiles_per_split ? left : p.tiles_per_split;
+    const int first = part.first, count = part.count;
     Walk<T, AKC, BKC> walk(p, batch, m0, n0, n1, GATED, first, count);
     const int64_t lower = 128 * (AKC ? p.lda : 1) * static_cast<int64_t>(sizeof(T));
 
@@ -1092,8 +1112,10 @@ __global__ __launch_bounds__(512, 2) void linear_wide(const TileArgs p) {
     for (int h = 0; h < 2; ++h) {
         epi_put<32>(mine, c[h][0], 0);
         epi_put<32>(mine, c[h][1], 1);
-        epi_rows<T, GATED, 32, 64>(p, batch, split, mine, m0 + h * 128 + wm * 64, n0 + wn * 32,
-                                   n1 + wn * 32);
+        const int row = h * 128 + wm * 64;
+        epi_rows<T, GATED, 32, 64>(
+            p, batch, part.sums == nullptr ? nullptr : part.sums + row * 256 + wn * 32, 256, mine,
+            m0 + row, n0 + wn * 32, n1 + wn * 32);
     }
 }
 
@@ -1101,8 +1123,9 @@ __global__ __launch_bounds__(512, 2) void linear_wide(const TileArgs p) {
 
 template <typename T, bool AKC, bool BKC, bool GATED>
 hipError_t launch_tile(const TilePlan &plan, const TileArgs &a, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(a.tiles_m) * static_cast<unsigned>(a.tiles_n) *
-                        static_cast<unsigned>(a.splits),
+    const unsigned tiles = static_cast<unsigned>(a.tiles_m) * static_cast<unsigned>(a.tiles_n);
+    const unsigned whole = static_cast<unsigned>(a.whole);
+    const dim3 grid(whole + (tiles - whole) * static_cast<unsigned>(a.splits),
                     static_cast<unsigned>(a.batch));
     if constexpr (AKC) {
         if (plan.few) {
