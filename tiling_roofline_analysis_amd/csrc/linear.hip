@@ -278,7 +278,7 @@ constexpr TileClass kClasses[2][2][4] = {
 //   over the CUs, whose K loops would leave most CUs idle.
 //   Few rows: the weights' bytes at the rate that their strips can ask for (one
 //   strip, of 512 lanes, about 25 GB/s; 64-byte pieces of rows K apart reach about
-//   half of the memory's rate in 16 bits; unaligned rows three quarters).
+//   half of the memory's rate in 16 bits; unaligned 16-bit rows three quarters).
 // `kept`: binary32 values stored besides each result (the pre-activations).
 TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, int64_t K, int segs,
                    int batch, bool direct, bool kept) {
@@ -297,12 +297,14 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
         const double most = kBytesPerUs * (form == tra::kFormKN && !f32 && c.bn == 64 ? 0.7 : 1.0);
         const double area = std::min<double>(M, c.bm) * std::min<double>(columns, c.bn);
         const double out = (kept ? 4.0 : 0.0) + (gated ? 0.5 : 1.0) * b;     // per column of z or u
-        // K loops of n workgroups of `per` K tiles
+        // K loops of n workgroups of `per` K tiles; a little to begin another round
         auto loops = [&](int64_t n, int64_t per) {
             const int64_t wave = kCUs * c.resident;
             const int64_t full = n / wave, rest = ceil_div(n % wave, kCUs);
             return per * (full * std::max(c.alone, c.resident * c.shared) +
-                          (rest > 0 ? std::max(c.alone, rest * c.shared) : 0.0));
+                          (rest > 0 ? std::max(c.alone, rest * c.shared) : 0.0)) +
+                   (c.resident == 1 ? 3.0 : 1.5) *
+                       std::max<int64_t>(0, full + (rest > 0 ? 1 : 0) - 1);
         };
         auto consider = [&](int64_t whole, int64_t want) {
             const int64_t per = ceil_div(k_tiles, want), splits = ceil_div(k_tiles, per);
@@ -314,7 +316,7 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
             const double sums = splits > 1 ? parts * area * 4.0 : 0.0;
             const double stored = sums + batch * (splits > 1 ? whole : tiles) * area * out;
             double us = c.base + loop + stored / kBytesPerUs;
-            if (splits > 1) us += 2.7 + sums / kBytesPerUs;
+            if (splits > 1) us += 2.5 + 0.12 * splits + sums / kBytesPerUs;
             if (best_us == 0.0 || us < best_us) {
                 best_us = us;
                 best.bm = c.bm;
@@ -341,7 +343,7 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
                                                  : (f32 ? 3.8e6 : 2.4e6);
         const double each = form == tra::kFormKK ? 2.6e4 : f32 ? 1.8e4 : 3.0e4;
         const double us = 2.8 + segs * static_cast<double>(K) * columns * b * (1.0 + M / 80.0) /
-                                    std::min(most, strips * each) / (direct ? 1.0 : 0.75);
+                                    std::min(most, strips * each) / (direct || f32 ? 1.0 : 0.75);
         if (us < best_us) {
             best = TilePlan{};
             best.few = true;
