@@ -1045,7 +1045,6 @@ __global__ __launch_bounds__(512, 2) void linear_wide(const TileArgs p) {
     auto compute = [&](auto vm, auto ha, auto hb) __attribute__((always_inline)) {
         constexpr int HA = decltype(ha)::value, HB = decltype(hb)::value;
         stage_sync<decltype(vm)::value>();
-        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int step = 0; step < 2; ++step)
 #pragma unroll
@@ -1053,7 +1052,6 @@ __global__ __launch_bounds__(512, 2) void linear_wide(const TileArgs p) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     c[HA][HB][i][j] = mma16<T>(w[HB][step][j], x[step][i], c[HA][HB][i][j]);
-        __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
