@@ -621,6 +621,22 @@ def test_expanded_and_transposed_output_gradients():
         assert all(torch.equal(a, f) for a, f in zip(got, full))
 
 
+def test_one_row_of_any_stride():
+    # a row whose own stride is shorter than it, as the transpose of a column has
+    x, ws, b, _, _ = make(1, 48, 40, torch.float32, "kn", gated=True)
+    col = torch.randn(48, 1, device="cuda")
+    assert col.t().stride() == (1, 1)
+    leaves = [t.detach().requires_grad_() for t in (x, *ws)]
+    for y in (tra.linear(*leaves[:2], act="silu"), tra.gated_linear(*leaves)):
+        got = torch.autograd.grad(y, leaves[0], col.t(), retain_graph=True)
+        want = torch.autograd.grad(y, leaves[0], col.t().clone(
+            memory_format=torch.contiguous_format).as_strided((1, 48), (48, 1)))
+        assert torch.equal(got[0], want[0])
+    z = torch.empty(1, 48, device="cuda")
+    assert torch.equal(tra.linear(col[:40].t(), ws[0], z=z), tra.linear(col[:40].flatten()[None], ws[0]))
+    tra.linear_backward(col.t(), x, ws[0], z, "silu")
+
+
 def test_only_what_is_asked_for():
     x, (w,), b, _, dy = make(20, 24, 32, torch.float32, "kn")
     for i in range(3):

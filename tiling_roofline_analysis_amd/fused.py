@@ -105,10 +105,6 @@ def _vector(b, name, x, N):
         raise ValueError(f"{name} must be {N} contiguous elements")
 
 
-def _empty_weight(K, N, trans, like):
-    return like.new_empty(N, K).t() if trans else like.new_empty(K, N)
-
-
 # Workspace bytes of the calls seen so far, by name, type, layout and sizes: what
 # to allocate before a call.  Alignment and which gradients are asked for count
 # too, so a call may need more; the library then refuses it, before anything is
@@ -182,17 +178,17 @@ def _forward(x, w, w2, bias, residual, act, out, z):
               0 if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy,
               0 if z is None else z.data_ptr(), ldz)
     _call("tra_linear", _ARGS, fields, x.device)
-    return out, z
+    return out, z, (ldx, trans, ldw, ldz, code)
 
 
 def _backward(dy, x, w, w2, z, act, need_dx, need_dw, need_bias):
+    """Checks the tensors of a backward call and makes it."""
     gated = w2 is not None
     code = _act(act)
     ldx = _matrix(x, "x")
     lddy = _matrix(dy, "dy", x)
-    M, K = x.shape
     trans, ldw = _weight(w, "w_gate" if gated else "w", x)
-    N = w.shape[1]
+    M, N = x.shape[0], w.shape[1]
     if gated and (_weight(w2, "w_up", x) != (trans, ldw) or w2.shape != w.shape):
         raise ValueError("w_gate and w_up must have the same shape and strides")
     if dy.shape[0] != M or dy.shape[1] != N:
@@ -207,35 +203,51 @@ def _backward(dy, x, w, w2, z, act, need_dx, need_dw, need_bias):
             raise ValueError(f"z must be {M} x {width}")
     else:
         z = None
-    dx = x.new_empty(M, K) if need_dx else None
-    dw = _empty_weight(K, N, trans, x) if need_dw else None
-    dw2 = _empty_weight(K, N, trans, x) if need_dw and gated else None
-    db = x.new_empty(N) if need_bias else None
+    return _grads(dy, lddy, x, ldx, w, w2, trans, ldw, z, ldz, code, need_dx, need_dw, need_bias)
 
-    def ptr(t):
-        return 0 if t is None else t.data_ptr()
 
-    fields = (DTYPES[x.dtype], code, trans, int(gated), M, N, K, dy.data_ptr(), lddy, ptr(z), ldz,
-              x.data_ptr(), ldx, w.data_ptr(), ptr(w2), ldw, ptr(dx), K, ptr(dw), ptr(dw2),
-              max(1, K) if trans else max(1, N), ptr(db))
+def _grads(dy, lddy, x, ldx, w, w2, trans, ldw, z, ldz, code, need_dx, need_dw, need_bias):
+    M, K = x.shape
+    N = w.shape[1]
+    dx = dw = dw2 = db = None
+    pdx = pdw = pdw2 = pdb = 0
+    if need_dx:
+        dx = x.new_empty(M, K)
+        pdx = dx.data_ptr()
+    if need_dw:
+        dw = x.new_empty(N, K) if trans else x.new_empty(K, N)
+        pdw = dw.data_ptr()
+        if w2 is not None:
+            dw2 = torch.empty_like(dw)
+            pdw2 = dw2.data_ptr()
+    if need_bias:
+        db = x.new_empty(N)
+        pdb = db.data_ptr()
+    fields = (DTYPES[x.dtype], code, trans, 0 if w2 is None else 1, M, N, K, dy.data_ptr(), lddy,
+              0 if z is None else z.data_ptr(), ldz, x.data_ptr(), ldx, w.data_ptr(),
+              0 if w2 is None else w2.data_ptr(), ldw, pdx, K, pdw, pdw2, K if trans else N, pdb)
     _call("tra_linear_backward", _GRAD_ARGS, fields, x.device)
+    if trans:
+        dw, dw2 = (None if t is None else t.t() for t in (dw, dw2))
     return dx, dw, dw2, db
 
 
 def _rows(dy):
-    """dy as the library takes it: autograd may pass an expanded or transposed one."""
-    if dy.stride(1) == 1 and dy.stride(0) >= dy.shape[1]:
-        return dy
-    return dy.contiguous()
+    """dy as the library takes it (autograd may pass an expanded or transposed
+    one), and its leading dimension."""
+    cols = dy.shape[1]
+    s0, s1 = dy.stride()
+    if s1 == 1 and s0 >= cols > 0:
+        return dy, s0
+    return dy.contiguous(), cols     # (one row may keep any stride)
 
 
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, residual, act):
         need = any(ctx.needs_input_grad[:3])
-        y, z = _forward(x, w, None, bias, residual, act, None,
-                        True if need and act != "none" else None)
-        ctx.act = act
+        y, z, ctx.layout = _forward(x, w, None, bias, residual, act, None,
+                                    True if need and act != "none" else None)
         ctx.save_for_backward(x, w, z)
         return y
 
@@ -243,19 +255,21 @@ class _Linear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         _no_capture()
-        x, w, z = ctx.saved_tensors
         need_x, need_w, need_b, need_r, _ = ctx.needs_input_grad
-        dx = dw = db = None
-        if need_x or need_w or need_b:
-            dx, dw, _, db = _backward(_rows(dy), x, w, None, z, ctx.act, need_x, need_w, need_b)
+        if not (need_x or need_w or need_b):
+            return None, None, None, dy, None
+        x, w, z = ctx.saved_tensors
+        ldx, trans, ldw, ldz, code = ctx.layout
+        rows, ld = _rows(dy)
+        dx, dw, _, db = _grads(rows, ld, x, ldx, w, None, trans, ldw, z, ldz, code,
+                               need_x, need_w, need_b)
         return dx, dw, db, dy if need_r else None, None
 
 
 class _GatedLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, act):
-        h, z = _forward(x, w_gate, w_up, None, None, act, None, True)
-        ctx.act = act
+        h, z, ctx.layout = _forward(x, w_gate, w_up, None, None, act, None, True)
         ctx.save_for_backward(x, w_gate, w_up, z)
         return h
 
@@ -264,9 +278,11 @@ class _GatedLinear(torch.autograd.Function):
     def backward(ctx, dh):
         _no_capture()
         x, w_gate, w_up, z = ctx.saved_tensors
+        ldx, trans, ldw, ldz, code = ctx.layout
         need_x, need_g, need_u, _ = ctx.needs_input_grad
-        dx, dg, du, _ = _backward(_rows(dh), x, w_gate, w_up, z, ctx.act, need_x,
-                                  need_g or need_u, False)
+        rows, ld = _rows(dh)
+        dx, dg, du, _ = _grads(rows, ld, x, ldx, w_gate, w_up, trans, ldw, z, ldz,
+                               code, need_x, need_g or need_u, False)
         return dx, dg if need_g else None, du if need_u else None, None
 
 
