@@ -466,7 +466,11 @@ __device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, float *su
 //   read step 0 of tile s + 1; compute step 1.
 // Without DIRECT (S = 2) tile s + 1 waits in registers until it is stored,
 // before the meeting, into the stage of tile s - 1.
-// (Reading both steps of tile s after the meeting: 1024^3 in binary32 31.9 us.)
+// Measured: 1024^3 in binary32 with bias, GELU and residual 21.3 us (64 x 64 tiles,
+// one a CU; with both steps of tile s read after the meeting, in a block of their
+// own, 31 us), per K tile 0.50 us against 0.43 of MFMAs at the datasheet's rate;
+// 128 x 128 tiles in binary32 1.77 us per K tile, 151 TFLOP/s; 16 bits, two a CU,
+// 0.83 us per two K tiles, 1.3 PFLOP/s, bounded by LDS reads and barriers.
 
 template <typename T, bool AKC, bool BKC, int BM, int BN>
 struct TileShape {
@@ -803,6 +807,8 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
 //                  of 8 (4) slices, and v_perm makes two operands of them.
 // Loads take any alignment, in bounds: columns past the last read the last, and
 // what lies past K is zeroed.
+// Measured: 1 x 2048 x 2048 bf16 5.3 us of device time (64 x 64 tiles split 4 ways,
+// and their join: 8.0); gated 1 x 12288 x 4096 bf16 37 us, 5.4 TB/s of weights.
 template <typename T, bool BKC>
 struct FewShape {
     static constexpr int WAVES = 8;
@@ -965,6 +971,10 @@ __global__ __launch_bounds__(512) void linear_few(const TileArgs p) {
 // barrier that follows them, and the group behind reads one barrier later.  In
 // phase 3 a wave waits until only its last three panels are in flight: all of tile
 // s + 1 is then in LDS two barriers on, when the first group reads it.
+// Measured: gated 8192 x 12288 x 4096 bf16 1130 us, 1.45 PFLOP/s, its matrix units
+// busy 79% of the cycles (128 x 128 tiles: 1490 us); 1.42 us per K tile with all
+// CUs at work, 1.28 with fewer than a tile a CU, so power, more than the schedule,
+// bounds it; the stores of a tile, 7 us, are not hidden.
 template <typename T, bool AKC, bool BKC, bool GATED>
 __global__ __launch_bounds__(512, 2) void linear_wide(const TileArgs p) {
     using PA = Panel<T, AKC, 128, 8>;
