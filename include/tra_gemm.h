@@ -278,10 +278,11 @@ TRA_API tra_status tra_gemm_describe(int variant, int64_t M, int64_t N, int64_t 
  *
  * Scratch: the caller's workspace, 256-byte aligned, at least the bytes that
  * the size query gives for the same arguments (its own workspace fields are
- * ignored; pointers count, since alignment decides the plan).  Nothing in it
- * needs to be set, nothing is kept in it between calls, and calls that may run
- * at the same time each need their own.  No call allocates, so all of them
- * may be captured into a graph; the graph keeps the pointers.
+ * ignored; pointers count, since alignment decides the plan), apart from every
+ * operand.  Nothing in it needs to be set, nothing is kept in it between
+ * calls, and calls that may run at the same time each need their own.  No call
+ * allocates, so all of them may be captured into a graph; the graph keeps the
+ * pointers.
  *
  * Sizes: any of M, N, K may be 0 (an empty sum is 0).  Outputs may share no
  * element with inputs or each other, but Y may be R itself.  Elements between

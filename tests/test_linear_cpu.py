@@ -129,6 +129,10 @@ def test_sizes_past_the_limits_are_unsupported():
     assert tra.load().tra_linear(fwd(M=1 << 29, N=1 << 29, ldw=1 << 29, ldy=1 << 29, W=1 << 58,
                                      Y=1 << 61), None) == UNSUPPORTED
     assert tra.load().tra_linear_backward(bwd(K=big, ldx=big, lddx=big), None) == UNSUPPORTED
+    wide = 1 << 28
+    assert tra.load().tra_linear_backward(
+        bwd(N=wide, K=1, lddy=wide, ldz=wide, ldw=wide, lddw=wide, ldx=1, lddx=1, dbias=DB),
+        None) == UNSUPPORTED
 
 
 def test_empty_results_need_nothing():

@@ -364,8 +364,10 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
 tra_status finish_args(const TilePlan &t, int dtype, TileArgs &a, float *partial) {
     const int64_t slice = 128 / elem_bytes(dtype);
     const int64_t tm = ceil_div(a.M, t.bm), tn = ceil_div(a.N, t.gated ? t.bn / 2 : t.bn);
-    // kMaxGridLanes work-items, and tile indices in 32 bits
-    if (static_cast<__int128>(tm) * tn * t.splits * 512 > tra::kMaxGridLanes)
+    // kMaxGridLanes work-items (512 a workgroup), and tile indices in 32 bits
+    const __int128 tiles = static_cast<__int128>(tm) * tn;
+    const __int128 whole = t.splits > 1 ? static_cast<__int128>(t.whole) : tiles;
+    if ((whole + (tiles - whole) * t.splits) * 512 > tra::kMaxGridLanes)
         return TRA_ERR_UNSUPPORTED;
     a.tiles_m = static_cast<int>(tm);
     a.tiles_n = static_cast<int>(tn);
@@ -557,6 +559,8 @@ tra_status check_backward(const tra_linear_grad_args *p) {
               : a.W2 != nullptr || a.dW2 != nullptr)
         return TRA_ERR_INVALID_ARG;
     if (a.M > kMaxSize || a.N > kMaxSize / 2 || a.K > kMaxSize / 2) return TRA_ERR_UNSUPPORTED;
+    // linear_colsum_join: 16 lanes a column
+    if (a.dbias != nullptr && a.N * 16 > tra::kMaxGridLanes - 256) return TRA_ERR_UNSUPPORTED;
     const int64_t b = elem_bytes(a.dtype);
     const bool slope = gated || a.act != TRA_ACT_NONE;
     const int64_t wz = gated ? 2 * a.N : a.N;
