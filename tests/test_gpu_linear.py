@@ -504,6 +504,19 @@ def test_same_bits_every_time():
             assert all(torch.equal(a, g) for a, g in zip(again, grads))
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_huge_pre_activations_stay_finite(act):
+    # values whose squares pass binary32: act and its slope are at their limits
+    x = torch.tensor([[1e20], [-1e20], [3e38], [-3e38], [0.0]], device="cuda")
+    w = torch.ones(1, 4, device="cuda")
+    z = torch.empty(5, 4, device="cuda")
+    y = tra.linear(x, w, act=act, z=z)
+    want, slope = act64(x.double(), act if act != "gelu_tanh" else "gelu")
+    assert torch.equal(y[:, 0], want[:, 0].float())
+    dx, _, _ = tra.linear_backward(torch.ones(5, 4, device="cuda"), x, w, z, act)
+    assert torch.equal(dx[:4], 4 * slope[:4].float())
+
+
 # --- streams, graphs, autograd -------------------------------------------------------
 
 def test_another_stream():

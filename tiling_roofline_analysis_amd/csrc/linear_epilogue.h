@@ -79,7 +79,8 @@ __device__ __forceinline__ float activate_slope(float z, float &y) {
     if constexpr (ACT == TRA_ACT_GELU_TANH) {
         const float s = sigmoid(z * (kGeluA + kGeluB * z * z));
         y = z * s;
-        return s + y * (1.0f - s) * (kGeluA + 3.0f * kGeluB * z * z);
+        // s is 0 or 1 long before |z| = 1000; z^2 must not overflow against it
+        return s + y * (1.0f - s) * (kGeluA + 3.0f * kGeluB * fminf(z * z, 1e6f));
     }
     if constexpr (ACT == TRA_ACT_SILU) {
         const float s = sigmoid(z);
