@@ -519,6 +519,22 @@ def test_huge_pre_activations_stay_finite(act):
 
 # --- streams, graphs, autograd -------------------------------------------------------
 
+def test_written_outputs_are_known_to_autograd():
+    # a tensor saved for another gradient and then overwritten is an error, not a
+    # wrong gradient
+    x, (w,), b, r, _ = make(8, 16, 24, torch.float32, "kn")
+    p = torch.ones(8, 16, device="cuda", requires_grad=True)
+    saved = torch.randn(8, 16, device="cuda")
+    loss = (p * saved).sum()
+    tra.linear(x, w, out=saved)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with pytest.raises(ValueError):
+        tra.linear(x, w, out=torch.empty(8, 16, device="cuda", requires_grad=True))
+    with pytest.raises(TypeError):
+        tra.linear(x, w, z=True)
+
+
 def test_another_stream():
     x, ws, b, r, _ = make(64, 256, 2048, torch.bfloat16, "nk", gated=True)
     want = tra.gated_linear(x, *ws)

@@ -140,8 +140,11 @@ def _call(name, fmt, fields, device):
         raise TraError(st, name)
 
 
+_KEEP = object()
+
+
 def _forward(x, w, w2, bias, residual, act, out, z):
-    """One forward call; z (True: allocate it) keeps the pre-activations."""
+    """One forward call; z (_KEEP: allocate it) keeps the pre-activations."""
     gated = w2 is not None
     code = _act(act)
     ldx = _matrix(x, "x")
@@ -168,7 +171,7 @@ def _forward(x, w, w2, bias, residual, act, out, z):
     ldz = 0
     if z is not None:
         width = 2 * N if gated else N
-        if z is True:
+        if z is _KEEP:
             z = torch.empty((M, width), dtype=torch.float32, device=x.device)
         ldz = _matrix(z, "z", x, torch.float32)
         if z.shape[0] != M or z.shape[1] != width:
@@ -247,7 +250,7 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, w, bias, residual, act):
         need = any(ctx.needs_input_grad[:3])
         y, z, ctx.layout = _forward(x, w, None, bias, residual, act, None,
-                                    True if need and act != "none" else None)
+                                    _KEEP if need and act != "none" else None)
         ctx.save_for_backward(x, w, z)
         return y
 
@@ -269,7 +272,7 @@ class _Linear(torch.autograd.Function):
 class _GatedLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, act):
-        h, z, ctx.layout = _forward(x, w_gate, w_up, None, None, act, None, True)
+        h, z, ctx.layout = _forward(x, w_gate, w_up, None, None, act, None, _KEEP)
         ctx.save_for_backward(x, w_gate, w_up, z)
         return h
 
@@ -290,16 +293,31 @@ def _wants_grad(*tensors) -> bool:
     if torch.is_grad_enabled():
         for t in tensors:
             if isinstance(t, torch.Tensor) and t.requires_grad:
-                _no_capture()
+                if t.is_cuda:
+                    _no_capture()
                 return True
     return False
+
+
+def _on(stream, x):
+    """The context of a caller's stream, which is one of x's device."""
+    if isinstance(x, torch.Tensor) and x.is_cuda and stream.device != x.device:
+        raise ValueError(f"stream is on {stream.device}, x on {x.device}")
+    return torch.cuda.stream(stream)
+
+
+def _written(*tensors):
+    """Tells autograd that these were written in place."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
 
 
 def _no_capture():
     # Autograd's engine orders a leaf's gradient behind the stream that the leaf
     # was first used on.  Inside a capture, with an eager graph of the same leaf
     # alive, that stream is outside the capture, and the process ends.
-    if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+    if torch.cuda.is_current_stream_capturing():
         raise RuntimeError("gradients cannot be recorded into a captured graph: capture the call "
                            "without gradients (z=...) and linear_backward or "
                            "gated_linear_backward")
@@ -316,13 +334,16 @@ def linear(x, w, bias=None, act="none", residual=None, out=None, z=None, stream=
     autograd records the call.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return linear(x, w, bias, act, residual, out, z)
-    if _wants_grad(x, w, bias, residual):
+    if _wants_grad(x, w, bias, residual, out):
         if out is not None or z is not None:
             raise ValueError("out and z cannot be given where gradients are recorded")
         return _Linear.apply(x, w, bias, residual, act)
-    return _forward(x, w, None, bias, residual, act, out, z)[0]
+    y = _forward(x, w, None, bias, residual, act, out, z)[0]
+    if out is not None or z is not None:
+        _written(out, z)
+    return y
 
 
 def gated_linear(x, w_gate, w_up, act="silu", out=None, z=None, stream=None):
@@ -334,15 +355,18 @@ def gated_linear(x, w_gate, w_up, act="silu", out=None, z=None, stream=None):
     ``linear``.
     """
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return gated_linear(x, w_gate, w_up, act, out, z)
     if w_up is None:
         raise TypeError("w_up must be a torch.Tensor")
-    if _wants_grad(x, w_gate, w_up):
+    if _wants_grad(x, w_gate, w_up, out):
         if out is not None or z is not None:
             raise ValueError("out and z cannot be given where gradients are recorded")
         return _GatedLinear.apply(x, w_gate, w_up, act)
-    return _forward(x, w_gate, w_up, None, None, act, out, z)[0]
+    h = _forward(x, w_gate, w_up, None, None, act, out, z)[0]
+    if out is not None or z is not None:
+        _written(out, z)
+    return h
 
 
 def linear_backward(dy, x, w, z=None, act="none", need_dx=True, need_dw=True, need_dbias=False,
@@ -351,7 +375,7 @@ def linear_backward(dy, x, w, z=None, act="none", need_dx=True, need_dw=True, ne
     of the residual is dy itself); None for each not asked for.  ``z`` is what
     ``linear`` kept, needed unless act is "none".  dw has w's layout."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return linear_backward(dy, x, w, z, act, need_dx, need_dw, need_dbias)
     dx, dw, _, db = _backward(dy, x, w, None, z, act, need_dx, need_dw, need_dbias)
     return dx, dw, db
@@ -362,7 +386,7 @@ def gated_linear_backward(dh, x, w_gate, w_up, z, act="silu", need_dx=True, need
     """(dx, dw_gate, dw_up) of ``gated_linear`` for dh, the gradient of its
     result; ``z`` is what it kept.  None for what is not asked for."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return gated_linear_backward(dh, x, w_gate, w_up, z, act, need_dx, need_dw)
     if w_up is None:
         raise TypeError("w_up must be a torch.Tensor")
