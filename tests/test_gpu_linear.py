@@ -650,6 +650,24 @@ def test_expanded_and_transposed_output_gradients():
         assert all(torch.equal(a, f) for a, f in zip(got, full))
 
 
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+def test_saved_tensors_of_other_strides(layout):
+    # hooks that hand back what was saved, contiguous: strides of the forward pass
+    # no longer hold
+    x, ws, b, r, dy = make(40, 48, 72, torch.bfloat16, layout, gated=True, pad=8)
+    leaves = [t.detach().requires_grad_() for t in (x, *ws, b)]
+
+    def grads():
+        y = tra.linear(leaves[0], leaves[1], leaves[3], "silu")
+        h = tra.gated_linear(*leaves[:3])
+        return torch.autograd.grad((y, h), leaves, (dy, dy))
+
+    want = grads()
+    with torch.autograd.graph.save_on_cpu():
+        got = grads()
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
 def test_one_row_of_any_stride():
     # a row whose own stride is shorter than it, as the transpose of a column has
     x, ws, b, _, _ = make(1, 48, 40, torch.float32, "kn", gated=True)

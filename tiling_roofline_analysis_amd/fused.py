@@ -181,7 +181,7 @@ def _forward(x, w, w2, bias, residual, act, out, z):
               0 if residual is None else residual.data_ptr(), ldr, out.data_ptr(), ldy,
               0 if z is None else z.data_ptr(), ldz)
     _call("tra_linear", _ARGS, fields, x.device)
-    return out, z, (ldx, trans, ldw, ldz, code)
+    return out, z
 
 
 def _backward(dy, x, w, w2, z, act, need_dx, need_dw, need_bias):
@@ -206,12 +206,7 @@ def _backward(dy, x, w, w2, z, act, need_dx, need_dw, need_bias):
             raise ValueError(f"z must be {M} x {width}")
     else:
         z = None
-    return _grads(dy, lddy, x, ldx, w, w2, trans, ldw, z, ldz, code, need_dx, need_dw, need_bias)
-
-
-def _grads(dy, lddy, x, ldx, w, w2, trans, ldw, z, ldz, code, need_dx, need_dw, need_bias):
-    M, K = x.shape
-    N = w.shape[1]
+    K = x.shape[1]
     dx = dw = dw2 = db = None
     pdx = pdw = pdw2 = pdb = 0
     if need_dx:
@@ -236,21 +231,18 @@ def _grads(dy, lddy, x, ldx, w, w2, trans, ldw, z, ldz, code, need_dx, need_dw, 
 
 
 def _rows(dy):
-    """dy as the library takes it (autograd may pass an expanded or transposed
-    one), and its leading dimension."""
-    cols = dy.shape[1]
+    """dy as the library takes it: autograd may pass an expanded or transposed one."""
     s0, s1 = dy.stride()
-    if s1 == 1 and s0 >= cols > 0:
-        return dy, s0
-    return dy.contiguous(), cols     # (one row may keep any stride)
+    return dy if s1 == 1 and s0 >= dy.shape[1] else dy.contiguous()
 
 
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, residual, act):
         need = any(ctx.needs_input_grad[:3])
-        y, z, ctx.layout = _forward(x, w, None, bias, residual, act, None,
-                                    _KEEP if need and act != "none" else None)
+        y, z = _forward(x, w, None, bias, residual, act, None,
+                        _KEEP if need and act != "none" else None)
+        ctx.act = act
         ctx.save_for_backward(x, w, z)
         return y
 
@@ -261,18 +253,17 @@ class _Linear(torch.autograd.Function):
         need_x, need_w, need_b, need_r, _ = ctx.needs_input_grad
         if not (need_x or need_w or need_b):
             return None, None, None, dy, None
+        # (saved-tensor hooks may have changed the strides: all is checked again)
         x, w, z = ctx.saved_tensors
-        ldx, trans, ldw, ldz, code = ctx.layout
-        rows, ld = _rows(dy)
-        dx, dw, _, db = _grads(rows, ld, x, ldx, w, None, trans, ldw, z, ldz, code,
-                               need_x, need_w, need_b)
+        dx, dw, _, db = _backward(_rows(dy), x, w, None, z, ctx.act, need_x, need_w, need_b)
         return dx, dw, db, dy if need_r else None, None
 
 
 class _GatedLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, act):
-        h, z, ctx.layout = _forward(x, w_gate, w_up, None, None, act, None, _KEEP)
+        h, z = _forward(x, w_gate, w_up, None, None, act, None, _KEEP)
+        ctx.act = act
         ctx.save_for_backward(x, w_gate, w_up, z)
         return h
 
@@ -281,11 +272,9 @@ class _GatedLinear(torch.autograd.Function):
     def backward(ctx, dh):
         _no_capture()
         x, w_gate, w_up, z = ctx.saved_tensors
-        ldx, trans, ldw, ldz, code = ctx.layout
         need_x, need_g, need_u, _ = ctx.needs_input_grad
-        rows, ld = _rows(dh)
-        dx, dg, du, _ = _grads(rows, ld, x, ldx, w_gate, w_up, trans, ldw, z, ldz,
-                               code, need_x, need_g or need_u, False)
+        dx, dg, du, _ = _backward(_rows(dh), x, w_gate, w_up, z, ctx.act, need_x,
+                                  need_g or need_u, False)
         return dx, dg if need_g else None, du if need_u else None, None
 
 
