@@ -259,8 +259,8 @@ TRA_API tra_status tra_gemm_describe(int variant, int64_t M, int64_t N, int64_t 
  * the same bits every time.
  *
  * Z (binary32, M rows of ldz) may be set to keep what the backward pass
- * needs: X W + bias, or, gated, [X W | X W2], 2 N wide.  It is binary32 so that the gradients carry no rounding
- * from it.
+ * needs: X W + bias, or, gated, [X W | X W2], 2 N wide.  It is binary32 so that
+ * the gradients carry no rounding from it.
  *
  * tra_linear_backward takes dY = the gradient of Y and writes the gradients
  * that are asked for (non-NULL):

@@ -129,6 +129,9 @@ def test_sizes_past_the_limits_are_unsupported():
     assert tra.load().tra_linear(fwd(M=1 << 29, N=1 << 29, ldw=1 << 29, ldy=1 << 29, W=1 << 58,
                                      Y=1 << 61), None) == UNSUPPORTED
     assert tra.load().tra_linear_backward(bwd(K=big, ldx=big, lddx=big), None) == UNSUPPORTED
+    # rows that a weight gradient sums over, within a tile of 32 bits
+    rows = (1 << 31) - 8
+    assert tra.load().tra_linear_backward(bwd(M=rows, dX=0), None) == UNSUPPORTED
     wide = 1 << 28
     assert tra.load().tra_linear_backward(
         bwd(N=wide, K=1, lddy=wide, ldz=wide, ldw=wide, lddw=wide, ldx=1, lddx=1, dbias=DB),

@@ -1,8 +1,9 @@
 // linear.hip -- the C-ABI entry points of the fused linear operators (declared
 // in include/tra_gemm.h): argument checks, choice of kernels, launches on the
 // caller's stream; and the small kernels around the products, which join a
-// split's partial sums and take the gradient of the epilogue.  Errors come back as status codes; nothing throws across
-// the ABI and nothing is allocated: scratch is the caller's workspace.
+// split's partial sums and take the gradient of the epilogue.  Errors come back
+// as status codes; nothing throws across the ABI and nothing is allocated: scratch
+// is the caller's workspace.
 #include "tra_gemm.h"
 
 #include <algorithm>
@@ -171,7 +172,9 @@ using tra::TileArgs;
 using tra::TileForm;
 using tra::TilePlan;
 
-constexpr int64_t kMaxSize = INT32_MAX;     // M, N, K: tile counts are 32-bit
+// M, N, K: indices along an axis, rounded up to whole tiles and doubled for a gated
+// result, fit 32 bits.
+constexpr int64_t kMaxSize = int64_t{1} << 30;
 constexpr size_t kAlign = 256;              // of the workspace's parts
 
 size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
@@ -439,7 +442,7 @@ tra_status check_forward(const tra_linear_args *p) {
     if (!gated && a.W2 != nullptr) return TRA_ERR_INVALID_ARG;
     if (a.M == 0 || a.N == 0) return TRA_OK;
     if (gated && a.W2 == nullptr && a.K > 0) return TRA_ERR_INVALID_ARG;
-    if (a.M > kMaxSize || a.N > kMaxSize / 2 || a.K > kMaxSize / 2) return TRA_ERR_UNSUPPORTED;
+    if (a.M > kMaxSize || a.N > kMaxSize || a.K > kMaxSize) return TRA_ERR_UNSUPPORTED;
     const int64_t b = elem_bytes(a.dtype);
     const View X{a.X, a.M, a.K, a.ldx, b};
     const View W = weight(a.W, a.w_trans, a.N, a.K, a.ldw, b);
@@ -523,7 +526,7 @@ GradPlan plan_backward(const tra_linear_grad_args &a) {
     const int64_t width = gated ? 2 * a.N : a.N;
     g.slope = gated || a.act != TRA_ACT_NONE;
     g.lddz = (width + 7) / 8 * 8;
-    g.dz_bytes = g.slope ? align_up(static_cast<size_t>(a.M * g.lddz * b)) : 0;
+    g.dz_bytes = g.slope ? align_up(static_cast<size_t>(a.M) * static_cast<size_t>(g.lddz * b)) : 0;
     plan_slope(a, g);
     g.colsum_bytes =
         a.dbias != nullptr ? align_up(static_cast<size_t>(g.chunks * a.N) * sizeof(float)) : 0;
@@ -558,7 +561,7 @@ tra_status check_backward(const tra_linear_grad_args *p) {
     if (gated ? a.dbias != nullptr || (a.dW == nullptr) != (a.dW2 == nullptr)
               : a.W2 != nullptr || a.dW2 != nullptr)
         return TRA_ERR_INVALID_ARG;
-    if (a.M > kMaxSize || a.N > kMaxSize / 2 || a.K > kMaxSize / 2) return TRA_ERR_UNSUPPORTED;
+    if (a.M > kMaxSize || a.N > kMaxSize || a.K > kMaxSize) return TRA_ERR_UNSUPPORTED;
     // linear_colsum_join: 16 lanes a column
     if (a.dbias != nullptr && a.N * 16 > tra::kMaxGridLanes - 256) return TRA_ERR_UNSUPPORTED;
     const int64_t b = elem_bytes(a.dtype);
