@@ -406,6 +406,33 @@ def test_rows_past_32_bit_offsets(dtype):
     del big, x, y
 
 
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("shape", [(70, 96, 130), (33, 2, 3)], ids=str)
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_rows_of_megabytes(dtype, shape, layout):
+    # rows so far apart that a tile's offsets pass 31 bits
+    dt = DTYPES[dtype]
+    M, N, K = shape
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    big = torch.empty(256, (1 << 21) + 1, device="cuda", dtype=dt)
+
+    def far(rows, cols, at):
+        t = big[:rows, at:at + cols]
+        t.copy_(ints((rows, cols), -3, 3, gen, dt))
+        return t
+
+    x, dy = far(M, K, 0), far(M, N, 1000)
+    ws = [far(K, N, 2000 + 500 * i) if layout == "kn" else far(N, K, 2000 + 500 * i).t()
+          for i in range(2)]
+    p, q = [x.double() @ w.double() for w in ws]
+    assert torch.equal(tra.linear(x, ws[0]), p.to(dt))
+    assert torch.equal(tra.gated_linear(x, *ws, act="relu"),
+                       (p.clamp(min=0).float() * q.float()).to(dt))
+    dx, dw, _ = tra.linear_backward(dy, x, ws[0])
+    assert torch.equal(dx, (dy.double() @ ws[0].double().t()).to(dt))
+    assert torch.equal(dw, (x.double().t() @ dy.double()).to(dt))
+
+
 def test_long_k():
     # long enough that no summation order keeps 16-bit products exact: the bound
     for dtype in DTYPES:

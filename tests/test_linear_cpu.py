@@ -210,7 +210,7 @@ def plan(M, N, K, dtype, layout, gated=0, pad=0):
     # ... not in binary32, nor unaligned
     ((4096, 4096, 4096, 0, "kn"), dict(tile="128x128", loads="direct")),
     ((4096, 4096, 4096, 1, "kn", 0, 1), dict(tile="128x128", loads="registers")),
-    ((4096, 4096, 4096, 0, "nk", 0, 1), dict(loads="registers")),
+    ((4096, 4096, 4096, 0, "nk", 0, 1), dict(tile="64x128", loads="direct")),
     # a tile a CU
     ((1024, 1024, 1024, 0, "kn"), dict(tile="64x64", splits="1")),
     ((333, 8192, 2048, 1, "nk"), dict(tile="128x128", splits="1")),

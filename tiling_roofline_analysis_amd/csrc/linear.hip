@@ -232,11 +232,17 @@ View weight(const void *p, int w_trans, int64_t N, int64_t K, int64_t ld, int64_
     return w_trans ? View{p, N, K, ld, bytes} : View{p, K, N, ld, bytes};
 }
 
-// Whether an operand can go straight into LDS: every line starts 16-byte
-// aligned and is whole chunks long, and a tile's byte offsets (256 lines) stay
-// below 2^31.
-bool direct_ok(const void *p, int64_t ld, int64_t line, int64_t bytes) {
-    return rows16(p, ld, bytes) && line * bytes % 16 == 0 && ld * bytes < (int64_t{1} << 22);
+// Bytes a lane with which an operand can go straight into LDS: 16 where every line
+// starts 16-byte aligned and is whole chunks long, 4 for any other binary32, 0 if a
+// tile's byte offsets (256 lines) may pass 2^31, and for 16 bits of any alignment.
+int direct_bytes(const void *p, int64_t ld, int64_t line, int64_t bytes) {
+    if (ld * bytes >= (int64_t{1} << 22)) return 0;
+    return rows16(p, ld, bytes) && line * bytes % 16 == 0 ? 16 : bytes == 4 ? 4 : 0;
+}
+
+// The same for `line` elements that start `offset` elements into lines that allow `d`.
+int at_offset(int d, int64_t offset, int64_t bytes) {
+    return d < 16 || offset * bytes % 16 == 0 ? d : bytes == 4 ? 4 : 0;
 }
 
 // How a kernel of one tile size goes, in microseconds, as measured on MI355X with
@@ -253,10 +259,11 @@ constexpr int64_t kCUs = 256;
 constexpr double kBytesPerUs = 4.8e6;     // memory, as a large copy reaches
 constexpr double kBytesPerUsWg = 2.2e4;   // what one workgroup's loads in flight can ask for
 
-// direct loads, 16-bit and binary32; through registers, the same.  The 256 x 256
-// kernel is built for direct 16-bit loads only; 128 x 128 through registers in
-// binary32 needs more VGPRs than there are.
-constexpr TileClass kClasses[2][2][4] = {
+// [loads][16-bit, binary32]: direct, 16 bytes a lane; through registers; direct, 4
+// bytes a lane.  The 256 x 256 kernel is built for direct 16-bit loads only; 128 x 128
+// in binary32 with other than 16-byte loads needs more VGPRs than there are.
+// Through registers binary32 goes only with rows of 4 MB or more, in one tile size.
+constexpr TileClass kClasses[3][2][4] = {
     {{{256, 256, 1, 1.28, 1.42, 5.7},
       {128, 128, 2, 0.50, 0.47, 5.2},
       {64, 128, 2, 0.30, 0.27, 4.5},
@@ -269,8 +276,10 @@ constexpr TileClass kClasses[2][2][4] = {
       {64, 128, 3, 0.85, 0.455, 4.5},
       {64, 64, 4, 0.70, 0.32, 4.0},
       {0, 0, 0, 0.0, 0.0, 0.0}},
-     {{64, 128, 2, 1.22, 1.04, 4.5},
-      {64, 64, 4, 0.74, 0.545, 4.0},
+     {{64, 64, 4, 0.74, 0.545, 4.0}}},
+    {{},
+     {{64, 128, 2, 1.05, 0.96, 4.5},
+      {64, 64, 3, 0.58, 0.52, 4.0},
       {0, 0, 0, 0.0, 0.0, 0.0},
       {0, 0, 0, 0.0, 0.0, 0.0}}}};
 
@@ -285,7 +294,7 @@ constexpr TileClass kClasses[2][2][4] = {
 //   half of the memory's rate in 16 bits; unaligned 16-bit rows three quarters).
 // `kept`: binary32 values stored besides each result (the pre-activations).
 TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, int64_t K, int segs,
-                   int batch, bool direct, bool kept) {
+                   int batch, int direct, bool kept) {
     const int64_t b = elem_bytes(dtype), slice = 128 / b;
     const bool f32 = dtype == TRA_DTYPE_F32;
     const int64_t k_tiles = std::max<int64_t>(1, segs * ceil_div(K, slice));
@@ -293,7 +302,7 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
     const double in = static_cast<double>(batch) * segs * K * (static_cast<double>(M) + columns) * b;
     TilePlan best{};
     double best_us = 0.0;
-    for (const TileClass &c : kClasses[direct ? 0 : 1][f32 ? 1 : 0]) {
+    for (const TileClass &c : kClasses[direct == 16 ? 0 : direct == 4 ? 2 : 1][f32 ? 1 : 0]) {
         if (c.bm == 0) break;
         const int64_t tiles = std::max<int64_t>(
             1, ceil_div(M, c.bm) * ceil_div(N, gated ? c.bn / 2 : c.bn));     // of a batch
@@ -327,7 +336,7 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
                 best.bn = c.bn;
                 best.whole = static_cast<int>(splits > 1 ? whole : tiles);
                 best.splits = static_cast<int>(splits);
-                best.deep = direct && n <= kCUs;
+                best.deep = direct == 16 && n <= kCUs;
                 best.partial_bytes =
                     splits > 1 ? static_cast<size_t>(parts) * c.bm * c.bn * sizeof(float) : 0;
             }
@@ -347,7 +356,7 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
                                                  : (f32 ? 3.8e6 : 2.4e6);
         const double each = form == tra::kFormKK ? 2.6e4 : f32 ? 1.8e4 : 3.0e4;
         const double us = 2.8 + segs * static_cast<double>(K) * columns * b * (1.0 + M / 80.0) /
-                                    std::min(most, strips * each) / (direct || f32 ? 1.0 : 0.75);
+                                    std::min(most, strips * each) / (direct != 0 || f32 ? 1.0 : 0.75);
         if (us < best_us) {
             best = TilePlan{};
             best.few = true;
@@ -423,10 +432,11 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K) { return M >= 0 && N >= 0 && K >=
 
 TilePlan plan_forward(const tra_linear_args &a) {
     const int64_t b = elem_bytes(a.dtype);
-    const bool direct = direct_ok(a.X, a.ldx, a.K, b) &&
-                        direct_ok(a.W, a.ldw, a.w_trans ? a.K : a.N, b) &&
-                        aligned16(a.W2);
-    return plan_tile(a.w_trans ? tra::kFormKK : tra::kFormKN, a.gated != 0, a.dtype, a.M, a.N,
+    const bool gated = a.gated != 0;
+    const int direct = std::min({direct_bytes(a.X, a.ldx, a.K, b),
+                                 direct_bytes(a.W, a.ldw, a.w_trans ? a.K : a.N, b),
+                                 gated ? direct_bytes(a.W2, a.ldw, a.w_trans ? a.K : a.N, b) : 16});
+    return plan_tile(a.w_trans ? tra::kFormKK : tra::kFormKN, gated, a.dtype, a.M, a.N,
                      a.K, 1, 1, direct, a.Z != nullptr);
 }
 
@@ -533,16 +543,16 @@ GradPlan plan_backward(const tra_linear_grad_args &a) {
     // dZ as an operand: the workspace's copy is aligned
     const int64_t ldz = g.slope ? g.lddz : a.lddy;
     const void *dz = g.slope ? nullptr : a.dY;
+    const int dz_direct = at_offset(direct_bytes(dz, ldz, a.N, b), gated ? a.N : 0, b);
     if (a.dX != nullptr) {
-        const bool direct = direct_ok(dz, ldz, a.N, b) && (!gated || a.N * b % 16 == 0) &&
-                            direct_ok(a.W, a.ldw, a.w_trans ? a.K : a.N, b) &&
-                            (!gated || aligned16(a.W2));
+        const int64_t line = a.w_trans ? a.K : a.N;
+        const int direct = std::min({dz_direct, direct_bytes(a.W, a.ldw, line, b),
+                                     gated ? direct_bytes(a.W2, a.ldw, line, b) : 16});
         g.dx = plan_tile(a.w_trans ? tra::kFormKN : tra::kFormKK, false, a.dtype, a.M, a.K, a.N,
                          gated ? 2 : 1, 1, direct, false);
     }
     if (a.dW != nullptr) {
-        const bool direct = direct_ok(dz, ldz, a.N, b) && (!gated || a.N * b % 16 == 0) &&
-                            direct_ok(a.X, a.ldx, a.K, b);
+        const int direct = std::min(dz_direct, direct_bytes(a.X, a.ldx, a.K, b));
         g.dw = plan_tile(tra::kFormNN, false, a.dtype, a.w_trans ? a.N : a.K,
                          a.w_trans ? a.K : a.N, a.M, 1, gated ? 2 : 1, direct, false);
     }
@@ -730,7 +740,7 @@ tra_status tra_linear_describe(const tra_linear_args *args, char *buf, size_t le
     const TilePlan t = plan_forward(*args);
     std::snprintf(buf, len, "kernel=%s tile=%dx%d loads=%s whole=%d splits=%d workspace_bytes=%zu",
                   t.few ? "linear_few" : "linear_tile", t.bm, t.bn,
-                  t.few || !t.direct ? "registers" : "direct", t.whole, t.splits,
+                  t.few || t.direct == 0 ? "registers" : "direct", t.whole, t.splits,
                   t.partial_bytes);
     return TRA_OK;
 }

@@ -69,7 +69,7 @@ struct TilePlan {
     bool gated;
     bool few;              // the kernel for few rows; bn: columns per workgroup
     int bm, bn;            // tile of P (gated: bn / 2 columns of each of z, u)
-    bool direct;           // operands go straight into LDS (16-byte aligned)
+    int direct;            // bytes a lane of loads straight into LDS, or 0: through registers
     bool deep;             // direct: one workgroup a CU, with more stages
     int whole;             // tiles of a batch not split along K (all when splits is 1)
     int splits;

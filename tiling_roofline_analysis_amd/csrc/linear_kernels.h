@@ -140,38 +140,60 @@ struct Panel {
         return (wave + i * WAVES) * 1024;
     }
 
-    // -- direct loads (buffer_load_dwordx4 .. lds): rows and K tile are whole
-    // chunks, bytes outside read as zero because their offset lies past the
-    // buffer's length.
+    // -- direct loads (buffer_load .. lds), G bytes a lane: 16 where lines are
+    // whole, aligned chunks, else 4 (binary32).  What lies outside reads as zero,
+    // because its offset lies past the buffer's length.  Of G = 4, a block is a
+    // quarter of the 1 KB.
     static constexpr uint32_t OUTSIDE = 0x80000000u;
 
-    // Offset of this lane's chunk of block i from the panel's corner, or
-    // OUTSIDE where the panel's `rows` rows inside the matrix end before it.
+    template <int G>
+    static constexpr int DINS = INS * (16 / G);       // loads per wave
+
+    // Byte that this lane moves (first) in load i, and its line and first element
+    // in the line.
+    template <int G>
+    static __device__ __forceinline__ int direct_line(int wave, int i) {
+        return ((wave + i * WAVES) * 64 + static_cast<int>(threadIdx.x & 63)) * G / LINE;
+    }
+    template <int G>
+    static __device__ __forceinline__ int direct_elem(int wave, int i) {
+        constexpr int PER = LINE / G, SUB = 16 / G;
+        const int at = ((wave + i * WAVES) * 64 + static_cast<int>(threadIdx.x & 63)) % PER;
+        const int c = (at / SUB) ^ swizzle(direct_line<G>(wave, i));
+        return (c * SUB + at % SUB) * (G / static_cast<int>(sizeof(T)));
+    }
+
+    // Offset of this lane's piece in load i from the panel's corner, or OUTSIDE
+    // where the panel's `rows` rows inside the matrix end before it.
+    template <int G>
     static __device__ __forceinline__ uint32_t offset(int wave, int i, int64_t rows, int64_t ld) {
-        const int r = KC ? line(wave, i) : chunk(wave, i) * kChunk<T>;
-        const uint32_t at =
-            static_cast<uint32_t>(line(wave, i)) * static_cast<uint32_t>(ld * sizeof(T)) +
-            static_cast<uint32_t>(chunk(wave, i)) * 16u;
-        return r < rows ? at : OUTSIDE;
+        const int n = direct_line<G>(wave, i), e = direct_elem<G>(wave, i);
+        const uint32_t at = static_cast<uint32_t>(n) * static_cast<uint32_t>(ld * sizeof(T)) +
+                            static_cast<uint32_t>(e) * static_cast<uint32_t>(sizeof(T));
+        return (KC ? n : e) < rows ? at : OUTSIDE;
     }
 
     // Loads the panel at `base` (its corner, wave-uniform) into `lds`; lines are
     // `pitch` bytes apart.  `rem` slices of K are inside (none when rem <= 0:
-    // zeros, and no memory is read).  Always INS loads and no branch, so that the
-    // number of loads in flight is the same on every path: where it is not, the
+    // zeros, and no memory is read).  Always the same loads and no branch, so that
+    // the number of loads in flight is the same on every path: where it is not, the
     // compiler waits for all of them before a fragment read.
+    template <int G>
     static __device__ __forceinline__ void load_direct(int wave, const char *base, int pitch,
-                                                       const uint32_t (&off)[INS], int rem,
+                                                       const uint32_t (&off)[DINS<G>], int rem,
                                                        char *lds) {
         // not KC: slices past the last lie past the buffer's end
         const int length = KC || rem >= kSlice<T> ? 0x7fffffff : (rem > 0 ? rem : 0) * pitch;
         const __amdgpu_buffer_rsrc_t rsrc =
             __builtin_amdgcn_make_buffer_rsrc((void *)base, (short)0, length, 0x00020000);
 #pragma unroll
-        for (int i = 0; i < INS; ++i) {
-            const uint32_t at = KC && chunk(wave, i) * kChunk<T> >= rem ? OUTSIDE : off[i];
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, lds + lds_block(wave, i), 16, at, 0, 0,
-                                                     0);
+        for (int i = 0; i < DINS<G>; ++i) {
+            const uint32_t at = KC && direct_elem<G>(wave, i) >= rem ? OUTSIDE : off[i];
+            char *to = lds + (wave + i * WAVES) * 64 * G;
+            if constexpr (G == 16)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to, 16, at, 0, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to, 4, at, 0, 0, 0);
         }
     }
 
@@ -478,7 +500,6 @@ struct TileShape {
     using PA = Panel<T, AKC, BM, WAVES>;
     using PB = Panel<T, BKC, BN / 2, WAVES>;
     static constexpr int STAGE = PA::BYTES + 2 * PB::BYTES;
-    static constexpr int LOADS = PA::INS + 2 * PB::INS;
     static constexpr int MINE = BM / 2 * HC * 8;     // a wave's sums in the epilogue
     // Workgroups a CU by LDS: two, where the stages leave room.
     static constexpr int per_cu(int stages) { return stages * STAGE <= 80 * 1024 ? 2 : 1; }
@@ -596,13 +617,14 @@ __device__ __forceinline__ bool for_each(std::integer_sequence<int, U...>, F f) 
     return (f(std::integral_constant<int, U>{}) && ...);
 }
 
-template <typename T, bool AKC, bool BKC, int BM, int BN, int S, bool DIRECT, bool GATED>
+template <typename T, bool AKC, bool BKC, int BM, int BN, int S, int DIRECT, bool GATED>
 __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) void linear_tile(const TileArgs p) {
     using X = TileShape<T, AKC, BKC, BM, BN>;
     using PA = typename X::PA;
     using PB = typename X::PB;
     constexpr int TI = X::TI, TJ = X::TJ, HC = X::HC;
-    static_assert(DIRECT || S == 2, "register staging keeps two stages");
+    static_assert(DIRECT == 16 || (DIRECT == 4 && sizeof(T) == 4) || (DIRECT == 0 && S == 2),
+                  "bytes of a direct load; register staging keeps two stages");
     static_assert(S >= 2 && S <= 6 && X::STAGE >= 2 * X::MINE, "LDS");
     // One array per stage, so that the compiler can tell a fragment read from
     // the direct loads in flight into the other stages.
@@ -659,14 +681,16 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
     constexpr std::integral_constant<int, 0> step0;
     constexpr std::integral_constant<int, 1> step1;
 
-    if constexpr (DIRECT) {
-        uint32_t oa[PA::INS], ob0[PB::INS], ob1[PB::INS];
+    if constexpr (DIRECT != 0) {
+        constexpr int IA = PA::template DINS<DIRECT>, IB = PB::template DINS<DIRECT>;
+        constexpr int LOADS = IA + 2 * IB;
+        uint32_t oa[IA], ob0[IB], ob1[IB];
 #pragma unroll
-        for (int i = 0; i < PA::INS; ++i) oa[i] = PA::offset(wave, i, rows_a, p.lda);
+        for (int i = 0; i < IA; ++i) oa[i] = PA::template offset<DIRECT>(wave, i, rows_a, p.lda);
 #pragma unroll
-        for (int i = 0; i < PB::INS; ++i) {
-            ob0[i] = PB::offset(wave, i, rows_b0, p.ldb);
-            ob1[i] = PB::offset(wave, i, rows_b1, p.ldb);
+        for (int i = 0; i < IB; ++i) {
+            ob0[i] = PB::template offset<DIRECT>(wave, i, rows_b0, p.ldb);
+            ob1[i] = PB::template offset<DIRECT>(wave, i, rows_b1, p.ldb);
         }
         const int pitch_a = static_cast<int>(p.lda * static_cast<int64_t>(sizeof(T)));
         const int pitch_b = static_cast<int>(p.ldb * static_cast<int64_t>(sizeof(T)));
@@ -674,9 +698,10 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
         // the count of loads in flight.  The waits count loads in tile order: none
         // may be moved past another's.
         auto issue = [&](char *st) __attribute__((always_inline)) {
-            PA::load_direct(wave, walk.a, pitch_a, oa, walk.rem, st);
-            PB::load_direct(wave, walk.b0, pitch_b, ob0, walk.rem, st + PA::BYTES);
-            PB::load_direct(wave, walk.b1, pitch_b, ob1, walk.rem, st + PA::BYTES + PB::BYTES);
+            PA::template load_direct<DIRECT>(wave, walk.a, pitch_a, oa, walk.rem, st);
+            PB::template load_direct<DIRECT>(wave, walk.b0, pitch_b, ob0, walk.rem, st + PA::BYTES);
+            PB::template load_direct<DIRECT>(wave, walk.b1, pitch_b, ob1, walk.rem,
+                                             st + PA::BYTES + PB::BYTES);
             walk.next();
         };
         for_each(std::make_integer_sequence<int, S>{}, [&](auto u) __attribute__((always_inline)) {
@@ -684,18 +709,18 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
             __builtin_amdgcn_sched_barrier(0);
             return true;
         });
-        stage_sync<(S - 1) * X::LOADS>();
+        stage_sync<(S - 1) * LOADS>();
         read(step0, st0);
         auto iteration = [&](auto u) __attribute__((always_inline)) {
             constexpr int U = decltype(u)::value;
             read(step1, stage(u));
             mma_step<T, 0>(x[0], w[0], c);
             interleave<MFMAS, READS, 0>();
-            stage_sync<(S - 2) * X::LOADS>();
+            stage_sync<(S - 2) * LOADS>();
             issue(stage(u));
             read(step0, stage(std::integral_constant<int, U + 1>{}));
             mma_step<T, 1>(x[1], w[1], c);
-            interleave<MFMAS, READS, X::LOADS>();
+            interleave<MFMAS, READS, LOADS>();
             __builtin_amdgcn_sched_barrier(0);
         };
         // Whole rounds of the ring, then what is left: a way out of the middle of
@@ -1008,10 +1033,10 @@ __global__ __launch_bounds__(512, 2) void linear_wide(const TileArgs p) {
     uint32_t oa0[L], oa1[L], ob0[L], ob1[L];
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-        oa0[i] = PA::offset(wave, i, p.M - m0, p.lda);
-        oa1[i] = PA::offset(wave, i, p.M - m0 - 128, p.lda);
-        ob0[i] = PB::offset(wave, i, p.N - n0, p.ldb);
-        ob1[i] = PB::offset(wave, i, p.N - n1, p.ldb);
+        oa0[i] = PA::template offset<16>(wave, i, p.M - m0, p.lda);
+        oa1[i] = PA::template offset<16>(wave, i, p.M - m0 - 128, p.lda);
+        ob0[i] = PB::template offset<16>(wave, i, p.N - n0, p.ldb);
+        ob1[i] = PB::template offset<16>(wave, i, p.N - n1, p.ldb);
     }
     const int pitch_a = static_cast<int>(p.lda * static_cast<int64_t>(sizeof(T)));
     const int pitch_b = static_cast<int>(p.ldb * static_cast<int64_t>(sizeof(T)));
@@ -1020,19 +1045,19 @@ __global__ __launch_bounds__(512, 2) void linear_wide(const TileArgs p) {
     const char *late = nullptr;
     int late_rem = 0;
     auto load_a0 = [&](char *st) __attribute__((always_inline)) {
-        PA::load_direct(wave, walk.a, pitch_a, oa0, walk.rem, st);
+        PA::template load_direct<16>(wave, walk.a, pitch_a, oa0, walk.rem, st);
     };
     auto load_b0 = [&](char *st) __attribute__((always_inline)) {
-        PB::load_direct(wave, walk.b0, pitch_b, ob0, walk.rem, st);
+        PB::template load_direct<16>(wave, walk.b0, pitch_b, ob0, walk.rem, st);
     };
     auto load_b1 = [&](char *st) __attribute__((always_inline)) {
-        PB::load_direct(wave, walk.b1, pitch_b, ob1, walk.rem, st);
+        PB::template load_direct<16>(wave, walk.b1, pitch_b, ob1, walk.rem, st);
         late = walk.a + lower;
         late_rem = walk.rem;
         walk.next();
     };
     auto load_a1 = [&](char *st) __attribute__((always_inline)) {
-        PA::load_direct(wave, late, pitch_a, oa1, late_rem, st);
+        PA::template load_direct<16>(wave, late, pitch_a, oa1, late_rem, st);
     };
 
     f32x4 c[2][2][4][2] = {};      // [A panel][B panel]
@@ -1148,33 +1173,31 @@ hipError_t launch_tile(const TilePlan &plan, const TileArgs &a, hipStream_t stre
             return hipGetLastError();
         }
     }
-    // Direct loads: two workgroups a CU, or, where the grid gives a CU no more
-    // than one, stages enough that a second does not fit (the dispatcher would put
-    // two on one CU and leave another idle).
-    // Binary32 through registers has no 128 x 128 tile: it needs more than 256 VGPRs.
-    if (plan.bm == 128) {
-        if (!plan.direct) {
-            if constexpr (sizeof(T) == 4) return hipErrorInvalidValue;
-            else linear_tile<T, AKC, BKC, 128, 128, 2, false, GATED><<<grid, 256, 0, stream>>>(a);
-        } else if (plan.deep)
-            linear_tile<T, AKC, BKC, 128, 128, 4, true, GATED><<<grid, 256, 0, stream>>>(a);
+    // Direct loads of 16 bytes: two workgroups a CU, or, where the grid gives a CU no
+    // more than one, stages enough that a second does not fit (the dispatcher would
+    // put two on one CU and leave another idle).
+#define TRA_TILE(BM, BN, S, DIRECT) \
+    linear_tile<T, AKC, BKC, BM, BN, S, DIRECT, GATED><<<grid, 256, 0, stream>>>(a)
+    constexpr bool F32 = sizeof(T) == 4;
+    const int size = plan.bm == 128 ? 2 : plan.bn == 128 ? 1 : 0;
+    if (plan.direct == 16) {
+        if (size == 2) plan.deep ? TRA_TILE(128, 128, 4, 16) : TRA_TILE(128, 128, 2, 16);
+        if (size == 1) plan.deep ? TRA_TILE(64, 128, 6, 16) : TRA_TILE(64, 128, 3, 16);
+        if (size == 0) plan.deep ? TRA_TILE(64, 64, 6, 16) : TRA_TILE(64, 64, 3, 16);
+    } else if constexpr (F32) {
+        if (size == 2 || (size == 1 && plan.direct == 0)) return hipErrorInvalidValue;
+        if (plan.direct == 0)
+            TRA_TILE(64, 64, 2, 0);
+        else if (size == 1)
+            TRA_TILE(64, 128, 3, 4);
         else
-            linear_tile<T, AKC, BKC, 128, 128, 2, true, GATED><<<grid, 256, 0, stream>>>(a);
-    } else if (plan.bn == 128) {
-        if (!plan.direct)
-            linear_tile<T, AKC, BKC, 64, 128, 2, false, GATED><<<grid, 256, 0, stream>>>(a);
-        else if (plan.deep)
-            linear_tile<T, AKC, BKC, 64, 128, 6, true, GATED><<<grid, 256, 0, stream>>>(a);
-        else
-            linear_tile<T, AKC, BKC, 64, 128, 3, true, GATED><<<grid, 256, 0, stream>>>(a);
+            TRA_TILE(64, 64, 3, 4);
     } else {
-        if (!plan.direct)
-            linear_tile<T, AKC, BKC, 64, 64, 2, false, GATED><<<grid, 256, 0, stream>>>(a);
-        else if (plan.deep)
-            linear_tile<T, AKC, BKC, 64, 64, 6, true, GATED><<<grid, 256, 0, stream>>>(a);
-        else
-            linear_tile<T, AKC, BKC, 64, 64, 3, true, GATED><<<grid, 256, 0, stream>>>(a);
+        if (size == 2) TRA_TILE(128, 128, 2, 0);
+        if (size == 1) TRA_TILE(64, 128, 2, 0);
+        if (size == 0) TRA_TILE(64, 64, 2, 0);
     }
+#undef TRA_TILE
     return hipGetLastError();
 }
 
