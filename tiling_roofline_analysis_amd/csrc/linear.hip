@@ -257,7 +257,7 @@ struct TileClass {
 
 constexpr int64_t kCUs = 256;
 constexpr double kBytesPerUs = 4.8e6;     // memory, as a large copy reaches
-constexpr double kBytesPerUsWg = 3.0e4;   // what one workgroup's loads in flight can ask for
+constexpr double kBytesPerUsWg = 2.6e4;   // what one workgroup's loads in flight can ask for
 
 // [loads][16-bit, binary32]: direct, 16 bytes a lane; through registers; direct, 4
 // bytes a lane.  The 256 x 256 kernel is built for direct 16-bit loads only; 128 x 128
