@@ -254,3 +254,14 @@ def test_binding_refuses_cpu_tensors_and_bad_arguments():
 def test_unknown_names_still_raise():
     with pytest.raises(AttributeError):
         tra.no_such_operator
+
+
+@pytest.mark.parametrize("bad", [
+    dict(X=Y), dict(W=Y), dict(bias=Y), dict(w_trans=1, W=Y), dict(M=1, X=Y), dict(M=1, bias=Y),
+], ids=str)
+def test_only_the_residual_may_be_the_result(bad):
+    # the residual in place, and another operand at the same address with it
+    a = dict(N=32, ldw=32, ldy=32, R=Y, ldr=32)
+    assert size(fwd(**a))[0] == OK
+    assert size(fwd(**{**a, **bad}))[0] == INVALID
+    assert tra.load().tra_linear(fwd(**{**a, **bad}), None) == INVALID

@@ -465,9 +465,12 @@ tra_status check_forward(const tra_linear_args *p) {
     for (const View &v : in)
         if (!v.valid()) return TRA_ERR_INVALID_ARG;
     if (!Y.valid() || !Z.valid() || share(Y, Z)) return TRA_ERR_INVALID_ARG;
-    for (const View &v : in)
-        if (share(v, Z) || (share(v, Y) && !(v.p == R.p && R.rows > 0 && same(R, Y))))
-            return TRA_ERR_INVALID_ARG;
+    // R in place: the lane that reads an element of R writes it, and no other.  That
+    // holds for R only, not for another operand that starts where R does.
+    for (const View &v : in) {
+        const bool in_place = &v == &in[4] && same(R, Y);
+        if (share(v, Z) || (share(v, Y) && !in_place)) return TRA_ERR_INVALID_ARG;
+    }
     return TRA_OK;
 }
 
