@@ -273,7 +273,10 @@ TRA_API tra_status tra_gemm_describe(int variant, int64_t M, int64_t N, int64_t 
  *
  * Weight gradients are stored like the weights (K x N, or N x K), both with
  * leading dimension lddw.  dZ is rounded to the element type, since the
- * matrix units take it so; dbias sums it unrounded.  Operands that a call
+ * matrix units take it so; dbias sums it unrounded.  That adds a rounding of
+ * half a step to each term of dX and dW.  In binary16 dZ is held times a power of
+ * two chosen from its largest finite value, so that none of it overflows, and what
+ * a term loses below binary16's range is at most 2^-25 of that value.  Operands that a call
  * does not need (Z with act NONE, X without dW, W without dX) may be NULL.
  *
  * Scratch: the caller's workspace, 256-byte aligned, at least the bytes that

@@ -55,20 +55,33 @@ __global__ __launch_bounds__(256) void linear_join(const TileArgs p, int bm, int
     });
 }
 
-// 64 chunks of columns by rows_per_chunk rows per workgroup; its four waves
-// take every fourth row and add their column sums in wave order.  Memory bounds
-// it: gated 4096 x 8192 bf16 moves 470 MB in 110 us, 4.3 TB/s.
+// Binary16 holds 40 binades, and dZ = dY u act' can lie outside them where the
+// gradients, its products with X and W, do not.  So it is stored times 2^12, which
+// fits where its largest finite |dZ| lies in [2^-12, 16); where that lies
+// elsewhere, times the power of two that takes it into [2^14, 2^15).  A rounding of
+// dZ is then off by half a step or by 2^-25 of the largest |dZ|, whatever dZ's size.
+constexpr float kUsualScale = 4096.0f;
+
+__device__ __forceinline__ float dz_scale(float largest) {
+    if (largest == 0.0f || (largest >= 1.0f / kUsualScale && largest * kUsualScale <= 65504.0f))
+        return kUsualScale;
+    // (of a subnormal: the least exponent; the scale and its inverse stay normal)
+    const int e = static_cast<int>(__float_as_uint(largest) >> 23) - 127;
+    return ldexpf(1.0f, 14 - e < 126 ? 14 - e : 126);
+}
+
+// dZ, times `scale`, of 64 chunks of columns (block `bx` of them) and
+// rows_per_chunk rows (block `by`), of which this wave takes every fourth; their
+// column sums and largest finite |dZ|, unscaled.
 template <typename T, bool GATED>
-__global__ __launch_bounds__(256) void linear_slope(const SlopeArgs p) {
+__device__ __forceinline__ void slope_block(const SlopeArgs &p, int bx, int by, float scale,
+                                            float (&sum)[kChunk<T>], float &largest) {
     constexpr int V = kChunk<T>;
-    __shared__ __align__(16) float part[4][64 * V];
-    lds_poison(&part[0][0], 4 * 64 * V);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n = (static_cast<int64_t>(blockIdx.x) * 64 + lane) * V;
-    const int64_t first = static_cast<int64_t>(blockIdx.y) * p.rows_per_chunk;
+    const int64_t n = (static_cast<int64_t>(bx) * 64 + lane) * V;
+    const int64_t first = static_cast<int64_t>(by) * p.rows_per_chunk;
     const int64_t end = first + p.rows_per_chunk < p.M ? first + p.rows_per_chunk : p.M;
     const int64_t valid = p.N - n;
-    float sum[V] = {};
     if (valid > 0) {
         with_act(p.act, [&](auto act) __attribute__((always_inline)) {
             constexpr int ACT = decltype(act)::value;
@@ -87,14 +100,52 @@ __global__ __launch_bounds__(256) void linear_slope(const SlopeArgs p) {
                     dz[e] = GATED ? dy[e] * u[e] * d : dy[e] * d;
                     if constexpr (GATED) u[e] = dy[e] * y;
                     sum[e] += dz[e];
+                    if constexpr (kScaled<T>) {
+                        const float a = fabsf(dz[e]), b = GATED ? fabsf(u[e]) : 0.0f;
+                        if (a < INFINITY) largest = fmaxf(largest, a);
+                        if (GATED && b < INFINITY) largest = fmaxf(largest, b);
+                        dz[e] *= scale;
+                        if constexpr (GATED) u[e] *= scale;
+                    }
                 }
                 if (GATED || p.dZ != nullptr) store_part<T, V>(out, valid, dz);
                 if constexpr (GATED) store_part<T, V>(out + p.N, valid, u);
             }
         });
     }
+}
+
+// The largest of every lane's value in the workgroup of four waves.
+__device__ __forceinline__ float largest_of(float v, float (&part)[4]) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+}
+
+// 64 chunks of columns by rows_per_chunk rows per workgroup; its four waves
+// take every fourth row and add their column sums in wave order.  Memory bounds
+// it: gated 4096 x 8192 bf16 moves 470 MB in 110 us, 4.3 TB/s.
+template <typename T, bool GATED>
+__global__ __launch_bounds__(256) void linear_slope(const SlopeArgs p) {
+    constexpr int V = kChunk<T>;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float sum[V] = {}, largest = 0.0f;
+    slope_block<T, GATED>(p, blockIdx.x, blockIdx.y, kUsualScale, sum, largest);
+    if constexpr (kScaled<T>) {
+        if (p.largest != nullptr) {
+            __shared__ float most[4];
+            lds_poison(most, 4);
+            largest = largest_of(largest, most);
+            if (threadIdx.x == 0)
+                p.largest[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = largest;
+        }
+    }
     if constexpr (!GATED) {
         if (p.colsum == nullptr) return;
+        __shared__ __align__(16) float part[4][64 * V];
+        lds_poison(&part[0][0], 4 * 64 * V);
 #pragma unroll
         for (int e = 0; e < V; ++e) part[wave][lane * V + e] = sum[e];
         __syncthreads();
@@ -104,6 +155,25 @@ __global__ __launch_bounds__(256) void linear_slope(const SlopeArgs p) {
                 p.colsum[static_cast<int64_t>(blockIdx.y) * p.N + col] =
                     ((part[0][i] + part[1][i]) + part[2][i]) + part[3][i];
         }
+    }
+}
+
+// Behind linear_slope, whose grid was blocks_x x blocks_y: notes what undoes dZ's
+// scale, and where the usual one does not fit writes dZ again.
+template <typename T, bool GATED>
+__global__ __launch_bounds__(256) void linear_rescale(const SlopeArgs p, int blocks_x,
+                                                      int64_t blocks) {
+    __shared__ float most[4];
+    lds_poison(most, 4);
+    float largest = 0.0f;
+    for (int64_t i = threadIdx.x; i < blocks; i += 256) largest = fmaxf(largest, p.largest[i]);
+    const float scale = dz_scale(largest_of(largest, most));
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.undo = 1.0f / scale;
+    if (scale == kUsualScale) return;
+    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+        float sum[kChunk<T>] = {};
+        slope_block<T, GATED>(p, static_cast<int>(b % blocks_x), static_cast<int>(b / blocks_x),
+                              scale, sum, largest);
     }
 }
 
@@ -151,6 +221,19 @@ hipError_t launch_slope(bool gated, const SlopeArgs &a, hipStream_t stream) {
         linear_slope<T, true><<<grid, 256, 0, stream>>>(a);
     else
         linear_slope<T, false><<<grid, 256, 0, stream>>>(a);
+    if constexpr (kScaled<T>) {
+        if (a.largest != nullptr) {
+            const hipError_t err = hipGetLastError();
+            if (err != hipSuccess) return err;
+            const int64_t blocks = static_cast<int64_t>(grid.x) * grid.y;
+            const dim3 again(static_cast<unsigned>(std::min<int64_t>(blocks, 1024)));
+            const int blocks_x = static_cast<int>(grid.x);
+            if (gated)
+                linear_rescale<T, true><<<again, 256, 0, stream>>>(a, blocks_x, blocks);
+            else
+                linear_rescale<T, false><<<again, 256, 0, stream>>>(a, blocks_x, blocks);
+        }
+    }
     return hipGetLastError();
 }
 
@@ -511,6 +594,7 @@ tra_status forward(const tra_linear_args *p, void *stream) {
 // The parts of a backward call and where they live in its workspace.
 struct GradPlan {
     bool slope;             // dZ differs from dY: an elementwise pass writes it
+    size_t scale_bytes;     // binary16: what undoes dZ's scale, then the largest |dZ| by workgroup
     int64_t lddz;           // elements
     size_t dz_bytes;
     int64_t chunks;         // row chunks of the column sums
@@ -543,6 +627,9 @@ GradPlan plan_backward(const tra_linear_grad_args &a) {
     plan_slope(a, g);
     g.colsum_bytes =
         a.dbias != nullptr ? align_up(static_cast<size_t>(g.chunks * a.N) * sizeof(float)) : 0;
+    if (g.slope && a.dtype == TRA_DTYPE_F16)
+        g.scale_bytes = align_up(
+            static_cast<size_t>(1 + ceil_div(a.N, 64 * (16 / b)) * g.chunks) * sizeof(float));
     // dZ as an operand: the workspace's copy is aligned
     const int64_t ldz = g.slope ? g.lddz : a.lddy;
     const void *dz = g.slope ? nullptr : a.dY;
@@ -560,7 +647,7 @@ GradPlan plan_backward(const tra_linear_grad_args &a) {
                          a.w_trans ? a.K : a.N, a.M, 1, gated ? 2 : 1, direct, false);
     }
     g.product_bytes = align_up(std::max(g.dx.partial_bytes, g.dw.partial_bytes));
-    g.total = g.dz_bytes + g.colsum_bytes + g.product_bytes;
+    g.total = g.dz_bytes + g.scale_bytes + g.colsum_bytes + g.product_bytes;
     return g;
 }
 
@@ -637,8 +724,10 @@ tra_status backward(const tra_linear_grad_args *p, void *stream_) {
     if (!workspace_ok(a.workspace, a.workspace_bytes, g.total)) return TRA_ERR_INVALID_ARG;
     char *ws = static_cast<char *>(a.workspace);
     void *dz_ws = ws;
-    float *colsum = reinterpret_cast<float *>(ws + g.dz_bytes);
-    float *partial = reinterpret_cast<float *>(ws + g.dz_bytes + g.colsum_bytes);
+    float *scale = reinterpret_cast<float *>(ws + g.dz_bytes);
+    float *colsum = reinterpret_cast<float *>(ws + g.dz_bytes + g.scale_bytes);
+    float *partial =
+        reinterpret_cast<float *>(ws + g.dz_bytes + g.scale_bytes + g.colsum_bytes);
     const void *dz = g.slope ? dz_ws : a.dY;
     const int64_t lddz = g.slope ? g.lddz : a.lddy;
 
@@ -646,6 +735,10 @@ tra_status backward(const tra_linear_grad_args *p, void *stream_) {
     const bool want_dx = a.dX != nullptr && a.M > 0 && a.K > 0;
     const bool want_dw = a.dW != nullptr && a.N > 0 && a.K > 0;
     TileArgs tx{}, tw{};
+    const bool need_dz = g.slope && ((want_dx && a.N > 0) || (want_dw && a.M > 0));
+    // (an empty sum needs nothing undone, and no pass notes it)
+    const bool scaled = need_dz && a.M > 0 && a.N > 0 && g.scale_bytes > 0;
+    tx.epi.undo = tw.epi.undo = scaled ? scale : nullptr;
     if (want_dx) {
         tx.A = dz;
         tx.lda = lddz;
@@ -684,7 +777,6 @@ tra_status backward(const tra_linear_grad_args *p, void *stream_) {
     }
 
     hipError_t err = hipSuccess;
-    const bool need_dz = g.slope && ((want_dx && a.N > 0) || (want_dw && a.M > 0));
     if (a.M > 0 && a.N > 0 && (need_dz || a.dbias != nullptr)) {
         tra::SlopeArgs s{};
         s.dY = a.dY;
@@ -694,6 +786,8 @@ tra_status backward(const tra_linear_grad_args *p, void *stream_) {
         s.dZ = need_dz ? dz_ws : nullptr;
         s.lddz = lddz;
         s.colsum = a.dbias != nullptr ? colsum : nullptr;
+        s.undo = scaled ? scale : nullptr;
+        s.largest = scaled ? scale + 1 : nullptr;
         s.M = a.M;
         s.N = a.N;
         s.rows_per_chunk = g.rows_per_chunk;

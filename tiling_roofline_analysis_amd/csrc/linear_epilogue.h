@@ -16,6 +16,10 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <typename T>
 constexpr int kChunk = 16 / sizeof(T);     // elements of a 16-byte chunk
 
+// dZ is stored times a power of two, which the epilogue of its products undoes.
+template <typename T>
+constexpr bool kScaled = std::is_same_v<T, _Float16>;
+
 // ---- activations -------------------------------------------------------------
 //
 // In binary32, with the formulas of the definitions:
@@ -170,6 +174,11 @@ template <typename T, bool GATED, int ACT, int V>
 __device__ __forceinline__ void finish(const EpiArgs &e, int batch, int64_t m, int64_t n,
                                        float (&z)[V], float (&u)[V]) {
     const int64_t valid = e.N - n;
+    if constexpr (kScaled<T> && !GATED) {
+        const float undo = e.undo != nullptr ? *e.undo : 1.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] *= undo;
+    }
     if (!GATED && e.bias != nullptr) {
         float b[V];
         load_part<T, V>(static_cast<const T *>(e.bias) + n, valid, b);

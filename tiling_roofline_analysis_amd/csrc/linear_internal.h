@@ -25,6 +25,7 @@ struct EpiArgs {
     int64_t ldy;
     float *Z;              // kept pre-activations: z at column n, u at column N + n; or null
     int64_t ldz;
+    const float *undo;     // binary16 gradients: what their sums are multiplied by, or null
     int64_t M, N;
     int act;
 };
@@ -90,6 +91,9 @@ struct SlopeArgs {
     void *dZ;              // null: only the column sums are wanted
     int64_t lddz;
     float *colsum;         // [row chunk][N], or null
+    // Binary16 with dZ: the largest finite |dZ| of each workgroup, and what the
+    // products' sums are multiplied by to undo dZ's scale.
+    float *largest, *undo;
     int64_t M, N;
     int rows_per_chunk;
     int act;

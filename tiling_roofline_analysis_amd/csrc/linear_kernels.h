@@ -423,6 +423,10 @@ __device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, float *su
         }
         return;
     }
+    float undo = 1.0f;
+    if constexpr (kScaled<T> && !GATED) {
+        if (e.undo != nullptr) undo = *e.undo;
+    }
     float b[V] = {};
     if (!GATED && e.bias != nullptr) load_row<T, V>(static_cast<const T *>(e.bias) + n, b);
     T *y = static_cast<T *>(batch == 0 ? e.Y[0] : e.Y[1]) + (m0 + first) * e.ldy + n;
@@ -445,7 +449,7 @@ __device__ __forceinline__ void epi_rows(const TileArgs &p, int batch, float *su
 #pragma unroll
             for (int k = 0; k < U; ++k)
 #pragma unroll
-                for (int i = 0; i < V; ++i) z[k][i] += b[i];
+                for (int i = 0; i < V; ++i) z[k][i] = kScaled<T> ? z[k][i] * undo + b[i] : z[k][i] + b[i];
         }
         if (e.Z != nullptr) {
 #pragma unroll

@@ -15,7 +15,9 @@ itself is refused inside a capture).
 x is M x K, the weights K x N: row-major, or the transposed view of a row-major
 N x K tensor (``w.t()`` of a torch.nn.Linear weight).  float32, bfloat16 or
 float16, one type per call.  Every element is summed in float32 and rounded
-once.
+once; the gradients of x and of the weights are sums over dz, the gradient of
+the pre-activations, which is itself rounded to the type (in float16 under a
+scale of its own, so that its range does not limit them).
 """
 from __future__ import annotations
 
