@@ -5,8 +5,15 @@
 
 Like ``matmul`` these check the tensors, pass their device pointers and torch's
 current stream to the library, and raise TraError on a non-OK status; scratch
-comes from torch's allocator, so calls may be captured into a graph.  With
-gradients enabled and an input that requires one they are differentiable
+comes from torch's allocator, so calls may be captured into a graph.
+
+``stream`` is a torch.cuda.Stream, or None for torch's current stream.  A call
+runs behind what is on that stream already, as under ``torch.cuda.stream``: it
+waits for no other stream, so the caller orders it behind whatever still writes its
+inputs elsewhere, and orders whatever reads its results behind it.  Memory needs no
+care: tensors may be dropped, and reused by the allocator, once the call returns.
+
+With gradients enabled and an input that requires one they are differentiable
 (once): the backward pass runs in the library too.  ``linear_backward`` and
 ``gated_linear_backward`` are those passes by themselves, for callers that
 keep their own order of work (a pipeline, a captured training step: autograd
@@ -290,11 +297,28 @@ def _wants_grad(*tensors) -> bool:
     return False
 
 
-def _on(stream, x):
-    """The context of a caller's stream, which is one of x's device."""
-    if isinstance(x, torch.Tensor) and x.is_cuda and stream.device != x.device:
-        raise ValueError(f"stream is on {stream.device}, x on {x.device}")
-    return torch.cuda.stream(stream)
+def _on(stream, call, *tensors):
+    """call() on a caller's stream, which is one of the tensors' device.
+
+    The allocator is told that ``stream`` uses the tensors given, and that the
+    caller's current stream uses the results, which are allocated on ``stream``:
+    either may be dropped once the call has returned.
+    """
+    device = next((t.device for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda),
+                  stream.device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        result = call()
+    if current != stream:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        for t in result if isinstance(result, tuple) else (result,):
+            if t is not None:
+                t.record_stream(current)
+    return result
 
 
 def _written(*tensors):
@@ -320,13 +344,14 @@ def linear(x, w, bias=None, act="none", residual=None, out=None, z=None, stream=
     ``bias`` (N elements) and ``residual`` (M x N; ``out`` may be the same
     tensor) are optional.  ``act``: none, relu, gelu, gelu_tanh, silu or
     sigmoid.  ``z``, if given, is a float32 M x N tensor that receives
-    x w + bias for ``linear_backward``.  ``stream`` is a torch.cuda.Stream or
-    None for torch's current stream.  ``out`` and ``z`` are refused where
-    autograd records the call.
+    x w + bias for ``linear_backward``.  ``stream``, None for the current
+    one, is not made to wait for others: inputs written elsewhere have to be done,
+    or waited for by it.  ``out`` and ``z`` are refused where autograd records the
+    call.
     """
     if stream is not None:
-        with _on(stream, x):
-            return linear(x, w, bias, act, residual, out, z)
+        return _on(stream, lambda: linear(x, w, bias, act, residual, out, z), x, w, bias,
+                   residual, out, z)
     if _wants_grad(x, w, bias, residual, out):
         if out is not None or z is not None:
             raise ValueError("out and z cannot be given where gradients are recorded")
@@ -342,12 +367,12 @@ def gated_linear(x, w_gate, w_up, act="silu", out=None, z=None, stream=None):
 
     The weights have the same shape and strides (two tensors, or the halves of
     a packed one).  ``z``, if given, is a float32 M x 2N tensor that receives
-    [x w_gate | x w_up] for ``gated_linear_backward``.  Other arguments as in
-    ``linear``.
+    [x w_gate | x w_up] for ``gated_linear_backward``.  Other arguments, and
+    what is asked of the caller of ``stream``, as in ``linear``.
     """
     if stream is not None:
-        with _on(stream, x):
-            return gated_linear(x, w_gate, w_up, act, out, z)
+        return _on(stream, lambda: gated_linear(x, w_gate, w_up, act, out, z), x, w_gate, w_up,
+                   out, z)
     if w_up is None:
         raise TypeError("w_up must be a torch.Tensor")
     if _wants_grad(x, w_gate, w_up, out):
@@ -364,10 +389,11 @@ def linear_backward(dy, x, w, z=None, act="none", need_dx=True, need_dw=True, ne
                     stream=None):
     """(dx, dw, dbias) of ``linear`` for dy, the gradient of its result (that
     of the residual is dy itself); None for each not asked for.  ``z`` is what
-    ``linear`` kept, needed unless act is "none".  dw has w's layout."""
+    ``linear`` kept, needed unless act is "none".  dw has w's layout.  ``stream``
+    as in ``linear``."""
     if stream is not None:
-        with _on(stream, x):
-            return linear_backward(dy, x, w, z, act, need_dx, need_dw, need_dbias)
+        return _on(stream, lambda: linear_backward(dy, x, w, z, act, need_dx, need_dw, need_dbias),
+                   dy, x, w, z)
     dx, dw, _, db = _backward(dy, x, w, None, z, act, need_dx, need_dw, need_dbias)
     return dx, dw, db
 
@@ -375,10 +401,11 @@ def linear_backward(dy, x, w, z=None, act="none", need_dx=True, need_dw=True, ne
 def gated_linear_backward(dh, x, w_gate, w_up, z, act="silu", need_dx=True, need_dw=True,
                           stream=None):
     """(dx, dw_gate, dw_up) of ``gated_linear`` for dh, the gradient of its
-    result; ``z`` is what it kept.  None for what is not asked for."""
+    result; ``z`` is what it kept.  None for what is not asked for.  ``stream`` as in
+    ``linear``."""
     if stream is not None:
-        with _on(stream, x):
-            return gated_linear_backward(dh, x, w_gate, w_up, z, act, need_dx, need_dw)
+        return _on(stream, lambda: gated_linear_backward(dh, x, w_gate, w_up, z, act, need_dx,
+                                                         need_dw), dh, x, w_gate, w_up, z)
     if w_up is None:
         raise TypeError("w_up must be a torch.Tensor")
     dx, dg, du, _ = _backward(dh, x, w_gate, w_up, z, act, need_dx, need_dw, False)
