@@ -265,3 +265,33 @@ def test_only_the_residual_may_be_the_result(bad):
     assert size(fwd(**a))[0] == OK
     assert size(fwd(**{**a, **bad}))[0] == INVALID
     assert tra.load().tra_linear(fwd(**{**a, **bad}), None) == INVALID
+
+
+CALLS = {"linear": lambda t: tra.linear(t, torch.ones(3, 4)),
+         "gated_linear": lambda t: tra.gated_linear(torch.ones(2, 3), t, torch.ones(3, 4)),
+         "linear_backward": lambda t: tra.linear_backward(t, torch.ones(2, 3), torch.ones(3, 4)),
+         "gated_linear_backward": lambda t: tra.gated_linear_backward(
+             torch.ones(2, 4), torch.ones(2, 3), t, torch.ones(3, 4), torch.ones(2, 8))}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_forward_mode_derivatives_are_refused(name):
+    # (before anything else is looked at, so also for tensors on the CPU)
+    from torch.autograd import forward_ad
+    call = CALLS[name]
+    with forward_ad.dual_level():
+        t = torch.ones(2, 3)
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            call(forward_ad.make_dual(t, t))
+        with torch.no_grad(), pytest.raises(NotImplementedError, match="forward-mode"):
+            call(forward_ad.make_dual(t, t))
+        with pytest.raises(TypeError):
+            call(t)                      # no tangent: the other checks answer
+    with pytest.raises(TypeError):
+        call(t)
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_tracing_is_refused(name):
+    with pytest.raises(RuntimeError, match="jit.trace"):
+        torch.jit.trace(CALLS[name], torch.ones(2, 3))

@@ -17,7 +17,8 @@ With gradients enabled and an input that requires one they are differentiable
 (once): the backward pass runs in the library too.  ``linear_backward`` and
 ``gated_linear_backward`` are those passes by themselves, for callers that
 keep their own order of work (a pipeline, a captured training step: autograd
-itself is refused inside a capture).
+itself is refused inside a capture).  Forward-mode derivatives and torch.jit.trace
+are refused.
 
 x is M x K, the weights K x N: row-major, or the transposed view of a row-major
 N x K tensor (``w.t()`` of a torch.nn.Linear weight).  float32, bfloat16 or
@@ -32,6 +33,7 @@ import ctypes
 import struct
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import TRA_ERR_INVALID_ARG, TRA_OK, TraError, _row_major_ld, load
@@ -297,6 +299,22 @@ def _wants_grad(*tensors) -> bool:
     return False
 
 
+_tracing = torch._C._get_tracing_state
+
+
+def _recorded_elsewhere(*tensors):
+    """Refuses what would lose the call without a word: forward-mode derivatives,
+    which the operators do not have, and torch.jit.trace, which records torch's own
+    operations only."""
+    if forward_ad._current_level >= 0 and torch._C._is_fwd_grad_enabled():
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("the fused linear operators have no forward-mode "
+                                          "derivatives")
+    if _tracing() is not None:
+        raise RuntimeError("torch.jit.trace cannot record the fused linear operators")
+
+
 def _on(stream, call, *tensors):
     """call() on a caller's stream, which is one of the tensors' device.
 
@@ -349,6 +367,7 @@ def linear(x, w, bias=None, act="none", residual=None, out=None, z=None, stream=
     or waited for by it.  ``out`` and ``z`` are refused where autograd records the
     call.
     """
+    _recorded_elsewhere(x, w, bias, residual, out, z)
     if stream is not None:
         return _on(stream, lambda: linear(x, w, bias, act, residual, out, z), x, w, bias,
                    residual, out, z)
@@ -370,6 +389,7 @@ def gated_linear(x, w_gate, w_up, act="silu", out=None, z=None, stream=None):
     [x w_gate | x w_up] for ``gated_linear_backward``.  Other arguments, and
     what is asked of the caller of ``stream``, as in ``linear``.
     """
+    _recorded_elsewhere(x, w_gate, w_up, out, z)
     if stream is not None:
         return _on(stream, lambda: gated_linear(x, w_gate, w_up, act, out, z), x, w_gate, w_up,
                    out, z)
@@ -391,6 +411,7 @@ def linear_backward(dy, x, w, z=None, act="none", need_dx=True, need_dw=True, ne
     of the residual is dy itself); None for each not asked for.  ``z`` is what
     ``linear`` kept, needed unless act is "none".  dw has w's layout.  ``stream``
     as in ``linear``."""
+    _recorded_elsewhere(dy, x, w, z)
     if stream is not None:
         return _on(stream, lambda: linear_backward(dy, x, w, z, act, need_dx, need_dw, need_dbias),
                    dy, x, w, z)
@@ -403,6 +424,7 @@ def gated_linear_backward(dh, x, w_gate, w_up, z, act="silu", need_dx=True, need
     """(dx, dw_gate, dw_up) of ``gated_linear`` for dh, the gradient of its
     result; ``z`` is what it kept.  None for what is not asked for.  ``stream`` as in
     ``linear``."""
+    _recorded_elsewhere(dh, x, w_gate, w_up, z)
     if stream is not None:
         return _on(stream, lambda: gated_linear_backward(dh, x, w_gate, w_up, z, act, need_dx,
                                                          need_dw), dh, x, w_gate, w_up, z)
