@@ -295,3 +295,15 @@ def test_forward_mode_derivatives_are_refused(name):
 def test_tracing_is_refused(name):
     with pytest.raises(RuntimeError, match="jit.trace"):
         torch.jit.trace(CALLS[name], torch.ones(2, 3))
+
+
+def test_a_kept_tensor_that_requires_a_gradient_is_refused():
+    # overwriting it would leave autograd with the gradient of what it was
+    x, w = torch.ones(2, 3), torch.ones(3, 4)
+    z = torch.empty(2, 8, requires_grad=True)
+    with pytest.raises(ValueError, match="out and z"):
+        tra.linear(x, w, z=z[:, :4])
+    with pytest.raises(ValueError, match="out and z"):
+        tra.gated_linear(x, w, w, z=z)
+    with torch.no_grad(), pytest.raises(TypeError):
+        tra.linear(x, w, z=z[:, :4])         # nothing is recorded: the other checks answer

@@ -371,7 +371,7 @@ def linear(x, w, bias=None, act="none", residual=None, out=None, z=None, stream=
     if stream is not None:
         return _on(stream, lambda: linear(x, w, bias, act, residual, out, z), x, w, bias,
                    residual, out, z)
-    if _wants_grad(x, w, bias, residual, out):
+    if _wants_grad(x, w, bias, residual, out, z):
         if out is not None or z is not None:
             raise ValueError("out and z cannot be given where gradients are recorded")
         return _Linear.apply(x, w, bias, residual, act)
@@ -395,7 +395,7 @@ def gated_linear(x, w_gate, w_up, act="silu", out=None, z=None, stream=None):
                    out, z)
     if w_up is None:
         raise TypeError("w_up must be a torch.Tensor")
-    if _wants_grad(x, w_gate, w_up, out):
+    if _wants_grad(x, w_gate, w_up, out, z):
         if out is not None or z is not None:
             raise ValueError("out and z cannot be given where gradients are recorded")
         return _GatedLinear.apply(x, w_gate, w_up, act)
