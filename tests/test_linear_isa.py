@@ -64,3 +64,28 @@ def test_m0_is_set(kernels):
     _, found = kernels
     for name, body in direct(found).items():
         assert any(re.match(r"s_\w+ m0,", x) for x in body), name
+
+
+@pytest.fixture(scope="module", params=["linear_bf16.hip", "linear_f32.hip"])
+def ir(request, tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("ir") / "k.ll")
+    cmd = [build.hipcc(), *build.FLAGS, "--cuda-device-only", "-emit-llvm", "-S",
+           os.path.join(build.CSRC, request.param), "-o", out]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    with open(out) as fh:
+        text = fh.read()
+    return {m.group(1): m.group(2) for m in
+            re.finditer(r"^define [^\n]*amdgpu_kernel void @(\w+)\(.*?\{\n(.*?)^\}", text,
+                        re.M | re.S)}
+
+
+def test_lanes_meet_between_the_sums_writes_and_reads(ir):
+    # the epilogue's lanes read what other lanes of the wave wrote to LDS: a fence of
+    # the wave stands between, and in the 256 x 256 kernel, which does so twice, also
+    # before the next write
+    kernels = {n: b for n, b in ir.items() if "linear_tile" in n or "linear_wide" in n}
+    assert len(kernels) >= 40
+    for name, body in kernels.items():
+        fences = len(re.findall(r'fence syncscope\("wavefront"\) acq_rel', body))
+        assert fences >= (3 if "linear_wide" in name else 1), name

@@ -50,6 +50,14 @@ __device__ __forceinline__ void stage_sync() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Between LDS accesses of one wave's lanes to what its other lanes wrote or have read.
+// A wave's LDS instructions run in order, so it needs no wait and is no instruction;
+// it keeps the compiler, which looks at one lane's addresses, from reordering them.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // ---- MFMA ----------------------------------------------------------------------
 
 // One chunk of K: c += w x^T on a 16 x 16 tile; lane l holds row l % 16, chunk
@@ -820,6 +828,7 @@ __global__ __launch_bounds__(256, (TileShape<T, AKC, BKC, BM, BN>::per_cu(S))) v
                 for (int j = 0; j < TJ; ++j) c[0][h][i][j] += c[a][h][i][j];
     epi_put<HC>(mine, c[0][0], 0);
     epi_put<HC>(mine, c[0][1], 1);
+    wave_sync();
     epi_rows<T, GATED, HC, BM / 2>(
         p, batch, part.sums == nullptr ? nullptr : part.sums + wm * (BM / 2) * BN + wn * HC, BN,
         mine, m0 + wm * (BM / 2), n0 + wn * HC, n1 + wn * HC);
@@ -1151,10 +1160,12 @@ __global__ __launch_bounds__(512, 2) void linear_wide(const TileArgs p) {
     for (int h = 0; h < 2; ++h) {
         epi_put<32>(mine, c[h][0], 0);
         epi_put<32>(mine, c[h][1], 1);
+        wave_sync();
         const int row = h * 128 + wm * 64;
         epi_rows<T, GATED, 32, 64>(
             p, batch, part.sums == nullptr ? nullptr : part.sums + row * 256 + wn * 32, 256, mine,
             m0 + row, n0 + wn * 32, n1 + wn * 32);
+        wave_sync();
     }
 }
 
