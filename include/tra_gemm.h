@@ -255,8 +255,10 @@ TRA_API tra_status tra_gemm_describe(int variant, int64_t M, int64_t N, int64_t 
  *
  * Numerics: products and sums, bias, activation, gate and residual are
  * binary32; each element is rounded to its type once, when it is stored.
- * The order of the sums depends on the sizes, never on timing: a call gives
- * the same bits every time.
+ * The order of the sums depends on the sizes, the type, the weights' layout and
+ * the alignment of the products' operands (addresses and leading dimensions
+ * modulo 16 bytes), never on timing or on which optional operands are given: a
+ * call gives the same bits every time, and Y's are the same with and without Z.
  *
  * Z (binary32, M rows of ldz) may be set to keep what the backward pass
  * needs: X W + bias, or, gated, [X W | X W2], 2 N wide.  It is binary32 so that

@@ -139,3 +139,25 @@ def test_captured_gradients_follow_the_scale():
         got = [t.clone() for t in out]
         want = tra.linear_backward(dy, x, w, z, "silu")[:2]
         assert all(torch.equal(a, b) for a, b in zip(got, want)), size
+
+
+# shapes whose fastest plan, with the stores of kept pre-activations counted, would
+# be another
+@pytest.mark.parametrize("case", [(193, 6280, 4264, "f32", "nk", 0), (1486, 272, 2256, "bf16", "kn", 0),
+                                  (554, 720, 5936, "bf16", "kn", 1), (78, 6080, 7040, "bf16", "nk", 0),
+                                  (9, 512, 1024, "f16", "nk", 1)], ids=str)
+def test_the_same_bits_with_and_without_gradients(case):
+    M, N, K, dtype, layout, gated = case
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": F16}[dtype]
+    x = normal(1, M, K).to(dt)
+    ws = [normal(2 + i, *((K, N) if layout == "kn" else (N, K)), scale=K ** -0.5).to(dt)
+          for i in range(1 + gated)]
+    ws = ws if layout == "kn" else [w.t() for w in ws]
+
+    def call(t, **kw):
+        return tra.gated_linear(*t, **kw) if gated else tra.linear(*t, act="silu", **kw)
+
+    want = call([x, *ws])
+    z = torch.empty(M, N * (1 + gated), device="cuda")
+    assert torch.equal(call([x, *ws], z=z), want)
+    assert torch.equal(call([t.detach().requires_grad_() for t in (x, *ws)]).detach(), want)

@@ -307,3 +307,25 @@ def test_a_kept_tensor_that_requires_a_gradient_is_refused():
         tra.gated_linear(x, w, w, z=z)
     with torch.no_grad(), pytest.raises(TypeError):
         tra.linear(x, w, z=z[:, :4])         # nothing is recorded: the other checks answer
+
+
+def test_plans_do_not_depend_on_what_is_kept():
+    # so that a result has the same bits with and without gradients
+    import math
+    import random
+    rng = random.Random(5)
+
+    def size(lo, hi):
+        return int(math.exp(rng.uniform(math.log(lo), math.log(hi))))
+
+    for _ in range(600):
+        M, N, K = size(1, 8192), size(64, 12288), size(64, 12288)
+        if rng.random() < 0.7:
+            N, K = -(-N // 8) * 8, -(-K // 8) * 8
+        nk, gated = rng.choice([0, 1]), rng.choice([0, 1])
+        a = dict(M=M, N=N, K=K, dtype=rng.choice([0, 1, 2]), w_trans=nk, gated=gated,
+                 W=1 << 50, W2=1 << 51 if gated else 0, ldx=K, ldw=K if nk else N, ldy=N)
+        want = describe(fwd(**a))
+        assert describe(fwd(**a, Z=1 << 60, ldz=N * (1 + gated))) == want, a
+        if not gated:
+            assert describe(fwd(**a, bias=1 << 52, R=1 << 53, ldr=N, act=4)) == want, a

@@ -375,9 +375,12 @@ constexpr TileClass kClasses[3][2][4] = {
 //   Few rows: the weights' bytes at the rate that their strips can ask for (one
 //   strip, of 512 lanes, about 25 GB/s; 64-byte pieces of rows K apart reach about
 //   half of the memory's rate in 16 bits; unaligned 16-bit rows three quarters).
-// `kept`: binary32 values stored besides each result (the pre-activations).
+// Kept pre-activations have no part in it, though their stores add to the time: a
+// forward pass that keeps them gives the same bits as one that does not (a
+// checkpoint's recomputation).  Of 3000 random forward calls 82 had another plan with
+// their stores counted.
 TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, int64_t K, int segs,
-                   int batch, int direct, bool kept) {
+                   int batch, int direct) {
     const int64_t b = elem_bytes(dtype), slice = 128 / b;
     const bool f32 = dtype == TRA_DTYPE_F32;
     const int64_t k_tiles = std::max<int64_t>(1, segs * ceil_div(K, slice));
@@ -392,7 +395,7 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
         // 64-byte lines (16-bit weights, 64 x 64 tiles, not k-contiguous)
         const double most = kBytesPerUs * (form == tra::kFormKN && !f32 && c.bn == 64 ? 0.7 : 1.0);
         const double area = std::min<double>(M, c.bm) * std::min<double>(columns, c.bn);
-        const double out = (kept ? 4.0 : 0.0) + (gated ? 0.5 : 1.0) * b;     // per column of z or u
+        const double out = (gated ? 0.5 : 1.0) * b;     // bytes stored per column of z or u
         // K loops of n workgroups of `per` K tiles; a little to begin another round
         auto loops = [&](int64_t n, int64_t per) {
             const int64_t wave = kCUs * c.resident;
@@ -520,7 +523,7 @@ TilePlan plan_forward(const tra_linear_args &a) {
                                  direct_bytes(a.W, a.ldw, a.w_trans ? a.K : a.N, b),
                                  gated ? direct_bytes(a.W2, a.ldw, a.w_trans ? a.K : a.N, b) : 16});
     return plan_tile(a.w_trans ? tra::kFormKK : tra::kFormKN, gated, a.dtype, a.M, a.N,
-                     a.K, 1, 1, direct, a.Z != nullptr);
+                     a.K, 1, 1, direct);
 }
 
 // Host-side checks; launches nothing.
@@ -639,12 +642,12 @@ GradPlan plan_backward(const tra_linear_grad_args &a) {
         const int direct = std::min({dz_direct, direct_bytes(a.W, a.ldw, line, b),
                                      gated ? direct_bytes(a.W2, a.ldw, line, b) : 16});
         g.dx = plan_tile(a.w_trans ? tra::kFormKN : tra::kFormKK, false, a.dtype, a.M, a.K, a.N,
-                         gated ? 2 : 1, 1, direct, false);
+                         gated ? 2 : 1, 1, direct);
     }
     if (a.dW != nullptr) {
         const int direct = std::min(dz_direct, direct_bytes(a.X, a.ldx, a.K, b));
         g.dw = plan_tile(tra::kFormNN, false, a.dtype, a.w_trans ? a.N : a.K,
-                         a.w_trans ? a.K : a.N, a.M, 1, gated ? 2 : 1, direct, false);
+                         a.w_trans ? a.K : a.N, a.M, 1, gated ? 2 : 1, direct);
     }
     g.product_bytes = align_up(std::max(g.dx.partial_bytes, g.dw.partial_bytes));
     g.total = g.dz_bytes + g.scale_bytes + g.colsum_bytes + g.product_bytes;
