@@ -340,7 +340,12 @@ struct TileClass {
 
 constexpr int64_t kCUs = 256;
 constexpr double kBytesPerUs = 4.8e6;     // memory, as a large copy reaches
-constexpr double kBytesPerUsWg = 2.6e4;   // what one workgroup's loads in flight can ask for
+// What one workgroup's loads in flight can ask for, as fitted: of 8300 random forward
+// products (M to 2048; N, K from 128 to 12288; weights from memory), the 900 whose plan
+// it changes between 22 and 32 GB/s took, against the best of those plans, 4.8% longer
+// in the geometric mean at 22, 3.8 at 24, 3.3 at 26, 3.3 at 28, 3.6 at 30 and 4.1 at 32;
+// 150 more with M to 64, 5.8, 4.7, 4.3, 3.7, 3.3 and 3.6.
+constexpr double kBytesPerUsWg = 2.8e4;
 
 // [loads][16-bit, binary32]: direct, 16 bytes a lane; through registers; direct, 4
 // bytes a lane.  The 256 x 256 kernel is built for direct 16-bit loads only; 128 x 128
