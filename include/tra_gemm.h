@@ -362,6 +362,10 @@ TRA_API tra_status tra_linear_backward_workspace_size(const tra_linear_grad_args
 /* Writes what a forward call would launch into buf as
  * "key=value ..." text; launches nothing. */
 TRA_API tra_status tra_linear_describe(const tra_linear_args *args, char *buf, size_t len);
+/* The same for a backward call's products: the keys of dX's begin with "dx_",
+ * those of dW's (one launch for dW and dW2) with "dw_". */
+TRA_API tra_status tra_linear_backward_describe(const tra_linear_grad_args *args, char *buf,
+                                                size_t len);
 
 /*
  * Measurement probes: the two roofs of the roofline model measured on the

@@ -332,8 +332,8 @@ def check_integers(shape, dtype, layout, lib, monkeypatch):
     assert torch.equal(du, (x.double().t() @ zu).to(dt))
 
 
-# products that the 256 x 256 kernel takes (16 bits): forward, dX and dW each,
-# with ragged rows and a K tile that ends early
+# large products with ragged rows and a K tile that ends early, some of which the 256 x
+# 256 kernel takes (test_gpu_linear_plans.py has every kernel, and checks that it has)
 WIDE = [(4090, 4104, 520), (4090, 520, 4104), (515, 4104, 4088)]
 
 

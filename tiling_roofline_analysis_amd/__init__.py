@@ -56,7 +56,7 @@ ABI_FUNCTIONS = ("gemm_f32", "gemm_f32_variant", "gemm_f32_variant_ws",
                  "tra_probe_copy_f32", "tra_probe_mfma_f32", "tra_probe_fma_f32",
                  "tra_probe_launch", "tra_linear", "tra_linear_workspace_size",
                  "tra_linear_backward", "tra_linear_backward_workspace_size",
-                 "tra_linear_describe")
+                 "tra_linear_describe", "tra_linear_backward_describe")
 
 # tra_probe
 PROBE_COPY = 0
@@ -152,8 +152,9 @@ def _open(path: str) -> ctypes.CDLL:
     for name in ("tra_linear_workspace_size", "tra_linear_backward_workspace_size"):
         getattr(lib, name).argtypes = [args, size]
         getattr(lib, name).restype = c_int
-    lib.tra_linear_describe.argtypes = [args, ctypes.c_char_p, ctypes.c_size_t]
-    lib.tra_linear_describe.restype = c_int
+    for name in ("tra_linear_describe", "tra_linear_backward_describe"):
+        getattr(lib, name).argtypes = [args, ctypes.c_char_p, ctypes.c_size_t]
+        getattr(lib, name).restype = c_int
     return lib
 
 

@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <cstdio>
+#include <cstring>
 
 #include "linear_epilogue.h"
 
@@ -570,7 +571,6 @@ tra_status forward(const tra_linear_args *p, void *stream) {
     if (st != TRA_OK || p->M == 0 || p->N == 0) return st;
     const tra_linear_args &a = *p;
     const bool gated = a.gated != 0;
-    const int64_t b = elem_bytes(a.dtype);
     const TilePlan plan = plan_forward(a);
     if (!workspace_ok(a.workspace, a.workspace_bytes, plan.partial_bytes))
         return TRA_ERR_INVALID_ARG;
@@ -726,7 +726,6 @@ tra_status backward(const tra_linear_grad_args *p, void *stream_) {
     if (st != TRA_OK) return st;
     const tra_linear_grad_args &a = *p;
     const bool gated = a.gated != 0;
-    const int64_t b = elem_bytes(a.dtype);
     const hipStream_t stream = static_cast<hipStream_t>(stream_);
     const GradPlan g = plan_backward(a);
     if (!workspace_ok(a.workspace, a.workspace_bytes, g.total)) return TRA_ERR_INVALID_ARG;
@@ -809,6 +808,19 @@ tra_status backward(const tra_linear_grad_args *p, void *stream_) {
     return status_of(err);
 }
 
+// Appends a plan to the text in buf.
+void describe_plan(const TilePlan &t, const char *prefix, char *buf, size_t len) {
+    const size_t used = std::strlen(buf);
+    const char *p = prefix;
+    std::snprintf(buf + used, len - used,
+                  "%s%skernel=%s %stile=%dx%d %sloads=%s %sload_bytes=%d %sstages=%d %swhole=%d "
+                  "%ssplits=%d",
+                  used > 0 ? " " : "", p,
+                  t.few ? "linear_few" : "linear_tile", p, t.bm, t.bn, p,
+                  t.few || t.direct == 0 ? "registers" : "direct", p, t.few ? 0 : t.direct, p,
+                  tra::plan_stages(t), p, t.whole, p, t.splits);
+}
+
 }  // namespace
 
 extern "C" {
@@ -838,15 +850,29 @@ tra_status tra_linear_describe(const tra_linear_args *args, char *buf, size_t le
     if (st != TRA_OK) return st;
     if (buf == nullptr) return len == 0 ? TRA_OK : TRA_ERR_INVALID_ARG;
     if (len == 0) return TRA_OK;
+    buf[0] = '\0';
     if (args->M == 0 || args->N == 0) {
         std::snprintf(buf, len, "kernel=none");
         return TRA_OK;
     }
     const TilePlan t = plan_forward(*args);
-    std::snprintf(buf, len, "kernel=%s tile=%dx%d loads=%s whole=%d splits=%d workspace_bytes=%zu",
-                  t.few ? "linear_few" : "linear_tile", t.bm, t.bn,
-                  t.few || t.direct == 0 ? "registers" : "direct", t.whole, t.splits,
-                  t.partial_bytes);
+    describe_plan(t, "", buf, len);
+    const size_t used = std::strlen(buf);
+    std::snprintf(buf + used, len - used, " workspace_bytes=%zu", t.partial_bytes);
+    return TRA_OK;
+}
+
+tra_status tra_linear_backward_describe(const tra_linear_grad_args *args, char *buf, size_t len) {
+    const tra_status st = check_backward(args);
+    if (st != TRA_OK) return st;
+    if (buf == nullptr) return len == 0 ? TRA_OK : TRA_ERR_INVALID_ARG;
+    if (len == 0) return TRA_OK;
+    const GradPlan g = plan_backward(*args);
+    buf[0] = '\0';
+    if (args->dX != nullptr && args->M > 0 && args->K > 0) describe_plan(g.dx, "dx_", buf, len);
+    if (args->dW != nullptr && args->N > 0 && args->K > 0) describe_plan(g.dw, "dw_", buf, len);
+    const size_t used = std::strlen(buf);
+    std::snprintf(buf + used, len - used, "%sworkspace_bytes=%zu", used > 0 ? " " : "", g.total);
     return TRA_OK;
 }
 

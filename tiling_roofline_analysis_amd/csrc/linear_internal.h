@@ -77,6 +77,15 @@ struct TilePlan {
     size_t partial_bytes;  // workspace of the split
 };
 
+// Stages of LDS that the tile kernel of a plan keeps (launch_tile): with direct loads of
+// 16 bytes two workgroups' worth, or, deep, one workgroup's.
+inline int plan_stages(const TilePlan &t) {
+    if (t.few) return 0;
+    if (t.bm == 256 || t.direct == 0) return 2;
+    if (t.direct == 4) return 3;
+    return t.bm == 128 ? (t.deep ? 4 : 2) : t.deep ? 6 : 3;
+}
+
 // Tile rows swept together by the tile kernels (grouped_tile32), by tile height.
 constexpr int kGroupTile = 8, kGroupWide = 4;
 
