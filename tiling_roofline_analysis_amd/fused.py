@@ -299,7 +299,7 @@ def _wants_grad(*tensors) -> bool:
     return False
 
 
-_tracing = torch._C._get_tracing_state
+_tracing = torch._C._is_tracing
 
 
 def _recorded_elsewhere(*tensors):
@@ -311,7 +311,7 @@ def _recorded_elsewhere(*tensors):
             if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
                 raise NotImplementedError("the fused linear operators have no forward-mode "
                                           "derivatives")
-    if _tracing() is not None:
+    if _tracing():
         raise RuntimeError("torch.jit.trace cannot record the fused linear operators")
 
 
