@@ -29,6 +29,28 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 template <typename T>
 constexpr int kSlice = 128 / sizeof(T);    // K tile: 8 chunks, two MFMA steps
 
+// A chunk's elements from `over` on, moved to its front, with zeros behind: over from 0
+// (as it is) to all of them.  In 32-bit steps only: as a shift of 128 bits it becomes
+// 64-bit shifts whose amount is in a VGPR, and where that is the last VGPR the kernel
+// has, gfx950 has taken v0 for it now and then (linear_few with 80 VGPRs shifted the
+// last chunk of K by its lane number, in one workgroup of some process's first calls).
+template <typename T>
+__device__ __forceinline__ u32x4 drop_elements(u32x4 v, int over) {
+    constexpr int PER = 4 / static_cast<int>(sizeof(T));     // elements of a dword
+    if constexpr (PER == 2) {
+        const uint32_t bits = over & 1 ? 16 : 0;
+        v = u32x4{__builtin_amdgcn_alignbit(v[1], v[0], bits),
+                  __builtin_amdgcn_alignbit(v[2], v[1], bits),
+                  __builtin_amdgcn_alignbit(v[3], v[2], bits),
+                  __builtin_amdgcn_alignbit(0, v[3], bits)};
+    }
+    const bool one = over & PER, two = over & (2 * PER), all = over & (4 * PER);
+    const uint32_t low = one ? v[1] : v[0], high = one ? v[3] : v[2];
+    const uint32_t mid = one ? v[2] : v[1], top = one ? 0u : v[3];
+    return u32x4{all ? 0u : two ? high : low, all ? 0u : two ? top : mid,
+                 all || two ? 0u : high, all || two ? 0u : top};
+}
+
 __device__ __forceinline__ int wave_id() {
     return __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
 }
@@ -256,13 +278,9 @@ struct Panel {
             for (int i = 0; i < INS; ++i) {
                 // elements by which the chunk was read too early
                 int64_t over = chunk(wave, i) * E + E - (KC ? rem : rows);
-                if (over < 0) over = 0;
-                if (!KC && line(wave, i) >= rem) over = E;
-                unsigned __int128 x;
-                __builtin_memcpy(&x, &reg[i], 16);
-                x = over < E ? x >> (static_cast<int>(over) * 8 * static_cast<int>(sizeof(T))) : 0;
-                u32x4 v;
-                __builtin_memcpy(&v, &x, 16);
+                over = over < 0 ? 0 : over < E ? over : E;
+                u32x4 v = drop_elements<T>(reg[i], static_cast<int>(over));
+                if (!KC && line(wave, i) >= rem) v = u32x4{};
                 put(wave, i, v, lds);
             }
         } else {
@@ -867,11 +885,7 @@ __device__ __forceinline__ u32x4 chunk_to_end(const T *line, int k, int K) {
     const int over = k + E - K;
     u32x4 v;
     __builtin_memcpy(&v, line + (over > 0 ? K - E : k), 16);
-    unsigned __int128 x;
-    __builtin_memcpy(&x, &v, 16);
-    x = over <= 0 ? x : over < E ? x >> (over * 8 * static_cast<int>(sizeof(T))) : 0;
-    __builtin_memcpy(&v, &x, 16);
-    return v;
+    return drop_elements<T>(v, over <= 0 ? 0 : over < E ? over : E);
 }
 
 template <typename T, bool BKC, bool GATED>
@@ -1001,8 +1015,8 @@ __global__ __launch_bounds__(512) void linear_few(const TileArgs p) {
 // The waves of the lower rows run half a phase behind those of the upper: there is
 // one of each on every SIMD, and while the one computes a quadrant the other
 // reads the fragments of its next.  (Two groups of four waves that take turns at
-// the matrix units, a barrier apart, each with a tile in four quadrants, is a publicly
-// described schedule for large products on this architecture, known as ping-pong; the
+// the matrix units, a barrier apart, with a tile in four quadrants, is a schedule that
+// AMD's published descriptions of large products on this architecture give; the
 // phases, panels and waits below are worked out here.)  A phase is
 //   read this quadrant's fragments and load one panel of a later tile; barrier;
 //   16 MFMAs; barrier.
