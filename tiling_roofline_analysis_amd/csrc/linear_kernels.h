@@ -1015,8 +1015,8 @@ __global__ __launch_bounds__(512) void linear_few(const TileArgs p) {
 // The waves of the lower rows run half a phase behind those of the upper: there is
 // one of each on every SIMD, and while the one computes a quadrant the other
 // reads the fragments of its next.  (Two groups of four waves that take turns at
-// the matrix units, a barrier apart, with a tile in four quadrants, is a schedule that
-// AMD's published descriptions of large products on this architecture give; the
+// the matrix units, a barrier apart, each with a tile in four quadrants, is a publicly
+// described schedule for large products on this architecture, known as ping-pong; the
 // phases, panels and waits below are worked out here.)  A phase is
 //   read this quadrant's fragments and load one panel of a later tile; barrier;
 //   16 MFMAs; barrier.
