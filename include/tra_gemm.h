@@ -368,6 +368,101 @@ TRA_API tra_status tra_linear_backward_describe(const tra_linear_grad_args *args
                                                 size_t len);
 
 /*
+ * Norms around a block, with its gate and the residual stream's scale:
+ *
+ *   R = scale X + gate * N_post(H)       (element by element; R = X without H)
+ *   Y = N(R)
+ *
+ *   N(v) = (v - mu) / sqrt(mean((v - mu)^2) + eps) * weight + bias
+ *
+ * per row of D elements, with mu = mean(v) (TRA_NORM_LAYER) or 0 (TRA_NORM_RMS);
+ * TRA_NORM_NONE leaves the row as it is (post) or computes no Y (norm).  Vectors
+ * (weight, bias, gate, post_weight, post_bias) that are NULL are left out.
+ *
+ * X, H, R, Y are M x D row-major, elements of `dtype`; the vectors are of
+ * `param_dtype`, which is `dtype` or TRA_DTYPE_F32.  A vector has D elements for
+ * all rows (its ld 0), or, with ld >= D, `groups` rows of D, `ld` elements apart:
+ * row m takes the (m / (M / groups))-th, and M is a multiple of groups.
+ *
+ * Numerics: everything is binary32, Y is taken from the unrounded R, each element of
+ * an output is rounded once.  Nothing depends on timing: a call gives the same bits
+ * every time.  Rows do not touch each other: NaN and infinities stay in theirs (and in
+ * the gradients of the vectors).
+ *
+ * tra_norm_backward takes dR and dY, the gradients of R and Y (either may be NULL, for
+ * zero; dR must be without H), computes the forward pass's values again, and writes
+ * the gradients asked for (non-NULL):
+ *
+ *   N'(v; d): with g = d weight, n = (v - mu) rstd:
+ *             rstd (g - mean(g) [TRA_NORM_LAYER only] - n mean(g n))
+ *   G = dR + N'(R; dY);  dX = scale G;  dH = N_post'(H; gate G)
+ *   dweight = sum dY n_R,  dbias = sum dY,  dgate = sum G N_post(H),
+ *   dpost_weight = sum gate G n_H,  dpost_bias = sum gate G
+ *
+ * with sums over the rows that share the vector.  A vector's gradient has its shape
+ * (D, or groups x D without gaps) and type.
+ *
+ * Sizes: any of M, D, groups from 0 (groups from 1); M = 0 leaves zeros in the vectors'
+ * gradients.  Outputs may share no element with inputs or each other, but R may be X
+ * itself.  Elements between a row's end and the next row are neither read nor
+ * written.  The backward call's workspace: as tra_linear's.  Errors:
+ * TRA_ERR_INVALID_ARG for a bad type, kind, size, leading dimension, pointer,
+ * overlap or workspace; TRA_ERR_UNSUPPORTED for sizes past 2^30; nothing is enqueued
+ * and no output touched.
+ */
+typedef enum tra_norm_kind {
+    TRA_NORM_NONE = 0,
+    TRA_NORM_RMS = 1,
+    TRA_NORM_LAYER = 2
+} tra_norm_kind;
+
+#define TRA_NORM_KIND_COUNT 3
+
+typedef struct tra_norm_args {
+    int32_t dtype, param_dtype, norm, post;
+    int64_t M, D, groups;
+    float scale, eps;
+    const void *X;
+    int64_t ldx;
+    const void *H;                     /* or NULL: no post, no gate, no R */
+    int64_t ldh;
+    const void *weight, *bias, *gate, *post_weight, *post_bias;    /* or NULL */
+    int64_t ld_weight, ld_bias, ld_gate, ld_post_weight, ld_post_bias;
+    void *R;                           /* or NULL */
+    int64_t ldr;
+    void *Y;                           /* NULL with norm NONE */
+    int64_t ldy;
+} tra_norm_args;
+
+typedef struct tra_norm_grad_args {
+    int32_t dtype, param_dtype, norm, post;
+    int64_t M, D, groups;
+    float scale, eps;
+    const void *X;
+    int64_t ldx;
+    const void *H;
+    int64_t ldh;
+    const void *weight, *bias, *gate, *post_weight, *post_bias;    /* biases are not read */
+    int64_t ld_weight, ld_bias, ld_gate, ld_post_weight, ld_post_bias;
+    const void *dR;
+    int64_t lddr;
+    const void *dY;
+    int64_t lddy;
+    void *dX;
+    int64_t lddx;
+    void *dH;
+    int64_t lddh;
+    void *dweight, *dbias, *dgate, *dpost_weight, *dpost_bias;
+    void *workspace;
+    uint64_t workspace_bytes;
+} tra_norm_grad_args;
+
+TRA_API tra_status tra_norm(const tra_norm_args *args, void *stream);
+TRA_API tra_status tra_norm_backward(const tra_norm_grad_args *args, void *stream);
+TRA_API tra_status tra_norm_backward_workspace_size(const tra_norm_grad_args *args,
+                                                    size_t *bytes);
+
+/*
  * Measurement probes: the two roofs of the roofline model measured on the
  * device (page "Roofline & Tiling notes", legato-user-group.github.io/
  * tensor2silicon-lab/week04/researchers/jaehyeong: performance is bounded

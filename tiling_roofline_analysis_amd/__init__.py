@@ -15,8 +15,9 @@ Low-level calls take raw device addresses (ints) and a hipStream_t handle:
                              stream) -> status
 
 ``linear`` and ``gated_linear`` (see ``fused``) are the GEMM with bias,
-activation, residual or gate fused in, with gradients; they take torch tensors
-and load with torch on first use.
+activation, residual or gate fused in, with gradients; ``norm`` and ``add_norm`` (see
+``norms``) are the norms around a block.  They take torch tensors and load with torch on
+first use.
 
 ``matmul(A, B, C=None, variant=AUTO)`` is the torch-tensor convenience
 form: it checks the tensors, passes their device pointers and torch's
@@ -56,7 +57,8 @@ ABI_FUNCTIONS = ("gemm_f32", "gemm_f32_variant", "gemm_f32_variant_ws",
                  "tra_probe_copy_f32", "tra_probe_mfma_f32", "tra_probe_fma_f32",
                  "tra_probe_launch", "tra_linear", "tra_linear_workspace_size",
                  "tra_linear_backward", "tra_linear_backward_workspace_size",
-                 "tra_linear_describe", "tra_linear_backward_describe")
+                 "tra_linear_describe", "tra_linear_backward_describe",
+                 "tra_norm", "tra_norm_backward", "tra_norm_backward_workspace_size")
 
 # tra_probe
 PROBE_COPY = 0
@@ -146,10 +148,11 @@ def _open(path: str) -> ctypes.CDLL:
     lib.tra_probe_launch.restype = c_int
     # the argument structs go as packed bytes
     args, size = ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)
-    for name in ("tra_linear", "tra_linear_backward"):
+    for name in ("tra_linear", "tra_linear_backward", "tra_norm", "tra_norm_backward"):
         getattr(lib, name).argtypes = [args, p]
         getattr(lib, name).restype = c_int
-    for name in ("tra_linear_workspace_size", "tra_linear_backward_workspace_size"):
+    for name in ("tra_linear_workspace_size", "tra_linear_backward_workspace_size",
+                 "tra_norm_backward_workspace_size"):
         getattr(lib, name).argtypes = [args, size]
         getattr(lib, name).restype = c_int
     for name in ("tra_linear_describe", "tra_linear_backward_describe"):
@@ -296,14 +299,19 @@ def matmul(A, B, C=None, variant: int = AUTO, stream=None, workspace=None):
     return C
 
 
-# --- fused linear operators (fused.py; imported on first use, since it needs torch) ---
+# --- operators on torch tensors (imported on first use, since they need torch) ---
 
-_FUSED = ("linear", "gated_linear", "linear_backward", "gated_linear_backward")
+_OPERATORS = {
+    "fused": ("linear", "gated_linear", "linear_backward", "gated_linear_backward"),
+    "norms": ("norm", "add_norm", "norm_backward", "add_norm_backward"),
+}
 
 
 def __getattr__(name):
-    if name in _FUSED:
-        from . import fused
-        globals().update({f: getattr(fused, f) for f in _FUSED})
-        return globals()[name]
+    for module, functions in _OPERATORS.items():
+        if name in functions:
+            import importlib
+            found = importlib.import_module("." + module, __name__)
+            globals().update({f: getattr(found, f) for f in functions})
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

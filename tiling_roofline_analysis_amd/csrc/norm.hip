@@ -1,0 +1,1062 @@
+// norm.hip -- the norms around a block with its gate and the residual stream's
+// scale, forward and backward (tra_norm, tra_norm_backward in include/tra_gemm.h).
+// Errors come back as status codes; nothing throws across the ABI and nothing is
+// allocated: scratch is the caller's workspace.
+//
+// Memory bounds all of it: a row is read once and kept in registers, E elements a
+// lane, while its sums are taken (one for the mean of squares; for a layer norm the mean
+// first, then the squares about it, so that a large mean costs no digits).  Rows too
+// wide for that are read again for each sum, from L2.
+#include "tra_gemm.h"
+
+#include <algorithm>
+#include <type_traits>
+
+#include "linear_epilogue.h"
+#include "operator_args.h"
+
+namespace tra {
+namespace {
+
+struct NormArgs {
+    int norm, post;
+    int64_t M, D, per_group;           // rows that share a row of the vectors
+    float scale, eps, inv_d;
+    const void *X;
+    int64_t ldx;
+    const void *H;
+    int64_t ldh;
+    const void *weight, *bias, *gate, *post_weight, *post_bias;
+    int64_t ld_weight, ld_bias, ld_gate, ld_post_weight, ld_post_bias;
+    void *R;
+    int64_t ldr;
+    void *Y;
+    int64_t ldy;
+};
+
+// The vectors' gradients, in the order of the sums.
+enum { kWeight = 0, kBias = 1, kGate = 2, kPostWeight = 3, kPostBias = 4, kVectors = 5 };
+
+struct NormGradArgs {
+    NormArgs f;                        // R, Y: not used
+    const void *dR;
+    int64_t lddr;
+    const void *dY;
+    int64_t lddy;
+    void *dX;
+    int64_t lddx;
+    void *dH;
+    int64_t lddh;
+    // Sums of one chunk of rows: chunk c of sum v at partial[v] + c * D; or null.
+    float *partial[kVectors];
+    int64_t chunks_per_group, rows_per_chunk;
+    float *stats;                      // wide rows: kStats floats a row
+};
+
+constexpr int kStats = 8;              // mean and 1 / deviation of H and R, means of g and g n
+
+// ---- sums over a row ------------------------------------------------------------------
+
+// Every lane's sum of its group of LANES lanes of the wave.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+    static_assert(LANES == 16 || LANES == 64, "a quarter of a wave, or all of it");
+#define TRA_DPP_ADD(ctrl) \
+    v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), ctrl, 0xf, 0xf, true))
+    TRA_DPP_ADD(0xb1);     // lane ^ 1
+    TRA_DPP_ADD(0x4e);     // lane ^ 2
+    TRA_DPP_ADD(0x141);    // mirrored in its 8
+    TRA_DPP_ADD(0x140);    // mirrored in its 16
+#undef TRA_DPP_ADD
+    if constexpr (LANES == 64) {
+        typedef uint32_t pair __attribute__((ext_vector_type(2)));
+        pair t = __builtin_bit_cast(pair, __builtin_amdgcn_permlane16_swap(
+                                              __float_as_uint(v), __float_as_uint(v), false, false));
+        v = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+        t = __builtin_bit_cast(pair, __builtin_amdgcn_permlane32_swap(
+                                         __float_as_uint(v), __float_as_uint(v), false, false));
+        v = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+    }
+    return v;
+}
+
+// Sums over the LANES lanes of a row, the same in each.  Rows of several waves meet in
+// LDS, in one of two places in turn: a wave that writes a place again has passed the
+// barrier of the sum between, behind which nobody reads the sum before it.
+template <int LANES, int BLOCK>
+struct RowSum {
+    static constexpr int WAVES = LANES / 64;     // of a row
+    float *lds;                                  // 2 * (BLOCK / 64) pairs
+    int turn = 0;
+
+    __device__ __forceinline__ void operator()(float &a, float &b) {
+        a = lanes_sum<LANES < 64 ? LANES : 64>(a);
+        b = lanes_sum<LANES < 64 ? LANES : 64>(b);
+        if constexpr (WAVES > 1) {
+            float *place = lds + turn * (BLOCK / 64) * 2;
+            turn ^= 1;
+            const int wave = static_cast<int>(threadIdx.x >> 6);
+            if ((threadIdx.x & 63) == 0) {
+                place[2 * wave] = a;
+                place[2 * wave + 1] = b;
+            }
+            __syncthreads();
+            const float *row = place + wave / WAVES * WAVES * 2;
+            a = b = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) {
+                a += row[2 * w];
+                b += row[2 * w + 1];
+            }
+        }
+    }
+    __device__ __forceinline__ float operator()(float a) {
+        float b = 0.0f;
+        (*this)(a, b);
+        return a;
+    }
+};
+
+// ---- a lane's part of a row ---------------------------------------------------------------
+
+// Chunk c of a lane: V elements from (c * LANES + lane) * V on, zeros past the row's end.
+template <typename T, int V, int LANES, int E>
+__device__ __forceinline__ void load_lane(const void *row, int lane, int64_t D, float (&v)[E]) {
+#pragma unroll
+    for (int c = 0; c < E / V; ++c) {
+        const int64_t at = (static_cast<int64_t>(c) * LANES + lane) * V;
+        float t[V];
+        load_part<T, V>(static_cast<const T *>(row) + at, D - at, t);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[c * V + e] = t[e];
+    }
+}
+
+template <typename T, int V, int LANES, int E>
+__device__ __forceinline__ void store_lane(void *row, int lane, int64_t D, const float (&v)[E]) {
+#pragma unroll
+    for (int c = 0; c < E / V; ++c) {
+        const int64_t at = (static_cast<int64_t>(c) * LANES + lane) * V;
+        float t[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) t[e] = v[c * V + e];
+        store_part<T, V>(static_cast<T *>(row) + at, D - at, t);
+    }
+}
+
+// v - mean inside the row, 0 past its end.
+template <int V, int LANES, int E>
+__device__ __forceinline__ void subtract_mean(float (&v)[E], float mean, int lane, int64_t D) {
+#pragma unroll
+    for (int c = 0; c < E / V; ++c) {
+        const int64_t left = D - (static_cast<int64_t>(c) * LANES + lane) * V;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[c * V + e] = e < left ? v[c * V + e] - mean : 0.0f;
+    }
+}
+
+__device__ __forceinline__ float inverse_deviation(float mean_square, float eps) {
+    return 1.0f / sqrtf(mean_square + eps);
+}
+
+// v becomes (v - mean) / deviation; returns 1 / deviation.
+template <int V, int LANES, int E, typename Sum>
+__device__ __forceinline__ float normalize(float (&v)[E], int kind, const NormArgs &p, int lane,
+                                           Sum &sum) {
+    if (kind == TRA_NORM_LAYER) {
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += v[e];
+        subtract_mean<V, LANES>(v, sum(s) * p.inv_d, lane, p.D);
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s += v[e] * v[e];
+    const float inverse = inverse_deviation(sum(s) * p.inv_d, p.eps);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= inverse;
+    return inverse;
+}
+
+// Group `group`'s row of a vector.
+template <typename P>
+__device__ __forceinline__ const P *vector_row(const void *v, int64_t ld, int64_t group) {
+    return static_cast<const P *>(v) + group * ld;
+}
+
+// v *= vector, v += vector: nothing where there is none.
+template <typename P, int V, int LANES, int E>
+__device__ __forceinline__ void times(float (&v)[E], const void *vec, int64_t ld, int64_t group,
+                                      int lane, int64_t D) {
+    if (vec == nullptr) return;
+    float t[E];
+    load_lane<P, V, LANES>(vector_row<P>(vec, ld, group), lane, D, t);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= t[e];
+}
+
+template <typename P, int V, int LANES, int E>
+__device__ __forceinline__ void plus(float (&v)[E], const void *vec, int64_t ld, int64_t group,
+                                     int lane, int64_t D) {
+    if (vec == nullptr) return;
+    float t[E];
+    load_lane<P, V, LANES>(vector_row<P>(vec, ld, group), lane, D, t);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] += t[e];
+}
+
+template <int LANES>
+constexpr int kBlock = LANES < 256 ? 256 : LANES;
+
+// ---- forward ------------------------------------------------------------------------------
+
+template <typename T, typename P, int LANES, int E>
+__global__ __launch_bounds__(kBlock<LANES>) void norm_forward(const NormArgs p) {
+    constexpr int V = kChunk<T>, BLOCK = kBlock<LANES>, ROWS = BLOCK / LANES;
+    __shared__ float lds[4 * (BLOCK / 64)];
+    lds_poison(lds, 4 * (BLOCK / 64));
+    RowSum<LANES, BLOCK> sum{lds};
+    const int lane = static_cast<int>(threadIdx.x) % LANES;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
+    for (int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS; first < p.M; first += step) {
+        const int64_t own = first + static_cast<int>(threadIdx.x) / LANES;
+        const bool inside = own < p.M;          // (a row past the last takes part, unseen)
+        const int64_t m = inside ? own : p.M - 1;
+        const int64_t group = m / p.per_group;
+        float x[E];
+        load_lane<T, V, LANES>(static_cast<const T *>(p.X) + m * p.ldx, lane, p.D, x);
+        if (p.H != nullptr) {
+            float h[E];
+            load_lane<T, V, LANES>(static_cast<const T *>(p.H) + m * p.ldh, lane, p.D, h);
+            if (p.post != TRA_NORM_NONE) {
+                normalize<V, LANES>(h, p.post, p, lane, sum);
+                times<P, V, LANES>(h, p.post_weight, p.ld_post_weight, group, lane, p.D);
+                plus<P, V, LANES>(h, p.post_bias, p.ld_post_bias, group, lane, p.D);
+            }
+            times<P, V, LANES>(h, p.gate, p.ld_gate, group, lane, p.D);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = p.scale * x[e] + h[e];
+            if (p.R != nullptr && inside)
+                store_lane<T, V, LANES>(static_cast<T *>(p.R) + m * p.ldr, lane, p.D, x);
+        }
+        if (p.norm != TRA_NORM_NONE) {
+            normalize<V, LANES>(x, p.norm, p, lane, sum);
+            times<P, V, LANES>(x, p.weight, p.ld_weight, group, lane, p.D);
+            plus<P, V, LANES>(x, p.bias, p.ld_bias, group, lane, p.D);
+            if (inside) store_lane<T, V, LANES>(static_cast<T *>(p.Y) + m * p.ldy, lane, p.D, x);
+        }
+    }
+}
+
+// ---- wide rows --------------------------------------------------------------------------------
+//
+// A workgroup of 1024 lanes a row; each chunk of the row is worked out again from
+// memory for every sum over it.
+
+constexpr int kWideLanes = 1024;
+
+// f(chunk) for each chunk of this lane's part of a row.
+template <int V, typename F>
+__device__ __forceinline__ void chunks_of(int64_t D, F f) {
+    for (int64_t at = static_cast<int64_t>(threadIdx.x) * V; at < D; at += kWideLanes * V) f(at);
+}
+
+template <int V>
+__device__ __forceinline__ void fill(float (&v)[V], float x) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = x;
+}
+
+// The vector's chunk, or `none`.
+template <typename P, int V>
+__device__ __forceinline__ void vector_chunk(const void *v, int64_t ld, int64_t group, int64_t at,
+                                             int64_t D, float none, float (&t)[V]) {
+    if (v == nullptr)
+        fill<V>(t, none);
+    else
+        load_part<P, V>(vector_row<P>(v, ld, group) + at, D - at, t);
+}
+
+// Mean and 1 / deviation of what get(at, v) gives chunk by chunk.
+template <int V, typename Get, typename Sum>
+__device__ __forceinline__ void wide_stats(int kind, const NormArgs &p, Get get, Sum &sum,
+                                           float &mean, float &inverse) {
+    mean = 0.0f;
+    float v[V], s = 0.0f;
+    if (kind == TRA_NORM_LAYER) {
+        chunks_of<V>(p.D, [&](int64_t at) {
+            get(at, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += at + e < p.D ? v[e] : 0.0f;
+        });
+        mean = sum(s) * p.inv_d;
+        s = 0.0f;
+    }
+    chunks_of<V>(p.D, [&](int64_t at) {
+        get(at, v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float d = v[e] - mean;
+            s += at + e < p.D ? d * d : 0.0f;
+        }
+    });
+    inverse = inverse_deviation(sum(s) * p.inv_d, p.eps);
+}
+
+// Chunks of row m of H, of N_post(H) from its statistics, and of R.
+template <typename T, typename P>
+struct WideRow {
+    static constexpr int V = kChunk<T>;
+    const NormArgs &p;
+    int64_t m, group;
+    float mean_h = 0.0f, inv_h = 1.0f;
+
+    __device__ __forceinline__ void h(int64_t at, float (&v)[V]) const {
+        load_part<T, V>(static_cast<const T *>(p.H) + m * p.ldh + at, p.D - at, v);
+    }
+    // n: (h - mean) / deviation (h itself without a norm); behind: N_post(h)
+    __device__ __forceinline__ void behind(int64_t at, float (&n)[V], float (&b)[V]) const {
+        h(at, n);
+#pragma unroll
+        for (int e = 0; e < V; ++e) b[e] = n[e];
+        if (p.post == TRA_NORM_NONE) return;
+        float w[V], c[V];
+        vector_chunk<P, V>(p.post_weight, p.ld_post_weight, group, at, p.D, 1.0f, w);
+        vector_chunk<P, V>(p.post_bias, p.ld_post_bias, group, at, p.D, 0.0f, c);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            n[e] = (n[e] - mean_h) * inv_h;
+            b[e] = n[e] * w[e] + c[e];
+        }
+    }
+    __device__ __forceinline__ void r(int64_t at, float (&v)[V]) const {
+        load_part<T, V>(static_cast<const T *>(p.X) + m * p.ldx + at, p.D - at, v);
+        if (p.H == nullptr) return;
+        float n[V], b[V], g[V];
+        behind(at, n, b);
+        vector_chunk<P, V>(p.gate, p.ld_gate, group, at, p.D, 1.0f, g);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = p.scale * v[e] + g[e] * b[e];
+    }
+};
+
+template <typename T, typename P>
+__global__ __launch_bounds__(kWideLanes) void norm_forward_wide(const NormArgs p) {
+    constexpr int V = kChunk<T>;
+    __shared__ float lds[4 * (kWideLanes / 64)];
+    lds_poison(lds, 4 * (kWideLanes / 64));
+    RowSum<kWideLanes, kWideLanes> sum{lds};
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        WideRow<T, P> row{p, m, m / p.per_group};
+        if (p.H != nullptr && p.post != TRA_NORM_NONE)
+            wide_stats<V>(p.post, p, [&](int64_t at, float (&v)[V]) { row.h(at, v); }, sum,
+                          row.mean_h, row.inv_h);
+        float mean = 0.0f, inverse = 1.0f;
+        if (p.norm != TRA_NORM_NONE)
+            wide_stats<V>(p.norm, p, [&](int64_t at, float (&v)[V]) { row.r(at, v); }, sum, mean,
+                          inverse);
+        // (R may be X: a lane reads its chunk for the last time before it writes it)
+        chunks_of<V>(p.D, [&](int64_t at) {
+            float v[V], w[V], b[V];
+            row.r(at, v);
+            if (p.R != nullptr)
+                store_part<T, V>(static_cast<T *>(p.R) + m * p.ldr + at, p.D - at, v);
+            if (p.norm == TRA_NORM_NONE) return;
+            vector_chunk<P, V>(p.weight, p.ld_weight, row.group, at, p.D, 1.0f, w);
+            vector_chunk<P, V>(p.bias, p.ld_bias, row.group, at, p.D, 0.0f, b);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = (v[e] - mean) * inverse * w[e] + b[e];
+            store_part<T, V>(static_cast<T *>(p.Y) + m * p.ldy + at, p.D - at, v);
+        });
+    }
+}
+
+// ---- backward, rows in registers -----------------------------------------------------------------
+
+// g: the gradient of a norm's normalized row n; becomes that of the row before it (0
+// past the row's end, as it was).
+template <int V, int LANES, int E, typename Sum>
+__device__ __forceinline__ void normalize_gradient(float (&g)[E], const float (&n)[E],
+                                                   float inverse, int kind, const NormArgs &p,
+                                                   int lane, Sum &sum) {
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        a += g[e] * n[e];
+        b += g[e];
+    }
+    sum(a, b);
+    a *= p.inv_d;
+    if (kind == TRA_NORM_LAYER) subtract_mean<V, LANES>(g, b * p.inv_d, lane, p.D);
+#pragma unroll
+    for (int e = 0; e < E; ++e) g[e] = inverse * (g[e] - n[e] * a);
+}
+
+// A workgroup takes a chunk of rows of one group, ROWS at a time, and keeps the sums of
+// the vectors' gradients in registers until its end.
+template <typename T, typename P, int LANES, int E>
+__global__ __launch_bounds__(kBlock<LANES>) void norm_backward(const NormGradArgs q) {
+    constexpr int V = kChunk<T>, BLOCK = kBlock<LANES>, ROWS = BLOCK / LANES;
+    const NormArgs &p = q.f;
+    __shared__ float lds[4 * (BLOCK / 64)];
+    __shared__ float part[ROWS > 1 ? (ROWS - 1) * LANES * E : 1];
+    lds_poison(lds, 4 * (BLOCK / 64));
+    lds_poison(part, ROWS > 1 ? (ROWS - 1) * LANES * E : 1);
+    RowSum<LANES, BLOCK> sum{lds};
+    const int lane = static_cast<int>(threadIdx.x) % LANES;
+    const int sub = static_cast<int>(threadIdx.x) / LANES;
+    const int64_t group = blockIdx.x / q.chunks_per_group;
+    const int64_t chunk = blockIdx.x - group * q.chunks_per_group;
+    const int64_t begin = group * p.per_group + chunk * q.rows_per_chunk;
+    const int64_t stop = (group + 1) * p.per_group;
+    const int64_t end = begin + q.rows_per_chunk < stop ? begin + q.rows_per_chunk : stop;
+    float total[kVectors][E] = {};
+
+    for (int64_t first = begin; first < end; first += ROWS) {
+        const bool inside = first + sub < end;
+        const int64_t m = inside ? first + sub : end - 1;
+        float r[E], h[E], behind[E], inv_h = 1.0f;
+        load_lane<T, V, LANES>(static_cast<const T *>(p.X) + m * p.ldx, lane, p.D, r);
+        float gate[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) gate[e] = 1.0f;
+        if (p.H != nullptr) {
+            load_lane<T, V, LANES>(static_cast<const T *>(p.H) + m * p.ldh, lane, p.D, h);
+            if (p.post != TRA_NORM_NONE) inv_h = normalize<V, LANES>(h, p.post, p, lane, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) behind[e] = h[e];
+            if (p.post != TRA_NORM_NONE) {
+                times<P, V, LANES>(behind, p.post_weight, p.ld_post_weight, group, lane, p.D);
+                plus<P, V, LANES>(behind, p.post_bias, p.ld_post_bias, group, lane, p.D);
+            }
+            times<P, V, LANES>(gate, p.gate, p.ld_gate, group, lane, p.D);
+#pragma unroll
+            for (int e = 0; e < E; ++e) r[e] = p.scale * r[e] + gate[e] * behind[e];
+        }
+        // G, the gradient of R
+        float g[E] = {};
+        if (q.dY != nullptr) {
+            const float inv_r = normalize<V, LANES>(r, p.norm, p, lane, sum);
+            load_lane<T, V, LANES>(static_cast<const T *>(q.dY) + m * q.lddy, lane, p.D, g);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                total[kWeight][e] += inside ? g[e] * r[e] : 0.0f;
+                total[kBias][e] += inside ? g[e] : 0.0f;
+            }
+            times<P, V, LANES>(g, p.weight, p.ld_weight, group, lane, p.D);
+            normalize_gradient<V, LANES>(g, r, inv_r, p.norm, p, lane, sum);
+        }
+        if (q.dR != nullptr) {
+            float d[E];
+            load_lane<T, V, LANES>(static_cast<const T *>(q.dR) + m * q.lddr, lane, p.D, d);
+#pragma unroll
+            for (int e = 0; e < E; ++e) g[e] += d[e];
+        }
+        if (q.dX != nullptr && inside) {
+            float d[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[e] = p.H != nullptr ? p.scale * g[e] : g[e];
+            store_lane<T, V, LANES>(static_cast<T *>(q.dX) + m * q.lddx, lane, p.D, d);
+        }
+        if (p.H != nullptr) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                total[kGate][e] += inside ? g[e] * behind[e] : 0.0f;
+                g[e] *= gate[e];
+                total[kPostWeight][e] += inside ? g[e] * h[e] : 0.0f;
+                total[kPostBias][e] += inside ? g[e] : 0.0f;
+            }
+            if (p.post != TRA_NORM_NONE) {
+                times<P, V, LANES>(g, p.post_weight, p.ld_post_weight, group, lane, p.D);
+                normalize_gradient<V, LANES>(g, h, inv_h, p.post, p, lane, sum);
+            }
+            if (q.dH != nullptr && inside)
+                store_lane<T, V, LANES>(static_cast<T *>(q.dH) + m * q.lddh, lane, p.D, g);
+        }
+    }
+    for (int k = 0; k < kVectors; ++k) {
+        if (q.partial[k] == nullptr) continue;
+        float t[E];
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j)
+            if (k == j) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) t[e] = total[j][e];
+            }
+        if constexpr (ROWS > 1) {
+            __syncthreads();
+            if (sub > 0) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) part[((sub - 1) * E + e) * LANES + lane] = t[e];
+            }
+            __syncthreads();
+            if (sub > 0) continue;
+            for (int s = 1; s < ROWS; ++s)
+#pragma unroll
+                for (int e = 0; e < E; ++e) t[e] += part[((s - 1) * E + e) * LANES + lane];
+        }
+        float *out = q.partial[k] + static_cast<int64_t>(blockIdx.x) * p.D;
+#pragma unroll
+        for (int c = 0; c < E / V; ++c) {
+            const int64_t at = (static_cast<int64_t>(c) * LANES + lane) * V;
+            float s[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[e] = t[c * V + e];
+            store_part<float, V>(out + at, p.D - at, s);
+        }
+    }
+}
+
+// ---- backward, wide rows ------------------------------------------------------------------------
+
+// What is taken from dY by the norm before the next block: G, chunk by chunk.
+template <typename T, typename P>
+struct WideGrad {
+    static constexpr int V = kChunk<T>;
+    const NormGradArgs &q;
+    const WideRow<T, P> &row;
+    float mean = 0.0f, inverse = 1.0f, a = 0.0f, b = 0.0f;
+
+    // n: R normalized; g: dY * weight
+    __device__ __forceinline__ void parts(int64_t at, float (&n)[V], float (&dy)[V],
+                                          float (&g)[V]) const {
+        const NormArgs &p = q.f;
+        row.r(at, n);
+        load_part<T, V>(static_cast<const T *>(q.dY) + row.m * q.lddy + at, p.D - at, dy);
+        vector_chunk<P, V>(p.weight, p.ld_weight, row.group, at, p.D, 1.0f, g);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            n[e] = (n[e] - mean) * inverse;
+            g[e] *= dy[e];
+        }
+    }
+    __device__ __forceinline__ void gradient(int64_t at, float (&n)[V], float (&dy)[V],
+                                             float (&g)[V]) const {
+        fill<V>(g, 0.0f);
+        if (q.dY != nullptr) {
+            parts(at, n, dy, g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) g[e] = inverse * (g[e] - n[e] * a - b);
+        }
+        if (q.dR != nullptr) {
+            float d[V];
+            load_part<T, V>(static_cast<const T *>(q.dR) + row.m * q.lddr + at, q.f.D - at, d);
+#pragma unroll
+            for (int e = 0; e < V; ++e) g[e] += d[e];
+        }
+    }
+};
+
+template <typename T, typename P>
+__global__ __launch_bounds__(kWideLanes) void norm_backward_wide(const NormGradArgs q) {
+    constexpr int V = kChunk<T>;
+    const NormArgs &p = q.f;
+    __shared__ float lds[4 * (kWideLanes / 64)];
+    lds_poison(lds, 4 * (kWideLanes / 64));
+    RowSum<kWideLanes, kWideLanes> sum{lds};
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        WideRow<T, P> row{p, m, m / p.per_group};
+        if (p.H != nullptr && p.post != TRA_NORM_NONE)
+            wide_stats<V>(p.post, p, [&](int64_t at, float (&v)[V]) { row.h(at, v); }, sum,
+                          row.mean_h, row.inv_h);
+        WideGrad<T, P> grad{q, row};
+        float n[V], dy[V], g[V], w[V], x[V];
+        if (q.dY != nullptr) {
+            wide_stats<V>(p.norm, p, [&](int64_t at, float (&v)[V]) { row.r(at, v); }, sum,
+                          grad.mean, grad.inverse);
+            float a = 0.0f, b = 0.0f;
+            chunks_of<V>(p.D, [&](int64_t at) {
+                grad.parts(at, n, dy, g);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    a += at + e < p.D ? g[e] * n[e] : 0.0f;
+                    b += at + e < p.D ? g[e] : 0.0f;
+                }
+            });
+            sum(a, b);
+            grad.a = a * p.inv_d;
+            grad.b = p.norm == TRA_NORM_LAYER ? b * p.inv_d : 0.0f;
+        }
+        if (q.stats != nullptr && threadIdx.x == 0) {
+            const float s[kStats] = {row.mean_h, row.inv_h, grad.mean, grad.inverse,
+                                     grad.a,     grad.b,    0.0f,      0.0f};
+#pragma unroll
+            for (int i = 0; i < kStats; ++i) q.stats[m * kStats + i] = s[i];
+        }
+        // the gradient of H normalized: G * gate * post_weight
+        auto behind = [&](int64_t at, float (&nh)[V], float (&d)[V]) {
+            grad.gradient(at, n, dy, d);
+            row.behind(at, nh, x);
+            vector_chunk<P, V>(p.gate, p.ld_gate, row.group, at, p.D, 1.0f, w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) d[e] *= w[e];
+            if (p.post == TRA_NORM_NONE) return;
+            vector_chunk<P, V>(p.post_weight, p.ld_post_weight, row.group, at, p.D, 1.0f, w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) d[e] *= w[e];
+        };
+        float a = 0.0f, b = 0.0f, nh[V], d[V];
+        if (q.dH != nullptr && p.post != TRA_NORM_NONE) {
+            chunks_of<V>(p.D, [&](int64_t at) {
+                behind(at, nh, d);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    a += at + e < p.D ? d[e] * nh[e] : 0.0f;
+                    b += at + e < p.D ? d[e] : 0.0f;
+                }
+            });
+            sum(a, b);
+            a *= p.inv_d;
+            b = p.post == TRA_NORM_LAYER ? b * p.inv_d : 0.0f;
+        }
+        chunks_of<V>(p.D, [&](int64_t at) {
+            if (q.dX != nullptr) {
+                grad.gradient(at, n, dy, g);
+#pragma unroll
+                for (int e = 0; e < V; ++e) g[e] *= p.H != nullptr ? p.scale : 1.0f;
+                store_part<T, V>(static_cast<T *>(q.dX) + m * q.lddx + at, p.D - at, g);
+            }
+            if (q.dH != nullptr) {
+                behind(at, nh, d);
+                if (p.post != TRA_NORM_NONE) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) d[e] = row.inv_h * (d[e] - nh[e] * a - b);
+                }
+                store_part<T, V>(static_cast<T *>(q.dH) + m * q.lddh + at, p.D - at, d);
+            }
+        });
+    }
+}
+
+// The vectors' gradients of wide rows, from the rows' statistics: 64 chunks of columns by
+// one chunk of rows per workgroup, whose four waves take every fourth row.
+template <typename T, typename P>
+__global__ __launch_bounds__(256) void norm_columns(const NormGradArgs q) {
+    constexpr int V = kChunk<T>;
+    const NormArgs &p = q.f;
+    __shared__ float part[3][64 * V];
+    lds_poison(&part[0][0], 3 * 64 * V);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t blocks = ceil_div(p.D, 64 * V);
+    const int64_t id = blockIdx.x / blocks, at = ((blockIdx.x - id * blocks) * 64 + lane) * V;
+    const int64_t group = id / q.chunks_per_group;
+    const int64_t begin =
+        group * p.per_group + (id - group * q.chunks_per_group) * q.rows_per_chunk;
+    const int64_t stop = (group + 1) * p.per_group;
+    const int64_t end = begin + q.rows_per_chunk < stop ? begin + q.rows_per_chunk : stop;
+    float total[kVectors][V] = {};
+    if (at < p.D) {
+        for (int64_t m = begin + wave; m < end; m += 4) {
+            const float *s = q.stats + m * kStats;
+            WideRow<T, P> row{p, m, group, s[0], s[1]};
+            WideGrad<T, P> grad{q, row, s[2], s[3], s[4], s[5]};
+            float n[V] = {}, dy[V] = {}, g[V], nh[V], b[V], w[V];
+            grad.gradient(at, n, dy, g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                total[kWeight][e] += dy[e] * n[e];
+                total[kBias][e] += dy[e];
+            }
+            if (p.H == nullptr) continue;
+            row.behind(at, nh, b);
+            vector_chunk<P, V>(p.gate, p.ld_gate, group, at, p.D, 1.0f, w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                total[kGate][e] += g[e] * b[e];
+                total[kPostWeight][e] += g[e] * w[e] * nh[e];
+                total[kPostBias][e] += g[e] * w[e];
+            }
+        }
+    }
+    for (int k = 0; k < kVectors; ++k) {
+        if (q.partial[k] == nullptr) continue;
+        float t[V];
+#pragma unroll
+        for (int j = 0; j < kVectors; ++j)
+            if (k == j) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) t[e] = total[j][e];
+            }
+        __syncthreads();
+        if (wave > 0) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) part[wave - 1][e * 64 + lane] = t[e];
+        }
+        __syncthreads();
+        if (wave > 0 || at >= p.D) continue;
+#pragma unroll
+        for (int w = 0; w < 3; ++w)
+#pragma unroll
+            for (int e = 0; e < V; ++e) t[e] += part[w][e * 64 + lane];
+        store_part<float, V>(q.partial[k] + id * p.D + at, p.D - at, t);
+    }
+}
+
+// Adds the chunks' sums in order: 16 columns of one gradient's row per workgroup, whose 16
+// groups of lanes take every 16th chunk and are added in order.
+struct NormJoinArgs {
+    const float *partial[kVectors];
+    void *out[kVectors];
+    int64_t rows[kVectors];            // of the gradient: 1, or the groups
+    int64_t D, chunks, chunks_per_group;
+};
+
+template <typename P>
+__global__ __launch_bounds__(256) void norm_join(const NormJoinArgs p) {
+    __shared__ float part[16][16];
+    const int j = threadIdx.x & 15, lanes = threadIdx.x >> 4;
+    const int64_t blocks = ceil_div(p.D, 16);
+    const int k = blockIdx.y;
+    if (p.out[k] == nullptr) return;
+    const int64_t rows = p.rows[k], each = rows == 1 ? p.chunks : p.chunks_per_group;
+    for (int64_t id = blockIdx.x; id < rows * blocks; id += gridDim.x) {
+        const int64_t row = id / blocks, n = (id - row * blocks) * 16 + j;
+        const float *from = p.partial[k] + row * each * p.D + n;
+        float sum = 0.0f;
+        if (n < p.D) {
+#pragma unroll 4
+            for (int64_t c = lanes; c < each; c += 16) sum += from[c * p.D];
+        }
+        __syncthreads();
+        part[lanes][j] = sum;
+        __syncthreads();
+        if (lanes == 0 && n < p.D) {
+            for (int i = 1; i < 16; ++i) sum += part[i][j];
+            static_cast<P *>(p.out[k])[row * p.D + n] = static_cast<P>(sum);
+        }
+    }
+}
+
+// ---- launches ----------------------------------------------------------------------------------
+
+constexpr int64_t kMaxBlocks = 1 << 20;      // workgroups that take rows in turn
+
+template <typename T, typename P, int LANES, int E>
+hipError_t launch_forward(const NormArgs &a, hipStream_t s) {
+    const int64_t blocks = ceil_div(a.M, kBlock<LANES> / LANES);
+    norm_forward<T, P, LANES, E><<<dim3(static_cast<unsigned>(std::min(blocks, kMaxBlocks))),
+                                   kBlock<LANES>, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, typename P>
+hipError_t forward_of(const NormArgs &a, hipStream_t s) {
+    if (a.D <= 128) return launch_forward<T, P, 16, 8>(a, s);
+    if (a.D <= 512) return launch_forward<T, P, 64, 8>(a, s);
+    if (a.D <= 2048) return launch_forward<T, P, 256, 8>(a, s);
+    if (a.D <= 4096) return launch_forward<T, P, 512, 8>(a, s);
+    if (a.D <= 8192) return launch_forward<T, P, 1024, 8>(a, s);
+    norm_forward_wide<T, P><<<dim3(static_cast<unsigned>(std::min(a.M, kMaxBlocks))), kWideLanes,
+                              0, s>>>(a);
+    return hipGetLastError();
+}
+
+constexpr int64_t kWide = 8192;              // the widest rows that the backward pass keeps
+
+template <typename T, typename P, int LANES>
+hipError_t launch_backward(const NormGradArgs &a, int64_t chunks, hipStream_t s) {
+    norm_backward<T, P, LANES, 8><<<dim3(static_cast<unsigned>(chunks)), kBlock<LANES>, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, typename P>
+hipError_t backward_of(const NormGradArgs &a, int64_t chunks, bool sums, hipStream_t s) {
+    const int64_t D = a.f.D;
+    if (D <= 128) return launch_backward<T, P, 16>(a, chunks, s);
+    if (D <= 512) return launch_backward<T, P, 64>(a, chunks, s);
+    if (D <= 2048) return launch_backward<T, P, 256>(a, chunks, s);
+    if (D <= 4096) return launch_backward<T, P, 512>(a, chunks, s);
+    if (D <= kWide) return launch_backward<T, P, 1024>(a, chunks, s);
+    norm_backward_wide<T, P><<<dim3(static_cast<unsigned>(std::min(a.f.M, kMaxBlocks))),
+                               kWideLanes, 0, s>>>(a);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || !sums) return err;
+    const int64_t blocks = ceil_div(D, 64 * kChunk<T>);
+    norm_columns<T, P><<<dim3(static_cast<unsigned>(chunks * blocks)), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename P>
+hipError_t launch_join(const NormJoinArgs &a, hipStream_t s) {
+    int64_t rows = 1;
+    for (int k = 0; k < kVectors; ++k)
+        if (a.out[k] != nullptr) rows = std::max(rows, a.rows[k]);
+    const dim3 grid(static_cast<unsigned>(std::min(rows * ceil_div(a.D, 16), kMaxBlocks)),
+                    kVectors);
+    norm_join<P><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace tra
+
+namespace {
+
+using namespace tra::host;
+using tra::ceil_div;
+using tra::NormArgs;
+using tra::NormGradArgs;
+
+constexpr int64_t kMaxGroups = 65535;
+
+bool valid_kind(int k) { return k >= TRA_NORM_NONE && k < TRA_NORM_KIND_COUNT; }
+
+// A vector: 1 or `groups` rows of D.
+View vector_view(const void *p, int64_t ld, int64_t groups, int64_t D, int64_t bytes) {
+    return View{p, p == nullptr ? 0 : ld == 0 ? 1 : groups, D, ld == 0 ? D : ld, bytes};
+}
+
+// What both directions check: types, kinds, sizes.
+template <typename A>
+tra_status check_common(const A &a) {
+    if (!valid_dtype(a.dtype) || !valid_kind(a.norm) || !valid_kind(a.post) ||
+        (a.param_dtype != a.dtype && a.param_dtype != TRA_DTYPE_F32) || a.M < 0 || a.D < 0 ||
+        a.groups < 1 || a.M % a.groups != 0 || !(a.eps >= 0.0f))
+        return TRA_ERR_INVALID_ARG;
+    // (an empty matrix may be at NULL)
+    if (a.H == nullptr && a.M > 0 && a.D > 0 && (a.post != TRA_NORM_NONE || a.gate != nullptr))
+        return TRA_ERR_INVALID_ARG;
+    if (a.post == TRA_NORM_NONE && (a.post_weight != nullptr || a.post_bias != nullptr))
+        return TRA_ERR_INVALID_ARG;
+    if (a.norm == TRA_NORM_NONE && (a.weight != nullptr || a.bias != nullptr))
+        return TRA_ERR_INVALID_ARG;
+    if (a.M > kMaxSize || a.D > kMaxSize || a.groups > kMaxGroups) return TRA_ERR_UNSUPPORTED;
+    return TRA_OK;
+}
+
+// The inputs that both directions read (`biases`: the forward pass reads them).
+template <typename A>
+bool inputs_of(const A &a, bool biases, View (&in)[7]) {
+    const int64_t b = elem_bytes(a.dtype), pb = elem_bytes(a.param_dtype);
+    in[0] = View{a.X, a.M, a.D, a.ldx, b};
+    in[1] = View{a.H, a.H != nullptr ? a.M : 0, a.D, a.ldh, b};
+    in[2] = vector_view(a.weight, a.ld_weight, a.groups, a.D, pb);
+    in[3] = vector_view(a.gate, a.ld_gate, a.groups, a.D, pb);
+    in[4] = vector_view(a.post_weight, a.ld_post_weight, a.groups, a.D, pb);
+    in[5] = vector_view(a.post_bias, a.ld_post_bias, a.groups, a.D, pb);
+    in[6] = vector_view(biases ? a.bias : nullptr, a.ld_bias, a.groups, a.D, pb);
+    for (const View &v : in)
+        if (!v.valid()) return false;
+    return true;
+}
+
+template <typename A>
+NormArgs device_args(const A &a) {
+    NormArgs d{};
+    d.norm = a.norm;
+    d.post = a.post;
+    d.M = a.M;
+    d.D = a.D;
+    d.per_group = a.M / a.groups;
+    d.scale = a.scale;
+    d.eps = a.eps;
+    d.inv_d = static_cast<float>(1.0 / static_cast<double>(a.D));
+    d.X = a.X;
+    d.ldx = a.ldx;
+    d.H = a.H;
+    d.ldh = a.ldh;
+    d.weight = a.weight;
+    d.bias = a.bias;
+    d.gate = a.gate;
+    d.post_weight = a.post_weight;
+    d.post_bias = a.post_bias;
+    d.ld_weight = a.ld_weight;
+    d.ld_bias = a.ld_bias;
+    d.ld_gate = a.ld_gate;
+    d.ld_post_weight = a.ld_post_weight;
+    d.ld_post_bias = a.ld_post_bias;
+    return d;
+}
+
+// f<element type, parameter type>()
+template <typename F>
+hipError_t by_type(int dtype, int param_dtype, F f) {
+    const bool f32 = param_dtype == TRA_DTYPE_F32;
+    switch (dtype) {
+        case TRA_DTYPE_F32: return f(0.0f, 0.0f);
+        case TRA_DTYPE_BF16:
+            return f32 ? f(__bf16(0.0f), 0.0f) : f(__bf16(0.0f), __bf16(0.0f));
+        default: return f32 ? f(_Float16(0.0f), 0.0f) : f(_Float16(0.0f), _Float16(0.0f));
+    }
+}
+
+// ---- forward ----------------------------------------------------------------------
+
+tra_status check_forward(const tra_norm_args *p) {
+    if (p == nullptr) return TRA_ERR_INVALID_ARG;
+    const tra_norm_args &a = *p;
+    const tra_status st = check_common(a);
+    if (st != TRA_OK) return st;
+    if ((a.norm != TRA_NORM_NONE) != (a.Y != nullptr) || (a.H == nullptr && a.R != nullptr) ||
+        (a.Y == nullptr && a.R == nullptr)) {
+        if (a.M > 0 && a.D > 0) return TRA_ERR_INVALID_ARG;
+    }
+    if (a.M == 0 || a.D == 0) return TRA_OK;
+    const int64_t b = elem_bytes(a.dtype);
+    View in[7];
+    if (!inputs_of(a, true, in)) return TRA_ERR_INVALID_ARG;
+    const View R{a.R, a.R != nullptr ? a.M : 0, a.D, a.ldr, b};
+    const View Y{a.Y, a.Y != nullptr ? a.M : 0, a.D, a.ldy, b};
+    if (!R.valid() || !Y.valid() || share(R, Y)) return TRA_ERR_INVALID_ARG;
+    for (const View &v : in) {
+        // X in place: the lane that reads an element of X writes it, after its last read
+        const bool in_place = &v == &in[0] && same(v, R);
+        if (share(v, Y) || (share(v, R) && !in_place)) return TRA_ERR_INVALID_ARG;
+    }
+    return TRA_OK;
+}
+
+tra_status forward(const tra_norm_args *p, void *stream) {
+    const tra_status st = check_forward(p);
+    if (st != TRA_OK || p->M == 0 || p->D == 0) return st;
+    NormArgs d = device_args(*p);
+    d.R = p->R;
+    d.ldr = p->ldr;
+    d.Y = p->Y;
+    d.ldy = p->ldy;
+    return status_of(by_type(p->dtype, p->param_dtype, [&](auto t, auto w) {
+        return tra::forward_of<decltype(t), decltype(w)>(d, static_cast<hipStream_t>(stream));
+    }));
+}
+
+// ---- backward ----------------------------------------------------------------------
+
+struct GradPlan {
+    int64_t chunks_per_group, rows_per_chunk, chunks;
+    int vectors;               // gradients of vectors asked for
+    size_t partial_bytes;      // of one
+    size_t stats_bytes;
+    size_t total;
+};
+
+bool wants(const tra_norm_grad_args &a, int k) {
+    const void *out[] = {a.dweight, a.dbias, a.dgate, a.dpost_weight, a.dpost_bias};
+    return out[k] != nullptr;
+}
+
+// Rows of the gradient of vector k.
+int64_t rows_of(const tra_norm_grad_args &a, int k) {
+    const int64_t ld[] = {a.ld_weight, a.ld_bias, a.ld_gate, a.ld_post_weight, a.ld_post_bias};
+    return ld[k] == 0 ? 1 : a.groups;
+}
+
+GradPlan plan_backward(const tra_norm_grad_args &a) {
+    GradPlan g{};
+    for (int k = 0; k < tra::kVectors; ++k) g.vectors += wants(a, k);
+    const int64_t per_group = a.M / a.groups;
+    const int64_t want = std::max<int64_t>(1, (g.vectors > 0 ? 256 : 4096) / a.groups);
+    g.rows_per_chunk = std::max<int64_t>(1, ceil_div(per_group, want));
+    g.chunks_per_group = std::max<int64_t>(1, ceil_div(per_group, g.rows_per_chunk));
+    g.chunks = a.groups * g.chunks_per_group;
+    if (g.vectors > 0) {
+        g.partial_bytes =
+            align_up(static_cast<size_t>(g.chunks) * static_cast<size_t>(a.D) * sizeof(float));
+        if (a.D > tra::kWide)
+            g.stats_bytes = align_up(static_cast<size_t>(a.M) * tra::kStats * sizeof(float));
+    }
+    g.total = g.vectors * g.partial_bytes + g.stats_bytes;
+    return g;
+}
+
+tra_status check_backward(const tra_norm_grad_args *p) {
+    if (p == nullptr) return TRA_ERR_INVALID_ARG;
+    const tra_norm_grad_args &a = *p;
+    const tra_status st = check_common(a);
+    if (st != TRA_OK) return st;
+    if (a.D == 0) return TRA_OK;
+    if (a.H == nullptr && a.M > 0 && (a.dR != nullptr || a.dH != nullptr))
+        return TRA_ERR_INVALID_ARG;
+    if (a.norm == TRA_NORM_NONE && a.dY != nullptr) return TRA_ERR_INVALID_ARG;
+    if ((a.dweight != nullptr && a.weight == nullptr) || (a.dgate != nullptr && a.gate == nullptr) ||
+        (a.dpost_weight != nullptr && a.post_weight == nullptr) ||
+        (a.dpost_bias != nullptr && a.post == TRA_NORM_NONE) ||
+        (a.dbias != nullptr && a.norm == TRA_NORM_NONE))
+        return TRA_ERR_INVALID_ARG;
+    const int64_t b = elem_bytes(a.dtype), pb = elem_bytes(a.param_dtype);
+    View in[7];
+    if (!inputs_of(a, false, in)) return TRA_ERR_INVALID_ARG;
+    const View dR{a.dR, a.dR != nullptr ? a.M : 0, a.D, a.lddr, b};
+    const View dY{a.dY, a.dY != nullptr ? a.M : 0, a.D, a.lddy, b};
+    if (!dR.valid() || !dY.valid()) return TRA_ERR_INVALID_ARG;
+    void *const vectors[] = {a.dweight, a.dbias, a.dgate, a.dpost_weight, a.dpost_bias};
+    View out[7];
+    out[0] = View{a.dX, a.dX != nullptr ? a.M : 0, a.D, a.lddx, b};
+    out[1] = View{a.dH, a.dH != nullptr ? a.M : 0, a.D, a.lddh, b};
+    for (int k = 0; k < tra::kVectors; ++k)
+        out[2 + k] = View{vectors[k], vectors[k] != nullptr ? rows_of(a, k) : 0, a.D, a.D, pb};
+    for (int i = 0; i < 7; ++i) {
+        if (!out[i].valid() || share(out[i], dR) || share(out[i], dY)) return TRA_ERR_INVALID_ARG;
+        for (const View &v : in)
+            if (share(out[i], v)) return TRA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (share(out[i], out[j])) return TRA_ERR_INVALID_ARG;
+    }
+    const GradPlan g = plan_backward(a);
+    if (g.chunks * ceil_div(a.D, 256) * 256 > tra::kMaxGridLanes) return TRA_ERR_UNSUPPORTED;
+    return TRA_OK;
+}
+
+tra_status backward(const tra_norm_grad_args *p, void *stream_) {
+    const tra_status st = check_backward(p);
+    if (st != TRA_OK || p->D == 0) return st;
+    const tra_norm_grad_args &a = *p;
+    const GradPlan g = plan_backward(a);
+    if (!workspace_ok(a.workspace, a.workspace_bytes, g.total)) return TRA_ERR_INVALID_ARG;
+    const hipStream_t stream = static_cast<hipStream_t>(stream_);
+    NormGradArgs d{};
+    d.f = device_args(a);
+    d.dR = a.dR;
+    d.lddr = a.lddr;
+    d.dY = a.dY;
+    d.lddy = a.lddy;
+    d.dX = a.dX;
+    d.lddx = a.lddx;
+    d.dH = a.dH;
+    d.lddh = a.lddh;
+    d.chunks_per_group = g.chunks_per_group;
+    d.rows_per_chunk = g.rows_per_chunk;
+    char *ws = static_cast<char *>(a.workspace);
+    if (g.stats_bytes > 0) d.stats = reinterpret_cast<float *>(ws);
+    ws += g.stats_bytes;
+    void *const vectors[] = {a.dweight, a.dbias, a.dgate, a.dpost_weight, a.dpost_bias};
+    tra::NormJoinArgs j{};
+    j.D = a.D;
+    j.chunks = a.M > 0 ? g.chunks : 0;
+    j.chunks_per_group = a.M > 0 ? g.chunks_per_group : 0;
+    for (int k = 0; k < tra::kVectors; ++k) {
+        if (!wants(a, k)) continue;
+        j.partial[k] = d.partial[k] = reinterpret_cast<float *>(ws);
+        ws += g.partial_bytes;
+        j.out[k] = vectors[k];
+        j.rows[k] = rows_of(a, k);
+    }
+    hipError_t err = hipSuccess;
+    if (a.M > 0 && (a.dX != nullptr || a.dH != nullptr || g.vectors > 0))
+        err = by_type(a.dtype, a.param_dtype, [&](auto t, auto w) {
+            return tra::backward_of<decltype(t), decltype(w)>(d, g.chunks, g.vectors > 0, stream);
+        });
+    if (err == hipSuccess && g.vectors > 0)
+        err = a.param_dtype == TRA_DTYPE_F32    ? tra::launch_join<float>(j, stream)
+              : a.param_dtype == TRA_DTYPE_BF16 ? tra::launch_join<__bf16>(j, stream)
+                                                : tra::launch_join<_Float16>(j, stream);
+    return status_of(err);
+}
+
+}  // namespace
+
+extern "C" {
+
+tra_status tra_norm(const tra_norm_args *args, void *stream) { return forward(args, stream); }
+
+tra_status tra_norm_backward(const tra_norm_grad_args *args, void *stream) {
+    return backward(args, stream);
+}
+
+tra_status tra_norm_backward_workspace_size(const tra_norm_grad_args *args, size_t *bytes) {
+    const tra_status st = check_backward(args);
+    if (st != TRA_OK || bytes == nullptr) return st != TRA_OK ? st : TRA_ERR_INVALID_ARG;
+    *bytes = args->D == 0 ? 0 : plan_backward(*args).total;
+    return TRA_OK;
+}
+
+}  // extern "C"

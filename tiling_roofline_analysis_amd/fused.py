@@ -309,10 +309,9 @@ def _recorded_elsewhere(*tensors):
     if forward_ad._current_level >= 0 and torch._C._is_fwd_grad_enabled():
         for t in tensors:
             if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
-                raise NotImplementedError("the fused linear operators have no forward-mode "
-                                          "derivatives")
+                raise NotImplementedError("the fused operators have no forward-mode derivatives")
     if _tracing():
-        raise RuntimeError("torch.jit.trace cannot record the fused linear operators")
+        raise RuntimeError("torch.jit.trace cannot record the fused operators")
 
 
 def _on(stream, call, *tensors):
@@ -352,8 +351,8 @@ def _no_capture():
     # alive, that stream is outside the capture, and the process ends.
     if torch.cuda.is_current_stream_capturing():
         raise RuntimeError("gradients cannot be recorded into a captured graph: capture the call "
-                           "without gradients (z=...) and linear_backward or "
-                           "gated_linear_backward")
+                           "without gradients (a linear one with z=...) and the operator's "
+                           "backward function, such as linear_backward")
 
 
 def linear(x, w, bias=None, act="none", residual=None, out=None, z=None, stream=None):
