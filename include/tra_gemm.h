@@ -368,6 +368,60 @@ TRA_API tra_status tra_linear_backward_describe(const tra_linear_grad_args *args
                                                 size_t len);
 
 /*
+ * Matrices in 8-bit floating point with a scale for each block of 128, and products of
+ * them.
+ *
+ * A block is 128 consecutive elements along the axis that a product sums over (the
+ * last one of a row may be shorter), of one row (block_rows 1) or of 128 rows
+ * (block_rows 128; the last ones may be fewer).  An element stands for value x scale.
+ * Values are e4m3fn (largest 448) or e5m2 (largest 57344).  Scales are binary32, or
+ * e8m0: one byte b for 2^(b - 127), 255 for NaN.
+ *
+ * tra_quantize takes X, M x K row-major, elements of `dtype`, and writes either form or
+ * both (values NULL: not that one):
+ *
+ *   rows      Q of M rows, blocks along K:  scale of row m, block k / 128 at
+ *             S[(m / block_rows) * ss_row + (k / 128) * ss_block]
+ *   columns   QT of K rows, blocks along M: the same of X's transpose, with ST, sts_row,
+ *             sts_block
+ *
+ * With largest = the largest finite magnitude of a block and F the type's largest value,
+ * a scale is the least power of two s with largest / s <= F (e8m0; at least 2^-127), or
+ * largest / F rounded to binary32 (at least 2^-126); 1 where largest is 0.  A value is
+ * x / s rounded once, to nearest even, exactly; NaN stays NaN, infinities become NaN
+ * (e4m3fn has none) or stay (e5m2).  Rows of values are filled up with zeros to a
+ * multiple of 16, so Q has (K + 15) / 16 * 16 columns and QT (M + 15) / 16 * 16, and
+ * leading dimensions of at least that, which are multiples of 16; both start 16-byte
+ * aligned.  Sizes: M or K may be 0.  No workspace.
+ */
+typedef enum tra_fp8 {
+    TRA_FP8_E4M3 = 0,
+    TRA_FP8_E5M2 = 1
+} tra_fp8;
+
+typedef enum tra_scale {
+    TRA_SCALE_F32 = 0,
+    TRA_SCALE_E8M0 = 1
+} tra_scale;
+
+typedef struct tra_quantize_args {
+    int32_t dtype, fp8, scale, block_rows;
+    int64_t M, K;
+    const void *X;
+    int64_t ldx;
+    void *Q;                   /* or NULL */
+    int64_t ldq;
+    void *S;
+    int64_t ss_row, ss_block;
+    void *QT;                  /* or NULL */
+    int64_t ldqt;
+    void *ST;
+    int64_t sts_row, sts_block;
+} tra_quantize_args;
+
+TRA_API tra_status tra_quantize(const tra_quantize_args *args, void *stream);
+
+/*
  * Norms around a block, with its gate and the residual stream's scale:
  *
  *   R = scale X + gate * N_post(H)       (element by element; R = X without H)

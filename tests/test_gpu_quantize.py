@@ -1,0 +1,236 @@
+"""quantize on the GPU: every value and every scale is the one of the definition."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import tiling_roofline_analysis_amd as tra
+from scaled_reference import FP8, SCALES, quantized, stands_for, up
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available()
+
+
+def same(got, want):
+    got = got.double()
+    assert got.shape == want.shape
+    assert torch.equal(torch.nan_to_num(got, 9e9, 8e8, -8e8), torch.nan_to_num(want, 9e9, 8e8, -8e8))
+
+
+def check(x, fp8="e4m3", scale="e8m0", block_rows=1, form="both", stream=None):
+    got = tra.quantize(x, (block_rows, 128), FP8[fp8], SCALES[scale], form, stream=stream)
+    if stream is not None:
+        torch.cuda.current_stream().wait_stream(stream)
+    sides = {"rows": [x], "columns": [x.t()], "both": [x, x.t()]}[form]
+    assert len(got) == 2 * len(sides)
+    for i, side in enumerate(sides):
+        values, scales = got[2 * i], got[2 * i + 1]
+        assert values.dtype == FP8[fp8] and scales.dtype == SCALES[scale]
+        q, s = quantized(side, fp8, scale, block_rows)
+        same(scales, s)
+        same(values, q)
+    return got
+
+
+def normal(M, K, dtype, seed=0, spread=2.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    size = torch.randn(M, K, generator=gen, device="cuda").mul_(spread).exp_()
+    return torch.randn(M, K, generator=gen, device="cuda").mul_(size).to(dtype)
+
+
+SIZES = [(1, 1), (1, 16), (3, 15), (7, 17), (1, 4096), (16, 128), (127, 129), (128, 128),
+         (129, 127), (130, 400), (257, 1531), (300, 2049), (5461, 131)]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_sizes(size, dtype):
+    x = normal(*size, DTYPES[dtype])
+    for form in ("rows", "columns", "both"):
+        check(x, form=form)
+        check(x, scale="f32", block_rows=128, form=form)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("scale", list(SCALES))
+@pytest.mark.parametrize("fp8", list(FP8))
+def test_formats(fp8, scale, block_rows, dtype):
+    for spread in (0.0, 1.0, 4.0):
+        check(normal(200, 333, DTYPES[dtype], 1, spread).nan_to_num(0.0, 6e4, -6e4), fp8, scale,
+              block_rows)
+
+
+@pytest.mark.parametrize("fp8", list(FP8))
+@pytest.mark.parametrize("scale", list(SCALES))
+def test_borders_between_values(fp8, scale):
+    # quotients at, just below and just above every border: x = border * s for scales of all
+    # kinds, and its neighbours; the block's largest element is the one that makes the scale
+    from scaled_reference import codes
+    table = codes(fp8, "cuda")
+    borders = (table[1:] + table[:-1]) / 2
+    rows = []
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    largest = torch.rand(500, generator=gen, device="cuda", dtype=torch.float64) + 0.5
+    largest = (largest * 2.0 ** torch.randint(-120, 120, (500,), generator=gen, device="cuda"))
+    for a in largest.float():
+        s = quantized(a.view(1, 1), fp8, scale)[1][0, 0]
+        mid = (borders * s).float()
+        rows.append(torch.cat([a.view(1), mid, torch.nextafter(mid, mid * 2),
+                               torch.nextafter(mid, mid * 0)])[:384])
+    x = torch.nn.utils.rnn.pad_sequence(rows, batch_first=True)
+    x = torch.nn.functional.pad(x, (0, 384 - x.shape[1]))
+    # one scale a row: the largest element goes into each of its three blocks
+    x = x.view(500, 3, 128)
+    x[:, :, 127] = largest.float()[:, None]
+    x = x.clamp(max=largest.float()[:, None, None]).view(500, 384)
+    check(x, fp8, scale)
+    check(-x.t().contiguous(), fp8, scale)
+
+
+@pytest.mark.parametrize("scale", list(SCALES))
+@pytest.mark.parametrize("fp8", list(FP8))
+def test_all_magnitudes(fp8, scale):
+    # every exponent that binary32 has, subnormals among them, also as the block's largest
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    e = torch.arange(-149, 128, device="cuda", dtype=torch.float64)
+    m = 1 + torch.rand(277, 128, generator=gen, device="cuda", dtype=torch.float64) * 0.999
+    top = (m * 2.0 ** e[:, None]).float()
+    check(top, fp8, scale)
+    # elements far below their block's largest
+    mixed = top.clone()
+    mixed[:, 1:] *= (2.0 ** -torch.arange(1, 128, device="cuda", dtype=torch.float64) / 4).float()
+    check(mixed, fp8, scale)
+    # magnitudes that are the type's largest times a power of two, and next to it
+    for f in (448.0, 57344.0):
+        v = (f * 2.0 ** torch.arange(-100, 100, 7, device="cuda", dtype=torch.float64)).float()
+        for w in (v, torch.nextafter(v, v * 2), torch.nextafter(v, v * 0)):
+            check(w[:, None].expand(-1, 3).contiguous(), fp8, scale)
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("scale", list(SCALES))
+@pytest.mark.parametrize("fp8", list(FP8))
+def test_zeros_nan_and_infinities(fp8, scale, block_rows):
+    x = normal(140, 300, torch.float32)
+    x[3] = 0.0
+    x[5, 7] = float("nan")
+    x[6, 8] = float("inf")
+    x[9, 250] = -float("inf")
+    x[11, :128] = float("nan")
+    x[12, 130:140] = -0.0
+    x[:, 128:256] = 0.0
+    x[20, 128:256] = float("inf")
+    values, scales = check(x, fp8, scale, block_rows)[:2]
+    clean = normal(140, 300, torch.float32)
+    if block_rows == 1:
+        assert float(scales[3, 0].float()) == 1.0 and float(scales[11, 0].float()) == 1.0
+        # the others of a block keep the values that they have without the strange one
+        q, _ = quantized(clean, fp8, scale)
+        assert torch.equal(values[5, :7].double(), q[5, :7])
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_strided_rows_and_alignment(dtype):
+    for pad, at in ((1, 0), (1, 1), (8, 3), (40, 5)):
+        big = normal(150, 400 + pad, DTYPES[dtype])
+        x = big[:, at:at + 300]
+        got = check(x)
+        again = tra.quantize(x.contiguous(), form="both")
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+                   for a, b in zip(got, again))
+
+
+def test_rows_past_32_bit_offsets():
+    big = torch.zeros(70000, 40000, device="cuda", dtype=torch.bfloat16)
+    x = big[:, 39000:39200]
+    x.copy_(normal(70000, 200, torch.bfloat16))
+    check(x)
+    del big, x
+    # values themselves past 2^32 bytes
+    M, K = 36000, 120000
+    x = torch.ones(M, K, device="cuda", dtype=torch.bfloat16)
+    x[-1, -1] = 3.0
+    values, scales, columns, column_scales = tra.quantize(x, form="both")
+    assert float(values[-1, K - 1].float()) * float(scales[-1, -1].float()) == 3.0
+    assert float(columns[K - 1, M - 1].float()) * float(column_scales[-1, -1].float()) == 3.0
+    del x, columns
+    assert (values[::1000, :K].float() * scales[::1000].float().repeat_interleave(128, 1)[:, :K]
+            .contiguous())[:-1].eq(1).all()
+
+
+def test_empty_sizes():
+    for M, K in ((0, 5), (5, 0), (0, 0)):
+        got = tra.quantize(torch.ones(M, K, device="cuda"), form="both")
+        assert got[0].shape == (M, up(K, 16) * 16) and got[2].shape == (K, up(M, 16) * 16)
+
+
+def test_what_the_values_stand_for():
+    # within half a step of x: 2^-4 of its size (e4m3fn; 2^-3 in e5m2) or of the type's
+    # least normal value, whichever is more
+    x = normal(300, 700, torch.float32)
+    for fp8, half, least in (("e4m3", 2.0 ** -4, 2.0 ** -6), ("e5m2", 2.0 ** -3, 2.0 ** -14)):
+        for scale in SCALES:
+            values, scales = tra.quantize(x, dtype=FP8[fp8], scale_dtype=SCALES[scale])
+            v = stands_for(values, scales)[:, :700]
+            s = scales.double().repeat_interleave(128, 1)[:, :700]
+            err = (v - x.double()).abs()
+            assert (err <= half * torch.maximum(x.double().abs(), least * s)).all()
+
+
+def test_poisoned_lds(monkeypatch):
+    import tiling_roofline_analysis_amd.scaled as scaled
+    poisoned = tra.load_poisoned()
+    monkeypatch.setattr(scaled, "load", lambda: poisoned)
+    for size in ((1, 300), (130, 257), (300, 129)):
+        for block_rows in (1, 128):
+            check(normal(*size, torch.bfloat16), block_rows=block_rows)
+            check(normal(*size, torch.float32), scale="f32", block_rows=block_rows)
+
+
+def test_streams_graphs_and_dropped_memory():
+    x = normal(300, 500, torch.bfloat16)
+    check(x, stream=torch.cuda.Stream())
+    want = [t.clone() for t in tra.quantize(x, form="both")]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = tra.quantize(x, form="both")
+    for i in range(3):
+        x.copy_(normal(300, 500, torch.bfloat16, i))
+        g.replay()
+        torch.cuda.synchronize()
+        again = tra.quantize(x, form="both")
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(out, again))
+    x.copy_(normal(300, 500, torch.bfloat16))
+    s, mine = torch.cuda.Stream(), x.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+    got = tra.quantize(mine, form="both", stream=s)
+    del mine
+    fill = torch.full_like(x, 7.0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+    del fill
+
+
+def test_refusals():
+    x = torch.ones(8, 32, device="cuda")
+    for error, call in [(TypeError, lambda: tra.quantize(x[0])),
+                        (TypeError, lambda: tra.quantize(x.double())),
+                        (TypeError, lambda: tra.quantize(x.cpu())),
+                        (ValueError, lambda: tra.quantize(x.t().contiguous().t())),
+                        (ValueError, lambda: tra.quantize(x[:1].expand(8, 32))),
+                        (ValueError, lambda: tra.quantize(x, block=(1, 64))),
+                        (ValueError, lambda: tra.quantize(x, dtype=torch.float16)),
+                        (ValueError, lambda: tra.quantize(x, scale_dtype=torch.bfloat16)),
+                        (ValueError, lambda: tra.quantize(x, form="rowwise"))]:
+        with pytest.raises(error):
+            call()

@@ -58,7 +58,8 @@ ABI_FUNCTIONS = ("gemm_f32", "gemm_f32_variant", "gemm_f32_variant_ws",
                  "tra_probe_launch", "tra_linear", "tra_linear_workspace_size",
                  "tra_linear_backward", "tra_linear_backward_workspace_size",
                  "tra_linear_describe", "tra_linear_backward_describe",
-                 "tra_norm", "tra_norm_backward", "tra_norm_backward_workspace_size")
+                 "tra_norm", "tra_norm_backward", "tra_norm_backward_workspace_size",
+                 "tra_quantize")
 
 # tra_probe
 PROBE_COPY = 0
@@ -148,7 +149,8 @@ def _open(path: str) -> ctypes.CDLL:
     lib.tra_probe_launch.restype = c_int
     # the argument structs go as packed bytes
     args, size = ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)
-    for name in ("tra_linear", "tra_linear_backward", "tra_norm", "tra_norm_backward"):
+    for name in ("tra_linear", "tra_linear_backward", "tra_norm", "tra_norm_backward",
+                 "tra_quantize"):
         getattr(lib, name).argtypes = [args, p]
         getattr(lib, name).restype = c_int
     for name in ("tra_linear_workspace_size", "tra_linear_backward_workspace_size",
@@ -304,6 +306,7 @@ def matmul(A, B, C=None, variant: int = AUTO, stream=None, workspace=None):
 _OPERATORS = {
     "fused": ("linear", "gated_linear", "linear_backward", "gated_linear_backward"),
     "norms": ("norm", "add_norm", "norm_backward", "add_norm_backward"),
+    "scaled": ("quantize",),
 }
 
 
