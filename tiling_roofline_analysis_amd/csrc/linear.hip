@@ -1,7 +1,7 @@
 // linear.hip -- the C-ABI entry points of the fused linear operators (declared
 // in include/tra_gemm.h): argument checks, choice of kernels, launches on the
-// caller's stream; and the small kernels around the products, which join a
-// split's partial sums and take the gradient of the epilogue.  Errors come back
+// caller's stream; and the small kernels around the products, which take the
+// gradient of the epilogue.  Errors come back
 // as status codes; nothing throws across the ABI and nothing is allocated: scratch
 // is the caller's workspace.
 #include "tra_gemm.h"
@@ -10,52 +10,14 @@
 #include <cstdio>
 #include <cstring>
 
-#include "linear_epilogue.h"
+#include "linear_join.h"
+#include "linear_plan.h"
 #include "operator_args.h"
 
 namespace tra {
 namespace {
 
-// ---- joining a split, gradients of the epilogue ----------------------------------------------
-
-// One chunk of columns of a split tile per lane: the partial sums in split order,
-// then the epilogue.
-template <typename T, bool GATED>
-__global__ __launch_bounds__(256) void linear_join(const TileArgs p, int bm, int bn, int blocks) {
-    constexpr int V = kChunk<T>;
-    const int cols = GATED ? bn / 2 : bn, per_row = cols / V;
-    const int at = static_cast<int>(blockIdx.x) / blocks;
-    const int item = (static_cast<int>(blockIdx.x) - at * blocks) * 256 + threadIdx.x;
-    const int row = item / per_row, col = (item - row * per_row) * V;
-    const int batch = blockIdx.y;
-    int tm, tn;
-    if (bm == 256)
-        grouped_tile32<kGroupWide>(p.whole + at, p.tiles_m, p.tiles_n, tm, tn);
-    else
-        grouped_tile32<kGroupTile>(p.whole + at, p.tiles_m, p.tiles_n, tm, tn);
-    const int64_t m = static_cast<int64_t>(tm) * bm + row, n = static_cast<int64_t>(tn) * cols + col;
-    if (row >= bm || m >= p.M || n >= p.N) return;
-    const int split_tiles = p.tiles_m * p.tiles_n - p.whole, area = bm * bn;
-    const float *in = p.partial +
-                      (static_cast<int64_t>(batch) * split_tiles + at) * p.splits * area +
-                      row * bn + col;
-    float z[V] = {}, u[V] = {};
-#pragma unroll 4
-    for (int s = 0; s < p.splits; ++s, in += area) {
-        float t[V];
-        load_row<float, V>(in, t);
-#pragma unroll
-        for (int e = 0; e < V; ++e) z[e] += t[e];
-        if constexpr (GATED) {
-            load_row<float, V>(in + cols, t);
-#pragma unroll
-            for (int e = 0; e < V; ++e) u[e] += t[e];
-        }
-    }
-    with_act(p.epi.act, [&](auto act) __attribute__((always_inline)) {
-        finish<T, GATED, decltype(act)::value, V>(p.epi, batch, m, n, z, u);
-    });
-}
+// ---- gradients of the epilogue ----------------------------------------------
 
 // Binary16 holds 40 binades, and dZ = dY u act' can lie outside them where the
 // gradients, its products with X and W, do not.  So it is stored times 2^12, which
@@ -205,20 +167,6 @@ __global__ __launch_bounds__(256) void linear_colsum_join(const float *colsum, i
 }
 
 template <typename T>
-hipError_t launch_join(const TilePlan &t, const TileArgs &a, hipStream_t stream) {
-    const int64_t rows = a.M < t.bm ? a.M : t.bm;
-    const int blocks =
-        static_cast<int>(ceil_div(rows * (t.gated ? t.bn / 2 : t.bn) / kChunk<T>, 256));
-    const dim3 grid(static_cast<unsigned>((a.tiles_m * a.tiles_n - a.whole) * blocks),
-                    static_cast<unsigned>(a.batch));
-    if (t.gated)
-        linear_join<T, true><<<grid, 256, 0, stream>>>(a, t.bm, t.bn, blocks);
-    else
-        linear_join<T, false><<<grid, 256, 0, stream>>>(a, t.bm, t.bn, blocks);
-    return hipGetLastError();
-}
-
-template <typename T>
 hipError_t launch_slope(bool gated, const SlopeArgs &a, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(ceil_div(a.N, 64 * kChunk<T>)),
                     static_cast<unsigned>(ceil_div(a.M, a.rows_per_chunk)));
@@ -279,25 +227,6 @@ int at_offset(int d, int64_t offset, int64_t bytes) {
     return d < 16 || offset * bytes % 16 == 0 ? d : bytes == 4 ? 4 : 0;
 }
 
-// How a kernel of one tile size goes, in microseconds, as measured on MI355X with
-// 1 to 12 workgroups a CU and 16 to 64 K tiles (a K tile is 128 bytes of a row).
-struct TileClass {
-    int bm, bn;
-    int resident;     // workgroups a CU holds
-    double alone;     // per K tile, one workgroup on a CU
-    double shared;    // per K tile and workgroup, CU full
-    double base;      // launch, first loads, epilogue without its stores
-};
-
-constexpr int64_t kCUs = 256;
-constexpr double kBytesPerUs = 4.8e6;     // memory, as a large copy reaches
-// What one workgroup's loads in flight can ask for, as fitted: of 8300 random forward
-// products (M to 2048; N, K from 128 to 12288; weights from memory), the 900 whose plan
-// it changes between 22 and 32 GB/s took, against the best of those plans, 4.8% longer
-// in the geometric mean at 22, 3.8 at 24, 3.3 at 26, 3.3 at 28, 3.6 at 30 and 4.1 at 32;
-// 150 more with M to 64, 5.8, 4.7, 4.3, 3.7, 3.3 and 3.6.
-constexpr double kBytesPerUsWg = 2.8e4;
-
 // [loads][16-bit, binary32]: direct, 16 bytes a lane; through registers; direct, 4
 // bytes a lane.  The 256 x 256 kernel is built for direct 16-bit loads only; 128 x 128
 // in binary32 with other than 16-byte loads needs more VGPRs than there are.
@@ -322,75 +251,21 @@ constexpr TileClass kClasses[3][2][4] = {
       {0, 0, 0, 0.0, 0.0, 0.0},
       {0, 0, 0, 0.0, 0.0, 0.0}}}};
 
-// The product's plan: the kernel, tile and split with the least predicted time.
-//   Tiles: a CU runs its share of the workgroups (tiles x splits), `resident` at a
-//   time; the K loop is bounded by the operands' bytes too; the results' stores
-//   add to it.  A split stores binary32 sums and adds a launch that reads them.
-//   Split are all tiles, where they are few, or those of the last, partial round
-//   over the CUs, whose K loops would leave most CUs idle.
+// The product's plan: the tile and split of plan_classes, or the kernel for few rows where
+// that is predicted to take less.
 //   Few rows: the weights' bytes at the rate that their strips can ask for (one
 //   strip, of 512 lanes, about 25 GB/s; 64-byte pieces of rows K apart reach about
 //   half of the memory's rate in 16 bits; unaligned 16-bit rows three quarters).
-// Kept pre-activations have no part in it, though their stores add to the time: a
-// forward pass that keeps them gives the same bits as one that does not (a
-// checkpoint's recomputation).  Of 3000 random forward calls 82 had another plan with
-// their stores counted.
 TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, int64_t K, int segs,
                    int batch, int direct) {
-    const int64_t b = elem_bytes(dtype), slice = 128 / b;
+    const int64_t b = elem_bytes(dtype);
     const bool f32 = dtype == TRA_DTYPE_F32;
-    const int64_t k_tiles = std::max<int64_t>(1, segs * ceil_div(K, slice));
     const double columns = static_cast<double>(N) * (gated ? 2 : 1);      // of z and u
-    const double in = static_cast<double>(batch) * segs * K * (static_cast<double>(M) + columns) * b;
-    TilePlan best{};
+    const PlanSizes z{M, N, K, segs, batch, gated, b, (gated ? 0.5 : 1.0) * b,
+                      form == tra::kFormKN && !f32, direct == 16};
     double best_us = 0.0;
-    for (const TileClass &c : kClasses[direct == 16 ? 0 : direct == 4 ? 2 : 1][f32 ? 1 : 0]) {
-        if (c.bm == 0) break;
-        const int64_t tiles = std::max<int64_t>(
-            1, ceil_div(M, c.bm) * ceil_div(N, gated ? c.bn / 2 : c.bn));     // of a batch
-        // 64-byte lines (16-bit weights, 64 x 64 tiles, not k-contiguous)
-        const double most = kBytesPerUs * (form == tra::kFormKN && !f32 && c.bn == 64 ? 0.7 : 1.0);
-        const double area = std::min<double>(M, c.bm) * std::min<double>(columns, c.bn);
-        const double out = (gated ? 0.5 : 1.0) * b;     // bytes stored per column of z or u
-        // K loops of n workgroups of `per` K tiles; a little to begin another round
-        auto loops = [&](int64_t n, int64_t per) {
-            const int64_t wave = kCUs * c.resident;
-            const int64_t full = n / wave, rest = ceil_div(n % wave, kCUs);
-            return per * (full * std::max(c.alone, c.resident * c.shared) +
-                          (rest > 0 ? std::max(c.alone, rest * c.shared) : 0.0)) +
-                   (c.resident == 1 ? 3.0 : 1.5) *
-                       std::max<int64_t>(0, full + (rest > 0 ? 1 : 0) - 1);
-        };
-        auto consider = [&](int64_t whole, int64_t want) {
-            const int64_t per = ceil_div(k_tiles, want), splits = ceil_div(k_tiles, per);
-            if (splits != want || want > k_tiles) return;
-            const int64_t parts = batch * (tiles - whole) * splits, n = batch * whole + parts;
-            double loop = (whole > 0 ? loops(batch * whole, k_tiles) : 0.0) +
-                          (parts > 0 ? loops(parts, per) : 0.0);
-            loop = std::max(loop, in / std::min(most, n * kBytesPerUsWg));
-            const double sums = splits > 1 ? parts * area * 4.0 : 0.0;
-            const double stored = sums + batch * (splits > 1 ? whole : tiles) * area * out;
-            double us = c.base + loop + stored / kBytesPerUs;
-            if (splits > 1) us += 2.5 + 0.12 * splits + sums / kBytesPerUs;
-            if (best_us == 0.0 || us < best_us) {
-                best_us = us;
-                best.bm = c.bm;
-                best.bn = c.bn;
-                best.whole = static_cast<int>(splits > 1 ? whole : tiles);
-                best.splits = static_cast<int>(splits);
-                best.deep = direct == 16 && n <= kCUs;
-                best.partial_bytes =
-                    splits > 1 ? static_cast<size_t>(parts) * c.bm * c.bn * sizeof(float) : 0;
-            }
-        };
-        // none split; all split; those past the last whole round over the CUs split
-        consider(tiles, 1);
-        for (int64_t want = 2; want <= 32 && tiles * batch * want <= 1024; ++want)
-            consider(0, want);
-        const int64_t rounds = tiles * batch / kCUs * kCUs / batch;
-        if (rounds > 0 && rounds < tiles && kCUs % batch == 0)
-            for (int64_t want = 2; want <= 16; ++want) consider(rounds, want);
-    }
+    TilePlan best = plan_classes(kClasses[direct == 16 ? 0 : direct == 4 ? 2 : 1][f32 ? 1 : 0], 4,
+                                 z, best_us);
     const int64_t strip = form == tra::kFormKK ? 16 : 64 / b;
     if (form != tra::kFormNN && M <= 16 && K >= 16 / b && N >= 4 / b) {
         const double strips = static_cast<double>(ceil_div(N, strip));
@@ -414,26 +289,8 @@ TilePlan plan_tile(TileForm form, bool gated, int dtype, int64_t M, int64_t N, i
     return best;
 }
 
-// Fills in what follows from the plan and checks the launch's size.
 tra_status finish_args(const TilePlan &t, int dtype, TileArgs &a, float *partial) {
-    const int64_t slice = 128 / elem_bytes(dtype);
-    const int64_t tm = ceil_div(a.M, t.bm), tn = ceil_div(a.N, t.gated ? t.bn / 2 : t.bn);
-    // kMaxGridLanes work-items (512 a workgroup), and tile indices in 32 bits
-    const __int128 tiles = static_cast<__int128>(tm) * tn;
-    const __int128 whole = t.splits > 1 ? static_cast<__int128>(t.whole) : tiles;
-    if ((whole + (tiles - whole) * t.splits) * 512 > tra::kMaxGridLanes)
-        return TRA_ERR_UNSUPPORTED;
-    a.tiles_m = static_cast<int>(tm);
-    a.tiles_n = static_cast<int>(tn);
-    a.seg_tiles = static_cast<int>(ceil_div(a.K, slice));
-    a.k_tiles = a.segs * a.seg_tiles;
-    a.whole = t.splits > 1 ? t.whole : a.tiles_m * a.tiles_n;
-    a.splits = t.splits;
-    a.tiles_per_split = static_cast<int>(ceil_div(std::max(a.k_tiles, 1), t.splits));
-    a.partial = t.splits > 1 ? partial : nullptr;
-    a.epi.M = a.M;
-    a.epi.N = a.N;
-    return TRA_OK;
+    return finish_tile_args(t, 128 / elem_bytes(dtype), a, partial);
 }
 
 hipError_t run_tile(int dtype, const TilePlan &t, const TileArgs &a, hipStream_t s) {
