@@ -422,6 +422,58 @@ typedef struct tra_quantize_args {
 TRA_API tra_status tra_quantize(const tra_quantize_args *args, void *stream);
 
 /*
+ * tra_scaled_linear: Y = X W^T + bias + R on 8-bit matrices with block scales.
+ *
+ * W is N x K, blocks along K: values (w_fp8) with scales SW of w_block_rows 1 or 128;
+ * scale of row n, block k / 128 at SW[(n / w_block_rows) * sw_row + (k / 128) * sw_block].
+ * X is M x K: with x_dtype TRA_X_SCALED values (x_fp8) with scales SX (one per row and
+ * block) at SX[m * sx_row + (k / 128) * sx_block]; else elements of x_dtype (ldx
+ * between rows), which the call quantizes itself as tra_quantize does, to x_fp8 with
+ * scales of the same type as SW's.  Both scales are of type `scale`; one of a scale's
+ * two strides is 1.  Y, R (M x N) and bias (N elements, or NULL) are of `dtype`.
+ *
+ * Rows of values have (K + 15) / 16 * 16 columns, those past K zero, and start 16-byte
+ * aligned; their leading dimensions are multiples of 16 below 2^22.  With binary32 scales
+ * w_block_rows is 128; x_fp8 and w_fp8 are not both e5m2, and w_fp8 e5m2 has e8m0 scales
+ * and X of TRA_X_SCALED.
+ *
+ * Numerics: products and sums are binary32.  e8m0 scales are applied by the matrix
+ * units, exactly; with binary32 scales a block's sum is multiplied by the product of
+ * its two scales (two roundings).  Each element is rounded once, when it is stored.  The
+ * order of the sums follows from the sizes and types, so a call gives the same bits every
+ * time.
+ *
+ * Workspace, sizes, overlap, padding and errors as in tra_linear; a scale's row stride
+ * is less than 2^22 bytes.
+ */
+#define TRA_X_SCALED (-1)
+
+typedef struct tra_scaled_args {
+    int32_t dtype, x_dtype, x_fp8, w_fp8, scale, w_block_rows;
+    int64_t M, N, K;
+    const void *X;
+    int64_t ldx;
+    const void *SX;            /* TRA_X_SCALED only */
+    int64_t sx_row, sx_block;
+    const void *W;
+    int64_t ldw;
+    const void *SW;
+    int64_t sw_row, sw_block;
+    const void *bias;
+    const void *R;             /* or NULL; Y may be R itself */
+    int64_t ldr;
+    void *Y;
+    int64_t ldy;
+    void *workspace;
+    uint64_t workspace_bytes;
+} tra_scaled_args;
+
+TRA_API tra_status tra_scaled_linear(const tra_scaled_args *args, void *stream);
+TRA_API tra_status tra_scaled_linear_workspace_size(const tra_scaled_args *args, size_t *bytes);
+/* Writes what the call would launch into buf as "key=value ..." text; launches nothing. */
+TRA_API tra_status tra_scaled_linear_describe(const tra_scaled_args *args, char *buf, size_t len);
+
+/*
  * Norms around a block, with its gate and the residual stream's scale:
  *
  *   R = scale X + gate * N_post(H)       (element by element; R = X without H)

@@ -63,3 +63,27 @@ def stands_for(values, scales, block_rows=None):
         block_rows = 1 if s.shape[0] == M else 128
     s = s.repeat_interleave(block_rows, 0)[:M].repeat_interleave(128, 1)[:, :K]
     return values.double() * s
+
+
+class Operand:
+    """What values with scales stand for (v), and for each 8 neighbours of a row the largest
+    magnitude that their matrix instruction may take one to have (g): a subnormal value
+    counts as the least normal one."""
+
+    def __init__(self, values, scales, block_rows=None, fp8=None):
+        fp8 = fp8 or {t: n for n, t in FP8.items()}[values.dtype]
+        self.v = stands_for(values, scales, block_rows)
+        least = 2.0 ** -6 if fp8 == "e4m3" else 2.0 ** -14
+        size = stands_for(values.double().abs().clamp(min=least), scales, block_rows)
+        self.g = size.nan_to_num(0.0).view(size.shape[0], -1, 8).amax(2)
+
+
+def product_bound(x, w, dtype):
+    """x w^T in 64 bits and how far the kernels' sums may be off: K roundings or truncations
+    of binary32, and with 16-bit results, 8 neighbouring products at a time, each cut off
+    13 binary places below the largest one's exponent: 8 x 2^-13 of it."""
+    z = x.v @ w.v.t()
+    err = (x.v.shape[1] + 4) * 2.0 ** -23 * (x.v.abs() @ w.v.abs().t())
+    if dtype != torch.float32:
+        err = err + 8 * 2.0 ** -13 * (x.g @ w.g.t())
+    return z, err

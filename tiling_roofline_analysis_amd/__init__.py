@@ -16,7 +16,8 @@ Low-level calls take raw device addresses (ints) and a hipStream_t handle:
 
 ``linear`` and ``gated_linear`` (see ``fused``) are the GEMM with bias,
 activation, residual or gate fused in, with gradients; ``norm`` and ``add_norm`` (see
-``norms``) are the norms around a block.  They take torch tensors and load with torch on
+``norms``) are the norms around a block; ``quantize`` and ``scaled_linear`` (see
+``scaled``) work on 8-bit matrices with block scales.  They take torch tensors and load with torch on
 first use.
 
 ``matmul(A, B, C=None, variant=AUTO)`` is the torch-tensor convenience
@@ -59,7 +60,8 @@ ABI_FUNCTIONS = ("gemm_f32", "gemm_f32_variant", "gemm_f32_variant_ws",
                  "tra_linear_backward", "tra_linear_backward_workspace_size",
                  "tra_linear_describe", "tra_linear_backward_describe",
                  "tra_norm", "tra_norm_backward", "tra_norm_backward_workspace_size",
-                 "tra_quantize")
+                 "tra_quantize", "tra_scaled_linear", "tra_scaled_linear_workspace_size",
+                 "tra_scaled_linear_describe")
 
 # tra_probe
 PROBE_COPY = 0
@@ -150,14 +152,16 @@ def _open(path: str) -> ctypes.CDLL:
     # the argument structs go as packed bytes
     args, size = ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)
     for name in ("tra_linear", "tra_linear_backward", "tra_norm", "tra_norm_backward",
-                 "tra_quantize"):
+                 "tra_quantize", "tra_scaled_linear", "tra_scaled_linear_workspace_size",
+                 "tra_scaled_linear_describe"):
         getattr(lib, name).argtypes = [args, p]
         getattr(lib, name).restype = c_int
     for name in ("tra_linear_workspace_size", "tra_linear_backward_workspace_size",
-                 "tra_norm_backward_workspace_size"):
+                 "tra_norm_backward_workspace_size", "tra_scaled_linear_workspace_size"):
         getattr(lib, name).argtypes = [args, size]
         getattr(lib, name).restype = c_int
-    for name in ("tra_linear_describe", "tra_linear_backward_describe"):
+    for name in ("tra_linear_describe", "tra_linear_backward_describe",
+                 "tra_scaled_linear_describe"):
         getattr(lib, name).argtypes = [args, ctypes.c_char_p, ctypes.c_size_t]
         getattr(lib, name).restype = c_int
     return lib
@@ -306,7 +310,7 @@ def matmul(A, B, C=None, variant: int = AUTO, stream=None, workspace=None):
 _OPERATORS = {
     "fused": ("linear", "gated_linear", "linear_backward", "gated_linear_backward"),
     "norms": ("norm", "add_norm", "norm_backward", "add_norm_backward"),
-    "scaled": ("quantize",),
+    "scaled": ("quantize", "scaled_linear", "scaled_linear_backward"),
 }
 
 

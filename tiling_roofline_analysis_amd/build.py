@@ -25,7 +25,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["tra_gemm.hip", "gemm_naive.hip", "gemm_lds_tiled.hip", "gemm_regblock.hip",
            "gemm_mfma.hip", "probes.hip", "linear.hip", "linear_bf16.hip", "linear_f16.hip", "linear_f32.hip",
-           "norm.hip", "quantize.hip"]
+           "norm.hip", "quantize.hip", "scaled.hip", "scaled_bf16.hip", "scaled_f16.hip",
+           "scaled_f32.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

@@ -1,0 +1,409 @@
+// scaled_kernels.h -- products of 8-bit matrices with block scales, results of type T.
+// Included once by each scaled_<type>.hip.
+//
+// Bytes move as in linear_kernels.h: both operands k-contiguous, a K tile of 128 bytes a
+// row straight into LDS, the same panels, waits, epilogue and split.  A K tile is one
+// block of 128 elements, of which lane l holds row l % 16 and 32 elements of each operand:
+// chunks l / 16 and 4 + l / 16 of its row.  (Which 32 does not matter, as long as both
+// operands have the same: a block's sum is over all of them, and all share one scale.)
+//
+// 16-bit results: a block is one v_mfma_f32_16x16x128_f8f6f4.  The 8-bit matrix
+// instructions of gfx950, this one and those of the generation before alike, add 8
+// neighbouring products as integers, cut off 13 binary places below the largest one's
+// exponent (measured: 2^16 + 2^3 is kept, 2^16 + 2^2 is not; between the groups of 8, and
+// to the sum so far, they add in binary32).  That costs a sum of normal values 1e-5 of
+// itself, against 2e-3 and 2e-4 by which its rounding to bfloat16 and binary16 is off in
+// the mean.
+// binary32 results: there it would be most of the error, so the operands are converted to
+// bfloat16, exactly, and multiplied by v_mfma_f32_16x16x32_bf16, four a block, at half the
+// rate.
+//
+// The scales come as part of the K tile: one word for each row of both panels, in one
+// direct load a wave.
+//   e8m0   16-bit results: the matrix unit multiplies by both scales; a lane passes its
+//          row's byte
+//   else   the block's sums start from zero and are added by v_fma_f32, times the product
+//          of the two scales: 4 instructions an MFMA, which run beside other MFMAs
+#pragma once
+
+#include "linear_kernels.h"
+#include "scaled_plan.h"
+
+namespace tra {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// The two operands' formats (ScaledFormats) for the instruction: 0 e4m3fn, 1 e5m2.
+template <int FORMATS>
+constexpr int kFormatX = FORMATS == kX5 ? 1 : 0;
+template <int FORMATS>
+constexpr int kFormatW = FORMATS == kW5 ? 1 : 0;
+
+// c + w x^T over a block, times the scales whose bytes are in sw and sx.
+template <int FORMATS>
+__device__ __forceinline__ f32x4 mma_scaled(i32x8 w, i32x8 x, f32x4 c, uint32_t sw, uint32_t sx) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        w, x, c, kFormatW<FORMATS>, kFormatX<FORMATS>, 0, static_cast<int>(sw), 0,
+        static_cast<int>(sx));
+}
+
+// w x^T over a block.  (Scales of zero, as constants, stand for the instruction without
+// scales.)
+template <int FORMATS>
+__device__ __forceinline__ f32x4 mma_plain(i32x8 w, i32x8 x) {
+    const f32x4 zero = {};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        w, x, zero, kFormatW<FORMATS>, kFormatX<FORMATS>, 0, 0, 0, 0);
+}
+
+// Words 2 q and 2 q + 1 of a fragment, 8 elements, in bfloat16.
+template <int FORMAT>
+__device__ __forceinline__ bf16x8 widen(const i32x8 &v, int q) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t a = static_cast<uint32_t>(v[2 * q]), b = static_cast<uint32_t>(v[2 * q + 1]);
+    bf16x2 t[4];
+    if constexpr (FORMAT == 0) {
+        t[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+        t[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+        t[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+        t[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+    } else {
+        t[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(a, 1.0f, false);
+        t[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(a, 1.0f, true);
+        t[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(b, 1.0f, false);
+        t[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(b, 1.0f, true);
+    }
+    return __builtin_shufflevector(__builtin_shufflevector(t[0], t[1], 0, 1, 2, 3),
+                                   __builtin_shufflevector(t[2], t[3], 0, 1, 2, 3), 0, 1, 2, 3, 4,
+                                   5, 6, 7);
+}
+
+// A scale's word as a binary32 number.
+template <int SCALE>
+__device__ __forceinline__ float scale_value(uint32_t word) {
+    // 0 and 255 stand for 2^-127, a subnormal, and NaN
+    if constexpr (SCALE == TRA_SCALE_E8M0)
+        word = word << 23 | (word == 0 || word == 255 ? 0x400000u : 0u);
+    return __uint_as_float(word);
+}
+
+using Bytes = uint8_t;
+
+// Rows row0 .. + 15 of a panel: chunks l / 16 and 4 + l / 16 of each.
+template <typename P>
+__device__ __forceinline__ i32x8 fragment8(const char *st, int panel, int row0) {
+    const u32x4 a = P::fragment(st, panel, row0, 0), b = P::fragment(st, panel, row0, 1);
+    return __builtin_bit_cast(
+        i32x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Scales of a K tile in LDS: a word for each of WAVES * 64 rows, BM of X's and then BN of
+// W's (and none for the rest).  A wave loads 64 of them, of one operand.
+template <int SCALE, int BM, int BN, int WAVES>
+struct ScalePanel {
+    static constexpr int BYTES = WAVES * 256;
+    static constexpr int SIZE = SCALE == TRA_SCALE_E8M0 ? 1 : 4;
+    static_assert(BM % 64 == 0 && BN % 64 == 0 && BM + BN <= WAVES * 64, "a wave has one operand");
+
+    const char *at;        // the tile's first row's scale, of the K tile to load
+    int64_t step;          // bytes from a K tile's to the next's
+    uint32_t offset;       // this lane's row's
+
+    __device__ __forceinline__ ScalePanel(const ScaledArgs &p, int wave, int64_t m0, int64_t n0,
+                                          int first) {
+        const int r = wave * 64 + static_cast<int>(threadIdx.x & 63);
+        constexpr uint32_t OUTSIDE = Panel<Bytes, true, 64, 4>::OUTSIDE;
+        if (wave * 64 < BM) {
+            at = static_cast<const char *>(p.SX) + m0 * p.sx_row * SIZE;
+            step = p.sx_block * SIZE;
+            offset = m0 + r < p.t.M ? static_cast<uint32_t>(r * p.sx_row * SIZE) : OUTSIDE;
+        } else {
+            const int64_t n = n0 + (r - BM), block = n0 >> p.w_shift;
+            at = static_cast<const char *>(p.SW) + block * p.sw_row * SIZE;
+            step = p.sw_block * SIZE;
+            offset = r - BM < BN && n < p.t.N
+                         ? static_cast<uint32_t>(((n >> p.w_shift) - block) * p.sw_row * SIZE)
+                         : OUTSIDE;
+        }
+        at += first * step;
+    }
+
+    // rem: elements of K left, as in Panel::load_direct; one load, whatever it is
+    __device__ __forceinline__ void load(int wave, int rem, char *lds) {
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc((void *)at, (short)0, rem > 0 ? 0x7fffffff : 0,
+                                              0x00020000);
+        // (a byte arrives as a word too)
+        if constexpr (SIZE == 1)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, lds + wave * 256, 1, offset, 0, 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, lds + wave * 256, 4, offset, 0, 0, 0);
+        at += step;
+    }
+
+    // The scales of rows row0 .. + 15 (of W's: from BM on), one a lane.
+    static __device__ __forceinline__ uint32_t of_rows(const char *st, int panel, int row0) {
+        return *reinterpret_cast<const uint32_t *>(
+            st + panel + (row0 + static_cast<int>(threadIdx.x & 15)) * 4);
+    }
+
+    // One row's, in every lane.
+    static __device__ __forceinline__ uint32_t of_row(const char *st, int panel, int row) {
+        return *reinterpret_cast<const uint32_t *>(st + panel + row * 4);
+    }
+
+    // The scales of the four rows whose sums a lane gets.
+    static __device__ __forceinline__ u32x4 of_sums(const char *st, int panel, int row0) {
+        return *reinterpret_cast<const u32x4 *>(
+            st + panel + (row0 + static_cast<int>(threadIdx.x >> 4 & 3) * 4) * 4);
+    }
+};
+
+// ---- the tile kernel ---------------------------------------------------------------------
+//
+// linear_tile for one-byte elements: BM x BN of Y per workgroup of four waves in 2 x 2.
+// A K tile is one MFMA step, computed in two halves, the columns of half 0 and of half
+// 1; iteration s:
+//   read half 1's fragments of tile s; compute half 0;
+//   wait for this wave's loads of tile s + 1, meet the other waves;
+//   load tile s + S into the stage of tile s;
+//   read X's and half 0's fragments of tile s + 1; compute half 1.
+template <int BM, int BN, int SCALE>
+struct ScaledShape {
+    static constexpr int WAVES = 4, TI = BM / 32, TJ = BN / 64, HC = BN / 4;
+    using PA = Panel<Bytes, true, BM, WAVES>;
+    using PB = Panel<Bytes, true, BN / 2, WAVES>;
+    using PS = ScalePanel<SCALE, BM, BN, WAVES>;
+    static constexpr int SCALES = PA::BYTES + 2 * PB::BYTES;     // where they begin
+    static constexpr int STAGE = SCALES + PS::BYTES;
+    static constexpr int MINE = BM / 2 * HC * 8;
+    static constexpr int per_cu(int stages) { return stages * STAGE <= 80 * 1024 ? 2 : 1; }
+};
+
+template <typename T, int FORMATS, int SCALE, int BM, int BN, int S>
+__global__ __launch_bounds__(256, (ScaledShape<BM, BN, SCALE>::per_cu(S))) void scaled_tile(
+    const ScaledArgs p) {
+    using X = ScaledShape<BM, BN, SCALE>;
+    using PA = typename X::PA;
+    using PB = typename X::PB;
+    using PS = typename X::PS;
+    constexpr int TI = X::TI, TJ = X::TJ, HC = X::HC;
+    constexpr bool WIDEN = std::is_same_v<T, float>;
+    constexpr bool UNIT = SCALE == TRA_SCALE_E8M0 && !WIDEN;    // the matrix unit scales
+    constexpr bool EACH = SCALE == TRA_SCALE_E8M0 && WIDEN;     // a scale for each row of W
+    static_assert(S == 2 || S == 4 || S == 6, "whole pairs of stages");
+    static_assert(X::STAGE >= 2 * X::MINE, "LDS");
+    __shared__ __align__(1024) char st0[X::STAGE], st1[X::STAGE];
+    __shared__ __align__(1024) char st2[S > 2 ? X::STAGE : 16], st3[S > 2 ? X::STAGE : 16];
+    __shared__ __align__(1024) char st4[S > 4 ? X::STAGE : 16], st5[S > 4 ? X::STAGE : 16];
+    auto stage = [&](auto u) __attribute__((always_inline))->char * {
+        constexpr int U = decltype(u)::value % S;
+        if constexpr (U == 0) return st0;
+        if constexpr (U == 1) return st1;
+        if constexpr (U == 2) return st2;
+        if constexpr (U == 3) return st3;
+        if constexpr (U == 4) return st4;
+        return st5;
+    };
+    for_each(std::make_integer_sequence<int, S>{}, [&](auto u) __attribute__((always_inline)) {
+        lds_poison(reinterpret_cast<float *>(stage(u)), X::STAGE / 4);
+        return true;
+    });
+
+    const TileArgs &a = p.t;
+    const Part part(a, 0, BM * BN);
+    int tm, tn;
+    grouped_tile32<kGroupTile>(part.tile, a.tiles_m, a.tiles_n, tm, tn);
+    const int64_t m0 = static_cast<int64_t>(tm) * BM;
+    const int64_t n0 = static_cast<int64_t>(tn) * BN, n1 = n0 + BN / 2;
+    const int first = part.first, count = part.count;
+    Walk<Bytes, true, true> walk(a, 0, m0, n0, n1, false, first, count);
+
+    const int wave = wave_id();
+    const int wm = wave >> 1, wn = wave & 1;
+    PS scales(p, wave, m0, n0, first);
+    // MFMAs that add to the same registers are too near each other in small tiles: two sets
+    // of sums there, for odd and even K tiles, added at the end
+    constexpr int SETS = UNIT && 2 * TI * TJ < 16 ? 2 : 1;
+    f32x4 c[SETS][2][TI][TJ] = {};
+
+    i32x8 x[2][TI], w[2][TJ];          // X's of odd and even tiles; W's of the halves
+    uint32_t sx[2][TI], sw[2][TJ];
+    u32x4 sws[2][TJ];
+    auto read_x = [&](auto parity, const char *st) __attribute__((always_inline)) {
+        constexpr int P = decltype(parity)::value;
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+            x[P][i] = fragment8<PA>(st, 0, wm * (BM / 2) + i * 16);
+            sx[P][i] = PS::of_rows(st, X::SCALES, wm * (BM / 2) + i * 16);
+        }
+    };
+    auto read_w = [&](auto half, const char *st) __attribute__((always_inline)) {
+        constexpr int H = decltype(half)::value;
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+            const int row = wn * HC + j * 16;
+            w[H][j] = fragment8<PB>(st, PA::BYTES + H * PB::BYTES, row);
+            // (binary32 scales: 128 rows of W share one)
+            if constexpr (EACH)
+                sws[H][j] = PS::of_sums(st, X::SCALES, BM + H * (BN / 2) + row);
+            else if constexpr (UNIT)
+                sw[H][j] = PS::of_rows(st, X::SCALES, BM + H * (BN / 2) + row);
+            else if (j == 0)
+                sw[H][j] = PS::of_row(st, X::SCALES, BM + H * (BN / 2));
+        }
+    };
+    auto compute = [&](auto half, auto parity) __attribute__((always_inline)) {
+        constexpr int H = decltype(half)::value, P = decltype(parity)::value;
+        f32x4 t[TI][TJ] = {};
+        if constexpr (WIDEN) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                bf16x8 wide[TJ];
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) wide[j] = widen<kFormatW<FORMATS>>(w[H][j], q);
+#pragma unroll
+                for (int i = 0; i < TI; ++i) {
+                    const bf16x8 v = widen<kFormatX<FORMATS>>(x[P][i], q);
+#pragma unroll
+                    for (int j = 0; j < TJ; ++j)
+                        t[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide[j], v, t[i][j], 0, 0,
+                                                                          0);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+            const float s = UNIT ? 0.0f : scale_value<SCALE>(sx[P][i]);
+            const float both = UNIT || EACH ? 0.0f : s * scale_value<SCALE>(sw[H][0]);
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) {
+                f32x4 &d = c[P % SETS][H][i][j];
+                if constexpr (UNIT) {
+                    d = mma_scaled<FORMATS>(w[H][j], x[P][i], d, sw[H][j], sx[P][i]);
+                } else {
+                    if constexpr (!WIDEN) t[i][j] = mma_plain<FORMATS>(w[H][j], x[P][i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        d[e] = fmaf(t[i][j][e],
+                                    EACH ? s * scale_value<SCALE>(sws[H][j][e]) : both, d[e]);
+                }
+            }
+        }
+    };
+    constexpr int MFMAS = TI * TJ * (WIDEN ? 4 : 1);
+    constexpr int READS_W = TJ * 2 + (UNIT || EACH ? TJ : 1), READS_X = TI * 3;
+    constexpr std::integral_constant<int, 0> zero;
+    constexpr std::integral_constant<int, 1> one;
+
+    constexpr int IA = PA::template DINS<16>, IB = PB::template DINS<16>;
+    constexpr int LOADS = IA + 2 * IB + 1;
+    uint32_t oa[IA], ob0[IB], ob1[IB];
+#pragma unroll
+    for (int i = 0; i < IA; ++i) oa[i] = PA::template offset<16>(wave, i, a.M - m0, a.lda);
+#pragma unroll
+    for (int i = 0; i < IB; ++i) {
+        ob0[i] = PB::template offset<16>(wave, i, a.N - n0, a.ldb);
+        ob1[i] = PB::template offset<16>(wave, i, a.N - n1, a.ldb);
+    }
+    const int pitch_a = static_cast<int>(a.lda), pitch_b = static_cast<int>(a.ldb);
+    auto issue = [&](char *st) __attribute__((always_inline)) {
+        PA::template load_direct<16>(wave, walk.a, pitch_a, oa, walk.rem, st);
+        PB::template load_direct<16>(wave, walk.b0, pitch_b, ob0, walk.rem, st + PA::BYTES);
+        PB::template load_direct<16>(wave, walk.b1, pitch_b, ob1, walk.rem,
+                                     st + PA::BYTES + PB::BYTES);
+        scales.load(wave, walk.rem, st + X::SCALES);
+        walk.next();
+    };
+    for_each(std::make_integer_sequence<int, S>{}, [&](auto u) __attribute__((always_inline)) {
+        issue(stage(u));
+        __builtin_amdgcn_sched_barrier(0);
+        return true;
+    });
+    stage_sync<(S - 1) * LOADS>();
+    read_x(zero, st0);
+    read_w(zero, st0);
+    auto iteration = [&](auto u) __attribute__((always_inline)) {
+        constexpr int U = decltype(u)::value;
+        constexpr std::integral_constant<int, U % 2> now;
+        constexpr std::integral_constant<int, (U + 1) % 2> next;
+        read_w(one, stage(u));
+        compute(zero, now);
+        interleave<MFMAS, READS_W, 0>();
+        stage_sync<(S - 2) * LOADS>();
+        issue(stage(u));
+        read_x(next, stage(std::integral_constant<int, U + 1>{}));
+        read_w(zero, stage(std::integral_constant<int, U + 1>{}));
+        compute(one, now);
+        interleave<MFMAS, READS_X + READS_W, LOADS>();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    int s = 0;
+    for (; s + S <= count; s += S)
+        for_each(std::make_integer_sequence<int, S>{}, [&](auto u) __attribute__((always_inline)) {
+            iteration(u);
+            return true;
+        });
+    for_each(std::make_integer_sequence<int, S - 1>{}, [&](auto u) __attribute__((always_inline)) {
+        if (s + decltype(u)::value >= count) return false;
+        iteration(u);
+        return true;
+    });
+
+    // Every wave has read its last fragments, and no load is in flight, before
+    // the stages are reused.
+    stage_sync<0>();
+    char *mine = (wave < 2 ? st0 : st1) + (wave & 1) * X::MINE;
+#pragma unroll
+    for (int k = 1; k < SETS; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) c[0][h][i][j] += c[k][h][i][j];
+    epi_put<HC>(mine, c[0][0], 0);
+    epi_put<HC>(mine, c[0][1], 1);
+    wave_sync();
+    epi_rows<T, false, HC, BM / 2>(
+        a, 0, part.sums == nullptr ? nullptr : part.sums + wm * (BM / 2) * BN + wn * HC, BN, mine,
+        m0 + wm * (BM / 2), n0 + wn * HC, n1 + wn * HC);
+}
+
+// ---- launches ----------------------------------------------------------------------------------
+
+template <typename T, int FORMATS, int SCALE>
+hipError_t launch_scaled(const TilePlan &plan, const ScaledArgs &p, hipStream_t stream) {
+    const TileArgs &a = p.t;
+    const unsigned tiles = static_cast<unsigned>(a.tiles_m) * static_cast<unsigned>(a.tiles_n);
+    const unsigned whole = static_cast<unsigned>(a.whole);
+    const dim3 grid(whole + (tiles - whole) * static_cast<unsigned>(a.splits));
+#define TRA_TILE(BM, BN, S) scaled_tile<T, FORMATS, SCALE, BM, BN, S><<<grid, 256, 0, stream>>>(p)
+    // (two of 128 x 128 with converted operands would need more VGPRs than a CU has)
+    constexpr int SHALLOW = std::is_same_v<T, float> ? 4 : 2;
+    if (plan.bm == 128) plan.deep ? TRA_TILE(128, 128, 4) : TRA_TILE(128, 128, SHALLOW);
+    else if (plan.bn == 128) plan.deep ? TRA_TILE(64, 128, 4) : TRA_TILE(64, 128, 2);
+    else plan.deep ? TRA_TILE(64, 64, 6) : TRA_TILE(64, 64, 4);
+#undef TRA_TILE
+    return hipGetLastError();
+}
+
+}  // namespace
+
+template <typename T>
+hipError_t ScaledKernels<T>::product(const ScaledPlan &plan, const ScaledArgs &p,
+                                     hipStream_t stream) {
+    const TilePlan &t = plan.tile;
+    if (plan.scale == TRA_SCALE_E8M0) {
+        switch (plan.formats) {
+            case kX4W4: return launch_scaled<T, kX4W4, TRA_SCALE_E8M0>(t, p, stream);
+            case kX5: return launch_scaled<T, kX5, TRA_SCALE_E8M0>(t, p, stream);
+            default: return launch_scaled<T, kW5, TRA_SCALE_E8M0>(t, p, stream);
+        }
+    }
+    return plan.formats == kX5 ? launch_scaled<T, kX5, TRA_SCALE_F32>(t, p, stream)
+                               : launch_scaled<T, kX4W4, TRA_SCALE_F32>(t, p, stream);
+}
+
+}  // namespace tra

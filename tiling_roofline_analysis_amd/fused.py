@@ -123,17 +123,17 @@ def _vector(b, name, x, N):
 _seen: dict = {}
 
 
-def _call(name, fmt, fields, device):
+def _call(name, fmt, fields, device, count=7):
     """Takes a workspace from torch's allocator, packs the arguments and makes
-    the call."""
+    the call.  Of the fields, the first `count` are types, layout and sizes."""
     index = device.index
     if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
-            return _call(name, fmt, fields, device)
+            return _call(name, fmt, fields, device, count)
     lib = load()
     stream = torch._C._cuda_getCurrentRawStream(index)
     call = getattr(lib, name)
-    key = (name, fields[:7])
+    key = (name, fields[:count])
     need = _seen.get(key, 0)
     # torch's blocks are 512-byte aligned, and 256 are wanted
     ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None

@@ -1,20 +1,36 @@
 """Matrices in 8-bit floating point with a scale for each block of 128, on torch tensors:
-``quantize`` and products of what it makes.
+``quantize`` makes them and ``scaled_linear`` multiplies them.
+
+    scaled_linear(x, w, x_scales, w_scales, bias, residual)      x w + bias + residual
 
 A block is 128 consecutive elements along the axis that a product sums over, of one row
 (activations, gradients) or of 128 rows (weights).  Its scale is float32 or, as the
 matrix units of MI355X take it, float8_e8m0fnu, a power of two.  A matrix is a pair of
 plain tensors: values (float8_e4m3fn or float8_e5m2, rows x columns filled up with zeros to
 a multiple of 16) and scales (rows, or rows / 128 rounded up, x columns / 128 rounded up).
+
+Serving: w is the transposed view of the values of an N x K weight that was quantized once,
+w_scales that of its scales; x is a tensor, quantized in the call, or values with x_scales.
+Training: x and w are tensors of one type; the call quantizes both (w in blocks of
+128 x 128) and is differentiable (once).  Each product sums over quantized operands,
+every one with blocks along that product's sum:
+
+    y = Q(x) Q(w)        dx = Q(dy) Q(w)^T        dw = Q(x)^T Q(dy)  (blocks along the rows)
+
+with the gradients passed on as if quantizing were the identity.  Streams, captured graphs
+and what is refused are as in ``linear``.
 """
 from __future__ import annotations
 
 import struct
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import TRA_OK, TraError, load
-from .fused import DTYPES, _matrix, _on, _recorded_elsewhere
+from . import TRA_OK, TraError, _row_major_ld, load
+from . import fused
+from .fused import (DTYPES, _matrix, _no_capture, _on, _recorded_elsewhere, _rows, _vector,
+                    _wants_grad, _weight, _written)
 
 # tra_fp8, tra_scale
 FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
@@ -24,6 +40,9 @@ BLOCK = 128
 
 # tra_quantize_args, field by field
 _QUANTIZE = struct.Struct("@4i2qPqPqPqqPqPqq")
+# tra_scaled_args
+_SCALED = struct.Struct("@6i3qPqPqqPqPqqPPqPqPQ")
+X_SCALED = -1
 
 
 def _up(n, m):
@@ -107,3 +126,250 @@ def quantize(x, block=(1, 128), dtype=torch.float8_e4m3fn, scale_dtype=torch.flo
     if form not in FORMS:
         raise ValueError(f"form must be one of {', '.join(FORMS)}; got {form!r}")
     return tuple(_quantize(x, block_rows, dtype, scale_dtype, form != "columns", form != "rows"))
+
+
+# --- products ---------------------------------------------------------------------
+
+def _values(t, name, rows, device):
+    """Checks 8-bit values, rows x K; returns their leading dimension."""
+    if t.dim() != 2 or t.device != device or not t.is_cuda:
+        raise TypeError(f"{name} must be a 2-D tensor on {device}")
+    if rows is not None and t.shape[0] != rows:
+        raise ValueError(f"{name} must have {rows} rows")
+    K = t.shape[1]
+    if K % 16 != 0:
+        raise ValueError(f"{name} must have a multiple of 16 columns (zeros at the end, as quantize "
+                         "leaves them)")
+    s0, s1 = t.stride()
+    ld = s0 if s1 == 1 and s0 >= K > 0 else _row_major_ld((t.shape[0], K), (s0, s1), name)
+    if K > 0 and ((ld % 16 != 0 and t.shape[0] > 1) or t.data_ptr() % 16 != 0):
+        raise ValueError(f"rows of {name} must start 16-byte aligned")
+    return ld
+
+
+def _scales(s, name, rows, cols, device):
+    """Checks scales of rows x cols values; returns (block rows, type, row's and block's
+    strides)."""
+    if not isinstance(s, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if s.dim() != 2 or s.dtype not in SCALES or s.device != device:
+        raise TypeError(f"{name} must be a 2-D float32 or float8_e8m0fnu tensor on {device}")
+    blocks = _up(cols, BLOCK)
+    if s.shape[1] != blocks or s.shape[0] not in (rows, _up(rows, BLOCK)):
+        raise ValueError(f"{name} must be {rows} or {_up(rows, BLOCK)} x {blocks}")
+    # (of a single row, either is the same)
+    block_rows = 1 if s.shape[0] == rows and rows > 1 else BLOCK
+    ss_row, ss_block = s.stride()
+    if s.shape[0] > 1 and blocks > 1 and ss_row != 1 and ss_block != 1:
+        raise ValueError(f"{name} must have contiguous rows or columns")
+    return block_rows, SCALES[s.dtype], ss_row, ss_block
+
+
+def _product(x, x_scales, w, w_scales, bias, residual, dtype, out, x_fp8=None):
+    """x w^T + bias + residual: w N x K values; x values with scales, or a tensor."""
+    device = x.device
+    if not isinstance(w, torch.Tensor) or w.dtype not in FP8:
+        raise TypeError("w must be 8-bit values")
+    ldw = _values(w, "w", None, device)
+    N, K = w.shape
+    block_rows, scale, sw_row, sw_block = _scales(w_scales, "w_scales", N, K, device)
+    if x_scales is None:
+        ldx = _matrix(x, "x")
+        M, kx = x.shape
+        if _up(kx, 16) * 16 != K:
+            raise ValueError(f"inner dimensions differ: x has {kx} columns, w {K}")
+        head = (DTYPES[x.dtype], FP8[torch.float8_e4m3fn if x_fp8 is None else x_fp8])
+        sx = (0, 0, 0)
+    else:
+        ldx = _values(x, "x", None, device)
+        M, kx = x.shape
+        if kx != K:
+            raise ValueError(f"inner dimensions differ: x has {kx} columns, w {K}")
+        one, kind, sx_row, sx_block = _scales(x_scales, "x_scales", M, K, device)
+        if (one != 1 and M > 1) or kind != scale:
+            raise ValueError("x_scales must have a row for each of x's, and w_scales' type")
+        head = (X_SCALED, FP8[x.dtype])
+        sx = (x_scales.data_ptr(), sx_row, sx_block)
+    if scale == 0 and block_rows == 1:
+        raise ValueError("float32 w_scales must be of blocks of 128 x 128")
+    w_fp8 = FP8[w.dtype]
+    if w_fp8 and (head[1] or scale == 0 or x_scales is None):
+        raise ValueError("float8_e5m2 w goes with float8_e4m3fn x and float8_e8m0fnu scales only")
+    like = x if x.dtype == dtype else torch.empty(0, dtype=dtype, device=device)
+    if bias is not None:
+        _vector(bias, "bias", like, N)
+    R, ldr = 0, 0
+    if residual is not None:
+        ldr = _matrix(residual, "residual", like)
+        if residual.shape[0] != M or residual.shape[1] != N:
+            raise ValueError(f"residual must be {M} x {N}")
+        R = residual.data_ptr()
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=device)
+        ldy = N
+    else:
+        ldy = _matrix(out, "out", like)
+        if out.shape[0] != M or out.shape[1] != N:
+            raise ValueError(f"out must be {M} x {N}")
+    fields = (DTYPES[dtype], *head, w_fp8, scale, block_rows, M, N, kx, x.data_ptr(), ldx, *sx,
+              w.data_ptr(), ldw, w_scales.data_ptr(), sw_row, sw_block,
+              0 if bias is None else bias.data_ptr(), R, ldr, out.data_ptr(), ldy)
+    fused._call("tra_scaled_linear", _SCALED, fields, device, 9)
+    return out
+
+
+def _weights(w, need_w, need_wt):
+    """([N x K values, scales], [K x N values, scales]) of a weight tensor, None for what is
+    not asked for: one set of blocks of 128 x 128."""
+    stored = w if w.stride(1) == 1 and w.stride(0) >= w.shape[1] else w.t()
+    transposed = stored is not w           # stored N x K
+    rows, columns = (need_w, need_wt) if transposed else (need_wt, need_w)
+    if not (rows or columns):
+        return None, None
+    got = _quantize(stored, BLOCK, torch.float8_e4m3fn, torch.float8_e8m0fnu, rows, columns)
+    first = got[:2] if rows else None
+    second = (got[2:] if rows else got) if columns else None
+    return (first, second) if transposed else (second, first)
+
+
+def _activations(x, dtype, rows, columns):
+    if not (rows or columns):
+        return None, None
+    got = _quantize(x, 1, dtype, torch.float8_e8m0fnu, rows, columns)
+    return got[:2] if rows else None, (got[2:] if rows else got) if columns else None
+
+
+def _column_sums(dy):
+    """The bias' gradient: sums of dy's columns, in float32."""
+    db = dy.new_empty(dy.shape[1])
+    fields = (DTYPES[dy.dtype], 0, 0, 0, dy.shape[0], dy.shape[1], 0, dy.data_ptr(),
+              _matrix(dy, "dy"), 0, 0, 0, 0, 0, 0, dy.shape[1], 0, 0, 0, 0, dy.shape[1],
+              db.data_ptr())
+    fused._call("tra_linear_backward", fused._GRAD_ARGS, fields, dy.device)
+    return db
+
+
+def _gradients(dy, xt, wt, K, transposed, grad_dtype, need_dx, need_dw, need_dbias):
+    """(dx, dw, dbias) from the column forms of x and of the weight."""
+    N = dy.shape[1]
+    dx = dw = None
+    rows, columns = _activations(dy, grad_dtype, need_dx, need_dw)
+    if need_dx:
+        dx = _product(rows[0], rows[1], wt[0], wt[1], None, None, dy.dtype, None)
+    if need_dw:
+        if transposed:
+            dw = _product(columns[0], columns[1], xt[0], xt[1], None, None, dy.dtype, None).t()
+        else:
+            dw = _product(xt[0], xt[1], columns[0], columns[1], None, None, dy.dtype, None)
+    return dx, dw, _column_sums(dy) if need_dbias else None
+
+
+def _is_transposed(w) -> bool:
+    """Whether a checked K x N weight is stored N x K."""
+    return not (w.stride(1) == 1 and w.stride(0) >= w.shape[1])
+
+
+class _ScaledLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, grad_dtype):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        xq, xt = _activations(x, torch.float8_e4m3fn, True, need_w)
+        wq, wt = _weights(w, True, need_x)
+        y = _product(xq[0], xq[1], wq[0], wq[1], bias, residual, x.dtype, None)
+        ctx.plan = (x.shape[1], _is_transposed(w), grad_dtype)
+        ctx.save_for_backward(*(xt or (None, None)), *(wt or (None, None)))
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        _no_capture()
+        need_x, need_w, need_b, need_r, _ = ctx.needs_input_grad
+        dx = dw = db = None
+        if need_x or need_w or need_b:
+            xt, xts, wt, wts = ctx.saved_tensors
+            dx, dw, db = _gradients(_rows(dy), (xt, xts), (wt, wts), *ctx.plan, need_x, need_w,
+                                    need_b)
+        return dx, dw, db, dy if need_r else None, None
+
+
+def _check_training(x, w):
+    """Both operands are tensors: checks them."""
+    _matrix(x, "x")
+    _weight(w, "w", x)
+
+
+def scaled_linear(x, w, x_scales=None, w_scales=None, bias=None, residual=None, dtype=None,
+                  out=None, grad_dtype=torch.float8_e4m3fn, stream=None):
+    """x w + bias + residual on 8-bit operands, as a new M x N tensor or in ``out``.
+
+    ``w`` is K x N: the transposed view of N x K values (float8_e4m3fn) with ``w_scales``, the
+    transposed view of their scales; or a tensor of x's type, in either layout of
+    ``linear``, which the call quantizes in blocks of 128 x 128.  ``x`` is M x K: values
+    with ``x_scales`` of w_scales' type, or a tensor, which the call quantizes.
+    ``dtype``, of the result, bias and residual, is x's by default, and bfloat16 where x is
+    values.  ``residual`` may be ``out``.
+
+    Differentiable where both x and w are tensors; ``grad_dtype`` is what the result's
+    gradient is quantized to, float8_e4m3fn or float8_e5m2.  ``out`` is refused where
+    autograd records the call, and so are quantized weights.  ``stream`` as in ``linear``.
+    """
+    tensors = (x, w, x_scales, w_scales, bias, residual, out)
+    _recorded_elsewhere(*tensors)
+    if stream is not None:
+        return _on(stream, lambda: scaled_linear(x, w, x_scales, w_scales, bias, residual, dtype,
+                                                 out, grad_dtype), *tensors)
+    if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor):
+        raise TypeError("x and w must be torch.Tensors")
+    if not x.is_cuda:
+        raise TypeError("x must be a tensor on a GPU")
+    given = x.dtype in FP8
+    if given != (x_scales is not None):
+        raise ValueError("x_scales goes with 8-bit x")
+    if (w.dtype in FP8) != (w_scales is not None):
+        raise ValueError("w_scales goes with 8-bit w")
+    if dtype is None:
+        dtype = torch.bfloat16 if given else x.dtype
+    if dtype not in DTYPES:
+        raise ValueError(f"dtype must be one of {', '.join(map(str, DTYPES))}; got {dtype!r}")
+    _code(FP8, grad_dtype, "grad_dtype")
+    wants = _wants_grad(*tensors)
+    if w_scales is None:
+        if given or dtype != x.dtype:
+            raise ValueError("a w that the call quantizes goes with a tensor x and a result of "
+                             "its type")
+        _check_training(x, w)
+        if wants:
+            if out is not None:
+                raise ValueError("out cannot be given where gradients are recorded")
+            return _ScaledLinear.apply(x, w, bias, residual, grad_dtype)
+        (wq, ws), _ = _weights(w, True, False)
+    else:
+        if wants:
+            raise ValueError("gradients cannot be recorded with quantized weights: give w as a "
+                             "tensor, or use torch.no_grad()")
+        wq, ws = w.t(), w_scales.t()
+    y = _product(x, x_scales, wq, ws, bias, residual, dtype, out)
+    if out is not None:
+        _written(out)
+    return y
+
+
+def scaled_linear_backward(dy, x, w, grad_dtype=torch.float8_e4m3fn, need_dx=True, need_dw=True,
+                           need_dbias=False, stream=None):
+    """(dx, dw, dbias) of ``scaled_linear`` for dy, the gradient of its result (that of the
+    residual is dy itself); None for each not asked for.  x and w are the tensors of the
+    forward call; dw has w's layout.  ``stream`` as in ``linear``."""
+    _recorded_elsewhere(dy, x, w)
+    if stream is not None:
+        return _on(stream, lambda: scaled_linear_backward(dy, x, w, grad_dtype, need_dx, need_dw,
+                                                          need_dbias), dy, x, w)
+    _check_training(x, w)
+    _matrix(dy, "dy", x)
+    if dy.shape[0] != x.shape[0] or dy.shape[1] != w.shape[1]:
+        raise ValueError(f"dy must be {x.shape[0]} x {w.shape[1]}")
+    _code(FP8, grad_dtype, "grad_dtype")
+    xt = _activations(x, torch.float8_e4m3fn, False, True)[1] if need_dw else None
+    wt = _weights(w, False, True)[1] if need_dx else None
+    return _gradients(dy, xt, wt, x.shape[1], _is_transposed(w), grad_dtype, need_dx, need_dw,
+                      need_dbias)
