@@ -9,7 +9,7 @@ from tiling_roofline_analysis_amd import scaled
 # (M, N, K)
 CALLS = [(1, 16, 128), (40, 60, 500), (64, 64, 4096), (130, 520, 264), (300, 700, 1040),
          (515, 1030, 520), (1000, 1100, 144), (1500, 2000, 300), (2100, 4100, 136),
-         (70, 4100, 6000)]
+         (70, 4100, 6000), (4100, 4200, 400), (1030, 4100, 2064)]
 
 # addresses that are never read
 X, SX, W, SW, BIAS, R, Y, WS = (i << 40 for i in range(1, 9))

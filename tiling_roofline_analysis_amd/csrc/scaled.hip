@@ -23,10 +23,19 @@ int64_t up16(int64_t n) { return ceil_div(n, 16) * 16; }
 
 // How the kernels go, in microseconds (TileClass): 16-bit results with binary32 and e8m0
 // scales, binary32 results.
-constexpr TileClass kClasses[3][3] = {
-    {{128, 128, 2, 0.60, 0.60, 5.2}, {64, 128, 2, 0.35, 0.33, 4.5}, {64, 64, 2, 0.24, 0.22, 4.0}},
-    {{128, 128, 2, 0.50, 0.47, 5.2}, {64, 128, 2, 0.30, 0.27, 4.5}, {64, 64, 2, 0.21, 0.185, 4.0}},
-    {{128, 128, 1, 1.00, 1.00, 5.2}, {64, 128, 2, 0.60, 0.55, 4.5}, {64, 64, 2, 0.40, 0.35, 4.0}}};
+constexpr TileClass kClasses[3][4] = {
+    {{256, 256, 1, 1.50, 1.60, 5.7},
+     {128, 128, 2, 0.60, 0.60, 5.2},
+     {64, 128, 2, 0.35, 0.33, 4.5},
+     {64, 64, 2, 0.24, 0.22, 4.0}},
+    {{256, 256, 1, 1.28, 1.42, 5.7},
+     {128, 128, 2, 0.50, 0.47, 5.2},
+     {64, 128, 2, 0.30, 0.27, 4.5},
+     {64, 64, 2, 0.21, 0.185, 4.0}},
+    {{128, 128, 1, 1.00, 1.00, 5.2},
+     {64, 128, 2, 0.60, 0.55, 4.5},
+     {64, 64, 2, 0.40, 0.35, 4.0},
+     {0, 0, 0, 0.0, 0.0, 0.0}}};
 
 bool x_given(const tra_scaled_args &a) { return a.x_dtype == TRA_X_SCALED; }
 
@@ -36,7 +45,7 @@ ScaledPlan plan_scaled(const tra_scaled_args &a) {
     const PlanSizes z{a.M, a.N, K, 1, 1, false, 1, static_cast<double>(b), false, true};
     double us = 0.0;
     s.tile = plan_classes(
-        kClasses[a.dtype == TRA_DTYPE_F32 ? 2 : a.scale == TRA_SCALE_E8M0 ? 1 : 0], 3, z, us);
+        kClasses[a.dtype == TRA_DTYPE_F32 ? 2 : a.scale == TRA_SCALE_E8M0 ? 1 : 0], 4, z, us);
     s.tile.form = tra::kFormKK;
     s.tile.direct = 16;
     s.formats = a.x_fp8 == TRA_FP8_E5M2   ? tra::kX5
@@ -200,7 +209,7 @@ tra_status tra_scaled_linear_describe(const tra_scaled_args *args, char *buf, si
     const ScaledPlan s = plan_scaled(*args);
     const tra::TilePlan &t = s.tile;
     std::snprintf(buf, len, "kernel=%s tile=%dx%d deep=%d whole=%d splits=%d workspace_bytes=%zu",
-                  "scaled_tile", t.bm, t.bn, t.deep, t.whole, t.splits, s.total);
+                  t.bm == 256 ? "scaled_wide" : "scaled_tile", t.bm, t.bn, t.deep, t.whole, t.splits, s.total);
     return TRA_OK;
 }
 

@@ -98,6 +98,48 @@ __device__ __forceinline__ i32x8 fragment8(const char *st, int panel, int row0) 
         i32x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// Loads a panel of k-contiguous rows, as Panel::load_direct does, but with buffers that end
+// with the panel's rows inside the matrix and, one a load, begin at the load's first row:
+// a lane's offset is the same in every load of an operand's panels.
+template <typename P>
+struct RowPanel {
+    static constexpr int L = P::INS;
+    static constexpr int ROWS = P::BYTES / 128 / L;      // a load's
+    static_assert(ROWS % 16 == 0, "every load's chunks are swizzled alike");
+
+    int64_t skip;              // bytes from a load's rows to the next's
+    int length[L];
+
+    // `rows` of the matrix from the panel's first row on, `ld` bytes apart.
+    __device__ __forceinline__ RowPanel(int64_t rows, int64_t ld) : skip(ROWS * ld) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int64_t n = (rows - i * ROWS) * ld;
+            length[i] = static_cast<int>(n <= 0 ? 0 : n < 0x7fffffff ? n : 0x7fffffff);
+        }
+    }
+    static __device__ __forceinline__ uint32_t offset(int wave, int64_t ld) {
+        return static_cast<uint32_t>(P::line(wave, 0)) * static_cast<uint32_t>(ld) +
+               static_cast<uint32_t>(P::chunk(wave, 0) * 16);
+    }
+    __device__ __forceinline__ void load(int wave, const char *corner, uint32_t off, int rem,
+                                         char *lds) const {
+        const uint32_t at = P::chunk(wave, 0) * 16 >= rem ? P::OUTSIDE : off;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            // (variables, whose types depend on no template parameter: from expressions that
+            // do, the compiler's host pass drops every kernel that calls this but the first,
+            // with no word before the link)
+            char *to = lds + P::lds_block(wave, i);
+            void *from = const_cast<char *>(corner) + i * skip;
+            const int bytes = length[i];
+            const __amdgpu_buffer_rsrc_t rsrc =
+                __builtin_amdgcn_make_buffer_rsrc(from, (short)0, bytes, 0x00020000);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to, 16, at, 0, 0, 0);
+        }
+    }
+};
+
 // Scales of a K tile in LDS: a word for each of WAVES * 64 rows, BM of X's and then BN of
 // W's (and none for the rest).  A wave loads 64 of them, of one operand.
 template <int SCALE, int BM, int BN, int WAVES>
@@ -371,6 +413,215 @@ __global__ __launch_bounds__(256, (ScaledShape<BM, BN, SCALE>::per_cu(S))) void 
         m0 + wm * (BM / 2), n0 + wn * HC, n1 + wn * HC);
 }
 
+// ---- the wide kernel -----------------------------------------------------------------------
+//
+// linear_wide for one-byte elements and 16-bit results: 256 x 256 of Y per workgroup of
+// eight waves in two groups half a phase apart, the same panels, phases and waits.  A
+// quadrant is 8 MFMAs.  The tile's scales are read panel by panel beside the fragments,
+// the last in phase 2, and loaded for tile s + 2 in phase 3.
+// With binary32 scales a row tile's sums are added while the next one's MFMAs run, the
+// quadrant's last behind the next phase's reads, while the other group's do.
+template <typename T, int FORMATS, int SCALE>
+__global__ __launch_bounds__(512, 2) void scaled_wide(const ScaledArgs p) {
+    using PP = Panel<Bytes, true, 128, 8>;
+    using PS = ScalePanel<SCALE, 256, 256, 8>;
+    constexpr int L = PP::INS;
+    constexpr bool UNIT = SCALE == TRA_SCALE_E8M0;
+    static_assert(sizeof(T) == 2 && L == 2 && PP::BYTES == 64 * 64 * 4,
+                  "panels of two loads a wave; a wave's sums fill one");
+    __shared__ __align__(1024) char a00[PP::BYTES], a01[PP::BYTES], a10[PP::BYTES], a11[PP::BYTES];
+    __shared__ __align__(1024) char b00[PP::BYTES], b01[PP::BYTES], b10[PP::BYTES], b11[PP::BYTES];
+    __shared__ __align__(1024) char s0[PS::BYTES], s1[PS::BYTES];
+    lds_poison(reinterpret_cast<float *>(a00), PP::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(a01), PP::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(a10), PP::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(a11), PP::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(b00), PP::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(b01), PP::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(b10), PP::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(b11), PP::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(s0), PS::BYTES / 4);
+    lds_poison(reinterpret_cast<float *>(s1), PS::BYTES / 4);
+
+    const TileArgs &a = p.t;
+    const Part part(a, 0, 256 * 256);
+    int tm, tn;
+    grouped_tile32<kGroupWide>(part.tile, a.tiles_m, a.tiles_n, tm, tn);
+    const int64_t m0 = static_cast<int64_t>(tm) * 256, n0 = static_cast<int64_t>(tn) * 256;
+    const int64_t n1 = n0 + 128;
+    const int first = part.first, count = part.count;
+    Walk<Bytes, true, true> walk(a, 0, m0, n0, n1, false, first, count);
+    const int64_t lower = 128 * a.lda;
+
+    const int wave = wave_id();
+    const int wm = wave >> 2, wn = wave & 3;
+    PS scales(p, wave, m0, n0, first);
+    using PR = RowPanel<PP>;
+    const uint32_t oa = PR::offset(wave, a.lda), ob = PR::offset(wave, a.ldb);
+    const PR pa0(a.M - m0, a.lda), pa1(a.M - m0 - 128, a.lda);
+    const PR pb0(a.N - n0, a.ldb), pb1(a.N - n1, a.ldb);
+
+    // A1 is loaded one tile behind the others: where its tile starts
+    const char *late = nullptr;
+    int late_rem = 0;
+    auto load_a0 = [&](char *st) __attribute__((always_inline)) {
+        pa0.load(wave, walk.a, oa, walk.rem, st);
+    };
+    auto load_b0 = [&](char *st) __attribute__((always_inline)) {
+        pb0.load(wave, walk.b0, ob, walk.rem, st);
+    };
+    auto load_b1 = [&](char *st, char *sc) __attribute__((always_inline)) {
+        pb1.load(wave, walk.b1, ob, walk.rem, st);
+        scales.load(wave, walk.rem, sc);
+        late = walk.a + lower;
+        late_rem = walk.rem;
+        walk.next();
+    };
+    auto load_a1 = [&](char *st) __attribute__((always_inline)) {
+        pa1.load(wave, late, oa, late_rem, st);
+    };
+
+    f32x4 c[2][2][4][2] = {};      // [A panel][B panel]
+    i32x8 x[4], w[2][2];           // [row tile]; [B panel][column tile]
+    uint32_t sx[4], sw[2][UNIT ? 2 : 1];
+    // binary32 scales: the last row tile's sums, which are added late, and their scale
+    f32x4 t[2];
+    float ts = 0.0f;
+    float both[2] = {};            // W's scale of each B panel, in a scalar register
+    auto read_a = [&](auto half, const char *st, const char *sc) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = fragment8<PP>(st, 0, wm * 64 + i * 16);
+            sx[i] =
+                PS::of_rows(sc, 0, decltype(half)::value * 128 + wm * 64 + i * 16);
+        }
+    };
+    auto read_b = [&](auto half, const char *st, const char *sc) __attribute__((always_inline)) {
+        constexpr int H = decltype(half)::value;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            w[H][j] = fragment8<PP>(st, 0, wn * 32 + j * 16);
+            if constexpr (UNIT)
+                sw[H][UNIT ? j : 0] = PS::of_rows(sc, 0, 256 + H * 128 + wn * 32 + j * 16);
+            else if (j == 0)
+                sw[H][0] = PS::of_row(sc, 0, 256 + H * 128);
+        }
+    };
+    auto scale_of = [&](int i, auto hb) __attribute__((always_inline)) {
+        return __uint_as_float(sx[i]) * both[decltype(hb)::value];
+    };
+    auto add_to = [&](f32x4 (&sum)[2], const f32x4 (&u)[2], float s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[j][e] = fmaf(u[j][e], s, sum[j][e]);
+    };
+    // The barrier behind the reads and loads, the MFMAs, the barrier behind them.
+    // VM: loads that may still be in flight (63: any).
+    auto compute = [&](auto vm, auto ha, auto hb) __attribute__((always_inline)) {
+        constexpr int HA = decltype(ha)::value, HB = decltype(hb)::value;
+        stage_sync<decltype(vm)::value>();
+        if constexpr (UNIT) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    c[HA][HB][i][j] =
+                        mma_scaled<FORMATS>(w[HB][j], x[i], c[HA][HB][i][j], sw[HB][j], sx[i]);
+        } else {
+            if constexpr (HA == 0)     // the phases that have read it
+                both[HB] = __int_as_float(__builtin_amdgcn_readfirstlane(static_cast<int>(sw[HB][0])));
+            // a row tile's sums are added two MFMAs behind its own
+            f32x4 u[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) u[i][j] = mma_plain<FORMATS>(w[HB][j], x[i]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (i > 0) add_to(c[HA][HB][i - 1], u[i - 1], scale_of(i - 1, hb));
+            }
+            t[0] = u[3][0];
+            t[1] = u[3][1];
+            ts = scale_of(3, hb);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Adds what is left of the quadrant computed last.
+    auto add = [&](auto ha, auto hb) __attribute__((always_inline)) {
+        if constexpr (!UNIT) {
+            __builtin_amdgcn_sched_barrier(0);
+            add_to(c[decltype(ha)::value][decltype(hb)::value][3], t, ts);
+        }
+    };
+    constexpr std::integral_constant<int, 0> zero;
+    constexpr std::integral_constant<int, 1> one;
+    constexpr std::integral_constant<int, 3 * L + 1> three_panels;
+    constexpr std::integral_constant<int, 63> any;
+    // Tile s, in the stages a0, a1, b0, b1, sc; `a1_next` is the other A1.
+    auto tile = [&](char *a0, char *a1, char *b0, char *b1, char *sc, char *a1_next)
+                    __attribute__((always_inline)) {
+        read_b(zero, b0, sc);
+        read_a(zero, a0, sc);
+        load_a1(a1_next);
+        compute(any, zero, zero);
+        read_b(one, b1, sc);
+        load_a0(a0);
+        add(zero, zero);
+        compute(any, zero, one);
+        read_a(one, a1, sc);
+        load_b0(b0);
+        add(zero, one);
+        compute(any, one, one);
+        load_b1(b1, sc);
+        add(one, one);
+        compute(three_panels, one, zero);
+        add(one, zero);
+    };
+
+    load_a0(a00);
+    __builtin_amdgcn_sched_barrier(0);
+    load_b0(b00);
+    __builtin_amdgcn_sched_barrier(0);
+    load_b1(b10, s0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_a1(a10);
+    __builtin_amdgcn_sched_barrier(0);
+    load_a0(a01);
+    __builtin_amdgcn_sched_barrier(0);
+    load_b0(b01);
+    __builtin_amdgcn_sched_barrier(0);
+    load_b1(b11, s1);
+    stage_sync<3 * L + 1>();
+    if (wm != 0) __builtin_amdgcn_s_barrier();
+    int s = 0;
+    for (; s + 2 <= count; s += 2) {
+        tile(a00, a10, b00, b10, s0, a11);
+        tile(a01, a11, b01, b11, s1, a10);
+    }
+    if (s < count) tile(a00, a10, b00, b10, s0, a11);
+    if (wm == 0) __builtin_amdgcn_s_barrier();
+    stage_sync<0>();
+
+    // One array takes a wave's sums of one A panel.
+    char *mine = wave < 4 ? (wave < 2 ? (wave < 1 ? a00 : a01) : (wave < 3 ? a10 : a11))
+                          : (wave < 6 ? (wave < 5 ? b00 : b01) : (wave < 7 ? b10 : b11));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        epi_put<32>(mine, c[h][0], 0);
+        epi_put<32>(mine, c[h][1], 1);
+        wave_sync();
+        const int row = h * 128 + wm * 64;
+        epi_rows<T, false, 32, 64>(
+            a, 0, part.sums == nullptr ? nullptr : part.sums + row * 256 + wn * 32, 256, mine,
+            m0 + row, n0 + wn * 32, n1 + wn * 32);
+        wave_sync();
+    }
+}
+
 // ---- launches ----------------------------------------------------------------------------------
 
 template <typename T, int FORMATS, int SCALE>
@@ -379,6 +630,12 @@ hipError_t launch_scaled(const TilePlan &plan, const ScaledArgs &p, hipStream_t 
     const unsigned tiles = static_cast<unsigned>(a.tiles_m) * static_cast<unsigned>(a.tiles_n);
     const unsigned whole = static_cast<unsigned>(a.whole);
     const dim3 grid(whole + (tiles - whole) * static_cast<unsigned>(a.splits));
+    if constexpr (sizeof(T) == 2) {
+        if (plan.bm == 256) {
+            scaled_wide<T, FORMATS, SCALE><<<grid, 512, 0, stream>>>(p);
+            return hipGetLastError();
+        }
+    }
 #define TRA_TILE(BM, BN, S) scaled_tile<T, FORMATS, SCALE, BM, BN, S><<<grid, 256, 0, stream>>>(p)
     // (two of 128 x 128 with converted operands would need more VGPRs than a CU has)
     constexpr int SHALLOW = std::is_same_v<T, float> ? 4 : 2;
