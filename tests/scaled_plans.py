@@ -7,7 +7,7 @@ import tiling_roofline_analysis_amd as tra
 from tiling_roofline_analysis_amd import scaled
 
 # (M, N, K)
-CALLS = [(1, 16, 128), (40, 60, 500), (64, 64, 4096), (130, 520, 264), (300, 700, 1040),
+CALLS = [(1, 16, 128), (1, 500, 4096), (3, 48, 9000), (16, 1030, 272), (9, 33, 16), (2, 4100, 1300), (40, 60, 500), (64, 64, 4096), (130, 520, 264), (300, 700, 1040),
          (515, 1030, 520), (1000, 1100, 144), (1500, 2000, 300), (2100, 4100, 136),
          (70, 4100, 6000), (4100, 4200, 400), (1030, 4100, 2064)]
 

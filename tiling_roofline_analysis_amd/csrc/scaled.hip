@@ -17,6 +17,7 @@ using tra::ceil_div;
 using tra::ScaledArgs;
 using tra::ScaledPlan;
 
+constexpr int64_t kFewBytes = tra::kFewBytes;
 constexpr int64_t kMaxPitch = int64_t{1} << 22;      // bytes: a tile's offsets fit 31 bits
 
 int64_t up16(int64_t n) { return ceil_div(n, 16) * 16; }
@@ -46,13 +47,28 @@ ScaledPlan plan_scaled(const tra_scaled_args &a) {
     double us = 0.0;
     s.tile = plan_classes(
         kClasses[a.dtype == TRA_DTYPE_F32 ? 2 : a.scale == TRA_SCALE_E8M0 ? 1 : 0], 4, z, us);
+    // Few rows: the weights' bytes at the rate that the strips of 16 columns can ask for.
+    if (a.M <= 16) {
+        const double strips = static_cast<double>(ceil_div(a.N, 16));
+        const double few_us = 2.8 + static_cast<double>(K) * a.N * (1.0 + a.M / 80.0) /
+                                        std::min(4.9e6, strips * 2.6e4);
+        if (few_us < us) {
+            s.tile = tra::TilePlan{};
+            s.tile.few = true;
+            s.tile.whole = static_cast<int>(strips);
+            s.tile.bm = s.tile.bn = 16;
+            s.tile.splits = 1;
+            s.make = a.x_dtype == a.dtype && a.x_fp8 == TRA_FP8_E4M3 && a.K > 0 &&
+                     a.M * ceil_div(a.K, 128) * 128 <= kFewBytes;
+        }
+    }
     s.tile.form = tra::kFormKK;
     s.tile.direct = 16;
     s.formats = a.x_fp8 == TRA_FP8_E5M2   ? tra::kX5
                 : a.w_fp8 == TRA_FP8_E5M2 ? tra::kW5
                                           : tra::kX4W4;
     s.scale = a.scale;
-    if (!x_given(a)) {
+    if (!x_given(a) && !s.make) {
         s.ldx = K;
         s.sx_block = a.M;
         s.values_bytes = align_up(static_cast<size_t>(a.M) * static_cast<size_t>(K));
@@ -159,7 +175,9 @@ tra_status scaled_linear(const tra_scaled_args *p, void *stream) {
              s.tile, 128, d.t,
              reinterpret_cast<float *>(ws + s.values_bytes + s.scales_bytes))) != TRA_OK)
         return st;
-    if (!x_given(a) && a.K > 0) {
+    if (s.make) {
+        d.x_cols = static_cast<int>(a.K);
+    } else if (!x_given(a) && a.K > 0) {
         tra_quantize_args q{};
         q.dtype = a.x_dtype;
         q.fp8 = a.x_fp8;
@@ -208,8 +226,9 @@ tra_status tra_scaled_linear_describe(const tra_scaled_args *args, char *buf, si
     }
     const ScaledPlan s = plan_scaled(*args);
     const tra::TilePlan &t = s.tile;
-    std::snprintf(buf, len, "kernel=%s tile=%dx%d deep=%d whole=%d splits=%d workspace_bytes=%zu",
-                  t.bm == 256 ? "scaled_wide" : "scaled_tile", t.bm, t.bn, t.deep, t.whole, t.splits, s.total);
+    std::snprintf(buf, len, "kernel=%s tile=%dx%d deep=%d whole=%d splits=%d quantizes=%d workspace_bytes=%zu",
+                  t.few ? "scaled_few" : t.bm == 256 ? "scaled_wide" : "scaled_tile", t.bm, t.bn, t.deep, t.whole, t.splits,
+                  s.make ? 1 : x_given(*args) ? 0 : 2, s.total);
     return TRA_OK;
 }
 

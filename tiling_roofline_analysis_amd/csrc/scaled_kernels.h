@@ -622,6 +622,157 @@ __global__ __launch_bounds__(512, 2) void scaled_wide(const ScaledArgs p) {
     }
 }
 
+// ---- the kernel for few rows --------------------------------------------------------------
+//
+// M <= 16: the weights are read once and nothing else counts.  As linear_few: a workgroup
+// of eight waves owns a strip of 16 columns, a wave takes a run of the blocks of K, weights
+// go from memory into the MFMA's registers (lane l loads chunks l / 16 and 4 + l / 16 of
+// column l % 16), and the waves' sums meet in LDS.
+// MAKE: X is of type T and quantized here, by every workgroup for itself, into LDS, while
+// its first weights are on their way; for a few thousand elements that takes less than a
+// launch of its own.  The bits are those of tra_quantize.
+template <typename T, int FORMATS, int SCALE, bool MAKE>
+__global__ __launch_bounds__(512) void scaled_few(const ScaledArgs p) {
+    constexpr int WAVES = 8, U = 4;    // U blocks in hand
+    constexpr int SIZE = SCALE == TRA_SCALE_E8M0 ? 1 : 4;
+    constexpr bool WIDEN = std::is_same_v<T, float>;
+    constexpr bool UNIT = SCALE == TRA_SCALE_E8M0 && !WIDEN;
+    constexpr bool EACH = SCALE == TRA_SCALE_E8M0 && WIDEN;
+    constexpr uint32_t OUTSIDE = 0x80000000u;
+    __shared__ __align__(16) float sums[WAVES][256];
+    __shared__ __align__(16) char made[MAKE ? kFewBytes : 16];
+    __shared__ uint32_t made_scales[MAKE ? kFewBytes / 128 : 1];
+    lds_poison(&sums[0][0], WAVES * 256);
+    lds_poison(reinterpret_cast<float *>(made), (MAKE ? kFewBytes : 16) / 4);
+    lds_poison(reinterpret_cast<float *>(made_scales), MAKE ? kFewBytes / 128 : 1);
+    const TileArgs &a = p.t;
+    const int wave = wave_id(), l16 = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+    const int M = static_cast<int>(a.M), N = static_cast<int>(a.N), K = static_cast<int>(a.K);
+    const int blocks = (K + 127) / 128;
+    const int n0 = xcd_remap32(blockIdx.x, gridDim.x) * 16;
+    const int own = n0 + l16 < N ? l16 : N - 1 - n0;         // this lane's column of the strip
+    const int m = l16 < M ? l16 : M - 1;
+    const int each = (blocks + WAVES - 1) / WAVES;
+    const int begin = wave * each, end = begin + each < blocks ? begin + each : blocks;
+
+    char *w_at = const_cast<char *>(static_cast<const char *>(a.B[0])) + n0 * a.ldb;
+    const __amdgpu_buffer_rsrc_t w_rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(w_at, (short)0, 0x7fffffff, 0x00020000);
+    const uint32_t w_off = static_cast<uint32_t>(own) * static_cast<uint32_t>(a.ldb) + g * 16;
+    const char *x_at = static_cast<const char *>(a.A) + m * a.lda + g * 16;
+    const char *sx_at = static_cast<const char *>(p.SX) + m * p.sx_row * SIZE;
+    const char *sw_at = static_cast<const char *>(p.SW);
+    auto scale_at = [&](const char *at) __attribute__((always_inline)) -> uint32_t {
+        if constexpr (SIZE == 1) return *reinterpret_cast<const uint8_t *>(at);
+        else return *reinterpret_cast<const uint32_t *>(at);
+    };
+    // W's scale of the strip's column j, block b
+    auto w_scale = [&](int j, int b) __attribute__((always_inline)) {
+        const int n = n0 + j < N ? n0 + j : N - 1;
+        return scale_at(sw_at + ((n >> p.w_shift) * p.sw_row + b * p.sw_block) * SIZE);
+    };
+
+    u32x4 w[U][2];
+    uint32_t sw[U], sws[U][4];
+    auto load = [&](int b0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int b = b0 + u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = b * 128 + h * 64 + g * 16;
+                const uint32_t at = b < end && k < K ? w_off + b * 128 + h * 64 : OUTSIDE;
+                w[u][h] = __builtin_amdgcn_raw_buffer_load_b128(w_rsrc, at, 0, 0);
+            }
+            const int bb = b < end ? b : end - 1;
+            if constexpr (EACH) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sws[u][e] = w_scale(4 * g + e, bb);
+            } else {
+                sw[u] = w_scale(UNIT ? l16 : 0, bb);
+            }
+        }
+    };
+    if (begin < end) load(begin);
+    if constexpr (MAKE) {
+        for (int i = static_cast<int>(threadIdx.x) >> 4; i < M * blocks; i += 32) {
+            const int row = i / blocks, b = i - row * blocks, k = b * 128 + l16 * 8;
+            float v[8], most = 0.0f;
+            load_part<T, 8>(static_cast<const T *>(a.A) + row * a.lda + k, p.x_cols - k, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = fmaxf(most, finite_size(v[e]));
+            const BlockScale s = block_scale<TRA_FP8_E4M3, SCALE>(largest_of_16(most));
+            uint32_t q[2];
+            to_fp8<TRA_FP8_E4M3, SCALE>(v, s, q);
+            __builtin_memcpy(__builtin_assume_aligned(made + i * 128 + l16 * 8, 8), q, 8);
+            if (l16 == 0) made_scales[i] = s.bits;
+        }
+        __syncthreads();
+    }
+
+    f32x4 c = {};
+    for (int b0 = begin; b0 < end; b0 += U) {
+        if (b0 > begin) load(b0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int b = b0 + u < end ? b0 + u : end - 1;
+            u32x4 x[2];
+            uint32_t sx;
+            if constexpr (MAKE) {
+                const int at = (m * blocks + b) * 128 + g * 16;
+                x[0] = *reinterpret_cast<const u32x4 *>(made + at);
+                x[1] = *reinterpret_cast<const u32x4 *>(made + at + 64);
+                sx = made_scales[m * blocks + b];
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // (past K the weights are zeros, and so are these: they are NaN-free)
+                    const int k = b * 128 + h * 64 + g * 16;
+                    x[h] = u32x4{};
+                    if (k < K)
+                        x[h] = *reinterpret_cast<const u32x4 *>(x_at + b * 128 + h * 64);
+                }
+                sx = scale_at(sx_at + b * p.sx_block * SIZE);
+            }
+            if (b0 + u >= end) continue;
+            const i32x8 w8 = __builtin_bit_cast(
+                i32x8, __builtin_shufflevector(w[u][0], w[u][1], 0, 1, 2, 3, 4, 5, 6, 7));
+            const i32x8 x8 = __builtin_bit_cast(
+                i32x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+            if constexpr (UNIT) {
+                c = mma_scaled<FORMATS>(w8, x8, c, sw[u], sx);
+            } else {
+                f32x4 t = {};
+                if constexpr (WIDEN) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            widen<kFormatW<FORMATS>>(w8, q), widen<kFormatX<FORMATS>>(x8, q), t, 0,
+                            0, 0);
+                } else {
+                    t = mma_plain<FORMATS>(w8, x8);
+                }
+                const float s = scale_value<SCALE>(sx);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    c[e] = fmaf(t[e], s * scale_value<SCALE>(EACH ? sws[u][e] : sw[u]), c[e]);
+            }
+        }
+    }
+
+    // Lane l holds token l % 16 of strip columns 4 (l / 16) .. + 3.
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sums[wave][l16 * 16 + 4 * g + r] = c[r];
+    __syncthreads();
+    const int i = static_cast<int>(threadIdx.x), row = i / 16, n = n0 + i % 16;
+    if (i < 256 && row < M && n < N) {
+        float z[1] = {}, none[1];
+#pragma unroll
+        for (int s = 0; s < WAVES; ++s) z[0] += sums[s][i];
+        finish<T, false, TRA_ACT_NONE, 1>(a.epi, 0, row, n, z, none);
+    }
+}
+
 // ---- launches ----------------------------------------------------------------------------------
 
 template <typename T, int FORMATS, int SCALE>
@@ -630,6 +781,17 @@ hipError_t launch_scaled(const TilePlan &plan, const ScaledArgs &p, hipStream_t 
     const unsigned tiles = static_cast<unsigned>(a.tiles_m) * static_cast<unsigned>(a.tiles_n);
     const unsigned whole = static_cast<unsigned>(a.whole);
     const dim3 grid(whole + (tiles - whole) * static_cast<unsigned>(a.splits));
+    if (plan.few) {
+        const dim3 strips(static_cast<unsigned>(a.tiles_n));
+        if constexpr (FORMATS == kX4W4) {
+            if (p.x_cols > 0) {
+                scaled_few<T, FORMATS, SCALE, true><<<strips, 512, 0, stream>>>(p);
+                return hipGetLastError();
+            }
+        }
+        scaled_few<T, FORMATS, SCALE, false><<<strips, 512, 0, stream>>>(p);
+        return hipGetLastError();
+    }
     if constexpr (sizeof(T) == 2) {
         if (plan.bm == 256) {
             scaled_wide<T, FORMATS, SCALE><<<grid, 512, 0, stream>>>(p);

@@ -11,6 +11,9 @@ namespace tra {
 // Formats of X's and W's values: both e4m3fn, or one of them e5m2.
 enum ScaledFormats { kX4W4 = 0, kX5 = 1, kW5 = 2 };
 
+// Few rows that the kernel quantizes itself: their bytes in LDS, filled up to whole blocks.
+constexpr int kFewBytes = 16384;
+
 // X is t.A and W is t.B[0], both k-contiguous; t.K is a multiple of 16.
 struct ScaledArgs {
     TileArgs t;
@@ -19,12 +22,14 @@ struct ScaledArgs {
     const void *SW;
     int64_t sw_row, sw_block;
     int w_shift;               // rows of W per scale: 1 << w_shift
+    int x_cols;                // few rows: X is the result's type and has that many columns, or 0
 };
 
 struct ScaledPlan {
     TilePlan tile;
     ScaledFormats formats;
     int scale;
+    bool make;                             // few rows: the kernel quantizes X itself
     size_t values_bytes, scales_bytes;     // workspace of a quantized X
     int64_t ldx, sx_block;                 // its layout
     size_t total;
