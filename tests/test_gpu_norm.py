@@ -287,12 +287,10 @@ def test_same_bits_every_time():
 
 def test_poisoned_lds(monkeypatch):
     import tiling_roofline_analysis_amd.fused as fused
-    import tiling_roofline_analysis_amd.norms as norms
     poisoned = tra.load_poisoned()
     cases = [(9, 100, "rms"), (40, 1000, "layer"), (7, 4096, "rms"), (5, 9001, "layer")]
     want = [check_all(M, D, torch.bfloat16, torch.float32, k, "rms") for M, D, k in cases]
     monkeypatch.setattr(fused, "load", lambda: poisoned)
-    monkeypatch.setattr(norms, "load", lambda: poisoned)
     for (M, D, k), (_, outs, grads) in zip(cases, want):
         _, o, g = check_all(M, D, torch.bfloat16, torch.float32, k, "rms")
         assert all(torch.equal(o[n], outs[n]) for n in outs)

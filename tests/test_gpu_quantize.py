@@ -185,9 +185,9 @@ def test_what_the_values_stand_for():
 
 
 def test_poisoned_lds(monkeypatch):
-    import tiling_roofline_analysis_amd.scaled as scaled
+    import tiling_roofline_analysis_amd.fused as fused
     poisoned = tra.load_poisoned()
-    monkeypatch.setattr(scaled, "load", lambda: poisoned)
+    monkeypatch.setattr(fused, "load", lambda: poisoned)
     for size in ((1, 300), (130, 257), (300, 129)):
         for block_rows in (1, 128):
             check(normal(*size, torch.bfloat16), block_rows=block_rows)

@@ -151,6 +151,16 @@ def _call(name, fmt, fields, device, count=7):
         raise TraError(st, name)
 
 
+def _launch(name, packed, index):
+    """A call that takes no workspace, on torch's current stream of device `index`."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _launch(name, packed, index)
+    st = getattr(load(), name)(packed, torch._C._cuda_getCurrentRawStream(index))
+    if st != TRA_OK:
+        raise TraError(st, name)
+
+
 _KEEP = object()
 
 

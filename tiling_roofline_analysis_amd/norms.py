@@ -24,8 +24,7 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import TRA_OK, TraError, load
-from .fused import (DTYPES, _call, _matrix, _no_capture, _on, _recorded_elsewhere, _rows,
+from .fused import (DTYPES, _call, _launch, _matrix, _no_capture, _on, _recorded_elsewhere, _rows,
                     _wants_grad, _written)
 
 # tra_norm_kind
@@ -49,42 +48,45 @@ def _kind(kind, name, least=0) -> int:
     return code
 
 
-def _vectors(vectors, x):
+def _vectors(vectors, x, M, D):
     """Checks the vectors; returns (type, groups, addresses, strides of their rows)."""
-    M, D = x.shape
+    device, own = x.device, x.dtype
     dtype, groups = None, 1
     at, ld = [0] * 5, [0] * 5
     for i, v in enumerate(vectors):
         if v is None:
             continue
-        name = _VECTORS[i]
         if not isinstance(v, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if v.device != x.device or (v.dtype != x.dtype and v.dtype != torch.float32):
-            raise TypeError(f"{name} must be a {x.dtype} or float32 tensor on {x.device}")
-        if dtype is None:
+            raise TypeError(f"{_VECTORS[i]} must be a torch.Tensor")
+        if v.dtype is not dtype:
+            if dtype is not None:
+                raise TypeError("weights, biases and gates must be of one type")
             dtype = v.dtype
-        elif v.dtype != dtype:
-            raise TypeError("weights, biases and gates must be of one type")
-        shape, stride = v.shape, v.stride()
+            if dtype is not own and dtype is not torch.float32:
+                raise TypeError(f"{_VECTORS[i]} must be {own} or float32")
+        if v.device != device:
+            raise TypeError(f"{_VECTORS[i]} must be on {device}")
+        shape = v.shape
         n = len(shape)
         if n not in (1, 2) or shape[-1] != D or (n == 2 and shape[0] < 1):
-            raise ValueError(f"{name} must have {D} elements, or a row of them per sequence")
-        if D > 1 and stride[-1] != 1:
-            raise ValueError(f"{name} must have contiguous rows")
+            raise ValueError(f"{_VECTORS[i]} must have {D} elements, or a row of them per sequence")
+        if not v.is_contiguous() and D > 1 and v.stride(-1) != 1:
+            raise ValueError(f"{_VECTORS[i]} must have contiguous rows")
         if n == 2 and shape[0] > 1:
             if M % shape[0] != 0 or groups not in (1, shape[0]):
-                raise ValueError(f"{name} has {shape[0]} rows: not one for each of some equal "
-                                 f"parts of {M} rows, or not as many as another vector's")
-            if stride[0] < max(1, D):
-                raise ValueError(f"{name} must be row-major")
+                raise ValueError(f"{_VECTORS[i]} has {shape[0]} rows: not one for each of some "
+                                 f"equal parts of {M} rows, or not as many as another vector's")
+            if v.stride(0) < max(1, D):
+                raise ValueError(f"{_VECTORS[i]} must be row-major")
             groups = shape[0]
-            ld[i] = stride[0]
+            ld[i] = v.stride(0)
         at[i] = v.data_ptr()
-    return DTYPES[x.dtype if dtype is None else dtype], groups, at, ld
+    return DTYPES[own if dtype is None else dtype], groups, at, ld
 
 
 def _number(v, name) -> float:
+    if type(v) is float:
+        return v
     if isinstance(v, torch.Tensor):
         raise TypeError(f"{name} must be a number")
     return float(v)
@@ -101,33 +103,32 @@ def _given(t, name, x):
 def _fields(x, h, vectors, kind, post, scale, eps):
     """The arguments that both directions begin with."""
     ldx = _matrix(x, "x")
+    M, D = x.shape
     H, ldh = (0, 0) if h is None else _given(h, "h", x)
-    pdtype, groups, at, ld = _vectors(vectors, x)
-    return (DTYPES[x.dtype], pdtype, kind, post, x.shape[0], x.shape[1], groups, scale, eps,
-            x.data_ptr(), ldx, H, ldh, *at, *ld)
+    pdtype, groups, at, ld = _vectors(vectors, x, M, D)
+    return (DTYPES[x.dtype], pdtype, kind, post, M, D, groups, scale, eps, x.data_ptr(), ldx, H,
+            ldh, *at, *ld)
 
 
 def _forward(x, h, vectors, kind, post, scale, eps, r=None, y=None):
     """One forward call; returns (r, y), None for what there is not."""
     fields = _fields(x, h, vectors, kind, post, scale, eps)
-    R = ldr = Y = ldy = 0
+    M, D = fields[4], fields[5]
+    R = Y = 0
+    ldr = ldy = D
     if h is not None:
         if r is None:
-            r = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        R, ldr = _given(r, "r_out", x)
+            r = x.new_empty(M, D)
+            R = r.data_ptr()
+        else:
+            R, ldr = _given(r, "r_out", x)
     if kind:
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        Y, ldy = _given(y, "out", x)
-    packed = _ARGS.pack(*fields, R, ldr, Y, ldy)
-    device = x.device
-    if torch.cuda.current_device() == device.index:
-        st = load().tra_norm(packed, torch._C._cuda_getCurrentRawStream(device.index))
-    else:
-        with torch.cuda.device(device):
-            st = load().tra_norm(packed, torch._C._cuda_getCurrentRawStream(device.index))
-    if st != TRA_OK:
-        raise TraError(st, "tra_norm")
+            y = x.new_empty(M, D)
+            Y = y.data_ptr()
+        else:
+            Y, ldy = _given(y, "out", x)
+    _launch("tra_norm", _ARGS.pack(*fields, R, ldr, Y, ldy), x.device.index)
     return r, y
 
 
@@ -139,12 +140,12 @@ def _backward(dr, dy, x, h, vectors, kind, post, scale, eps, need_dx, need_dh, n
     dx = dh = None
     X = H = 0
     if need_dx:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = x.new_empty(x.shape)
         X = dx.data_ptr()
     if need_dh and h is not None:
-        dh = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dh = x.new_empty(x.shape)
         H = dh.data_ptr()
-    grads = [torch.empty(v.shape, dtype=v.dtype, device=v.device) if v is not None and n else None
+    grads = [v.new_empty(v.shape) if v is not None and n else None
              for v, n in zip(vectors, need)]
     D = x.shape[1]
     _call("tra_norm_backward", _GRAD_ARGS,

@@ -27,9 +27,8 @@ import struct
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import TRA_OK, TraError, _row_major_ld, load
-from . import fused
-from .fused import (DTYPES, _matrix, _no_capture, _on, _recorded_elsewhere, _rows, _vector,
+from . import _row_major_ld, fused
+from .fused import (DTYPES, _launch, _matrix, _no_capture, _on, _recorded_elsewhere, _rows, _vector,
                     _wants_grad, _weight, _written)
 
 # tra_fp8, tra_scale
@@ -64,24 +63,13 @@ def _block_rows(block) -> int:
     raise ValueError(f"block must be (1, 128) or (128, 128); got {block!r}")
 
 
-def _empty(rows, cols, block_rows, dtype, scale_dtype, device):
+def _empty(x, rows, cols, block_rows, dtype, scale_dtype):
     """An 8-bit matrix: values, scales and the scales' strides.  Scales of rows lie next
     to each other for one block of columns: a product reads them so."""
-    values = torch.empty((rows, _up(cols, 16) * 16), dtype=dtype, device=device)
+    values = x.new_empty(rows, _up(cols, 16) * 16, dtype=dtype)
     r, b = _up(rows, block_rows), _up(cols, BLOCK)
-    if block_rows == 1:
-        return values, torch.empty((b, r), dtype=scale_dtype, device=device).t(), 1, r
-    return values, torch.empty((r, b), dtype=scale_dtype, device=device), b, 1
-
-
-def _call(name, packed, device):
-    if torch.cuda.current_device() == device.index:
-        st = getattr(load(), name)(packed, torch._C._cuda_getCurrentRawStream(device.index))
-    else:
-        with torch.cuda.device(device):
-            st = getattr(load(), name)(packed, torch._C._cuda_getCurrentRawStream(device.index))
-    if st != TRA_OK:
-        raise TraError(st, name)
+    stride = (1, max(1, r)) if block_rows == 1 else (max(1, b), 1)
+    return values, x.new_empty_strided((r, b), stride, dtype=scale_dtype), *stride
 
 
 def _quantize(x, block_rows, dtype, scale_dtype, rows, columns):
@@ -93,11 +81,12 @@ def _quantize(x, block_rows, dtype, scale_dtype, rows, columns):
         if not want:
             fields += [0, 0, 0, 0, 0]
             continue
-        values, scales, ss_row, ss_block = _empty(r, c, block_rows, dtype, scale_dtype, x.device)
+        values, scales, ss_row, ss_block = _empty(x, r, c, block_rows, dtype, scale_dtype)
         fields += [values.data_ptr(), values.shape[1], scales.data_ptr(), ss_row, ss_block]
         got += [values, scales]
-    _call("tra_quantize", _QUANTIZE.pack(DTYPES[x.dtype], FP8[dtype], SCALES[scale_dtype],
-                                         block_rows, M, K, x.data_ptr(), ldx, *fields), x.device)
+    _launch("tra_quantize", _QUANTIZE.pack(DTYPES[x.dtype], FP8[dtype], SCALES[scale_dtype],
+                                           block_rows, M, K, x.data_ptr(), ldx, *fields),
+            x.device.index)
     return got
 
 
@@ -130,62 +119,68 @@ def quantize(x, block=(1, 128), dtype=torch.float8_e4m3fn, scale_dtype=torch.flo
 
 # --- products ---------------------------------------------------------------------
 
-def _values(t, name, rows, device):
-    """Checks 8-bit values, rows x K; returns their leading dimension."""
-    if t.dim() != 2 or t.device != device or not t.is_cuda:
-        raise TypeError(f"{name} must be a 2-D tensor on {device}")
-    if rows is not None and t.shape[0] != rows:
-        raise ValueError(f"{name} must have {rows} rows")
-    K = t.shape[1]
+def _values(t, name, rows, K, stride, device):
+    """Checks 8-bit values, rows x K with these strides; returns their leading dimension."""
+    if t.device != device or not t.is_cuda:
+        raise TypeError(f"{name} must be on {device}")
     if K % 16 != 0:
-        raise ValueError(f"{name} must have a multiple of 16 columns (zeros at the end, as quantize "
-                         "leaves them)")
-    s0, s1 = t.stride()
-    ld = s0 if s1 == 1 and s0 >= K > 0 else _row_major_ld((t.shape[0], K), (s0, s1), name)
-    if K > 0 and ((ld % 16 != 0 and t.shape[0] > 1) or t.data_ptr() % 16 != 0):
+        raise ValueError(f"rows of {name} must be a multiple of 16 long (zeros at the end, as "
+                         "quantize leaves them)")
+    s0, s1 = stride
+    ld = s0 if s1 == 1 and s0 >= K > 0 else _row_major_ld((rows, K), stride, name)
+    if K > 0 and ((ld % 16 != 0 and rows > 1) or t.data_ptr() % 16 != 0):
         raise ValueError(f"rows of {name} must start 16-byte aligned")
     return ld
 
 
-def _scales(s, name, rows, cols, device):
-    """Checks scales of rows x cols values; returns (block rows, type, row's and block's
-    strides)."""
-    if not isinstance(s, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if s.dim() != 2 or s.dtype not in SCALES or s.device != device:
-        raise TypeError(f"{name} must be a 2-D float32 or float8_e8m0fnu tensor on {device}")
+def _scales(s, name, shape, stride, rows, cols, device):
+    """Checks scales, of this shape and strides, of rows x cols values; returns (block rows,
+    type, row's and block's strides)."""
+    if s.dtype not in SCALES or s.device != device:
+        raise TypeError(f"{name} must be a float32 or float8_e8m0fnu tensor on {device}")
     blocks = _up(cols, BLOCK)
-    if s.shape[1] != blocks or s.shape[0] not in (rows, _up(rows, BLOCK)):
-        raise ValueError(f"{name} must be {rows} or {_up(rows, BLOCK)} x {blocks}")
+    if shape[1] != blocks or shape[0] not in (rows, _up(rows, BLOCK)):
+        raise ValueError(f"{name} must be of {rows} or {_up(rows, BLOCK)} rows by {blocks} blocks")
     # (of a single row, either is the same)
-    block_rows = 1 if s.shape[0] == rows and rows > 1 else BLOCK
-    ss_row, ss_block = s.stride()
-    if s.shape[0] > 1 and blocks > 1 and ss_row != 1 and ss_block != 1:
+    block_rows = 1 if shape[0] == rows and rows > 1 else BLOCK
+    ss_row, ss_block = stride
+    if ss_row != 1 and ss_block != 1 and shape[0] > 1 and blocks > 1:
         raise ValueError(f"{name} must have contiguous rows or columns")
     return block_rows, SCALES[s.dtype], ss_row, ss_block
 
 
-def _product(x, x_scales, w, w_scales, bias, residual, dtype, out, x_fp8=None):
-    """x w^T + bias + residual: w N x K values; x values with scales, or a tensor."""
+def _two_dim(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D torch.Tensor")
+
+
+def _product(x, x_scales, w, w_scales, bias, residual, dtype, out):
+    """x w + bias + residual: w K x N, the transposed view of values, w_scales of theirs; x
+    values with scales, or a tensor."""
     device = x.device
-    if not isinstance(w, torch.Tensor) or w.dtype not in FP8:
+    if w.dtype not in FP8:
         raise TypeError("w must be 8-bit values")
-    ldw = _values(w, "w", None, device)
-    N, K = w.shape
-    block_rows, scale, sw_row, sw_block = _scales(w_scales, "w_scales", N, K, device)
+    _two_dim(x, "x")
+    _two_dim(w, "w")
+    _two_dim(w_scales, "w_scales")
+    K, N = w.shape
+    ldw = _values(w, "w", N, K, w.stride()[::-1], device)
+    block_rows, scale, sw_row, sw_block = _scales(w_scales, "w_scales", w_scales.shape[::-1],
+                                                  w_scales.stride()[::-1], N, K, device)
+    M, kx = x.shape
     if x_scales is None:
         ldx = _matrix(x, "x")
-        M, kx = x.shape
         if _up(kx, 16) * 16 != K:
-            raise ValueError(f"inner dimensions differ: x has {kx} columns, w {K}")
-        head = (DTYPES[x.dtype], FP8[torch.float8_e4m3fn if x_fp8 is None else x_fp8])
+            raise ValueError(f"inner dimensions differ: x has {kx} columns, w {K} rows")
+        head = (DTYPES[x.dtype], 0)
         sx = (0, 0, 0)
     else:
-        ldx = _values(x, "x", None, device)
-        M, kx = x.shape
+        ldx = _values(x, "x", M, kx, x.stride(), device)
         if kx != K:
-            raise ValueError(f"inner dimensions differ: x has {kx} columns, w {K}")
-        one, kind, sx_row, sx_block = _scales(x_scales, "x_scales", M, K, device)
+            raise ValueError(f"inner dimensions differ: x has {kx} columns, w {K} rows")
+        _two_dim(x_scales, "x_scales")
+        one, kind, sx_row, sx_block = _scales(x_scales, "x_scales", x_scales.shape,
+                                              x_scales.stride(), M, K, device)
         if (one != 1 and M > 1) or kind != scale:
             raise ValueError("x_scales must have a row for each of x's, and w_scales' type")
         head = (X_SCALED, FP8[x.dtype])
@@ -195,25 +190,26 @@ def _product(x, x_scales, w, w_scales, bias, residual, dtype, out, x_fp8=None):
     w_fp8 = FP8[w.dtype]
     if w_fp8 and (head[1] or scale == 0 or x_scales is None):
         raise ValueError("float8_e5m2 w goes with float8_e4m3fn x and float8_e8m0fnu scales only")
-    like = x if x.dtype == dtype else torch.empty(0, dtype=dtype, device=device)
+    like = x if x.dtype is dtype else x.new_empty(0, dtype=dtype)
+    B = R = 0
+    ldr = ldy = N
     if bias is not None:
         _vector(bias, "bias", like, N)
-    R, ldr = 0, 0
+        B = bias.data_ptr()
     if residual is not None:
         ldr = _matrix(residual, "residual", like)
         if residual.shape[0] != M or residual.shape[1] != N:
             raise ValueError(f"residual must be {M} x {N}")
         R = residual.data_ptr()
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=device)
-        ldy = N
+        out = like.new_empty(M, N)
     else:
         ldy = _matrix(out, "out", like)
         if out.shape[0] != M or out.shape[1] != N:
             raise ValueError(f"out must be {M} x {N}")
     fields = (DTYPES[dtype], *head, w_fp8, scale, block_rows, M, N, kx, x.data_ptr(), ldx, *sx,
-              w.data_ptr(), ldw, w_scales.data_ptr(), sw_row, sw_block,
-              0 if bias is None else bias.data_ptr(), R, ldr, out.data_ptr(), ldy)
+              w.data_ptr(), ldw, w_scales.data_ptr(), sw_row, sw_block, B, R, ldr, out.data_ptr(),
+              ldy)
     fused._call("tra_scaled_linear", _SCALED, fields, device, 9)
     return out
 
@@ -255,12 +251,12 @@ def _gradients(dy, xt, wt, K, transposed, grad_dtype, need_dx, need_dw, need_dbi
     dx = dw = None
     rows, columns = _activations(dy, grad_dtype, need_dx, need_dw)
     if need_dx:
-        dx = _product(rows[0], rows[1], wt[0], wt[1], None, None, dy.dtype, None)
+        dx = _product(*rows, wt[0].t(), wt[1].t(), None, None, dy.dtype, None)
     if need_dw:
         if transposed:
-            dw = _product(columns[0], columns[1], xt[0], xt[1], None, None, dy.dtype, None).t()
+            dw = _product(*columns, xt[0].t(), xt[1].t(), None, None, dy.dtype, None).t()
         else:
-            dw = _product(xt[0], xt[1], columns[0], columns[1], None, None, dy.dtype, None)
+            dw = _product(*xt, columns[0].t(), columns[1].t(), None, None, dy.dtype, None)
     return dx, dw, _column_sums(dy) if need_dbias else None
 
 
@@ -275,7 +271,7 @@ class _ScaledLinear(torch.autograd.Function):
         need_x, need_w = ctx.needs_input_grad[:2]
         xq, xt = _activations(x, torch.float8_e4m3fn, True, need_w)
         wq, wt = _weights(w, True, need_x)
-        y = _product(xq[0], xq[1], wq[0], wq[1], bias, residual, x.dtype, None)
+        y = _product(*xq, wq[0].t(), wq[1].t(), bias, residual, x.dtype, None)
         ctx.plan = (x.shape[1], _is_transposed(w), grad_dtype)
         ctx.save_for_backward(*(xt or (None, None)), *(wt or (None, None)))
         return y
@@ -344,12 +340,11 @@ def scaled_linear(x, w, x_scales=None, w_scales=None, bias=None, residual=None, 
                 raise ValueError("out cannot be given where gradients are recorded")
             return _ScaledLinear.apply(x, w, bias, residual, grad_dtype)
         (wq, ws), _ = _weights(w, True, False)
-    else:
-        if wants:
-            raise ValueError("gradients cannot be recorded with quantized weights: give w as a "
-                             "tensor, or use torch.no_grad()")
-        wq, ws = w.t(), w_scales.t()
-    y = _product(x, x_scales, wq, ws, bias, residual, dtype, out)
+        w, w_scales = wq.t(), ws.t()
+    elif wants:
+        raise ValueError("gradients cannot be recorded with quantized weights: give w as a "
+                         "tensor, or use torch.no_grad()")
+    y = _product(x, x_scales, w, w_scales, bias, residual, dtype, out)
     if out is not None:
         _written(out)
     return y
