@@ -152,6 +152,28 @@ __device__ __forceinline__ void store_row(T *p, const float (&v)[V]) {
     }
 }
 
+// A chunk's elements from `over` on, moved to its front, with zeros behind: over from 0
+// (as it is) to all of them.  In 32-bit steps only: as a shift of 128 bits it becomes
+// 64-bit shifts whose amount is in a VGPR, and where that is the last VGPR the kernel
+// has, gfx950 has taken v0 for it now and then (linear_few with 80 VGPRs shifted the
+// last chunk of K by its lane number, in one workgroup of some process's first calls).
+template <typename T>
+__device__ __forceinline__ u32x4 drop_elements(u32x4 v, int over) {
+    constexpr int PER = 4 / static_cast<int>(sizeof(T));     // elements of a dword
+    if constexpr (PER == 2) {
+        const uint32_t bits = over & 1 ? 16 : 0;
+        v = u32x4{__builtin_amdgcn_alignbit(v[1], v[0], bits),
+                  __builtin_amdgcn_alignbit(v[2], v[1], bits),
+                  __builtin_amdgcn_alignbit(v[3], v[2], bits),
+                  __builtin_amdgcn_alignbit(0, v[3], bits)};
+    }
+    const bool one = over & PER, two = over & (2 * PER), all = over & (4 * PER);
+    const uint32_t low = one ? v[1] : v[0], high = one ? v[3] : v[2];
+    const uint32_t mid = one ? v[2] : v[1], top = one ? 0u : v[3];
+    return u32x4{all ? 0u : two ? high : low, all ? 0u : two ? top : mid,
+                 all || two ? 0u : high, all || two ? 0u : top};
+}
+
 // The same for a row that ends after `valid` of the V elements (the others
 // read as zero).
 template <typename T, int V>

@@ -86,51 +86,88 @@ __device__ __forceinline__ float lanes_sum(float v) {
 template <int LANES, int BLOCK>
 struct RowSum {
     static constexpr int WAVES = LANES / 64;     // of a row
-    float *lds;                                  // 2 * (BLOCK / 64) pairs
+    float *lds;                                  // 2 * (BLOCK / 64) pairs, 16-byte aligned
     int turn = 0;
 
-    __device__ __forceinline__ void operator()(float &a, float &b) {
-        a = lanes_sum<LANES < 64 ? LANES : 64>(a);
-        b = lanes_sum<LANES < 64 ? LANES : 64>(b);
+    // N sums at once.
+    template <int N>
+    __device__ __forceinline__ void all(float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = lanes_sum<LANES < 64 ? LANES : 64>(v[i]);
         if constexpr (WAVES > 1) {
             float *place = lds + turn * (BLOCK / 64) * 2;
             turn ^= 1;
             const int wave = static_cast<int>(threadIdx.x >> 6);
             if ((threadIdx.x & 63) == 0) {
-                place[2 * wave] = a;
-                place[2 * wave + 1] = b;
+#pragma unroll
+                for (int i = 0; i < N; ++i) place[wave * N + i] = v[i];
             }
             __syncthreads();
-            const float *row = place + wave / WAVES * WAVES * 2;
-            a = b = 0.0f;
+            const float *row = place + wave / WAVES * WAVES * N;
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) {
-                a += row[2 * w];
-                b += row[2 * w + 1];
-            }
+            for (int i = 0; i < N; ++i) v[i] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] += row[w * N + i];
         }
     }
+    __device__ __forceinline__ void operator()(float &a, float &b) {
+        float v[2] = {a, b};
+        all(v);
+        a = v[0];
+        b = v[1];
+    }
     __device__ __forceinline__ float operator()(float a) {
-        float b = 0.0f;
-        (*this)(a, b);
-        return a;
+        float v[1] = {a};
+        all(v);
+        return v[0];
     }
 };
 
 // ---- a lane's part of a row ---------------------------------------------------------------
 
 // Chunk c of a lane: V elements from (c * LANES + lane) * V on, zeros past the row's end.
-template <typename T, int V, int LANES, int E>
-__device__ __forceinline__ void load_lane(const void *row, int lane, int64_t D, float (&v)[E]) {
+// RAGGED: the row may end inside a chunk.  It has V elements or more, so every load is of V
+// elements inside the row: a chunk past the end is read where it ends with the row and
+// moved into place afterwards.  (With a path of its own for such a chunk the compiler waits
+// for each load where the paths meet: the four rows that the backward pass reads came one
+// after the other, 5.5 us a row of 4096 instead of 4.8.)
+template <typename T, int LANES, int E, bool RAGGED>
+struct LanePart {
+    static constexpr int V = kChunk<T>;
+    u32x4 chunk[E / V];
+
+    __device__ __forceinline__ void load(const void *row, int lane, int D) {
 #pragma unroll
-    for (int c = 0; c < E / V; ++c) {
-        const int64_t at = (static_cast<int64_t>(c) * LANES + lane) * V;
-        float t[V];
-        load_part<T, V>(static_cast<const T *>(row) + at, D - at, t);
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[c * V + e] = t[e];
+        for (int c = 0; c < E / V; ++c) {
+            const int at = (c * LANES + lane) * V;
+            const T *p = static_cast<const T *>(row);
+            if constexpr (RAGGED) {
+                __builtin_memcpy(&chunk[c], p + (at < D - V ? at : D - V), 16);
+            } else {
+                chunk[c] = u32x4{};
+                if (at < D) __builtin_memcpy(&chunk[c], p + at, 16);
+            }
+        }
     }
-}
+    __device__ __forceinline__ void get(int lane, int D, float (&v)[E]) {
+        if (RAGGED && D < LANES * E) {
+#pragma unroll
+            for (int c = 0; c < E / V; ++c) {
+                const int over = (c * LANES + lane + 1) * V - D;
+                chunk[c] = drop_elements<T>(chunk[c], over < 0 ? 0 : over < V ? over : V);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < E / V; ++c) {
+            T t[V];
+            __builtin_memcpy(t, &chunk[c], 16);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[c * V + e] = static_cast<float>(t[e]);
+        }
+    }
+};
 
 template <typename T, int V, int LANES, int E>
 __device__ __forceinline__ void store_lane(void *row, int lane, int64_t D, const float (&v)[E]) {
@@ -184,25 +221,21 @@ __device__ __forceinline__ const P *vector_row(const void *v, int64_t ld, int64_
     return static_cast<const P *>(v) + group * ld;
 }
 
-// v *= vector, v += vector: nothing where there is none.
-template <typename P, int V, int LANES, int E>
-__device__ __forceinline__ void times(float (&v)[E], const void *vec, int64_t ld, int64_t group,
-                                      int lane, int64_t D) {
-    if (vec == nullptr) return;
-    float t[E];
-    load_lane<P, V, LANES>(vector_row<P>(vec, ld, group), lane, D, t);
+// A lane's part of a vector (of its own element type P, the rows' being T).  It is waited
+// for where it is loaded, which is where it is used.
+template <typename T, typename P, int LANES, int E>
+__device__ __forceinline__ void vector_lane(const void *vec, int64_t ld, int64_t group, int lane,
+                                            int D, float (&v)[E]) {
+    constexpr int V = kChunk<T>;
+    const P *row = vector_row<P>(vec, ld, group);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= t[e];
-}
-
-template <typename P, int V, int LANES, int E>
-__device__ __forceinline__ void plus(float (&v)[E], const void *vec, int64_t ld, int64_t group,
-                                     int lane, int64_t D) {
-    if (vec == nullptr) return;
-    float t[E];
-    load_lane<P, V, LANES>(vector_row<P>(vec, ld, group), lane, D, t);
+    for (int c = 0; c < E / V; ++c) {
+        const int at = (c * LANES + lane) * V;
+        float t[V];
+        load_part<P, V>(row + at, D - at, t);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] += t[e];
+        for (int e = 0; e < V; ++e) v[c * V + e] = t[e];
+    }
 }
 
 template <int LANES>
@@ -210,40 +243,58 @@ constexpr int kBlock = LANES < 256 ? 256 : LANES;
 
 // ---- forward ------------------------------------------------------------------------------
 
-template <typename T, typename P, int LANES, int E>
-__global__ __launch_bounds__(kBlock<LANES>) void norm_forward(const NormArgs p) {
+// What hides the memory's latency is the number of waves: 8 a SIMD, where the VGPRs allow it.
+template <typename T, typename P, int LANES, int E, bool RAGGED>
+__global__ __launch_bounds__(kBlock<LANES>, RAGGED ? 4 : LANES < 256 ? 7 : 8) void norm_forward(const NormArgs p) {
     constexpr int V = kChunk<T>, BLOCK = kBlock<LANES>, ROWS = BLOCK / LANES;
-    __shared__ float lds[4 * (BLOCK / 64)];
+    __shared__ __align__(16) float lds[4 * (BLOCK / 64)];
     lds_poison(lds, 4 * (BLOCK / 64));
     RowSum<LANES, BLOCK> sum{lds};
-    const int lane = static_cast<int>(threadIdx.x) % LANES;
+    const int lane = static_cast<int>(threadIdx.x) % LANES, D = static_cast<int>(p.D);
     const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
     for (int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS; first < p.M; first += step) {
         const int64_t own = first + static_cast<int>(threadIdx.x) / LANES;
         const bool inside = own < p.M;          // (a row past the last takes part, unseen)
         const int64_t m = inside ? own : p.M - 1;
         const int64_t group = m / p.per_group;
+        LanePart<T, LANES, E, RAGGED> px, ph;
+        px.load(static_cast<const T *>(p.X) + m * p.ldx, lane, D);
+        if (p.H != nullptr) ph.load(static_cast<const T *>(p.H) + m * p.ldh, lane, D);
+        auto times = [&](float (&v)[E], const void *vec, int64_t ld) __attribute__((always_inline)) {
+            if (vec == nullptr) return;
+            float t[E];
+            vector_lane<T, P, LANES>(vec, ld, group, lane, D, t);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] *= t[e];
+        };
+        auto plus = [&](float (&v)[E], const void *vec, int64_t ld) __attribute__((always_inline)) {
+            if (vec == nullptr) return;
+            float t[E];
+            vector_lane<T, P, LANES>(vec, ld, group, lane, D, t);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] += t[e];
+        };
         float x[E];
-        load_lane<T, V, LANES>(static_cast<const T *>(p.X) + m * p.ldx, lane, p.D, x);
+        px.get(lane, D, x);
         if (p.H != nullptr) {
             float h[E];
-            load_lane<T, V, LANES>(static_cast<const T *>(p.H) + m * p.ldh, lane, p.D, h);
+            ph.get(lane, D, h);
             if (p.post != TRA_NORM_NONE) {
                 normalize<V, LANES>(h, p.post, p, lane, sum);
-                times<P, V, LANES>(h, p.post_weight, p.ld_post_weight, group, lane, p.D);
-                plus<P, V, LANES>(h, p.post_bias, p.ld_post_bias, group, lane, p.D);
+                times(h, p.post_weight, p.ld_post_weight);
+                plus(h, p.post_bias, p.ld_post_bias);
             }
-            times<P, V, LANES>(h, p.gate, p.ld_gate, group, lane, p.D);
+            times(h, p.gate, p.ld_gate);
 #pragma unroll
             for (int e = 0; e < E; ++e) x[e] = p.scale * x[e] + h[e];
             if (p.R != nullptr && inside)
-                store_lane<T, V, LANES>(static_cast<T *>(p.R) + m * p.ldr, lane, p.D, x);
+                store_lane<T, V, LANES>(static_cast<T *>(p.R) + m * p.ldr, lane, D, x);
         }
         if (p.norm != TRA_NORM_NONE) {
             normalize<V, LANES>(x, p.norm, p, lane, sum);
-            times<P, V, LANES>(x, p.weight, p.ld_weight, group, lane, p.D);
-            plus<P, V, LANES>(x, p.bias, p.ld_bias, group, lane, p.D);
-            if (inside) store_lane<T, V, LANES>(static_cast<T *>(p.Y) + m * p.ldy, lane, p.D, x);
+            times(x, p.weight, p.ld_weight);
+            plus(x, p.bias, p.ld_bias);
+            if (inside) store_lane<T, V, LANES>(static_cast<T *>(p.Y) + m * p.ldy, lane, D, x);
         }
     }
 }
@@ -343,7 +394,7 @@ struct WideRow {
 template <typename T, typename P>
 __global__ __launch_bounds__(kWideLanes) void norm_forward_wide(const NormArgs p) {
     constexpr int V = kChunk<T>;
-    __shared__ float lds[4 * (kWideLanes / 64)];
+    __shared__ __align__(16) float lds[4 * (kWideLanes / 64)];
     lds_poison(lds, 4 * (kWideLanes / 64));
     RowSum<kWideLanes, kWideLanes> sum{lds};
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
@@ -373,6 +424,39 @@ __global__ __launch_bounds__(kWideLanes) void norm_forward_wide(const NormArgs p
 
 // ---- backward, rows in registers -----------------------------------------------------------------
 
+// v: a row; g: the gradient of its norm's normalized row n.  v becomes n, and g the
+// gradient of v, both 0 past the row's end.  The sums that depend on v only through its
+// deviation are taken along with the one for that.
+template <int V, int LANES, int E, typename Sum>
+__device__ __forceinline__ void normalize_both(float (&v)[E], float (&g)[E], int kind,
+                                               const NormArgs &p, int lane, Sum &sum) {
+    if (kind == TRA_NORM_LAYER) {
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            a += v[e];
+            b += g[e];
+        }
+        sum(a, b);
+        subtract_mean<V, LANES>(v, a * p.inv_d, lane, p.D);
+        subtract_mean<V, LANES>(g, b * p.inv_d, lane, p.D);
+    }
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        a += v[e] * v[e];
+        b += g[e] * v[e];
+    }
+    sum(a, b);
+    const float inverse = inverse_deviation(a * p.inv_d, p.eps);
+    const float along = b * inverse * p.inv_d;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        v[e] *= inverse;
+        g[e] = inverse * (g[e] - v[e] * along);
+    }
+}
+
 // g: the gradient of a norm's normalized row n; becomes that of the row before it (0
 // past the row's end, as it was).
 template <int V, int LANES, int E, typename Sum>
@@ -393,81 +477,125 @@ __device__ __forceinline__ void normalize_gradient(float (&g)[E], const float (&
 }
 
 // A workgroup takes a chunk of rows of one group, ROWS at a time, and keeps the sums of
-// the vectors' gradients in registers until its end.
-template <typename T, typename P, int LANES, int E>
-__global__ __launch_bounds__(kBlock<LANES>) void norm_backward(const NormGradArgs q) {
-    constexpr int V = kChunk<T>, BLOCK = kBlock<LANES>, ROWS = BLOCK / LANES;
+// the vectors' gradients in registers until its end.  There are about as many chunks as
+// CUs, since each costs a row of sums in memory, so a CU has one workgroup.
+// POST: there is a norm of H.
+// BIAS: gradients of biases are asked for.
+constexpr int kBackwardBlock = 512;
+// Workgroups a CU that the VGPRs leave room for.
+constexpr int backward_per_cu(int64_t bytes, int64_t D, bool bias) {
+    return bytes == 2 && D <= 4096 && !bias ? 2 : 1;
+}
+
+template <typename T, typename P, int LANES, int E, bool POST, bool BIAS>
+__global__ __launch_bounds__(kBackwardBlock, (2 * backward_per_cu(sizeof(T), LANES * E, BIAS))) void norm_backward(const NormGradArgs q) {
+    constexpr int V = kChunk<T>, BLOCK = kBackwardBlock, ROWS = BLOCK / LANES;
     const NormArgs &p = q.f;
-    __shared__ float lds[4 * (BLOCK / 64)];
+    __shared__ __align__(16) float lds[4 * (BLOCK / 64)];
     __shared__ float part[ROWS > 1 ? (ROWS - 1) * LANES * E : 1];
+    __shared__ __align__(16) float vectors[POST ? 4 : 2][LANES * E];
+    lds_poison(&vectors[0][0], (POST ? 4 : 2) * LANES * E);
     lds_poison(lds, 4 * (BLOCK / 64));
     lds_poison(part, ROWS > 1 ? (ROWS - 1) * LANES * E : 1);
     RowSum<LANES, BLOCK> sum{lds};
     const int lane = static_cast<int>(threadIdx.x) % LANES;
-    const int sub = static_cast<int>(threadIdx.x) / LANES;
+    const int sub = static_cast<int>(threadIdx.x) / LANES, D = static_cast<int>(p.D);
     const int64_t group = blockIdx.x / q.chunks_per_group;
     const int64_t chunk = blockIdx.x - group * q.chunks_per_group;
     const int64_t begin = group * p.per_group + chunk * q.rows_per_chunk;
     const int64_t stop = (group + 1) * p.per_group;
     const int64_t end = begin + q.rows_per_chunk < stop ? begin + q.rows_per_chunk : stop;
-    float total[kVectors][E] = {};
+    constexpr int SUMS = POST ? BIAS ? kVectors : kPostWeight + 1 : kGate + 1;
+    float total[SUMS][E] = {};
+
+    // The group's vectors, in LDS: waiting for a load from memory would wait for the rows
+    // loaded ahead, too.
+    auto keep = [&](float (&to)[LANES * E], const void *vec, int64_t ld, float none)
+                    __attribute__((always_inline)) {
+        float t[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) t[e] = none;
+        if (vec != nullptr) vector_lane<T, P, LANES>(vec, ld, group, lane, D, t);
+#pragma unroll
+        for (int e = 0; e < E; ++e) to[(e / V * LANES + lane) * V + e % V] = t[e];
+    };
+    auto kept = [&](const float (&from)[LANES * E], int e) __attribute__((always_inline)) {
+        return from[(e / V * LANES + lane) * V + e % V];
+    };
+    if (sub == 0) {
+        keep(vectors[0], p.weight, p.ld_weight, 1.0f);
+        keep(vectors[1], p.gate, p.ld_gate, 1.0f);
+        if constexpr (POST) {
+            keep(vectors[2], p.post_weight, p.ld_post_weight, 1.0f);
+            keep(vectors[3], p.post_bias, p.ld_post_bias, 0.0f);
+        }
+    }
+    __syncthreads();
 
     for (int64_t first = begin; first < end; first += ROWS) {
-        const bool inside = first + sub < end;
+        // (a row past the last takes part, with gradients of zero, unseen)
+        const bool inside = ROWS == 1 || first + sub < end;
         const int64_t m = inside ? first + sub : end - 1;
-        float r[E], h[E], behind[E], inv_h = 1.0f;
-        load_lane<T, V, LANES>(static_cast<const T *>(p.X) + m * p.ldx, lane, p.D, r);
-        float gate[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) gate[e] = 1.0f;
+        LanePart<T, LANES, E, true> x, y, dy, dr;          // (y: H)
+        x.load(static_cast<const T *>(p.X) + m * p.ldx, lane, D);
+        if (p.H != nullptr) y.load(static_cast<const T *>(p.H) + m * p.ldh, lane, D);
+        if (q.dY != nullptr) dy.load(static_cast<const T *>(q.dY) + m * q.lddy, lane, D);
+        if (q.dR != nullptr) dr.load(static_cast<const T *>(q.dR) + m * q.lddr, lane, D);
+        float r[E], h[E] = {}, inv_h = 1.0f;
+        x.get(lane, D, r);
+        if (p.H != nullptr) y.get(lane, D, h);
+        // N_post(H), from H normalized
+        auto behind = [&](int e) __attribute__((always_inline)) {
+            return POST ? h[e] * kept(vectors[POST ? 2 : 0], e) + kept(vectors[POST ? 3 : 0], e)
+                        : h[e];
+        };
         if (p.H != nullptr) {
-            load_lane<T, V, LANES>(static_cast<const T *>(p.H) + m * p.ldh, lane, p.D, h);
-            if (p.post != TRA_NORM_NONE) inv_h = normalize<V, LANES>(h, p.post, p, lane, sum);
+            if constexpr (POST) inv_h = normalize<V, LANES>(h, p.post, p, lane, sum);
 #pragma unroll
-            for (int e = 0; e < E; ++e) behind[e] = h[e];
-            if (p.post != TRA_NORM_NONE) {
-                times<P, V, LANES>(behind, p.post_weight, p.ld_post_weight, group, lane, p.D);
-                plus<P, V, LANES>(behind, p.post_bias, p.ld_post_bias, group, lane, p.D);
-            }
-            times<P, V, LANES>(gate, p.gate, p.ld_gate, group, lane, p.D);
-#pragma unroll
-            for (int e = 0; e < E; ++e) r[e] = p.scale * r[e] + gate[e] * behind[e];
+            for (int e = 0; e < E; ++e) r[e] = p.scale * r[e] + kept(vectors[1], e) * behind(e);
         }
         // G, the gradient of R
         float g[E] = {};
         if (q.dY != nullptr) {
-            const float inv_r = normalize<V, LANES>(r, p.norm, p, lane, sum);
-            load_lane<T, V, LANES>(static_cast<const T *>(q.dY) + m * q.lddy, lane, p.D, g);
+            float d[E];
+            dy.get(lane, D, d);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                total[kWeight][e] += inside ? g[e] * r[e] : 0.0f;
-                total[kBias][e] += inside ? g[e] : 0.0f;
+                d[e] = inside ? d[e] : 0.0f;
+                g[e] = d[e] * kept(vectors[0], e);
             }
-            times<P, V, LANES>(g, p.weight, p.ld_weight, group, lane, p.D);
-            normalize_gradient<V, LANES>(g, r, inv_r, p.norm, p, lane, sum);
+            normalize_both<V, LANES>(r, g, p.norm, p, lane, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                total[kWeight][e] += d[e] * r[e];
+                if constexpr (BIAS) total[kBias][e] += d[e];
+            }
         }
         if (q.dR != nullptr) {
             float d[E];
-            load_lane<T, V, LANES>(static_cast<const T *>(q.dR) + m * q.lddr, lane, p.D, d);
+            dr.get(lane, D, d);
 #pragma unroll
-            for (int e = 0; e < E; ++e) g[e] += d[e];
+            for (int e = 0; e < E; ++e) g[e] += inside ? d[e] : 0.0f;
         }
         if (q.dX != nullptr && inside) {
-            float d[E];
+            const float scale = p.H != nullptr ? p.scale : 1.0f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) d[e] = p.H != nullptr ? p.scale * g[e] : g[e];
-            store_lane<T, V, LANES>(static_cast<T *>(q.dX) + m * q.lddx, lane, p.D, d);
+            for (int e = 0; e < E; ++e) r[e] = scale * g[e];
+            store_lane<T, V, LANES>(static_cast<T *>(q.dX) + m * q.lddx, lane, p.D, r);
         }
         if (p.H != nullptr) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                total[kGate][e] += inside ? g[e] * behind[e] : 0.0f;
-                g[e] *= gate[e];
-                total[kPostWeight][e] += inside ? g[e] * h[e] : 0.0f;
-                total[kPostBias][e] += inside ? g[e] : 0.0f;
+                total[kGate][e] += g[e] * behind(e);
+                g[e] *= kept(vectors[1], e);
             }
-            if (p.post != TRA_NORM_NONE) {
-                times<P, V, LANES>(g, p.post_weight, p.ld_post_weight, group, lane, p.D);
+            if constexpr (POST) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    total[kPostWeight][e] += g[e] * h[e];
+                    if constexpr (BIAS) total[kPostBias][e] += g[e];
+                    g[e] *= kept(vectors[2], e);
+                }
                 normalize_gradient<V, LANES>(g, h, inv_h, p.post, p, lane, sum);
             }
             if (q.dH != nullptr && inside)
@@ -478,7 +606,7 @@ __global__ __launch_bounds__(kBlock<LANES>) void norm_backward(const NormGradArg
         if (q.partial[k] == nullptr) continue;
         float t[E];
 #pragma unroll
-        for (int j = 0; j < kVectors; ++j)
+        for (int j = 0; j < SUMS; ++j)
             if (k == j) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) t[e] = total[j][e];
@@ -551,7 +679,7 @@ template <typename T, typename P>
 __global__ __launch_bounds__(kWideLanes) void norm_backward_wide(const NormGradArgs q) {
     constexpr int V = kChunk<T>;
     const NormArgs &p = q.f;
-    __shared__ float lds[4 * (kWideLanes / 64)];
+    __shared__ __align__(16) float lds[4 * (kWideLanes / 64)];
     lds_poison(lds, 4 * (kWideLanes / 64));
     RowSum<kWideLanes, kWideLanes> sum{lds};
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
@@ -692,8 +820,8 @@ __global__ __launch_bounds__(256) void norm_columns(const NormGradArgs q) {
     }
 }
 
-// Adds the chunks' sums in order: 16 columns of one gradient's row per workgroup, whose 16
-// groups of lanes take every 16th chunk and are added in order.
+// Adds the chunks' sums in order: 32 columns of one gradient's row per workgroup, whose 8
+// groups of lanes take every 8th chunk and are added in order.
 struct NormJoinArgs {
     const float *partial[kVectors];
     void *out[kVectors];
@@ -701,27 +829,30 @@ struct NormJoinArgs {
     int64_t D, chunks, chunks_per_group;
 };
 
+constexpr int kJoin = 32;
+
 template <typename P>
 __global__ __launch_bounds__(256) void norm_join(const NormJoinArgs p) {
-    __shared__ float part[16][16];
-    const int j = threadIdx.x & 15, lanes = threadIdx.x >> 4;
-    const int64_t blocks = ceil_div(p.D, 16);
+    __shared__ float part[8][kJoin];
+    lds_poison(&part[0][0], 8 * kJoin);
+    const int j = threadIdx.x % kJoin, lanes = threadIdx.x / kJoin;
+    const int64_t blocks = ceil_div(p.D, kJoin);
     const int k = blockIdx.y;
     if (p.out[k] == nullptr) return;
     const int64_t rows = p.rows[k], each = rows == 1 ? p.chunks : p.chunks_per_group;
     for (int64_t id = blockIdx.x; id < rows * blocks; id += gridDim.x) {
-        const int64_t row = id / blocks, n = (id - row * blocks) * 16 + j;
+        const int64_t row = id / blocks, n = (id - row * blocks) * kJoin + j;
         const float *from = p.partial[k] + row * each * p.D + n;
         float sum = 0.0f;
         if (n < p.D) {
-#pragma unroll 4
-            for (int64_t c = lanes; c < each; c += 16) sum += from[c * p.D];
+#pragma unroll 8
+            for (int64_t c = lanes; c < each; c += 8) sum += from[c * p.D];
         }
         __syncthreads();
         part[lanes][j] = sum;
         __syncthreads();
         if (lanes == 0 && n < p.D) {
-            for (int i = 1; i < 16; ++i) sum += part[i][j];
+            for (int i = 1; i < 8; ++i) sum += part[i][j];
             static_cast<P *>(p.out[k])[row * p.D + n] = static_cast<P>(sum);
         }
     }
@@ -731,42 +862,69 @@ __global__ __launch_bounds__(256) void norm_join(const NormJoinArgs p) {
 
 constexpr int64_t kMaxBlocks = 1 << 20;      // workgroups that take rows in turn
 
+// Whether rows of D elements of `bytes` bytes are kept in registers: not those longer than
+// 1024 lanes' 8 elements, nor those shorter than a chunk of 16 bytes.
+constexpr bool in_registers(int64_t D, int64_t bytes) { return D * bytes >= 16 && D <= 8192; }
+
 template <typename T, typename P, int LANES, int E>
 hipError_t launch_forward(const NormArgs &a, hipStream_t s) {
     const int64_t blocks = ceil_div(a.M, kBlock<LANES> / LANES);
-    norm_forward<T, P, LANES, E><<<dim3(static_cast<unsigned>(std::min(blocks, kMaxBlocks))),
-                                   kBlock<LANES>, 0, s>>>(a);
+    const dim3 grid(static_cast<unsigned>(std::min(blocks, kMaxBlocks)));
+    if (a.D % kChunk<T> == 0)
+        norm_forward<T, P, LANES, E, false><<<grid, kBlock<LANES>, 0, s>>>(a);
+    else
+        norm_forward<T, P, LANES, E, true><<<grid, kBlock<LANES>, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <typename T, typename P>
 hipError_t forward_of(const NormArgs &a, hipStream_t s) {
-    if (a.D <= 128) return launch_forward<T, P, 16, 8>(a, s);
-    if (a.D <= 512) return launch_forward<T, P, 64, 8>(a, s);
-    if (a.D <= 2048) return launch_forward<T, P, 256, 8>(a, s);
-    if (a.D <= 4096) return launch_forward<T, P, 512, 8>(a, s);
-    if (a.D <= 8192) return launch_forward<T, P, 1024, 8>(a, s);
+    if (in_registers(a.D, sizeof(T))) {
+        if (a.D <= 128) return launch_forward<T, P, 16, 8>(a, s);
+        if (a.D <= 512) return launch_forward<T, P, 64, 8>(a, s);
+        if (a.D <= 2048) return launch_forward<T, P, 256, 8>(a, s);
+        if (a.D <= 4096) return launch_forward<T, P, 512, 8>(a, s);
+        return launch_forward<T, P, 1024, 8>(a, s);
+    }
     norm_forward_wide<T, P><<<dim3(static_cast<unsigned>(std::min(a.M, kMaxBlocks))), kWideLanes,
                               0, s>>>(a);
     return hipGetLastError();
 }
 
-constexpr int64_t kWide = 8192;              // the widest rows that the backward pass keeps
+// Whether the backward pass has a kernel that keeps such rows and the sums of the vectors'
+// gradients in registers: with a norm of H, rows past 4096 leave room for few sums.
+constexpr bool backward_fits(int64_t D, int64_t bytes, bool post, bool bias) {
+    return in_registers(D, bytes) && (D <= 4096 || !post || (bytes == 2 && !bias));
+}
 
-template <typename T, typename P, int LANES>
+template <typename T, typename P, int LANES, int E = 8>
 hipError_t launch_backward(const NormGradArgs &a, int64_t chunks, hipStream_t s) {
-    norm_backward<T, P, LANES, 8><<<dim3(static_cast<unsigned>(chunks)), kBlock<LANES>, 0, s>>>(a);
+    const dim3 grid(static_cast<unsigned>(chunks));
+    const bool post = a.f.post != TRA_NORM_NONE;
+    const bool bias = a.partial[kBias] != nullptr || a.partial[kPostBias] != nullptr;
+#define TRA_BACKWARD(POST, BIAS) \
+    norm_backward<T, P, LANES, E, POST, BIAS><<<grid, kBackwardBlock, 0, s>>>(a)
+    if (!post) {
+        bias ? TRA_BACKWARD(false, true) : TRA_BACKWARD(false, false);
+    } else if (!bias) {
+        if constexpr (backward_fits(LANES * E, sizeof(T), true, false)) TRA_BACKWARD(true, false);
+    } else {
+        if constexpr (backward_fits(LANES * E, sizeof(T), true, true)) TRA_BACKWARD(true, true);
+    }
+#undef TRA_BACKWARD
     return hipGetLastError();
 }
 
 template <typename T, typename P>
-hipError_t backward_of(const NormGradArgs &a, int64_t chunks, bool sums, hipStream_t s) {
+hipError_t backward_of(const NormGradArgs &a, int64_t chunks, bool wide, bool sums, hipStream_t s) {
     const int64_t D = a.f.D;
-    if (D <= 128) return launch_backward<T, P, 16>(a, chunks, s);
-    if (D <= 512) return launch_backward<T, P, 64>(a, chunks, s);
-    if (D <= 2048) return launch_backward<T, P, 256>(a, chunks, s);
-    if (D <= 4096) return launch_backward<T, P, 512>(a, chunks, s);
-    if (D <= kWide) return launch_backward<T, P, 1024>(a, chunks, s);
+    if (!wide) {
+        if (D <= 128) return launch_backward<T, P, 16>(a, chunks, s);
+        if (D <= 512) return launch_backward<T, P, 64>(a, chunks, s);
+        if (D <= 2048) return launch_backward<T, P, 256>(a, chunks, s);
+        if (D <= 4096) return launch_backward<T, P, 512>(a, chunks, s);
+        return launch_backward<T, P, 512, 16>(a, chunks, s);
+    }
     norm_backward_wide<T, P><<<dim3(static_cast<unsigned>(std::min(a.f.M, kMaxBlocks))),
                                kWideLanes, 0, s>>>(a);
     hipError_t err = hipGetLastError();
@@ -781,7 +939,7 @@ hipError_t launch_join(const NormJoinArgs &a, hipStream_t s) {
     int64_t rows = 1;
     for (int k = 0; k < kVectors; ++k)
         if (a.out[k] != nullptr) rows = std::max(rows, a.rows[k]);
-    const dim3 grid(static_cast<unsigned>(std::min(rows * ceil_div(a.D, 16), kMaxBlocks)),
+    const dim3 grid(static_cast<unsigned>(std::min(rows * ceil_div(a.D, kJoin), kMaxBlocks)),
                     kVectors);
     norm_join<P><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
@@ -927,6 +1085,7 @@ struct GradPlan {
     size_t partial_bytes;      // of one
     size_t stats_bytes;
     size_t total;
+    bool wide;                 // rows are read again for each sum
 };
 
 bool wants(const tra_norm_grad_args &a, int k) {
@@ -943,15 +1102,20 @@ int64_t rows_of(const tra_norm_grad_args &a, int k) {
 GradPlan plan_backward(const tra_norm_grad_args &a) {
     GradPlan g{};
     for (int k = 0; k < tra::kVectors; ++k) g.vectors += wants(a, k);
+    const bool bias = wants(a, tra::kBias) || wants(a, tra::kPostBias);
+    const int64_t bytes = elem_bytes(a.dtype);
+    g.wide = !tra::backward_fits(a.D, bytes, a.post != TRA_NORM_NONE, bias);
     const int64_t per_group = a.M / a.groups;
-    const int64_t want = std::max<int64_t>(1, (g.vectors > 0 ? 256 : 4096) / a.groups);
+    // as many workgroups as run at once where their sums are kept, else a row each
+    const int64_t most = g.vectors > 0 ? 256 * tra::backward_per_cu(bytes, a.D, bias) : 4096;
+    const int64_t want = std::max<int64_t>(1, most / a.groups);
     g.rows_per_chunk = std::max<int64_t>(1, ceil_div(per_group, want));
     g.chunks_per_group = std::max<int64_t>(1, ceil_div(per_group, g.rows_per_chunk));
     g.chunks = a.groups * g.chunks_per_group;
     if (g.vectors > 0) {
         g.partial_bytes =
             align_up(static_cast<size_t>(g.chunks) * static_cast<size_t>(a.D) * sizeof(float));
-        if (a.D > tra::kWide)
+        if (g.wide)
             g.stats_bytes = align_up(static_cast<size_t>(a.M) * tra::kStats * sizeof(float));
     }
     g.total = g.vectors * g.partial_bytes + g.stats_bytes;
@@ -1033,7 +1197,8 @@ tra_status backward(const tra_norm_grad_args *p, void *stream_) {
     hipError_t err = hipSuccess;
     if (a.M > 0 && (a.dX != nullptr || a.dH != nullptr || g.vectors > 0))
         err = by_type(a.dtype, a.param_dtype, [&](auto t, auto w) {
-            return tra::backward_of<decltype(t), decltype(w)>(d, g.chunks, g.vectors > 0, stream);
+            return tra::backward_of<decltype(t), decltype(w)>(d, g.chunks, g.wide, g.vectors > 0,
+                                                             stream);
         });
     if (err == hipSuccess && g.vectors > 0)
         err = a.param_dtype == TRA_DTYPE_F32    ? tra::launch_join<float>(j, stream)
