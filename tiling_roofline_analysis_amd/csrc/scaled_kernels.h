@@ -88,6 +88,22 @@ __device__ __forceinline__ float scale_value(uint32_t word) {
     return __uint_as_float(word);
 }
 
+// A barrier that no load is waited for at; and a wait for this wave's direct loads but
+// the last VM (stage_sync does both).
+__device__ __forceinline__ void step_sync() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <int VM>
+__device__ __forceinline__ void stage_wait() {
+    static_assert(VM >= 0 && VM < 64, "vmcnt range");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
 using Bytes = uint8_t;
 
 // Rows row0 .. + 15 of a panel: chunks l / 16 and 4 + l / 16 of each.
@@ -415,12 +431,24 @@ __global__ __launch_bounds__(256, (ScaledShape<BM, BN, SCALE>::per_cu(S))) void 
 
 // ---- the wide kernel -----------------------------------------------------------------------
 //
-// linear_wide for one-byte elements and 16-bit results: 256 x 256 of Y per workgroup of
-// eight waves in two groups half a phase apart, the same panels, phases and waits.  A
-// quadrant is 8 MFMAs.  The tile's scales are read panel by panel beside the fragments,
-// the last in phase 2, and loaded for tile s + 2 in phase 3.
-// With binary32 scales a row tile's sums are added while the next one's MFMAs run, the
-// quadrant's last behind the next phase's reads, while the other group's do.
+// 256 x 256 of Y per workgroup of eight waves, for 16-bit results of many tiles, which the
+// matrix units bound.  The panels and the two groups of waves, half a step apart, are
+// linear_wide's: A0, A1, B0, B1 of 128 rows each, in two stages, an array each; a wave
+// computes 64 rows of each A panel by 32 columns of each B panel; there is one wave of each
+// group on every SIMD, and while the one computes the other reads fragments.  A K tile is
+// two steps of 16 MFMAs (with four of 8, half as many MFMAs between two barriers, the K
+// tile took 1.2 times as long).  Tile s:
+//   R0  reads B0, A0, all scales;  loads A1 > s + 1;          barrier
+//   C0  reads B1 behind the first MFMAs;  A0 x B0, A0 x B1;   barrier
+//   R1  reads A1;  loads A0, B0, scales > s + 2;              barrier
+//   C1  loads B1 > s + 2;  A1 x B1, A1 x B0;                  barrier
+// The group behind does each one barrier later, so what is read in one of these may be
+// loaded anew from the second one after it on; every load is issued there.  What is to
+// be read in one of them has to be in LDS, of both groups' loads, at the end of the second
+// one before it: behind R0, R1 and C1 a wave waits until its last 4 panels and scales, in
+// the order above, are all that is in flight.
+// Binary32 scales: a row tile's sums are added while the next ones' MFMAs run, a step's last
+// behind the next step's reads, while the other group's do.
 template <typename T, int FORMATS, int SCALE>
 __global__ __launch_bounds__(512, 2) void scaled_wide(const ScaledArgs p) {
     using PP = Panel<Bytes, true, 128, 8>;
@@ -461,54 +489,63 @@ __global__ __launch_bounds__(512, 2) void scaled_wide(const ScaledArgs p) {
     const PR pa0(a.M - m0, a.lda), pa1(a.M - m0 - 128, a.lda);
     const PR pb0(a.N - n0, a.ldb), pb1(a.N - n1, a.ldb);
 
-    // A1 is loaded one tile behind the others: where its tile starts
-    const char *late = nullptr;
+    // A1 and B1 are loaded behind the others, when `walk` is a tile on.
+    const char *late_a = nullptr, *late_b = nullptr;
     int late_rem = 0;
-    auto load_a0 = [&](char *st) __attribute__((always_inline)) {
-        pa0.load(wave, walk.a, oa, walk.rem, st);
-    };
-    auto load_b0 = [&](char *st) __attribute__((always_inline)) {
-        pb0.load(wave, walk.b0, ob, walk.rem, st);
-    };
-    auto load_b1 = [&](char *st, char *sc) __attribute__((always_inline)) {
-        pb1.load(wave, walk.b1, ob, walk.rem, st);
+    auto load_a0_b0 = [&](char *a0, char *b0, char *sc) __attribute__((always_inline)) {
+        pa0.load(wave, walk.a, oa, walk.rem, a0);
+        pb0.load(wave, walk.b0, ob, walk.rem, b0);
         scales.load(wave, walk.rem, sc);
-        late = walk.a + lower;
+        late_a = walk.a + lower;
+        late_b = walk.b1;
         late_rem = walk.rem;
         walk.next();
     };
     auto load_a1 = [&](char *st) __attribute__((always_inline)) {
-        pa1.load(wave, late, oa, late_rem, st);
+        pa1.load(wave, late_a, oa, late_rem, st);
+    };
+    auto load_b1 = [&](char *st) __attribute__((always_inline)) {
+        pb1.load(wave, late_b, ob, late_rem, st);
     };
 
     f32x4 c[2][2][4][2] = {};      // [A panel][B panel]
     i32x8 x[4], w[2][2];           // [row tile]; [B panel][column tile]
-    uint32_t sx[4], sw[2][UNIT ? 2 : 1];
+    // e8m0: a byte for each row tile (column tile) of each panel.  f32: X's of each row tile,
+    // and W's of each B panel, in a scalar register.
+    uint32_t sx[2][UNIT ? 1 : 4], sw[2];
+    float both[2] = {};
     // binary32 scales: the last row tile's sums, which are added late, and their scale
     f32x4 t[2];
     float ts = 0.0f;
-    float both[2] = {};            // W's scale of each B panel, in a scalar register
-    auto read_a = [&](auto half, const char *st, const char *sc) __attribute__((always_inline)) {
+    auto read_scales = [&](const char *sc) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[i] = fragment8<PP>(st, 0, wm * 64 + i * 16);
-            sx[i] =
-                PS::of_rows(sc, 0, decltype(half)::value * 128 + wm * 64 + i * 16);
+        for (int h = 0; h < 2; ++h) {
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = PS::of_rows(sc, 0, h * 128 + wm * 64 + i * 16);
+            if constexpr (UNIT) {
+                sx[h][0] = v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24;
+                const uint32_t w0 = PS::of_rows(sc, 0, 256 + h * 128 + wn * 32);
+                const uint32_t w1 = PS::of_rows(sc, 0, 256 + h * 128 + wn * 32 + 16);
+                sw[h] = w0 | w1 << 8;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sx[h][UNIT ? 0 : i] = v[i];
+                sw[h] = PS::of_row(sc, 0, 256 + h * 128);
+            }
         }
     };
-    auto read_b = [&](auto half, const char *st, const char *sc) __attribute__((always_inline)) {
-        constexpr int H = decltype(half)::value;
+    auto read_a = [&](const char *st) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            w[H][j] = fragment8<PP>(st, 0, wn * 32 + j * 16);
-            if constexpr (UNIT)
-                sw[H][UNIT ? j : 0] = PS::of_rows(sc, 0, 256 + H * 128 + wn * 32 + j * 16);
-            else if (j == 0)
-                sw[H][0] = PS::of_row(sc, 0, 256 + H * 128);
-        }
+        for (int i = 0; i < 4; ++i) x[i] = fragment8<PP>(st, 0, wm * 64 + i * 16);
     };
-    auto scale_of = [&](int i, auto hb) __attribute__((always_inline)) {
-        return __uint_as_float(sx[i]) * both[decltype(hb)::value];
+    auto read_b = [&](auto half, const char *st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            w[decltype(half)::value][j] = fragment8<PP>(st, 0, wn * 32 + j * 16);
+    };
+    auto scale_of = [&](auto ha, int i, auto hb) __attribute__((always_inline)) {
+        return __uint_as_float(sx[decltype(ha)::value][UNIT ? 0 : i]) * both[decltype(hb)::value];
     };
     auto add_to = [&](f32x4 (&sum)[2], const f32x4 (&u)[2], float s) __attribute__((always_inline)) {
 #pragma unroll
@@ -516,41 +553,38 @@ __global__ __launch_bounds__(512, 2) void scaled_wide(const ScaledArgs p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[j][e] = fmaf(u[j][e], s, sum[j][e]);
     };
-    // The barrier behind the reads and loads, the MFMAs, the barrier behind them.
-    // VM: loads that may still be in flight (63: any).
-    auto compute = [&](auto vm, auto ha, auto hb) __attribute__((always_inline)) {
+    // One MFMA of e8m0: the bytes of the scales are immediate operands.
+    auto scaled = [&](auto ha, auto hb, auto ii, auto jj) __attribute__((always_inline)) {
         constexpr int HA = decltype(ha)::value, HB = decltype(hb)::value;
-        stage_sync<decltype(vm)::value>();
+        constexpr int I = decltype(ii)::value, J = decltype(jj)::value;
+        c[HA][HB][I][J] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            w[HB][J], x[I], c[HA][HB][I][J], kFormatW<FORMATS>, kFormatX<FORMATS>, J,
+            static_cast<int>(sw[HB]), I, static_cast<int>(sx[HA][0]));
+    };
+    // The 8 MFMAs of a quadrant; binary32: and the sums of all but its last row tile.
+    auto quadrant = [&](auto ha, auto hb) __attribute__((always_inline)) {
+        constexpr int HA = decltype(ha)::value, HB = decltype(hb)::value;
         if constexpr (UNIT) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    c[HA][HB][i][j] =
-                        mma_scaled<FORMATS>(w[HB][j], x[i], c[HA][HB][i][j], sw[HB][j], sx[i]);
+            for_each(std::make_integer_sequence<int, 8>{}, [&](auto n) __attribute__((always_inline)) {
+                constexpr int U = decltype(n)::value;
+                scaled(ha, hb, std::integral_constant<int, U / 2>{},
+                       std::integral_constant<int, U % 2>{});
+                return true;
+            });
         } else {
-            if constexpr (HA == 0)     // the phases that have read it
-                both[HB] = __int_as_float(__builtin_amdgcn_readfirstlane(static_cast<int>(sw[HB][0])));
-            // a row tile's sums are added two MFMAs behind its own
             f32x4 u[4][2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) u[i][j] = mma_plain<FORMATS>(w[HB][j], x[i]);
                 __builtin_amdgcn_sched_barrier(0);
-                if (i > 0) add_to(c[HA][HB][i - 1], u[i - 1], scale_of(i - 1, hb));
+                if (i > 0) add_to(c[HA][HB][i - 1], u[i - 1], scale_of(ha, i - 1, hb));
             }
             t[0] = u[3][0];
             t[1] = u[3][1];
-            ts = scale_of(3, hb);
+            ts = scale_of(ha, 3, hb);
         }
-        __builtin_amdgcn_sched_barrier(0);
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
     };
-    // Adds what is left of the quadrant computed last.
     auto add = [&](auto ha, auto hb) __attribute__((always_inline)) {
         if constexpr (!UNIT) {
             __builtin_amdgcn_sched_barrier(0);
@@ -559,50 +593,60 @@ __global__ __launch_bounds__(512, 2) void scaled_wide(const ScaledArgs p) {
     };
     constexpr std::integral_constant<int, 0> zero;
     constexpr std::integral_constant<int, 1> one;
-    constexpr std::integral_constant<int, 3 * L + 1> three_panels;
-    constexpr std::integral_constant<int, 63> any;
+    constexpr int FLIGHT = 4 * L + 1;      // loads of the last 4 panels and scales
     // Tile s, in the stages a0, a1, b0, b1, sc; `a1_next` is the other A1.
     auto tile = [&](char *a0, char *a1, char *b0, char *b1, char *sc, char *a1_next)
                     __attribute__((always_inline)) {
-        read_b(zero, b0, sc);
-        read_a(zero, a0, sc);
+        read_b(zero, b0);
+        read_a(a0);
+        read_scales(sc);
         load_a1(a1_next);
-        compute(any, zero, zero);
-        read_b(one, b1, sc);
-        load_a0(a0);
-        add(zero, zero);
-        compute(any, zero, one);
-        read_a(one, a1, sc);
-        load_b0(b0);
-        add(zero, one);
-        compute(any, one, one);
-        load_b1(b1, sc);
-        add(one, one);
-        compute(three_panels, one, zero);
         add(one, zero);
+        stage_sync<FLIGHT>();
+
+        read_b(one, b1);
+        if constexpr (!UNIT) {
+            both[0] = __int_as_float(__builtin_amdgcn_readfirstlane(static_cast<int>(sw[0])));
+            both[1] = __int_as_float(__builtin_amdgcn_readfirstlane(static_cast<int>(sw[1])));
+        }
+        quadrant(zero, zero);
+        add(zero, zero);
+        quadrant(zero, one);
+        step_sync();
+
+        read_a(a1);
+        load_a0_b0(a0, b0, sc);
+        add(zero, one);
+        stage_sync<FLIGHT>();
+
+        load_b1(b1);
+        quadrant(one, one);
+        add(one, one);
+        quadrant(one, zero);
+        stage_wait<FLIGHT>();
+        step_sync();
     };
 
-    load_a0(a00);
+    load_a0_b0(a00, b00, s0);
     __builtin_amdgcn_sched_barrier(0);
-    load_b0(b00);
-    __builtin_amdgcn_sched_barrier(0);
-    load_b1(b10, s0);
+    load_b1(b10);
     __builtin_amdgcn_sched_barrier(0);
     load_a1(a10);
     __builtin_amdgcn_sched_barrier(0);
-    load_a0(a01);
+    load_a0_b0(a01, b01, s1);
     __builtin_amdgcn_sched_barrier(0);
-    load_b0(b01);
-    __builtin_amdgcn_sched_barrier(0);
-    load_b1(b11, s1);
+    load_b1(b11);
+    // A0, B0, B1, A1 and the scales of the first tile
     stage_sync<3 * L + 1>();
     if (wm != 0) __builtin_amdgcn_s_barrier();
+    if constexpr (!UNIT) t[0] = t[1] = f32x4{};
     int s = 0;
     for (; s + 2 <= count; s += 2) {
         tile(a00, a10, b00, b10, s0, a11);
         tile(a01, a11, b01, b11, s1, a10);
     }
     if (s < count) tile(a00, a10, b00, b10, s0, a11);
+    add(one, zero);
     if (wm == 0) __builtin_amdgcn_s_barrier();
     stage_sync<0>();
 
