@@ -85,6 +85,8 @@ __global__ __launch_bounds__(256) void quantize_tile(const QuantizeArgs p) {
     if (p.Q != nullptr) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            // (the 16 lanes of a row go the same way; of a few rows' tile most do nothing)
+            if (m + i >= p.M) continue;
             if constexpr (ROWS == 1) {
                 float a = 0.0f;
 #pragma unroll
@@ -94,7 +96,7 @@ __global__ __launch_bounds__(256) void quantize_tile(const QuantizeArgs p) {
             }
             uint32_t w[2];
             to_fp8<FP8, SCALE>(x[i], s, w);
-            if (m + i < p.M && k < up16(p.K))
+            if (k < up16(p.K))
                 __builtin_memcpy(__builtin_assume_aligned(p.Q + (m + i) * p.ldq + k, 8), w, 8);
         }
         if constexpr (ROWS == 1) {
@@ -150,8 +152,37 @@ __global__ __launch_bounds__(256) void quantize_tile(const QuantizeArgs p) {
     }
 }
 
+// Rows alone, a block for each 16 lanes, blocks of one column of them next to each other:
+// for matrices whose tiles would leave CUs idle.  A lane of the tile kernel rounds 64
+// elements one after the other, which takes 2 to 6 us however few there are: 16 x 512 bf16 to
+// binary32 scales 9.1 us in tiles, 2.6 this way, 1024 x 4096 8.2 and 5.6; from 512 tiles on
+// the two are alike (2048 x 4096 to e8m0 scales 6.6 us in tiles, 7.3 this way).
+template <typename T, int FP8, int SCALE>
+__global__ __launch_bounds__(256) void quantize_rows(const QuantizeArgs p) {
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+    if (id >= p.M * p.tiles_k) return;
+    const int64_t b = id / p.M, m = id - b * p.M;
+    const int c = static_cast<int>(threadIdx.x & 15);
+    const int64_t k = b * 128 + c * 8;
+    float x[8], most = 0.0f;
+    load_part<T, 8>(static_cast<const T *>(p.X) + m * p.ldx + k, p.K - k, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = fmaxf(most, finite_size(x[e]));
+    const BlockScale s = block_scale<FP8, SCALE>(largest_of_16(most));
+    uint32_t w[2];
+    to_fp8<FP8, SCALE>(x, s, w);
+    if (k < up16(p.K))
+        __builtin_memcpy(__builtin_assume_aligned(p.Q + m * p.ldq + k, 8), w, 8);
+    if (c == 0) store_scale<SCALE>(p.S, m * p.ss_row + b * p.ss_block, s.bits);
+}
+
 template <typename T, int FP8, int SCALE>
 hipError_t launch_rows(int block_rows, unsigned tiles, const QuantizeArgs &a, hipStream_t s) {
+    if (block_rows == 1 && a.QT == nullptr && tiles < 512) {
+        const unsigned groups = static_cast<unsigned>(ceil_div(a.M * a.tiles_k, 16));
+        quantize_rows<T, FP8, SCALE><<<dim3(groups), 256, 0, s>>>(a);
+        return hipGetLastError();
+    }
     if (block_rows == 1)
         quantize_tile<T, FP8, SCALE, 1><<<dim3(tiles), 256, 0, s>>>(a);
     else

@@ -25,17 +25,17 @@ int64_t up16(int64_t n) { return ceil_div(n, 16) * 16; }
 // How the kernels go, in microseconds (TileClass): 16-bit results with binary32 and e8m0
 // scales, binary32 results.
 constexpr TileClass kClasses[3][4] = {
-    {{256, 256, 1, 1.50, 1.60, 5.7},
-     {128, 128, 2, 0.60, 0.60, 5.2},
-     {64, 128, 2, 0.35, 0.33, 4.5},
-     {64, 64, 2, 0.24, 0.22, 4.0}},
-    {{256, 256, 1, 1.28, 1.42, 5.7},
-     {128, 128, 2, 0.50, 0.47, 5.2},
-     {64, 128, 2, 0.30, 0.27, 4.5},
-     {64, 64, 2, 0.21, 0.185, 4.0}},
-    {{128, 128, 1, 1.00, 1.00, 5.2},
-     {64, 128, 2, 0.60, 0.55, 4.5},
-     {64, 64, 2, 0.40, 0.35, 4.0},
+    {{256, 256, 1, 1.52, 1.63, 8.0},
+     {128, 128, 2, 0.65, 0.49, 5.0},
+     {64, 128, 2, 0.41, 0.34, 4.0},
+     {64, 64, 2, 0.284, 0.215, 3.5}},
+    {{256, 256, 1, 1.34, 1.34, 4.5},
+     {128, 128, 2, 0.45, 0.425, 5.0},
+     {64, 128, 2, 0.34, 0.33, 3.8},
+     {64, 64, 2, 0.242, 0.205, 3.2}},
+    {{128, 128, 1, 1.26, 1.29, 6.0},
+     {64, 128, 2, 0.85, 0.62, 4.5},
+     {64, 64, 2, 0.56, 0.37, 4.0},
      {0, 0, 0, 0.0, 0.0, 0.0}}};
 
 bool x_given(const tra_scaled_args &a) { return a.x_dtype == TRA_X_SCALED; }
@@ -58,8 +58,13 @@ ScaledPlan plan_scaled(const tra_scaled_args &a) {
             s.tile.whole = static_cast<int>(strips);
             s.tile.bm = s.tile.bn = 16;
             s.tile.splits = 1;
+            // X quantized by every workgroup, 32 blocks at a time, or by a launch before: a CU's
+            // rounds of 32 take about 0.6 us each with binary32 scales, the launch 2.5 (4 x 2048
+            // x 2048: 5.7 against 7.5 us; 4 x 12288 x 4096, 12 rounds: 18.8 against 15.5).
+            const int64_t x_blocks = a.M * ceil_div(a.K, 128);
             s.make = a.x_dtype == a.dtype && a.x_fp8 == TRA_FP8_E4M3 && a.K > 0 &&
-                     a.M * ceil_div(a.K, 128) * 128 <= kFewBytes;
+                     x_blocks * 128 <= kFewBytes &&
+                     ceil_div(x_blocks, 32) * ceil_div(s.tile.whole, kCUs) <= 4;
         }
     }
     s.tile.form = tra::kFormKK;
