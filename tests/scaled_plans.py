@@ -6,10 +6,14 @@ import ctypes
 import tiling_roofline_analysis_amd as tra
 from tiling_roofline_analysis_amd import scaled
 
-# (M, N, K)
-CALLS = [(1, 16, 128), (1, 500, 4096), (3, 48, 9000), (16, 1030, 272), (9, 33, 16), (2, 4100, 1300), (40, 60, 500), (64, 64, 4096), (130, 520, 264), (300, 700, 1040),
-         (515, 1030, 520), (1000, 1100, 144), (1500, 2000, 300), (2100, 4100, 136),
-         (70, 4100, 6000), (4100, 4200, 400), (1030, 4100, 2064)]
+# (M, N, K): few rows, quantized by the kernel and before it; then the tiles (found by a
+# search of 60000 random products, the cheapest that reach them all)
+CALLS = [(1, 16, 128), (1, 500, 4096), (3, 48, 9000), (16, 1030, 272), (9, 33, 16),
+         (2, 4100, 1300), (19, 9, 16), (18, 9, 2069), (73, 8900, 17), (6878, 264, 16),
+         (816, 5074, 268), (680, 1513, 3341), (1135, 273, 7425), (2944, 66, 3777),
+         (2527, 1619, 1986), (1233, 777, 6251), (796, 1382, 6786), (2604, 4666, 736),
+         (1977, 1462, 4526), (7203, 2255, 640), (1675, 1250, 10057), (69, 4183, 8929),
+         (7356, 2239, 2451)]
 
 # addresses that are never read
 X, SX, W, SW, BIAS, R, Y, WS = (i << 40 for i in range(1, 9))
@@ -29,3 +33,10 @@ def describe(M, N, K, scale, **kw) -> str:
         pack(M, N, K, scale=1 if scale == "e8m0" else 0, **kw), buf, len(buf))
     assert st == tra.TRA_OK, st
     return buf.value.decode()
+
+
+def reached(M, N, K, scale, **kw):
+    """(kernel, tile, deep, split) of a call: split is no, all tiles, or the last ones."""
+    d = dict(kv.split("=") for kv in describe(M, N, K, scale, **kw).split())
+    split = "no" if d["splits"] == "1" else "all" if d["whole"] == "0" else "last"
+    return d["kernel"], d["tile"], int(d["deep"]) if d["kernel"] == "scaled_tile" else 0, split

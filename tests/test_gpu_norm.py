@@ -101,6 +101,17 @@ def test_kinds(kind, post, D):
         check_all(12, D, torch.float32, torch.float32, kind, post, has=("x",))
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [24, 100, 129, 500, 701, 2048, 2055, 4096, 4097, 6000, 8191])
+def test_without_biases(D, dtype):
+    # (their gradients' sums are left out of the kernels then)
+    has = ("x", "h", "gate", "post_weight", "weight")
+    for M in (1, 37, 600 if D < 3000 else 270):
+        check_all(M, D, DTYPES[dtype], torch.float32, "rms", "rms", has=has)
+    check_all(19, D, DTYPES[dtype], DTYPES[dtype], "layer", "layer", has=has)
+    check_all(19, D, DTYPES[dtype], DTYPES[dtype], "layer", "none", has=("x", "h", "gate", "weight"))
+
+
 @pytest.mark.parametrize("D", [72, 700, 2100, 8200])
 @pytest.mark.parametrize("groups,rows", [(2, 1), (3, 5), (4, 70), (130, 2)])
 def test_vectors_of_sequences(groups, rows, D):

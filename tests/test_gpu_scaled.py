@@ -105,7 +105,7 @@ def test_formats(fx, fw, scale, block_rows, size):
         check(y, Operand(x, xs), Operand(w, ws, block_rows))
 
 
-def ints(M, K, block_rows, scale, gen, most=4):
+def ints(M, K, block_rows, scale, gen, fp8="e4m3", most=4):
     """Small integers in 8 bits, with scales that are small integers or powers of two."""
     v = torch.randint(-most, most + 1, (M, up(K, 16) * 16), generator=gen, device="cuda").float()
     v[:, K:] = 0
@@ -114,34 +114,37 @@ def ints(M, K, block_rows, scale, gen, most=4):
         s = 2.0 ** torch.randint(-1, 3, shape, generator=gen, device="cuda").float()
     else:
         s = torch.randint(1, 4, shape, generator=gen, device="cuda").float()
-    return v.to(FP8["e4m3"]), s.to(SCALES[scale])
+    return v.to(FP8[fp8]), s.to(SCALES[scale])
 
 
-def exact(M, N, K, scale, block_rows, dt, seed=0):
+def exact(M, N, K, fx, fw, scale, block_rows, dt, seed=0):
     gen = torch.Generator(device="cuda").manual_seed(seed)
-    x, xs = ints(M, K, 1, scale, gen)
-    w, ws = ints(N, K, block_rows, scale, gen)
-    want = stands_for(x, xs) @ stands_for(w, ws, block_rows).t()
-    # (quarters: 2^-2 is the least unit)
-    assert float((stands_for(x, xs).abs() @ stands_for(w, ws, block_rows).abs().t()).max()) < 2 ** 22
+    x, xs = ints(M, K, 1, scale, gen, fx)
+    w, ws = ints(N, K, block_rows, scale, gen, fw)
+    a, b = stands_for(x, xs, 1), stands_for(w, ws, block_rows)
+    # a unit is 2^-2 at least, and no sum passes 2^22
+    assert float(a.abs().max() * b.abs().max()) * K < 2 ** 22
     got = tra.scaled_linear(x, w.t(), xs, ws.t(), dtype=dt)
-    assert torch.equal(got, want.to(dt)), (M, N, K, scale, block_rows)
+    assert torch.equal(got, (a @ b.t()).to(dt)), (M, N, K, fx, fw, scale, block_rows)
 
 
-# the sizes reach every kernel, deep and shallow, split and whole (test_scaled_plans has the
-# list and checks that they do)
+# the sizes reach every kernel, deep and shallow, split and whole (test_operators_cpu.py
+# checks that they do)
 from scaled_plans import CALLS, describe  # noqa: E402
+
+FORMATS = [("e4m3", "e4m3", "e8m0", 1), ("e4m3", "e4m3", "e8m0", 128), ("e5m2", "e4m3", "e8m0", 128),
+           ("e4m3", "e5m2", "e8m0", 1), ("e4m3", "e4m3", "f32", 128), ("e5m2", "e4m3", "f32", 128)]
 
 
 @pytest.mark.parametrize("lib", ["product", "poison"])
-@pytest.mark.parametrize("scale,block_rows", [("e8m0", 1), ("e8m0", 128), ("f32", 128)])
+@pytest.mark.parametrize("form", FORMATS, ids=str)
 @pytest.mark.parametrize("call", CALLS, ids=str)
-def test_integers_are_exact(call, scale, block_rows, lib, monkeypatch):
+def test_integers_are_exact(call, form, lib, monkeypatch):
     if lib == "poison":
         import tiling_roofline_analysis_amd.fused as fused
         monkeypatch.setattr(fused, "load", POISON.load)
-    for dt in (torch.float32, torch.bfloat16):
-        exact(*call, scale, block_rows, dt)
+    for dt in (torch.float32, torch.bfloat16, torch.float16):
+        exact(*call, *form, dt)
 
 
 class POISON:

@@ -33,9 +33,10 @@ constexpr TileClass kClasses[3][4] = {
      {128, 128, 2, 0.45, 0.425, 5.0},
      {64, 128, 2, 0.34, 0.33, 3.8},
      {64, 64, 2, 0.242, 0.205, 3.2}},
-    {{128, 128, 1, 1.26, 1.29, 6.0},
-     {64, 128, 2, 0.85, 0.62, 4.5},
+    // (128 x 128, one a CU for its VGPRs: 1.29, twice what 64 x 128 takes)
+    {{64, 128, 2, 0.85, 0.62, 4.5},
      {64, 64, 2, 0.56, 0.37, 4.0},
+     {0, 0, 0, 0.0, 0.0, 0.0},
      {0, 0, 0, 0.0, 0.0, 0.0}}};
 
 bool x_given(const tra_scaled_args &a) { return a.x_dtype == TRA_X_SCALED; }

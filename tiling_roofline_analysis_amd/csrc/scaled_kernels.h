@@ -843,11 +843,14 @@ hipError_t launch_scaled(const TilePlan &plan, const ScaledArgs &p, hipStream_t 
         }
     }
 #define TRA_TILE(BM, BN, S) scaled_tile<T, FORMATS, SCALE, BM, BN, S><<<grid, 256, 0, stream>>>(p)
-    // (two of 128 x 128 with converted operands would need more VGPRs than a CU has)
-    constexpr int SHALLOW = std::is_same_v<T, float> ? 4 : 2;
-    if (plan.bm == 128) plan.deep ? TRA_TILE(128, 128, 4) : TRA_TILE(128, 128, SHALLOW);
-    else if (plan.bn == 128) plan.deep ? TRA_TILE(64, 128, 4) : TRA_TILE(64, 128, 2);
-    else plan.deep ? TRA_TILE(64, 64, 6) : TRA_TILE(64, 64, 4);
+    if (plan.bm == 128) {
+        if constexpr (sizeof(T) == 2) plan.deep ? TRA_TILE(128, 128, 4) : TRA_TILE(128, 128, 2);
+        else return hipErrorInvalidValue;
+    } else if (plan.bn == 128) {
+        plan.deep ? TRA_TILE(64, 128, 4) : TRA_TILE(64, 128, 2);
+    } else {
+        plan.deep ? TRA_TILE(64, 64, 6) : TRA_TILE(64, 64, 4);
+    }
 #undef TRA_TILE
     return hipGetLastError();
 }
