@@ -220,6 +220,18 @@ def test_nan_and_inf_stay_in_their_rows(D):
     assert torch.isnan(got[1][~keep]).all()
 
 
+@pytest.mark.parametrize("D", [40, 300, 1500, 4000, 9000])
+def test_an_infinity_in_the_last_row_is_counted_once(D):
+    # (rows are taken several at a time; 0 times it would be NaN)
+    t, dr, _ = make(5, D, torch.float32, torch.float32, has=("x", "h", "gate"))
+    dr, h = dr.abs() + 1, t["h"].clone()
+    h[4, 7] = float("inf")
+    dx, dh, dgate = tra.add_norm_backward(dr, None, t["x"], h, t["gate"], kind="none")[:3]
+    assert dgate[7] == float("inf")
+    assert torch.isfinite(dgate[:7]).all() and torch.isfinite(dgate[8:]).all()
+    assert torch.equal(dx, dr) and torch.equal(dh, dr * t["gate"])
+
+
 def test_missing_gradients_of_outputs():
     # either output may go unused
     for D in (50, 2000, 9000):

@@ -533,9 +533,10 @@ __global__ __launch_bounds__(kBackwardBlock, (2 * backward_per_cu(sizeof(T), LAN
     __syncthreads();
 
     for (int64_t first = begin; first < end; first += ROWS) {
-        // (a row past the last takes part, with gradients of zero, unseen)
+        // (a row past the last takes part, unseen: the last again, left out of the totals)
         const bool inside = ROWS == 1 || first + sub < end;
         const int64_t m = inside ? first + sub : end - 1;
+        auto counted = [&](float v) __attribute__((always_inline)) { return inside ? v : 0.0f; };
         LanePart<T, LANES, E, true> x, y, dy, dr;          // (y: H)
         x.load(static_cast<const T *>(p.X) + m * p.ldx, lane, D);
         if (p.H != nullptr) y.load(static_cast<const T *>(p.H) + m * p.ldh, lane, D);
@@ -560,22 +561,19 @@ __global__ __launch_bounds__(kBackwardBlock, (2 * backward_per_cu(sizeof(T), LAN
             float d[E];
             dy.get(lane, D, d);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                d[e] = inside ? d[e] : 0.0f;
-                g[e] = d[e] * kept(vectors[0], e);
-            }
+            for (int e = 0; e < E; ++e) g[e] = d[e] * kept(vectors[0], e);
             normalize_both<V, LANES>(r, g, p.norm, p, lane, sum);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                total[kWeight][e] += d[e] * r[e];
-                if constexpr (BIAS) total[kBias][e] += d[e];
+                total[kWeight][e] += counted(d[e] * r[e]);
+                if constexpr (BIAS) total[kBias][e] += counted(d[e]);
             }
         }
         if (q.dR != nullptr) {
             float d[E];
             dr.get(lane, D, d);
 #pragma unroll
-            for (int e = 0; e < E; ++e) g[e] += inside ? d[e] : 0.0f;
+            for (int e = 0; e < E; ++e) g[e] += d[e];
         }
         if (q.dX != nullptr && inside) {
             const float scale = p.H != nullptr ? p.scale : 1.0f;
@@ -586,14 +584,14 @@ __global__ __launch_bounds__(kBackwardBlock, (2 * backward_per_cu(sizeof(T), LAN
         if (p.H != nullptr) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                total[kGate][e] += g[e] * behind(e);
+                total[kGate][e] += counted(g[e] * behind(e));
                 g[e] *= kept(vectors[1], e);
             }
             if constexpr (POST) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    total[kPostWeight][e] += g[e] * h[e];
-                    if constexpr (BIAS) total[kPostBias][e] += g[e];
+                    total[kPostWeight][e] += counted(g[e] * h[e]);
+                    if constexpr (BIAS) total[kPostBias][e] += counted(g[e]);
                     g[e] *= kept(vectors[2], e);
                 }
                 normalize_gradient<V, LANES>(g, h, inv_h, p.post, p, lane, sum);
