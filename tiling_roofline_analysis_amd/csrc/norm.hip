@@ -818,8 +818,8 @@ __global__ __launch_bounds__(256) void norm_columns(const NormGradArgs q) {
     }
 }
 
-// Adds the chunks' sums in order: 32 columns of one gradient's row per workgroup, whose 8
-// groups of lanes take every 8th chunk and are added in order.
+// Adds the chunks' sums in order: 32 columns of one gradient's row per workgroup, whose
+// groups of lanes take every GROUPS-th chunk and are added in order.
 struct NormJoinArgs {
     const float *partial[kVectors];
     void *out[kVectors];
@@ -829,10 +829,14 @@ struct NormJoinArgs {
 
 constexpr int kJoin = 32;
 
-template <typename P>
-__global__ __launch_bounds__(256) void norm_join(const NormJoinArgs p) {
-    __shared__ float part[8][kJoin];
-    lds_poison(&part[0][0], 8 * kJoin);
+// The loads' latency bounds it: with many chunks there are more groups (512 chunks of three
+// sums of 4096 take 6.9 us with 8, 6.4 with 32), and a lane's loads go eight at a time, the last
+// of them at the last chunk again (one at a time for the rest, 63 chunks of three sums of
+// 5461 took 9.0 us, so 6.6).
+template <typename P, int GROUPS>
+__global__ __launch_bounds__(kJoin * GROUPS) void norm_join(const NormJoinArgs p) {
+    __shared__ float part[GROUPS][kJoin];
+    lds_poison(&part[0][0], GROUPS * kJoin);
     const int j = threadIdx.x % kJoin, lanes = threadIdx.x / kJoin;
     const int64_t blocks = ceil_div(p.D, kJoin);
     const int k = blockIdx.y;
@@ -843,14 +847,23 @@ __global__ __launch_bounds__(256) void norm_join(const NormJoinArgs p) {
         const float *from = p.partial[k] + row * each * p.D + n;
         float sum = 0.0f;
         if (n < p.D) {
-#pragma unroll 8
-            for (int64_t c = lanes; c < each; c += 8) sum += from[c * p.D];
+            for (int64_t c = lanes; c < each; c += 8 * GROUPS) {
+                float v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int64_t at = c + u * GROUPS;
+                    v[u] = from[(at < each ? at : each - 1) * p.D];
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) sum = c + u * GROUPS < each ? sum + v[u] : sum;
+            }
         }
         __syncthreads();
         part[lanes][j] = sum;
         __syncthreads();
         if (lanes == 0 && n < p.D) {
-            for (int i = 1; i < 8; ++i) sum += part[i][j];
+#pragma unroll
+            for (int i = 1; i < GROUPS; ++i) sum += part[i][j];
             static_cast<P *>(p.out[k])[row * p.D + n] = static_cast<P>(sum);
         }
     }
@@ -939,7 +952,10 @@ hipError_t launch_join(const NormJoinArgs &a, hipStream_t s) {
         if (a.out[k] != nullptr) rows = std::max(rows, a.rows[k]);
     const dim3 grid(static_cast<unsigned>(std::min(rows * ceil_div(a.D, kJoin), kMaxBlocks)),
                     kVectors);
-    norm_join<P><<<grid, 256, 0, s>>>(a);
+    if (a.chunks_per_group > 128)
+        norm_join<P, 32><<<grid, kJoin * 32, 0, s>>>(a);
+    else
+        norm_join<P, 8><<<grid, kJoin * 8, 0, s>>>(a);
     return hipGetLastError();
 }
 
