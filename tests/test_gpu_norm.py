@@ -264,6 +264,23 @@ def test_only_what_is_asked_for():
         assert torch.equal(g, want[name]), name
 
 
+@pytest.mark.parametrize("D", [5, 700, 4097, 5461, 8192, 9000, 16384, 16392])
+def test_rows_without_the_vectors_gradients(D):
+    for post in ("none", "layer"):
+        t, dr, dy = make(9, D, torch.float32, torch.float32)
+        args = {k: v for k, v in t.items() if k not in ("x", "h")}
+        if post == "none":
+            args.pop("post_weight"), args.pop("post_bias")
+        call = lambda **k: tra.add_norm_backward(  # noqa: E731
+            dr, dy, t["x"], t["h"], scale=0.75, post=post, kind="layer", **args, **k)
+        dx, dh = call()[:2]
+        got = call(need_vectors=False)
+        assert torch.equal(got[0], dx) and torch.equal(got[1], dh)
+        assert all(g is None for g in got[2:])
+        assert torch.equal(call(need_dh=False)[0], dx)
+        assert torch.equal(call(need_dx=False, need_vectors=False)[1], dh)
+
+
 def test_gradients_against_differences():
     gen = torch.Generator(device="cuda").manual_seed(3)
     t, dr, dy = make(4, 24, torch.float32, torch.float32, groups=2)

@@ -50,7 +50,7 @@ struct NormGradArgs {
     // Sums of one chunk of rows: chunk c of sum v at partial[v] + c * D; or null.
     float *partial[kVectors];
     int64_t chunks_per_group, rows_per_chunk;
-    float *stats;                      // wide rows: kStats floats a row
+    float *stats;                      // kStats floats a row, where the sums are a kernel of their own
 };
 
 constexpr int kStats = 8;              // mean and 1 / deviation of H and R, means of g and g n
@@ -199,12 +199,14 @@ __device__ __forceinline__ float inverse_deviation(float mean_square, float eps)
 // v becomes (v - mean) / deviation; returns 1 / deviation.
 template <int V, int LANES, int E, typename Sum>
 __device__ __forceinline__ float normalize(float (&v)[E], int kind, const NormArgs &p, int lane,
-                                           Sum &sum) {
+                                           Sum &sum, float &mean) {
+    mean = 0.0f;
     if (kind == TRA_NORM_LAYER) {
         float s = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) s += v[e];
-        subtract_mean<V, LANES>(v, sum(s) * p.inv_d, lane, p.D);
+        mean = sum(s) * p.inv_d;
+        subtract_mean<V, LANES>(v, mean, lane, p.D);
     }
     float s = 0.0f;
 #pragma unroll
@@ -213,6 +215,12 @@ __device__ __forceinline__ float normalize(float (&v)[E], int kind, const NormAr
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] *= inverse;
     return inverse;
+}
+template <int V, int LANES, int E, typename Sum>
+__device__ __forceinline__ float normalize(float (&v)[E], int kind, const NormArgs &p, int lane,
+                                           Sum &sum) {
+    float mean;
+    return normalize<V, LANES>(v, kind, p, lane, sum, mean);
 }
 
 // Group `group`'s row of a vector.
@@ -245,7 +253,7 @@ constexpr int kBlock = LANES < 256 ? 256 : LANES;
 
 // What hides the memory's latency is the number of waves: 8 a SIMD, where the VGPRs allow it.
 template <typename T, typename P, int LANES, int E, bool RAGGED>
-__global__ __launch_bounds__(kBlock<LANES>, RAGGED ? 4 : LANES < 256 ? 7 : 8) void norm_forward(const NormArgs p) {
+__global__ __launch_bounds__(kBlock<LANES>, RAGGED || E > 8 ? 4 : LANES < 256 ? 7 : 8) void norm_forward(const NormArgs p) {
     constexpr int V = kChunk<T>, BLOCK = kBlock<LANES>, ROWS = BLOCK / LANES;
     __shared__ __align__(16) float lds[4 * (BLOCK / 64)];
     lds_poison(lds, 4 * (BLOCK / 64));
@@ -427,9 +435,14 @@ __global__ __launch_bounds__(kWideLanes) void norm_forward_wide(const NormArgs p
 // v: a row; g: the gradient of its norm's normalized row n.  v becomes n, and g the
 // gradient of v, both 0 past the row's end.  The sums that depend on v only through its
 // deviation are taken along with the one for that.
+struct RowStats {
+    float mean = 0.0f, inverse = 1.0f;     // of v
+    float along = 0.0f, mean_g = 0.0f;     // means of g n and g
+};
 template <int V, int LANES, int E, typename Sum>
-__device__ __forceinline__ void normalize_both(float (&v)[E], float (&g)[E], int kind,
-                                               const NormArgs &p, int lane, Sum &sum) {
+__device__ __forceinline__ RowStats normalize_both(float (&v)[E], float (&g)[E], int kind,
+                                                   const NormArgs &p, int lane, Sum &sum) {
+    RowStats s;
     if (kind == TRA_NORM_LAYER) {
         float a = 0.0f, b = 0.0f;
 #pragma unroll
@@ -438,8 +451,10 @@ __device__ __forceinline__ void normalize_both(float (&v)[E], float (&g)[E], int
             b += g[e];
         }
         sum(a, b);
-        subtract_mean<V, LANES>(v, a * p.inv_d, lane, p.D);
-        subtract_mean<V, LANES>(g, b * p.inv_d, lane, p.D);
+        s.mean = a * p.inv_d;
+        s.mean_g = b * p.inv_d;
+        subtract_mean<V, LANES>(v, s.mean, lane, p.D);
+        subtract_mean<V, LANES>(g, s.mean_g, lane, p.D);
     }
     float a = 0.0f, b = 0.0f;
 #pragma unroll
@@ -448,13 +463,14 @@ __device__ __forceinline__ void normalize_both(float (&v)[E], float (&g)[E], int
         b += g[e] * v[e];
     }
     sum(a, b);
-    const float inverse = inverse_deviation(a * p.inv_d, p.eps);
-    const float along = b * inverse * p.inv_d;
+    s.inverse = inverse_deviation(a * p.inv_d, p.eps);
+    s.along = b * s.inverse * p.inv_d;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        v[e] *= inverse;
-        g[e] = inverse * (g[e] - v[e] * along);
+        v[e] *= s.inverse;
+        g[e] = s.inverse * (g[e] - v[e] * s.along);
     }
+    return s;
 }
 
 // g: the gradient of a norm's normalized row n; becomes that of the row before it (0
@@ -633,6 +649,98 @@ __global__ __launch_bounds__(kBackwardBlock, (2 * backward_per_cu(sizeof(T), LAN
     }
 }
 
+// ---- backward, rows in registers, sums by themselves -----------------------------------------------
+//
+// Rows that leave no registers for sums of the vectors' gradients: 1024 lanes a row; the rows'
+// statistics go to memory and norm_columns, which reads the rows again, takes the sums from
+// them.  2048 x 16384 bf16 without a norm of H: 116 us (3.5 TB/s) and 87 (3.1 TB/s read); with
+// the rows read again from L2 for each of their sums, as norm_backward_wide does, 193 and 92.
+
+template <typename T, typename P, int E>
+__global__ __launch_bounds__(1024) void norm_backward_rows(const NormGradArgs q) {
+    constexpr int V = kChunk<T>, LANES = 1024;
+    constexpr bool LATE = E * sizeof(T) > 32;      // dY and dR are loaded where they are used
+    const NormArgs &p = q.f;
+    __shared__ __align__(16) float lds[4 * (LANES / 64)];
+    lds_poison(lds, 4 * (LANES / 64));
+    RowSum<LANES, LANES> sum{lds};
+    const int lane = static_cast<int>(threadIdx.x), D = static_cast<int>(p.D);
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        const int64_t group = m / p.per_group;
+        LanePart<T, LANES, E, true> x, y, dy, dr;          // (y: H)
+        x.load(static_cast<const T *>(p.X) + m * p.ldx, lane, D);
+        if (p.H != nullptr) y.load(static_cast<const T *>(p.H) + m * p.ldh, lane, D);
+        if (!LATE && q.dY != nullptr)
+            dy.load(static_cast<const T *>(q.dY) + m * q.lddy, lane, D);
+        if (!LATE && q.dR != nullptr)
+            dr.load(static_cast<const T *>(q.dR) + m * q.lddr, lane, D);
+        auto times = [&](float (&v)[E], const void *vec, int64_t ld) __attribute__((always_inline)) {
+            if (vec == nullptr) return;
+            float t[E];
+            vector_lane<T, P, LANES>(vec, ld, group, lane, D, t);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] *= t[e];
+        };
+        float r[E], h[E], g[E], mean_h = 0.0f, inv_h = 1.0f;
+        x.get(lane, D, r);
+        if (p.H != nullptr) {
+            y.get(lane, D, h);
+            if (p.post != TRA_NORM_NONE)
+                inv_h = normalize<V, LANES>(h, p.post, p, lane, sum, mean_h);
+            float b[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) b[e] = h[e];
+            if (p.post != TRA_NORM_NONE) {
+                times(b, p.post_weight, p.ld_post_weight);
+                if (p.post_bias != nullptr) {
+                    float t[E];
+                    vector_lane<T, P, LANES>(p.post_bias, p.ld_post_bias, group, lane, D, t);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) b[e] += t[e];
+                }
+            }
+            times(b, p.gate, p.ld_gate);
+#pragma unroll
+            for (int e = 0; e < E; ++e) r[e] = p.scale * r[e] + b[e];
+        }
+        RowStats s;
+#pragma unroll
+        for (int e = 0; e < E; ++e) g[e] = 0.0f;
+        if (q.dY != nullptr) {
+            if (LATE) dy.load(static_cast<const T *>(q.dY) + m * q.lddy, lane, D);
+            dy.get(lane, D, g);
+            times(g, p.weight, p.ld_weight);
+            s = normalize_both<V, LANES>(r, g, p.norm, p, lane, sum);
+        }
+        if (q.stats != nullptr && threadIdx.x == 0) {
+            const float all[kStats] = {mean_h,  inv_h,    s.mean, s.inverse,
+                                       s.along, s.mean_g, 0.0f,   0.0f};
+#pragma unroll
+            for (int i = 0; i < kStats; ++i) q.stats[m * kStats + i] = all[i];
+        }
+        if (q.dR != nullptr) {
+            if (LATE) dr.load(static_cast<const T *>(q.dR) + m * q.lddr, lane, D);
+            dr.get(lane, D, r);
+#pragma unroll
+            for (int e = 0; e < E; ++e) g[e] += r[e];
+        }
+        if (q.dX != nullptr) {
+            const float scale = p.H != nullptr ? p.scale : 1.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) r[e] = scale * g[e];
+            store_lane<T, V, LANES>(static_cast<T *>(q.dX) + m * q.lddx, lane, p.D, r);
+        }
+        if (q.dH != nullptr) {
+            times(g, p.gate, p.ld_gate);
+            if (p.post != TRA_NORM_NONE) {
+                times(g, p.post_weight, p.ld_post_weight);
+                normalize_gradient<V, LANES>(g, h, inv_h, p.post, p, lane, sum);
+            }
+            store_lane<T, V, LANES>(static_cast<T *>(q.dH) + m * q.lddh, lane, p.D, g);
+        }
+    }
+}
+
 // ---- backward, wide rows ------------------------------------------------------------------------
 
 // What is taken from dY by the norm before the next block: G, chunk by chunk.
@@ -754,9 +862,31 @@ __global__ __launch_bounds__(kWideLanes) void norm_backward_wide(const NormGradA
     }
 }
 
-// The vectors' gradients of wide rows, from the rows' statistics: 64 chunks of columns by
-// one chunk of rows per workgroup, whose four waves take every fourth row.
-template <typename T, typename P>
+// V elements from `at` on, zeros past the row's end; TINY: of rows shorter than a chunk of 16
+// bytes.  (As LanePart: with a path of its own for the end each load is waited for by itself.)
+template <typename T, int V, bool TINY>
+__device__ __forceinline__ void load_columns(const T *row, int64_t at, int64_t D, float (&v)[V]) {
+    if constexpr (TINY) {
+        load_part<T, V>(row + at, D - at, v);
+    } else {
+        constexpr int W = kChunk<T>;
+#pragma unroll
+        for (int c = 0; c < V; c += W) {
+            const int64_t over = at + c + W - D;
+            u32x4 chunk;
+            __builtin_memcpy(&chunk, row + (over > 0 ? D - W : at + c), 16);
+            chunk = drop_elements<T>(chunk, over <= 0 ? 0 : over < W ? static_cast<int>(over) : W);
+            T t[W];
+            __builtin_memcpy(t, &chunk, 16);
+#pragma unroll
+            for (int e = 0; e < W; ++e) v[c + e] = static_cast<float>(t[e]);
+        }
+    }
+}
+
+// The vectors' gradients from the rows' statistics: 64 chunks of columns by one chunk of
+// rows per workgroup, whose four waves take every fourth row.
+template <typename T, typename P, bool TINY>
 __global__ __launch_bounds__(256) void norm_columns(const NormGradArgs q) {
     constexpr int V = kChunk<T>;
     const NormArgs &p = q.f;
@@ -772,25 +902,44 @@ __global__ __launch_bounds__(256) void norm_columns(const NormGradArgs q) {
     const int64_t end = begin + q.rows_per_chunk < stop ? begin + q.rows_per_chunk : stop;
     float total[kVectors][V] = {};
     if (at < p.D) {
+        float weight[V], gate[V], post_weight[V], post_bias[V];
+        auto vector = [&](float (&v)[V], const void *vec, int64_t ld, float none)
+                          __attribute__((always_inline)) {
+            vector_chunk<P, V>(vec, ld, group, at, p.D, none, v);
+        };
+        vector(weight, p.weight, p.ld_weight, 1.0f);
+        vector(gate, p.gate, p.ld_gate, 1.0f);
+        vector(post_weight, p.post_weight, p.ld_post_weight, 1.0f);
+        vector(post_bias, p.post_bias, p.ld_post_bias, 0.0f);
+        auto row = [&](const void *v, int64_t ld, int64_t m, float (&to)[V])
+                       __attribute__((always_inline)) {
+            load_columns<T, V, TINY>(static_cast<const T *>(v) + m * ld, at, p.D, to);
+        };
         for (int64_t m = begin + wave; m < end; m += 4) {
-            const float *s = q.stats + m * kStats;
-            WideRow<T, P> row{p, m, group, s[0], s[1]};
-            WideGrad<T, P> grad{q, row, s[2], s[3], s[4], s[5]};
-            float n[V] = {}, dy[V] = {}, g[V], nh[V], b[V], w[V];
-            grad.gradient(at, n, dy, g);
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                total[kWeight][e] += dy[e] * n[e];
-                total[kBias][e] += dy[e];
+            float n[V] = {}, h[V] = {}, dy[V] = {}, g[V] = {};
+            if (q.dY != nullptr) {
+                row(p.X, p.ldx, m, n);
+                row(q.dY, q.lddy, m, dy);
             }
-            if (p.H == nullptr) continue;
-            row.behind(at, nh, b);
-            vector_chunk<P, V>(p.gate, p.ld_gate, group, at, p.D, 1.0f, w);
+            if (p.H != nullptr) row(p.H, p.ldh, m, h);
+            if (q.dR != nullptr) row(q.dR, q.lddr, m, g);
+            const float *s = q.stats + m * kStats;
+            const float mean_h = s[0], inv_h = s[1], mean = s[2], inverse = s[3], along = s[4],
+                        mean_g = s[5];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                total[kGate][e] += g[e] * b[e];
-                total[kPostWeight][e] += g[e] * w[e] * nh[e];
-                total[kPostBias][e] += g[e] * w[e];
+                // (of a post of none: 0 and 1)
+                const float nh = (h[e] - mean_h) * inv_h, b = nh * post_weight[e] + post_bias[e];
+                const float r = p.H != nullptr ? p.scale * n[e] + gate[e] * b : n[e];
+                const float nr = (r - mean) * inverse;
+                if (q.dY != nullptr)
+                    g[e] += inverse * (dy[e] * weight[e] - nr * along - mean_g);
+                const float gg = g[e] * gate[e];
+                total[kWeight][e] += dy[e] * nr;
+                total[kBias][e] += dy[e];
+                total[kGate][e] += g[e] * b;
+                total[kPostWeight][e] += gg * nh;
+                total[kPostBias][e] += gg;
             }
         }
     }
@@ -874,8 +1023,8 @@ __global__ __launch_bounds__(kJoin * GROUPS) void norm_join(const NormJoinArgs p
 constexpr int64_t kMaxBlocks = 1 << 20;      // workgroups that take rows in turn
 
 // Whether rows of D elements of `bytes` bytes are kept in registers: not those longer than
-// 1024 lanes' 8 elements, nor those shorter than a chunk of 16 bytes.
-constexpr bool in_registers(int64_t D, int64_t bytes) { return D * bytes >= 16 && D <= 8192; }
+// 1024 lanes' 16 elements, nor those shorter than a chunk of 16 bytes.
+constexpr bool in_registers(int64_t D, int64_t bytes) { return D * bytes >= 16 && D <= 16384; }
 
 template <typename T, typename P, int LANES, int E>
 hipError_t launch_forward(const NormArgs &a, hipStream_t s) {
@@ -895,7 +1044,8 @@ hipError_t forward_of(const NormArgs &a, hipStream_t s) {
         if (a.D <= 512) return launch_forward<T, P, 64, 8>(a, s);
         if (a.D <= 2048) return launch_forward<T, P, 256, 8>(a, s);
         if (a.D <= 4096) return launch_forward<T, P, 512, 8>(a, s);
-        return launch_forward<T, P, 1024, 8>(a, s);
+        if (a.D <= 8192) return launch_forward<T, P, 1024, 8>(a, s);
+        return launch_forward<T, P, 1024, 16>(a, s);
     }
     norm_forward_wide<T, P><<<dim3(static_cast<unsigned>(std::min(a.M, kMaxBlocks))), kWideLanes,
                               0, s>>>(a);
@@ -905,7 +1055,8 @@ hipError_t forward_of(const NormArgs &a, hipStream_t s) {
 // Whether the backward pass has a kernel that keeps such rows and the sums of the vectors'
 // gradients in registers: with a norm of H, rows past 4096 leave room for few sums.
 constexpr bool backward_fits(int64_t D, int64_t bytes, bool post, bool bias) {
-    return in_registers(D, bytes) && (D <= 4096 || !post || (bytes == 2 && !bias));
+    return in_registers(D, bytes) && D <= 8192 &&
+           (D <= 4096 || !post || (bytes == 2 && !bias));
 }
 
 template <typename T, typename P, int LANES, int E = 8>
@@ -927,21 +1078,30 @@ hipError_t launch_backward(const NormGradArgs &a, int64_t chunks, hipStream_t s)
 }
 
 template <typename T, typename P>
-hipError_t backward_of(const NormGradArgs &a, int64_t chunks, bool wide, bool sums, hipStream_t s) {
+hipError_t backward_of(const NormGradArgs &a, int64_t chunks, bool fits, bool sums, hipStream_t s) {
     const int64_t D = a.f.D;
-    if (!wide) {
+    if (fits) {
         if (D <= 128) return launch_backward<T, P, 16>(a, chunks, s);
         if (D <= 512) return launch_backward<T, P, 64>(a, chunks, s);
         if (D <= 2048) return launch_backward<T, P, 256>(a, chunks, s);
         if (D <= 4096) return launch_backward<T, P, 512>(a, chunks, s);
         return launch_backward<T, P, 512, 16>(a, chunks, s);
     }
-    norm_backward_wide<T, P><<<dim3(static_cast<unsigned>(std::min(a.f.M, kMaxBlocks))),
-                               kWideLanes, 0, s>>>(a);
+    const dim3 rows(static_cast<unsigned>(std::min(a.f.M, kMaxBlocks)));
+    if (!in_registers(D, sizeof(T)))
+        norm_backward_wide<T, P><<<rows, kWideLanes, 0, s>>>(a);
+    else if (D <= 8192)
+        norm_backward_rows<T, P, 8><<<rows, 1024, 0, s>>>(a);
+    else
+        norm_backward_rows<T, P, 16><<<rows, 1024, 0, s>>>(a);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || !sums) return err;
     const int64_t blocks = ceil_div(D, 64 * kChunk<T>);
-    norm_columns<T, P><<<dim3(static_cast<unsigned>(chunks * blocks)), 256, 0, s>>>(a);
+    const dim3 grid(static_cast<unsigned>(chunks * blocks));
+    if (D < kChunk<T>)
+        norm_columns<T, P, true><<<grid, 256, 0, s>>>(a);
+    else
+        norm_columns<T, P, false><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -1099,7 +1259,7 @@ struct GradPlan {
     size_t partial_bytes;      // of one
     size_t stats_bytes;
     size_t total;
-    bool wide;                 // rows are read again for each sum
+    bool fits;                 // rows and sums in registers; else the rows' statistics are kept
 };
 
 bool wants(const tra_norm_grad_args &a, int k) {
@@ -1118,10 +1278,15 @@ GradPlan plan_backward(const tra_norm_grad_args &a) {
     for (int k = 0; k < tra::kVectors; ++k) g.vectors += wants(a, k);
     const bool bias = wants(a, tra::kBias) || wants(a, tra::kPostBias);
     const int64_t bytes = elem_bytes(a.dtype);
-    g.wide = !tra::backward_fits(a.D, bytes, a.post != TRA_NORM_NONE, bias);
+    g.fits = tra::backward_fits(a.D, bytes, a.post != TRA_NORM_NONE, bias);
     const int64_t per_group = a.M / a.groups;
-    // as many workgroups as run at once where their sums are kept, else a row each
-    const int64_t most = g.vectors > 0 ? 256 * tra::backward_per_cu(bytes, a.D, bias) : 4096;
+    // as many workgroups as run at once where their sums are kept, or 8 a CU of those that
+    // take sums alone (2048 x 16384 bf16: 100 us and 9 for the join of 256 chunks, 87 and 5
+    // of 64); without sums a row each
+    int64_t most = 4096;
+    if (g.vectors > 0)
+        most = g.fits ? 256 * tra::backward_per_cu(bytes, a.D, bias)
+                      : std::max<int64_t>(1, 2048 / ceil_div(a.D, 1024 / bytes));
     const int64_t want = std::max<int64_t>(1, most / a.groups);
     g.rows_per_chunk = std::max<int64_t>(1, ceil_div(per_group, want));
     g.chunks_per_group = std::max<int64_t>(1, ceil_div(per_group, g.rows_per_chunk));
@@ -1129,7 +1294,7 @@ GradPlan plan_backward(const tra_norm_grad_args &a) {
     if (g.vectors > 0) {
         g.partial_bytes =
             align_up(static_cast<size_t>(g.chunks) * static_cast<size_t>(a.D) * sizeof(float));
-        if (g.wide)
+        if (!g.fits)
             g.stats_bytes = align_up(static_cast<size_t>(a.M) * tra::kStats * sizeof(float));
     }
     g.total = g.vectors * g.partial_bytes + g.stats_bytes;
@@ -1211,7 +1376,7 @@ tra_status backward(const tra_norm_grad_args *p, void *stream_) {
     hipError_t err = hipSuccess;
     if (a.M > 0 && (a.dX != nullptr || a.dH != nullptr || g.vectors > 0))
         err = by_type(a.dtype, a.param_dtype, [&](auto t, auto w) {
-            return tra::backward_of<decltype(t), decltype(w)>(d, g.chunks, g.wide, g.vectors > 0,
+            return tra::backward_of<decltype(t), decltype(w)>(d, g.chunks, g.fits, g.vectors > 0,
                                                              stream);
         });
     if (err == hipSuccess && g.vectors > 0)
