@@ -392,7 +392,9 @@ TRA_API tra_status tra_linear_backward_describe(const tra_linear_grad_args *args
  * (e4m3fn has none) or stay (e5m2).  Rows of values are filled up with zeros to a
  * multiple of 16, so Q has (K + 15) / 16 * 16 columns and QT (M + 15) / 16 * 16, and
  * leading dimensions of at least that, which are multiples of 16; both start 16-byte
- * aligned.  Sizes: M or K may be 0.  No workspace.
+ * aligned.  Sizes: M or K may be 0.  No workspace.  Outputs share no element with X or each
+ * other.  Errors: TRA_ERR_INVALID_ARG, TRA_ERR_UNSUPPORTED for sizes past 2^30 or for more
+ * tiles of 128 x 128 than a launch takes (16777215); nothing is enqueued.
  */
 typedef enum tra_fp8 {
     TRA_FP8_E4M3 = 0,
@@ -513,8 +515,8 @@ TRA_API tra_status tra_scaled_linear_describe(const tra_scaled_args *args, char 
  * itself.  Elements between a row's end and the next row are neither read nor
  * written.  The backward call's workspace: as tra_linear's.  Errors:
  * TRA_ERR_INVALID_ARG for a bad type, kind, size, leading dimension, pointer,
- * overlap or workspace; TRA_ERR_UNSUPPORTED for sizes past 2^30; nothing is enqueued
- * and no output touched.
+ * overlap or workspace; TRA_ERR_UNSUPPORTED for sizes past 2^30 or groups past 65535;
+ * nothing is enqueued and no output touched.
  */
 typedef enum tra_norm_kind {
     TRA_NORM_NONE = 0,

@@ -1,5 +1,6 @@
 // linear_kernels.h -- kernels of the fused linear operators, for one element
-// type T (float, __bf16 or _Float16).  Included once by each linear_<type>.hip.
+// type T (float, __bf16 or _Float16).  Included once by each linear_<type>.hip,
+// and for its panels, loads and epilogue by scaled_kernels.h.
 //
 // The product runs on 16 x 16 MFMA tiles whose K step is one 16-byte chunk per
 // lane: 8 elements of 16 bits (v_mfma_f32_16x16x32) or 4 floats (four

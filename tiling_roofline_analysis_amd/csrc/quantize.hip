@@ -6,7 +6,9 @@
 // the tile: a row's block is 16 lanes' (their largest by DPP), a column's is the tile's
 // 16 groups of lanes' (theirs through LDS), and a lane's 8 rows of one column are 8
 // consecutive bytes of the transposed form, which is put together in LDS and leaves in
-// lines of 128 bytes.  Memory bounds it.
+// lines of 128 bytes.  Memory bounds it: 8192 x 4096 bf16 to both forms with e8m0 scales 29 us
+// (4.6 TB/s); with binary32 scales, whose exact quotients cost five steps an element, also
+// the vector units (rows of 8192 x 8192 bf16: 48 us, with e8m0 scales 35).
 #include "tra_gemm.h"
 
 #include "scaled_internal.h"
