@@ -50,7 +50,7 @@ struct NormGradArgs {
     // Sums of one chunk of rows: chunk c of sum v at partial[v] + c * D; or null.
     float *partial[kVectors];
     int64_t chunks_per_group, rows_per_chunk;
-    float *stats;                      // kStats floats a row, where the sums are a kernel of their own
+    float *stats;                      // kStats floats a row, where sums are a kernel of their own
 };
 
 constexpr int kStats = 8;              // mean and 1 / deviation of H and R, means of g and g n
@@ -256,7 +256,8 @@ constexpr int kBlock = LANES < 256 ? 256 : LANES;
 // memory (5.1 TB/s); 1000 x 5461 f32, layer, with a gate: 23 (3.8 TB/s), two workgroups a
 // CU whose rows end inside a chunk.
 template <typename T, typename P, int LANES, int E, bool RAGGED>
-__global__ __launch_bounds__(kBlock<LANES>, RAGGED || E > 8 ? 4 : LANES < 256 ? 7 : 8) void norm_forward(const NormArgs p) {
+__global__ __launch_bounds__(kBlock<LANES>, RAGGED || E > 8 ? 4 : LANES < 256 ? 7 : 8)
+void norm_forward(const NormArgs p) {
     constexpr int V = kChunk<T>, BLOCK = kBlock<LANES>, ROWS = BLOCK / LANES;
     __shared__ __align__(16) float lds[4 * (BLOCK / 64)];
     lds_poison(lds, 4 * (BLOCK / 64));
@@ -509,7 +510,8 @@ constexpr int backward_per_cu(int64_t bytes, int64_t D, bool bias) {
 }
 
 template <typename T, typename P, int LANES, int E, bool POST, bool BIAS>
-__global__ __launch_bounds__(kBackwardBlock, (2 * backward_per_cu(sizeof(T), LANES * E, BIAS))) void norm_backward(const NormGradArgs q) {
+__global__ __launch_bounds__(kBackwardBlock, (2 * backward_per_cu(sizeof(T), LANES * E, BIAS)))
+void norm_backward(const NormGradArgs q) {
     constexpr int V = kChunk<T>, BLOCK = kBackwardBlock, ROWS = BLOCK / LANES;
     const NormArgs &p = q.f;
     __shared__ __align__(16) float lds[4 * (BLOCK / 64)];
@@ -654,7 +656,7 @@ __global__ __launch_bounds__(kBackwardBlock, (2 * backward_per_cu(sizeof(T), LAN
     }
 }
 
-// ---- backward, rows in registers, sums by themselves -----------------------------------------------
+// ---- backward, rows in registers, sums by themselves -----------------------------------
 //
 // Rows that leave no registers for sums of the vectors' gradients: 1024 lanes a row; the rows'
 // statistics go to memory and norm_columns, which reads the rows again, takes the sums from
@@ -984,7 +986,7 @@ struct NormJoinArgs {
 constexpr int kJoin = 32;
 
 // The loads' latency bounds it: with many chunks there are more groups (512 chunks of three
-// sums of 4096 take 6.9 us with 8, 6.4 with 32), and a lane's loads go eight at a time, the last
+// sums of 4096 take 6.9 us with 8, 6.4 with 32; 63 of two sums 4 us less with 8), and a lane's loads go eight at a time, the last
 // of them at the last chunk again (one at a time for the rest, 63 chunks of three sums of
 // 5461 took 9.0 us, so 6.6).
 template <typename P, int GROUPS>
@@ -1028,7 +1030,8 @@ __global__ __launch_bounds__(kJoin * GROUPS) void norm_join(const NormJoinArgs p
 constexpr int64_t kMaxBlocks = 1 << 20;      // workgroups that take rows in turn
 
 // Whether rows of D elements of `bytes` bytes are kept in registers: not those longer than
-// 1024 lanes' 16 elements, nor those shorter than a chunk of 16 bytes.
+// 1024 lanes' 16 elements (2048 x 16384 bf16 forward 64 us, read again for each sum 79), nor
+// those shorter than a chunk of 16 bytes.
 constexpr bool in_registers(int64_t D, int64_t bytes) { return D * bytes >= 16 && D <= 16384; }
 
 template <typename T, typename P, int LANES, int E>
@@ -1042,6 +1045,9 @@ hipError_t launch_forward(const NormArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// 8 elements a lane, and as few lanes as that takes.  With the next larger number of them
+// add_norm takes, in us (forward; backward): 65536 x 128 bf16 33 instead of 13; 47 instead of
+// 22, 16384 x 512 30, 13; 46, 21, 4096 x 2048 18, 13; 28, 22, 2048 x 4096 20, 13 (forward).
 template <typename T, typename P>
 hipError_t forward_of(const NormArgs &a, hipStream_t s) {
     if (in_registers(a.D, sizeof(T))) {
@@ -1058,7 +1064,9 @@ hipError_t forward_of(const NormArgs &a, hipStream_t s) {
 }
 
 // Whether the backward pass has a kernel that keeps such rows and the sums of the vectors'
-// gradients in registers: with a norm of H, rows past 4096 leave room for few sums.
+// gradients in registers: with a norm of H, rows past 4096 leave room for few sums.  (Of
+// 4096 x 5120 without a norm of H: bf16 59 us, in two kernels 109, f32 99 and 166; with one: bf16
+// 95 and 142.)
 constexpr bool backward_fits(int64_t D, int64_t bytes, bool post, bool bias) {
     return in_registers(D, bytes) && D <= 8192 &&
            (D <= 4096 || !post || (bytes == 2 && !bias));
@@ -1287,7 +1295,7 @@ GradPlan plan_backward(const tra_norm_grad_args &a) {
     const int64_t per_group = a.M / a.groups;
     // as many workgroups as run at once where their sums are kept, or 8 a CU of those that
     // take sums alone (2048 x 16384 bf16: 100 us and 9 for the join of 256 chunks, 87 and 5
-    // of 64); without sums a row each
+    // of 64); without sums as many as there are rows, to 4096
     int64_t most = 4096;
     if (g.vectors > 0)
         most = g.fits ? 256 * tra::backward_per_cu(bytes, a.D, bias)
