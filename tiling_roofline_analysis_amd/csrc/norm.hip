@@ -230,8 +230,9 @@ __device__ __forceinline__ const P *vector_row(const void *v, int64_t ld, int64_
 }
 
 // A lane's part of a vector (of its own element type P, the rows' being T).  It is waited
-// for where it is loaded, which is where it is used.
-template <typename T, typename P, int LANES, int E>
+// for where it is loaded, which is where it is used.  Not RAGGED: no row ends inside a chunk
+// (8192 x 4096 bf16, norm: 25.3 us, 26.5 with a way for that).
+template <typename T, typename P, int LANES, int E, bool RAGGED = true>
 __device__ __forceinline__ void vector_lane(const void *vec, int64_t ld, int64_t group, int lane,
                                             int D, float (&v)[E]) {
     constexpr int V = kChunk<T>;
@@ -239,8 +240,12 @@ __device__ __forceinline__ void vector_lane(const void *vec, int64_t ld, int64_t
 #pragma unroll
     for (int c = 0; c < E / V; ++c) {
         const int at = (c * LANES + lane) * V;
-        float t[V];
-        load_part<P, V>(row + at, D - at, t);
+        float t[V] = {};
+        if constexpr (RAGGED) {
+            load_part<P, V>(row + at, D - at, t);
+        } else {
+            if (at < D) load_row<P, V>(row + at, t);
+        }
 #pragma unroll
         for (int e = 0; e < V; ++e) v[c * V + e] = t[e];
     }
@@ -275,14 +280,14 @@ void norm_forward(const NormArgs p) {
         auto times = [&](float (&v)[E], const void *vec, int64_t ld) __attribute__((always_inline)) {
             if (vec == nullptr) return;
             float t[E];
-            vector_lane<T, P, LANES>(vec, ld, group, lane, D, t);
+            vector_lane<T, P, LANES, E, RAGGED>(vec, ld, group, lane, D, t);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[e] *= t[e];
         };
         auto plus = [&](float (&v)[E], const void *vec, int64_t ld) __attribute__((always_inline)) {
             if (vec == nullptr) return;
             float t[E];
-            vector_lane<T, P, LANES>(vec, ld, group, lane, D, t);
+            vector_lane<T, P, LANES, E, RAGGED>(vec, ld, group, lane, D, t);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[e] += t[e];
         };

@@ -190,23 +190,22 @@ def _product(x, x_scales, w, w_scales, bias, residual, dtype, out):
     w_fp8 = FP8[w.dtype]
     if w_fp8 and (head[1] or scale == 0 or x_scales is None):
         raise ValueError("float8_e5m2 w goes with float8_e4m3fn x and float8_e8m0fnu scales only")
-    like = x if x.dtype is dtype else x.new_empty(0, dtype=dtype)
     B = R = 0
     ldr = ldy = N
+    if out is None:
+        out = x.new_empty(M, N, dtype=dtype)
+    else:
+        ldy = _matrix(out, "out", x, dtype)
+        if out.shape[0] != M or out.shape[1] != N:
+            raise ValueError(f"out must be {M} x {N}")
     if bias is not None:
-        _vector(bias, "bias", like, N)
+        _vector(bias, "bias", out, N)
         B = bias.data_ptr()
     if residual is not None:
-        ldr = _matrix(residual, "residual", like)
+        ldr = _matrix(residual, "residual", out)
         if residual.shape[0] != M or residual.shape[1] != N:
             raise ValueError(f"residual must be {M} x {N}")
         R = residual.data_ptr()
-    if out is None:
-        out = like.new_empty(M, N)
-    else:
-        ldy = _matrix(out, "out", like)
-        if out.shape[0] != M or out.shape[1] != N:
-            raise ValueError(f"out must be {M} x {N}")
     fields = (DTYPES[dtype], *head, w_fp8, scale, block_rows, M, N, kx, x.data_ptr(), ldx, *sx,
               w.data_ptr(), ldw, w_scales.data_ptr(), sw_row, sw_block, B, R, ldr, out.data_ptr(),
               ldy)
