@@ -232,6 +232,22 @@ def test_an_infinity_in_the_last_row_is_counted_once(D):
     assert torch.equal(dx, dr) and torch.equal(dh, dr * t["gate"])
 
 
+@pytest.mark.parametrize("D", [5, 50, 2000, 5461, 9000, 17000])
+@pytest.mark.parametrize("post", ["none", "layer"])
+def test_an_unused_norm_has_gradients_of_zero(post, D):
+    # whatever the rows hold: there is no 0 times an infinity
+    t, dr, _ = make(6, D, torch.float32, torch.float32)
+    h = t["h"].clone()
+    h[2, 1] = float("inf")
+    args = {k: v for k, v in t.items() if k not in ("x", "h")}
+    if post == "none":
+        args.pop("post_weight"), args.pop("post_bias")
+    got = tra.add_norm_backward(dr, None, t["x"], h, post=post, kind="rms", **args)
+    dweight, dbias = got[5:]
+    assert not dweight.any() and not dbias.any()
+    assert torch.equal(got[0], dr)
+
+
 def test_missing_gradients_of_outputs():
     # either output may go unused
     for D in (50, 2000, 9000):

@@ -944,11 +944,12 @@ __global__ __launch_bounds__(256) void norm_columns(const NormGradArgs q) {
                 const float nh = (h[e] - mean_h) * inv_h, b = nh * post_weight[e] + post_bias[e];
                 const float r = p.H != nullptr ? p.scale * n[e] + gate[e] * b : n[e];
                 const float nr = (r - mean) * inverse;
-                if (q.dY != nullptr)
+                if (q.dY != nullptr) {
                     g[e] += inverse * (dy[e] * weight[e] - nr * along - mean_g);
+                    total[kWeight][e] += dy[e] * nr;
+                    total[kBias][e] += dy[e];
+                }
                 const float gg = g[e] * gate[e];
-                total[kWeight][e] += dy[e] * nr;
-                total[kBias][e] += dy[e];
                 total[kGate][e] += g[e] * b;
                 total[kPostWeight][e] += gg * nh;
                 total[kPostBias][e] += gg;

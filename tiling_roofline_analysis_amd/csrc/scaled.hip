@@ -232,9 +232,11 @@ tra_status tra_scaled_linear_describe(const tra_scaled_args *args, char *buf, si
     }
     const ScaledPlan s = plan_scaled(*args);
     const tra::TilePlan &t = s.tile;
-    std::snprintf(buf, len, "kernel=%s tile=%dx%d deep=%d whole=%d splits=%d quantizes=%d workspace_bytes=%zu",
-                  t.few ? "scaled_few" : t.bm == 256 ? "scaled_wide" : "scaled_tile", t.bm, t.bn, t.deep, t.whole, t.splits,
-                  s.make ? 1 : x_given(*args) ? 0 : 2, s.total);
+    // quantizes: 0 nothing, 1 in the kernel, 2 in a launch before it
+    std::snprintf(buf, len,
+                  "kernel=%s tile=%dx%d deep=%d whole=%d splits=%d quantizes=%d workspace_bytes=%zu",
+                  t.few ? "scaled_few" : t.bm == 256 ? "scaled_wide" : "scaled_tile", t.bm, t.bn,
+                  t.deep, t.whole, t.splits, s.make ? 1 : x_given(*args) ? 0 : 2, s.total);
     return TRA_OK;
 }
 
