@@ -13,7 +13,8 @@ CALLS = [(1, 16, 128), (1, 500, 4096), (3, 48, 9000), (16, 1030, 272), (9, 33, 1
          (816, 5074, 268), (680, 1513, 3341), (1135, 273, 7425), (2944, 66, 3777),
          (2527, 1619, 1986), (1233, 777, 6251), (796, 1382, 6786), (2604, 4666, 736),
          (1977, 1462, 4526), (7203, 2255, 640), (1675, 1250, 10057), (69, 4183, 8929),
-         (7356, 2239, 2451)]
+         (7356, 2239, 2451), (7177, 1736, 16), (763, 2792, 1140), (2695, 386, 5244),
+         (2735, 75, 2875)]
 
 # addresses that are never read
 X, SX, W, SW, BIAS, R, Y, WS = (i << 40 for i in range(1, 9))

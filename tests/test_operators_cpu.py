@@ -209,19 +209,18 @@ def test_scaled_linear_checks_its_workspace():
     assert size(M=1, N=64, K=256, x_dtype=1) == (OK, 0)
 
 
-@pytest.mark.parametrize("scale,dtype", [("e8m0", 1), ("f32", 1), ("e8m0", 0), ("f32", 0)])
-def test_plans_reach_every_kernel(scale, dtype):
-    seen = {sp.reached(*c, scale, dtype=dtype) for c in sp.CALLS}
-    tiles = ["64x64", "64x128"] + (["128x128"] if dtype else [])
+@pytest.mark.parametrize("scale,dtype,block_rows", [
+    ("e8m0", 1, 128), ("e8m0", 1, 1), ("f32", 1, 128), ("e8m0", 0, 128), ("e8m0", 0, 1),
+    ("f32", 0, 128)])
+def test_plans_reach_every_kernel(scale, dtype, block_rows):
+    seen = {sp.reached(*c, scale, dtype=dtype, w_block_rows=block_rows) for c in sp.CALLS}
+    # binary32 results with a scale for each row of the weights have no 128 x 128
+    tiles = ["64x64", "64x128"] + (["128x128"] if dtype or block_rows == 128 else [])
     want = {("scaled_tile", t, deep) for t in tiles for deep in (0, 1)} | {("scaled_few", "16x16", 0)}
     want |= {("scaled_wide", "256x256", 0)} if dtype else set()
-    # (binary32 results in 64 x 128 tiles one a CU: only where they are split)
     assert {s[:3] for s in seen} == want
-    # of the kinds of a split, each kind of tile has those that a plan gives it
-    splits = {(t, d, s) for k, t, d, s in seen if k == "scaled_tile"}
-    for tile in tiles:
-        assert {s for t, d, s in splits if t == tile} >= {"no", "all", "last"} - (
-            {"last"} if (tile, dtype) == ("128x128", 0) else set())
+    splits = {(t, s) for k, t, _, s in seen if k == "scaled_tile"}
+    assert splits >= {(t, s) for t in tiles for s in ("no", "all", "last")}
     if dtype:
         assert {s for k, _, _, s in seen if k == "scaled_wide"} == {"no", "last"}
 

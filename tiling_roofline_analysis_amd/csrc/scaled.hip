@@ -23,8 +23,8 @@ constexpr int64_t kMaxPitch = int64_t{1} << 22;      // bytes: a tile's offsets 
 int64_t up16(int64_t n) { return ceil_div(n, 16) * 16; }
 
 // How the kernels go, in microseconds (TileClass): 16-bit results with binary32 and e8m0
-// scales, binary32 results.
-constexpr TileClass kClasses[3][4] = {
+// scales; binary32 results with a scale for 128 rows of W, and with one for each.
+constexpr TileClass kClasses[4][4] = {
     {{256, 256, 1, 1.52, 1.63, 8.0},
      {128, 128, 2, 0.65, 0.49, 5.0},
      {64, 128, 2, 0.41, 0.34, 4.0},
@@ -33,11 +33,22 @@ constexpr TileClass kClasses[3][4] = {
      {128, 128, 2, 0.45, 0.425, 5.0},
      {64, 128, 2, 0.34, 0.33, 3.8},
      {64, 64, 2, 0.242, 0.205, 3.2}},
+    {{128, 128, 2, 1.03, 0.87, 9.0},
+     {64, 128, 2, 0.635, 0.53, 6.0},
+     {64, 64, 2, 0.466, 0.333, 5.0},
+     {0, 0, 0, 0.0, 0.0, 0.0}},
     // (128 x 128, one a CU for its VGPRs: 1.29, twice what 64 x 128 takes)
     {{64, 128, 2, 0.85, 0.62, 4.5},
      {64, 64, 2, 0.56, 0.37, 4.0},
      {0, 0, 0, 0.0, 0.0, 0.0},
      {0, 0, 0, 0.0, 0.0, 0.0}}};
+
+// The row of kClasses.
+int classes_of(const tra_scaled_args &a) {
+    const bool e8m0 = a.scale == TRA_SCALE_E8M0;
+    if (a.dtype == TRA_DTYPE_F32) return e8m0 && a.w_block_rows == 1 ? 3 : 2;
+    return e8m0 ? 1 : 0;
+}
 
 bool x_given(const tra_scaled_args &a) { return a.x_dtype == TRA_X_SCALED; }
 
@@ -46,8 +57,7 @@ ScaledPlan plan_scaled(const tra_scaled_args &a) {
     const int64_t K = up16(a.K), b = elem_bytes(a.dtype);
     const PlanSizes z{a.M, a.N, K, 1, 1, false, 1, static_cast<double>(b), false, true};
     double us = 0.0;
-    s.tile = plan_classes(
-        kClasses[a.dtype == TRA_DTYPE_F32 ? 2 : a.scale == TRA_SCALE_E8M0 ? 1 : 0], 4, z, us);
+    s.tile = plan_classes(kClasses[classes_of(a)], 4, z, us);
     // Few rows: the weights' bytes at the rate that the strips of 16 columns can ask for.
     if (a.M <= 16) {
         const double strips = static_cast<double>(ceil_div(a.N, 16));

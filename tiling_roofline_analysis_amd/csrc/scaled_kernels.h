@@ -229,8 +229,8 @@ struct ScalePanel {
 //   read X's and half 0's fragments of tile s + 1; compute half 1.
 // For products of few tiles, which latency bounds as much as the matrix units, and for
 // binary32 results, whose widening keeps the vector units as busy as those: 512 x 4096 x 4096
-// with e8m0 scales to bfloat16 16.9 us (1.02 PFLOP/s), to binary32 30.1 (0.57);
-// 4096 x 8192 x 4096 to binary32 with binary32 scales 258 (1.07 PFLOP/s).
+// with e8m0 scales to bfloat16 17.0 us (1.01 PFLOP/s), to binary32 29.2 (0.59);
+// 4096 x 8192 x 4096 to binary32 237 (1.16 PFLOP/s).
 template <int BM, int BN, int SCALE>
 struct ScaledShape {
     static constexpr int WAVES = 4, TI = BM / 32, TJ = BN / 64, HC = BN / 4;
@@ -244,7 +244,8 @@ struct ScaledShape {
 };
 
 // EACH: binary32 results and e8m0 scales, one for each row of W; else 128 rows share one, as
-// with binary32 scales (4096 x 8192 x 4096: 344 us with EACH, 282 without).
+// with binary32 scales (4096 x 8192 x 4096: 335 us with EACH in 64 x 128 tiles, 237 without in 128 x 128, whose
+// VGPRs EACH would leave one workgroup a CU).
 template <typename T, int FORMATS, int SCALE, bool EACH, int BM, int BN, int S>
 __global__ __launch_bounds__(256, (ScaledShape<BM, BN, SCALE>::per_cu(S))) void scaled_tile(
     const ScaledArgs p) {
@@ -855,7 +856,8 @@ hipError_t launch_scaled(const TilePlan &plan, const ScaledArgs &p, hipStream_t 
 #define TRA_TILE(BM, BN, S) \
     scaled_tile<T, FORMATS, SCALE, EACH, BM, BN, S><<<grid, 256, 0, stream>>>(p)
     if (plan.bm == 128) {
-        if constexpr (sizeof(T) == 2) plan.deep ? TRA_TILE(128, 128, 4) : TRA_TILE(128, 128, 2);
+        // (never planned with EACH)
+        if constexpr (!EACH) plan.deep ? TRA_TILE(128, 128, 4) : TRA_TILE(128, 128, 2);
         else return hipErrorInvalidValue;
     } else if (plan.bn == 128) {
         plan.deep ? TRA_TILE(64, 128, 4) : TRA_TILE(64, 128, 2);
