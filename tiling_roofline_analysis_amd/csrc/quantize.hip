@@ -157,8 +157,10 @@ __global__ __launch_bounds__(256) void quantize_tile(const QuantizeArgs p) {
 // Rows alone, a block for each 16 lanes, blocks of one column of them next to each other:
 // for matrices whose tiles would leave CUs idle.  A lane of the tile kernel rounds 64
 // elements one after the other, which takes 2 to 6 us however few there are: 16 x 512 bf16 to
-// binary32 scales 9.1 us in tiles, 2.6 this way, 1024 x 4096 8.2 and 5.6; from 512 tiles on
-// the two are alike (2048 x 4096 to e8m0 scales 6.6 us in tiles, 7.3 this way).
+// binary32 scales 9.1 us in tiles, 2.6 this way, 1024 x 4096 8.2 and 5.6.  With e8m0 scales
+// the two are alike from 512 tiles on (2048 x 4096 bf16 6.5 us in tiles, 7.1 this way,
+// 4096 x 8192 19.7 and 22.3), with binary32 scales from 2048 on (2048 x 4096 10.1 and 9.3,
+// 4096 x 4096 17.6 and 15.5, 8192 x 8192 48 and 50).
 template <typename T, int FP8, int SCALE>
 __global__ __launch_bounds__(256) void quantize_rows(const QuantizeArgs p) {
     const int64_t id = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
@@ -180,7 +182,8 @@ __global__ __launch_bounds__(256) void quantize_rows(const QuantizeArgs p) {
 
 template <typename T, int FP8, int SCALE>
 hipError_t launch_rows(int block_rows, unsigned tiles, const QuantizeArgs &a, hipStream_t s) {
-    if (block_rows == 1 && a.QT == nullptr && tiles < 512) {
+    if (block_rows == 1 && a.QT == nullptr &&
+        tiles < (SCALE == TRA_SCALE_F32 ? 2048u : 512u)) {
         const unsigned groups = static_cast<unsigned>(ceil_div(a.M * a.tiles_k, 16));
         quantize_rows<T, FP8, SCALE><<<dim3(groups), 256, 0, s>>>(a);
         return hipGetLastError();
