@@ -441,7 +441,8 @@ TRA_API tra_status tra_quantize(const tra_quantize_args *args, void *stream);
  *
  * Numerics: products and sums are binary32.  e8m0 scales are applied by the matrix
  * units, exactly; with binary32 scales a block's sum is multiplied by the product of
- * its two scales (two roundings).  Each element is rounded once, when it is stored.  The
+ * its two scales (two roundings; no product or sum of theirs leaves binary32's range unless the
+ * result does).  Each element is rounded once, when it is stored.  The
  * order of the sums follows from the sizes and types, so a call gives the same bits every
  * time.
  *

@@ -88,6 +88,53 @@ __device__ __forceinline__ float scale_value(uint32_t word) {
     return __uint_as_float(word);
 }
 
+// ---- scales whose product leaves binary32's range ----------------------------------------
+//
+// A block's sum t is 0 or between 2^-25 and 2^32 in size.  It is multiplied by the product of its
+// two scales, which may lie past either end of binary32's range though t times it does not.
+// So sums are taken 2^32 times as large.  A product of scales that is subnormal even then is off by
+// 2^-150 at most, and t times it, brought down again, by no more: half of the least number.  Where
+// a sum comes out infinite or NaN (results past 2^96, products of scales past it, operands that are
+// infinite or NaN themselves) the wave takes its sums once more with add_scaled, whose steps leave
+// the range only where their result does.  What it costs is mostly the look at the sums at a tile's
+// end: 8192 x 12288 x 4096 with binary32 scales 378 us, 369 without; with the extremes of the scales
+// kept in the K loop instead, to find such products, 393.
+constexpr float kUp = 4294967296.0f, kDown = 1.0f / kUp;
+
+// d + t a b for two scales: t times their product where that is a normal number, else times the
+// larger and then the smaller one.  (Of a product past the range's end the smaller one is above 1,
+// so t times the larger overflows only with the result.  Of one below the least normal number t
+// times the larger is normal, or both scales are below 2^-101 and the result is 0.)
+__device__ __forceinline__ float add_scaled(float d, float t, float a, float b) {
+    const float both = a * b;
+    const bool normal = __builtin_amdgcn_classf(both, 0x108);      // of either sign
+    const bool less = fabsf(a) < fabsf(b);
+    return fmaf(normal ? t : t * (less ? b : a), normal ? both : less ? a : b, d);
+}
+
+// The larger size of two, NaN if either is.
+__device__ __forceinline__ float larger(float a, float b) {
+    return __builtin_elementwise_maximum(fabsf(a), fabsf(b));
+}
+
+// Sums of 16 x 16 tiles down by 2^32; whether some of the wave's were infinite or NaN.
+template <int N, int TI, int TJ>
+__device__ __forceinline__ bool bring_down(f32x4 (&c)[N][TI][TJ]) {
+    float most = 0.0f;
+#pragma unroll
+    for (int h = 0; h < N; ++h)
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int j = 0; j < TJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    most = larger(most, c[h][i][j][e]);
+                    c[h][i][j][e] *= kDown;
+                }
+    return __builtin_amdgcn_ballot_w64(!(most < __builtin_huge_valf())) != 0;
+}
+
 // A barrier that no load is waited for at; and a wait for this wave's direct loads but
 // the last VM (stage_sync does both).
 __device__ __forceinline__ void step_sync() {
@@ -218,6 +265,94 @@ struct ScalePanel {
     }
 };
 
+// The kernel's arguments again, behind all that was before: read there, they and what follows
+// from them take no registers in the K loop (where they cost scaled_wide 70 SGPRs and spills).
+__device__ __forceinline__ const ScaledArgs &arguments_again() {
+    auto *at = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(at));
+    return *(const ScaledArgs *)at;
+}
+
+// The 16 x 16 sums of rows m0 .. and columns n0 .., K tiles first .. + count - 1.
+template <int FORMATS, int SCALE, bool WIDEN>
+__device__ __forceinline__ f32x4 sums_by_parts(const ScaledArgs &p, int64_t m0, int64_t n0,
+                                               int first, int count) {
+    constexpr int SIZE = SCALE == TRA_SCALE_E8M0 ? 1 : 4;
+    const TileArgs &a = p.t;
+    const int l16 = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+    auto inside = [](int64_t i, int64_t n) __attribute__((always_inline)) {
+        return i < n ? i : n - 1;
+    };
+    const int64_t m = inside(m0 + l16, a.M);
+    const char *x_at = static_cast<const char *>(a.A) + m * a.lda;
+    const char *w_at = static_cast<const char *>(a.B[0]) + inside(n0 + l16, a.N) * a.ldb;
+    const char *sx_at = static_cast<const char *>(p.SX) + m * p.sx_row * SIZE;
+    auto scale_at = [](const char *at) __attribute__((always_inline)) {
+        if constexpr (SIZE == 1)
+            return scale_value<SCALE>(*reinterpret_cast<const uint8_t *>(at));
+        else
+            return scale_value<SCALE>(*reinterpret_cast<const uint32_t *>(at));
+    };
+    f32x4 c = {};
+    for (int b = first; b < first + count; ++b) {
+        u32x4 x[2] = {}, w[2] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t k = static_cast<int64_t>(b) * 128 + h * 64 + g * 16;
+            if (k < a.K) {
+                x[h] = *reinterpret_cast<const u32x4 *>(x_at + k);
+                w[h] = *reinterpret_cast<const u32x4 *>(w_at + k);
+            }
+        }
+        const float sx = scale_at(sx_at + b * p.sx_block * SIZE);
+        float sw[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t n = inside(n0 + 4 * g + e, a.N) >> p.w_shift;
+            sw[e] = scale_at(static_cast<const char *>(p.SW) +
+                             (n * p.sw_row + b * p.sw_block) * SIZE);
+        }
+        const i32x8 x8 = __builtin_bit_cast(
+            i32x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        const i32x8 w8 = __builtin_bit_cast(
+            i32x8, __builtin_shufflevector(w[0], w[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        f32x4 t = {};
+        if constexpr (WIDEN) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen<kFormatW<FORMATS>>(w8, q),
+                                                            widen<kFormatX<FORMATS>>(x8, q), t, 0,
+                                                            0, 0);
+        } else {
+            t = mma_plain<FORMATS>(w8, x8);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = add_scaled(c[e], t[e], sx, sw[e]);
+    }
+    return c;
+}
+
+// What epi_put has put into `lds` of a wave's sums, TI x TJ of 16 x 16 from `row` and, in both
+// halves of the tile's columns, `col` on.
+template <int FORMATS, int SCALE, bool WIDEN, int BM, int BN, int HC, int TI, int TJ>
+__device__ __forceinline__ void sums_again(char *lds, int row, int col) {
+    const ScaledArgs &p = arguments_again();
+    const Part part(p.t, 0, BM * BN);
+    int tm, tn;
+    grouped_tile32<BM == 256 ? kGroupWide : kGroupTile>(part.tile, p.t.tiles_m, p.t.tiles_n, tm,
+                                                        tn);
+    const int l16 = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+#pragma unroll 1
+    for (int n = 0; n < 2 * TI * TJ; ++n) {
+        const int h = n / (TI * TJ), i = n / TJ % TI, j = n % TJ;
+        *reinterpret_cast<f32x4 *>(lds + epi_at<HC>(i * 16 + l16, h * (HC / 4) + j * 4 + g)) =
+            sums_by_parts<FORMATS, SCALE, WIDEN>(
+                p, static_cast<int64_t>(tm) * BM + row + i * 16,
+                static_cast<int64_t>(tn) * BN + h * (BN / 2) + col + j * 16, part.first,
+                part.count);
+    }
+}
+
 // ---- the tile kernel ---------------------------------------------------------------------
 //
 // linear_tile for one-byte elements: BM x BN of Y per workgroup of four waves in 2 x 2.
@@ -339,8 +474,8 @@ __global__ __launch_bounds__(256, (ScaledShape<BM, BN, SCALE>::per_cu(S))) void 
         }
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
-            const float s = UNIT ? 0.0f : scale_value<SCALE>(sx[P][i]);
-            const float both = UNIT || EACH ? 0.0f : s * scale_value<SCALE>(sw[H][0]);
+            const float s = UNIT ? 0.0f : scale_value<SCALE>(sx[P][i]) * (EACH ? kUp : 1.0f);
+            const float both = UNIT || EACH ? 0.0f : s * (scale_value<SCALE>(sw[H][0]) * kUp);
 #pragma unroll
             for (int j = 0; j < TJ; ++j) {
                 f32x4 &d = c[P % SETS][H][i][j];
@@ -427,8 +562,14 @@ __global__ __launch_bounds__(256, (ScaledShape<BM, BN, SCALE>::per_cu(S))) void 
             for (int i = 0; i < TI; ++i)
 #pragma unroll
                 for (int j = 0; j < TJ; ++j) c[0][h][i][j] += c[k][h][i][j];
+    bool again = false;
+    if constexpr (!UNIT) again = bring_down(c[0]);
     epi_put<HC>(mine, c[0][0], 0);
     epi_put<HC>(mine, c[0][1], 1);
+    if constexpr (!UNIT) {
+        if (again)
+            sums_again<FORMATS, SCALE, WIDEN, BM, BN, HC, TI, TJ>(mine, wm * (BM / 2), wn * HC);
+    }
     wave_sync();
     epi_rows<T, false, HC, BM / 2>(
         a, 0, part.sums == nullptr ? nullptr : part.sums + wm * (BM / 2) * BN + wn * HC, BN, mine,
@@ -615,8 +756,10 @@ __global__ __launch_bounds__(512, 2) void scaled_wide(const ScaledArgs p) {
 
         read_b(one, b1);
         if constexpr (!UNIT) {
-            both[0] = __int_as_float(__builtin_amdgcn_readfirstlane(static_cast<int>(sw[0])));
-            both[1] = __int_as_float(__builtin_amdgcn_readfirstlane(static_cast<int>(sw[1])));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                both[h] = __int_as_float(__builtin_amdgcn_readfirstlane(
+                    __float_as_int(__uint_as_float(sw[h]) * kUp)));
         }
         quadrant(zero, zero);
         add(zero, zero);
@@ -662,6 +805,26 @@ __global__ __launch_bounds__(512, 2) void scaled_wide(const ScaledArgs p) {
     // One array takes a wave's sums of one A panel.
     char *mine = wave < 4 ? (wave < 2 ? (wave < 1 ? a00 : a01) : (wave < 3 ? a10 : a11))
                           : (wave < 6 ? (wave < 5 ? b00 : b01) : (wave < 7 ? b10 : b11));
+    if constexpr (!UNIT) {
+        bool again = bring_down(c[0]);
+        again |= bring_down(c[1]);
+        if (again) {
+            const TileArgs &q = arguments_again().t;
+            const Part own(q, 0, 256 * 256);
+            grouped_tile32<kGroupWide>(own.tile, q.tiles_m, q.tiles_n, tm, tn);
+            const int64_t n = static_cast<int64_t>(tn) * 256 + wn * 32;
+#pragma unroll 1
+            for (int row = wm * 64; row < 256; row += 128) {
+                sums_again<FORMATS, SCALE, false, 256, 256, 32, 4, 2>(mine, row, wn * 32);
+                wave_sync();
+                epi_rows<T, false, 32, 64>(
+                    q, 0, own.sums == nullptr ? nullptr : own.sums + row * 256 + wn * 32, 256, mine,
+                    static_cast<int64_t>(tm) * 256 + row, n, n + 128);
+                wave_sync();
+            }
+            return;
+        }
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         epi_put<32>(mine, c[h][0], 0);
@@ -764,52 +927,67 @@ __global__ __launch_bounds__(512) void scaled_few(const ScaledArgs p) {
     }
 
     f32x4 c = {};
-    for (int b0 = begin; b0 < end; b0 += U) {
-        if (b0 > begin) load(b0);
+    auto run = [&](auto careful) __attribute__((always_inline)) {
+        constexpr bool CAREFUL = decltype(careful)::value;
+        for (int b0 = begin; b0 < end; b0 += U) {
+            if (CAREFUL || b0 > begin) load(b0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int b = b0 + u < end ? b0 + u : end - 1;
-            u32x4 x[2];
-            uint32_t sx;
-            if constexpr (MAKE) {
-                const int at = (m * blocks + b) * 128 + g * 16;
-                x[0] = *reinterpret_cast<const u32x4 *>(made + at);
-                x[1] = *reinterpret_cast<const u32x4 *>(made + at + 64);
-                sx = made_scales[m * blocks + b];
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // (past K the weights are zeros, and so are these: they are NaN-free)
-                    const int k = b * 128 + h * 64 + g * 16;
-                    x[h] = u32x4{};
-                    if (k < K)
-                        x[h] = *reinterpret_cast<const u32x4 *>(x_at + b * 128 + h * 64);
-                }
-                sx = scale_at(sx_at + b * p.sx_block * SIZE);
-            }
-            if (b0 + u >= end) continue;
-            const i32x8 w8 = __builtin_bit_cast(
-                i32x8, __builtin_shufflevector(w[u][0], w[u][1], 0, 1, 2, 3, 4, 5, 6, 7));
-            const i32x8 x8 = __builtin_bit_cast(
-                i32x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
-            if constexpr (UNIT) {
-                c = mma_scaled<FORMATS>(w8, x8, c, sw[u], sx);
-            } else {
-                f32x4 t = {};
-                if constexpr (WIDEN) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            widen<kFormatW<FORMATS>>(w8, q), widen<kFormatX<FORMATS>>(x8, q), t, 0,
-                            0, 0);
+            for (int u = 0; u < U; ++u) {
+                const int b = b0 + u < end ? b0 + u : end - 1;
+                u32x4 x[2];
+                uint32_t sx;
+                if constexpr (MAKE) {
+                    const int at = (m * blocks + b) * 128 + g * 16;
+                    x[0] = *reinterpret_cast<const u32x4 *>(made + at);
+                    x[1] = *reinterpret_cast<const u32x4 *>(made + at + 64);
+                    sx = made_scales[m * blocks + b];
                 } else {
-                    t = mma_plain<FORMATS>(w8, x8);
-                }
-                const float s = scale_value<SCALE>(sx);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    c[e] = fmaf(t[e], s * scale_value<SCALE>(EACH ? sws[u][e] : sw[u]), c[e]);
+                    for (int h = 0; h < 2; ++h) {
+                        // (past K the weights are zeros, and so are these: they are NaN-free)
+                        const int k = b * 128 + h * 64 + g * 16;
+                        x[h] = u32x4{};
+                        if (k < K)
+                            x[h] = *reinterpret_cast<const u32x4 *>(x_at + b * 128 + h * 64);
+                    }
+                    sx = scale_at(sx_at + b * p.sx_block * SIZE);
+                }
+                if (b0 + u >= end) continue;
+                const i32x8 w8 = __builtin_bit_cast(
+                    i32x8, __builtin_shufflevector(w[u][0], w[u][1], 0, 1, 2, 3, 4, 5, 6, 7));
+                const i32x8 x8 = __builtin_bit_cast(
+                    i32x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                if constexpr (UNIT) {
+                    c = mma_scaled<FORMATS>(w8, x8, c, sw[u], sx);
+                } else {
+                    f32x4 t = {};
+                    if constexpr (WIDEN) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                widen<kFormatW<FORMATS>>(w8, q), widen<kFormatX<FORMATS>>(x8, q), t, 0,
+                                0, 0);
+                    } else {
+                        t = mma_plain<FORMATS>(w8, x8);
+                    }
+                    const float s = scale_value<SCALE>(sx) * (CAREFUL ? 1.0f : kUp);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = scale_value<SCALE>(EACH ? sws[u][e] : sw[u]);
+                        c[e] = CAREFUL ? add_scaled(c[e], t[e], s, v) : fmaf(t[e], s * v, c[e]);
+                    }
+                }
             }
+        }
+    };
+    run(std::false_type{});
+    if constexpr (!UNIT) {
+        f32x4 sum[1][1][1] = {{{c}}};
+        const bool again = bring_down(sum);
+        c = sum[0][0][0];
+        if (again) {
+            c = f32x4{};
+            run(std::true_type{});
         }
     }
 
