@@ -514,6 +514,15 @@ constexpr int backward_per_cu(int64_t bytes, int64_t D, bool bias) {
     return bytes == 2 && D <= 4096 && !bias ? 2 : 1;
 }
 
+// Lanes of a row, and the rows that a workgroup takes at once: a chunk is of whole rounds of
+// those, since a round takes its time however many of its rows are there (4096 x 128 bf16 in
+// 4096 chunks of one row instead of 128 of 32: 30 us instead of 5; 1000 x 128 with the vectors'
+// gradients in 500 chunks of two 16 instead of 13, and 16 times the workspace).
+constexpr int backward_lanes(int64_t D) {
+    return D <= 128 ? 16 : D <= 512 ? 64 : D <= 2048 ? 256 : 512;
+}
+constexpr int64_t backward_rows(int64_t D) { return kBackwardBlock / backward_lanes(D); }
+
 template <typename T, typename P, int LANES, int E, bool POST, bool BIAS>
 __global__ __launch_bounds__(kBackwardBlock, (2 * backward_per_cu(sizeof(T), LANES * E, BIAS)))
 void norm_backward(const NormGradArgs q) {
@@ -1100,11 +1109,14 @@ template <typename T, typename P>
 hipError_t backward_of(const NormGradArgs &a, int64_t chunks, bool fits, bool sums, hipStream_t s) {
     const int64_t D = a.f.D;
     if (fits) {
-        if (D <= 128) return launch_backward<T, P, 16>(a, chunks, s);
-        if (D <= 512) return launch_backward<T, P, 64>(a, chunks, s);
-        if (D <= 2048) return launch_backward<T, P, 256>(a, chunks, s);
-        if (D <= 4096) return launch_backward<T, P, 512>(a, chunks, s);
-        return launch_backward<T, P, 512, 16>(a, chunks, s);
+        switch (backward_lanes(D)) {
+            case 16: return launch_backward<T, P, 16>(a, chunks, s);
+            case 64: return launch_backward<T, P, 64>(a, chunks, s);
+            case 256: return launch_backward<T, P, 256>(a, chunks, s);
+            default:
+                if (D <= 4096) return launch_backward<T, P, 512>(a, chunks, s);
+                return launch_backward<T, P, 512, 16>(a, chunks, s);
+        }
     }
     const dim3 rows(static_cast<unsigned>(std::min(a.f.M, kMaxBlocks)));
     if (!in_registers(D, sizeof(T)))
@@ -1308,6 +1320,10 @@ GradPlan plan_backward(const tra_norm_grad_args &a) {
                       : std::max<int64_t>(1, 2048 / ceil_div(a.D, 1024 / bytes));
     const int64_t want = std::max<int64_t>(1, most / a.groups);
     g.rows_per_chunk = std::max<int64_t>(1, ceil_div(per_group, want));
+    if (g.fits) {
+        const int64_t rows = tra::backward_rows(a.D);
+        g.rows_per_chunk = ceil_div(g.rows_per_chunk, rows) * rows;
+    }
     g.chunks_per_group = std::max<int64_t>(1, ceil_div(per_group, g.rows_per_chunk));
     g.chunks = a.groups * g.chunks_per_group;
     if (g.vectors > 0) {
