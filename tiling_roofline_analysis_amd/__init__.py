@@ -152,8 +152,7 @@ def _open(path: str) -> ctypes.CDLL:
     # the argument structs go as packed bytes
     args, size = ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)
     for name in ("tra_linear", "tra_linear_backward", "tra_norm", "tra_norm_backward",
-                 "tra_quantize", "tra_scaled_linear", "tra_scaled_linear_workspace_size",
-                 "tra_scaled_linear_describe"):
+                 "tra_quantize", "tra_scaled_linear"):
         getattr(lib, name).argtypes = [args, p]
         getattr(lib, name).restype = c_int
     for name in ("tra_linear_workspace_size", "tra_linear_backward_workspace_size",

@@ -251,9 +251,8 @@ def _column_sums(dy):
     return db
 
 
-def _gradients(dy, xt, wt, K, transposed, grad_dtype, need_dx, need_dw, need_dbias):
+def _gradients(dy, xt, wt, transposed, grad_dtype, need_dx, need_dw, need_dbias):
     """(dx, dw, dbias) from the column forms of x and of the weight."""
-    N = dy.shape[1]
     dx = dw = None
     rows, columns = _activations(dy, grad_dtype, need_dx, need_dw)
     if need_dx:
@@ -278,7 +277,7 @@ class _ScaledLinear(torch.autograd.Function):
         xq, xt = _activations(x, torch.float8_e4m3fn, True, need_w)
         wq, wt = _weights(w, True, need_x)
         y = _product(*xq, wq[0].t(), wq[1].t(), bias, residual, x.dtype, None)
-        ctx.plan = (x.shape[1], _is_transposed(w), grad_dtype)
+        ctx.plan = (_is_transposed(w), grad_dtype)
         ctx.save_for_backward(*(xt or (None, None)), *(wt or (None, None)))
         return y
 
@@ -372,5 +371,4 @@ def scaled_linear_backward(dy, x, w, grad_dtype=torch.float8_e4m3fn, need_dx=Tru
     _code(FP8, grad_dtype, "grad_dtype")
     xt = _activations(x, torch.float8_e4m3fn, False, True)[1] if need_dw else None
     wt = _weights(w, False, True)[1] if need_dx else None
-    return _gradients(dy, xt, wt, x.shape[1], _is_transposed(w), grad_dtype, need_dx, need_dw,
-                      need_dbias)
+    return _gradients(dy, xt, wt, _is_transposed(w), grad_dtype, need_dx, need_dw, need_dbias)
