@@ -223,8 +223,8 @@ def _product(x, x_scales, w, w_scales, bias, residual, dtype, out):
 def _weights(w, need_w, need_wt):
     """([N x K values, scales], [K x N values, scales]) of a weight tensor, None for what is
     not asked for: one set of blocks of 128 x 128."""
-    stored = w if w.stride(1) == 1 and w.stride(0) >= w.shape[1] else w.t()
-    transposed = stored is not w           # stored N x K
+    transposed = _is_transposed(w)
+    stored = w.t() if transposed else w
     rows, columns = (need_w, need_wt) if transposed else (need_wt, need_w)
     if not (rows or columns):
         return None, None
@@ -267,7 +267,9 @@ def _gradients(dy, xt, wt, transposed, grad_dtype, need_dx, need_dw, need_dbias)
 
 def _is_transposed(w) -> bool:
     """Whether a checked K x N weight is stored N x K."""
-    return not (w.stride(1) == 1 and w.stride(0) >= w.shape[1])
+    s0, s1 = w.stride()
+    # (a single column's elements may lie any way apart)
+    return not (s1 == 1 and s0 >= w.shape[1]) and (w.shape[1] > 1 or s0 == 1 or w.shape[0] == 1)
 
 
 class _ScaledLinear(torch.autograd.Function):
