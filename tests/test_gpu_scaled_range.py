@@ -28,6 +28,7 @@ ROUTES = [
     ((2527, 1619, 386), "any"), ((2000, 2049, 144), "any"),
 ]
 FORMS = [("f32", 128, torch.float32), ("f32", 128, torch.bfloat16), ("e8m0", 128, torch.float32),
+         ("e8m0", 128, torch.bfloat16), ("e8m0", 1, torch.bfloat16),
          ("e8m0", 1, torch.float32)]
 
 
@@ -78,7 +79,8 @@ def test_a_block_whose_sum_is_zero_adds_nothing(size, kernel, scale, block_rows,
 @pytest.mark.parametrize("size,kernel", ROUTES, ids=str)
 @pytest.mark.parametrize("value,ex,ew", [(448.0, -75, -75), (448.0, -126, -24), (448.0, -20, -126),
                                          (2.0 ** -9, 70, 60), (2.0 ** -9, 115, 14),
-                                         (2.0 ** -9, 10, 119)], ids=str)
+                                         (2.0 ** -9, 10, 119), (448.0, -110, 115),
+                                         (448.0, 115, -110)], ids=str)
 def test_products_of_scales_past_the_range(value, ex, ew, size, kernel, scale, block_rows, dtype):
     # 448 x 448 x 128 is 2^24.6: results from 2^-131.4 (a subnormal) on; 2^-18 x 2^130: 2^112
     M, N, K = size
@@ -156,3 +158,22 @@ def test_rows_inside_the_range_keep_their_bits(scale, block_rows, dtype):
             far = product(x, w, xs, ws, scale, dtype)
             assert torch.equal(far[rows], near[rows]) and not torch.equal(near, want)
             assert torch.isfinite(far).all() and not torch.equal(far, near)
+
+
+@pytest.mark.parametrize("scale,block_rows,dtype", FORMS, ids=str)
+def test_nan_stays_in_its_row(scale, block_rows, dtype):
+    # a row of NaN beside ordinary ones, and beside one whose scales leave the range
+    for M, N, K in ((16, 64, 640), (150, 300, 1300), (2527, 1619, 386)):
+        gen = torch.Generator(device="cuda").manual_seed(4)
+        x, w, xs, ws = operands(M, N, K, block_rows)
+        x[:, :K] = torch.randn(M, K, generator=gen, device="cuda")
+        w[:, :K] = torch.randn(N, K, generator=gen, device="cuda")
+        for ex in (0, 115):
+            xs[M // 2 - 1, 1], ws[:, 1] = ex, -3
+            x[M // 2, 7] = 1.0
+            want = product(x, w, xs, ws, scale, dtype)
+            x[M // 2, 7] = float("nan")
+            got = product(x, w, xs, ws, scale, dtype)
+            rows = torch.arange(M, device="cuda") != M // 2
+            assert torch.equal(got[rows], want[rows]) and torch.isnan(got[M // 2]).all()
+            assert torch.isfinite(want).all()

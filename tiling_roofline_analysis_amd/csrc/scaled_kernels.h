@@ -94,11 +94,11 @@ __device__ __forceinline__ float scale_value(uint32_t word) {
 // two scales, which may lie past either end of binary32's range though t times it does not.
 // So sums are taken 2^32 times as large.  A product of scales that is subnormal even then is off by
 // 2^-150 at most, and t times it, brought down again, by no more: half of the least number.  Where
-// a sum comes out infinite or NaN (results past 2^96, products of scales past it, operands that are
-// infinite or NaN themselves) the wave takes its sums once more with add_scaled, whose steps leave
-// the range only where their result does.  What it costs is mostly the look at the sums at a tile's
-// end: 8192 x 12288 x 4096 with binary32 scales 378 us, 369 without; with the extremes of the scales
-// kept in the K loop instead, to find such products, 393.
+// a sum comes out infinite or NaN and the scales are large enough for it (results past 2^96, products
+// of scales past it; else the operands are infinite or NaN themselves) the wave takes its sums once
+// more with add_scaled, whose steps leave the range only where their result does: 13 to 18 times the time of a tile.  Otherwise it costs
+// the look at the sums at a tile's end: 8192 x 12288 x 4096 with binary32 scales 380 us, 368 without;
+// with the extremes of the scales kept in the K loop instead, to find such products, 393.
 constexpr float kUp = 4294967296.0f, kDown = 1.0f / kUp;
 
 // d + t a b for two scales: t times their product where that is a normal number, else times the
@@ -133,6 +133,25 @@ __device__ __forceinline__ bool bring_down(f32x4 (&c)[N][TI][TJ]) {
                     c[h][i][j][e] *= kDown;
                 }
     return __builtin_amdgcn_ballot_w64(!(most < __builtin_huge_valf())) != 0;
+}
+
+// Whether scales no larger than a lane's x and w, of any lanes, can make sums infinite of finite
+// values: 2^15 blocks of 2^32 each, 2^32 times as large; or one of the scales that by itself.
+__device__ __forceinline__ bool far_scales(float x, float w) {
+    auto of_lane = [](float v, int l) __attribute__((always_inline)) {
+        return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+    };
+#pragma unroll 1
+    for (int l = 0; l < 64; ++l) {
+        x = larger(x, of_lane(x, l));
+        w = larger(w, of_lane(w, l));
+    }
+    return __builtin_amdgcn_ballot_w64(!(x * w < 0x1p48f && larger(x, w) < 0x1p95f)) != 0;
+}
+
+// threadIdx.x & 63, which takes no register before it is asked for.
+__device__ __forceinline__ int lane_id() {
+    return static_cast<int>(__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u)));
 }
 
 // A barrier that no load is waited for at; and a wait for this wave's direct loads but
@@ -273,26 +292,52 @@ __device__ __forceinline__ const ScaledArgs &arguments_again() {
     return *(const ScaledArgs *)at;
 }
 
+template <int SCALE>
+__device__ __forceinline__ float scale_at(const void *s, int64_t at) {
+    if constexpr (SCALE == TRA_SCALE_E8M0)
+        return scale_value<SCALE>(static_cast<const uint8_t *>(s)[at]);
+    else
+        return scale_value<SCALE>(static_cast<const uint32_t *>(s)[at]);
+}
+
+__device__ __forceinline__ int64_t at_most_last(int64_t i, int64_t n) { return i < n ? i : n - 1; }
+
+// Whether the scales of a wave's rows and columns can make sums infinite: BM / 2 rows of X from
+// `row` on and, WIDE, as many BM / 2 further on; HC columns from `col` on in both halves of the
+// tile's.
+template <int SCALE, bool WIDE, int BM, int BN, int HC>
+__device__ __forceinline__ bool far_scales(int row, int col) {
+    constexpr int ROWS = WIDE ? BM / 4 : BM / 2;
+    static_assert(ROWS <= 64 && 2 * HC <= 64, "a lane each");
+    const ScaledArgs &p = arguments_again();
+    const Part part(p.t, 0, BM * BN);
+    int tm, tn;
+    grouped_tile32<WIDE ? kGroupWide : kGroupTile>(part.tile, p.t.tiles_m, p.t.tiles_n, tm, tn);
+    const int lane = lane_id(), r = row + lane % ROWS, c = lane % (2 * HC);
+    const int64_t m = static_cast<int64_t>(tm) * BM + r;
+    const int64_t n = static_cast<int64_t>(tn) * BN + c / HC * (BN / 2) + col + c % HC;
+    const int64_t x0 = at_most_last(m, p.t.M) * p.sx_row;
+    const int64_t x1 = at_most_last(WIDE ? m + BM / 2 : m, p.t.M) * p.sx_row;
+    const int64_t w0 = (at_most_last(n, p.t.N) >> p.w_shift) * p.sw_row;
+    float x = 0.0f, w = 0.0f;
+#pragma unroll 1
+    for (int b = part.first; b < part.first + part.count; ++b) {
+        x = larger(x, scale_at<SCALE>(p.SX, x0 + b * p.sx_block));
+        if (WIDE) x = larger(x, scale_at<SCALE>(p.SX, x1 + b * p.sx_block));
+        w = larger(w, scale_at<SCALE>(p.SW, w0 + b * p.sw_block));
+    }
+    return far_scales(x, w);
+}
+
 // The 16 x 16 sums of rows m0 .. and columns n0 .., K tiles first .. + count - 1.
 template <int FORMATS, int SCALE, bool WIDEN>
 __device__ __forceinline__ f32x4 sums_by_parts(const ScaledArgs &p, int64_t m0, int64_t n0,
                                                int first, int count) {
-    constexpr int SIZE = SCALE == TRA_SCALE_E8M0 ? 1 : 4;
     const TileArgs &a = p.t;
-    const int l16 = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
-    auto inside = [](int64_t i, int64_t n) __attribute__((always_inline)) {
-        return i < n ? i : n - 1;
-    };
-    const int64_t m = inside(m0 + l16, a.M);
+    const int l16 = lane_id() & 15, g = lane_id() >> 4;
+    const int64_t m = at_most_last(m0 + l16, a.M);
     const char *x_at = static_cast<const char *>(a.A) + m * a.lda;
-    const char *w_at = static_cast<const char *>(a.B[0]) + inside(n0 + l16, a.N) * a.ldb;
-    const char *sx_at = static_cast<const char *>(p.SX) + m * p.sx_row * SIZE;
-    auto scale_at = [](const char *at) __attribute__((always_inline)) {
-        if constexpr (SIZE == 1)
-            return scale_value<SCALE>(*reinterpret_cast<const uint8_t *>(at));
-        else
-            return scale_value<SCALE>(*reinterpret_cast<const uint32_t *>(at));
-    };
+    const char *w_at = static_cast<const char *>(a.B[0]) + at_most_last(n0 + l16, a.N) * a.ldb;
     f32x4 c = {};
     for (int b = first; b < first + count; ++b) {
         u32x4 x[2] = {}, w[2] = {};
@@ -304,14 +349,12 @@ __device__ __forceinline__ f32x4 sums_by_parts(const ScaledArgs &p, int64_t m0, 
                 w[h] = *reinterpret_cast<const u32x4 *>(w_at + k);
             }
         }
-        const float sx = scale_at(sx_at + b * p.sx_block * SIZE);
+        const float sx = scale_at<SCALE>(p.SX, m * p.sx_row + b * p.sx_block);
         float sw[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t n = inside(n0 + 4 * g + e, a.N) >> p.w_shift;
-            sw[e] = scale_at(static_cast<const char *>(p.SW) +
-                             (n * p.sw_row + b * p.sw_block) * SIZE);
-        }
+        for (int e = 0; e < 4; ++e)
+            sw[e] = scale_at<SCALE>(p.SW, (at_most_last(n0 + 4 * g + e, a.N) >> p.w_shift) *
+                                              p.sw_row + b * p.sw_block);
         const i32x8 x8 = __builtin_bit_cast(
             i32x8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
         const i32x8 w8 = __builtin_bit_cast(
@@ -341,7 +384,7 @@ __device__ __forceinline__ void sums_again(char *lds, int row, int col) {
     int tm, tn;
     grouped_tile32<BM == 256 ? kGroupWide : kGroupTile>(part.tile, p.t.tiles_m, p.t.tiles_n, tm,
                                                         tn);
-    const int l16 = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+    const int l16 = lane_id() & 15, g = lane_id() >> 4;
 #pragma unroll 1
     for (int n = 0; n < 2 * TI * TJ; ++n) {
         const int h = n / (TI * TJ), i = n / TJ % TI, j = n % TJ;
@@ -563,7 +606,8 @@ __global__ __launch_bounds__(256, (ScaledShape<BM, BN, SCALE>::per_cu(S))) void 
 #pragma unroll
                 for (int j = 0; j < TJ; ++j) c[0][h][i][j] += c[k][h][i][j];
     bool again = false;
-    if constexpr (!UNIT) again = bring_down(c[0]);
+    if constexpr (!UNIT)
+        again = bring_down(c[0]) && far_scales<SCALE, false, BM, BN, HC>(wm * (BM / 2), wn * HC);
     epi_put<HC>(mine, c[0][0], 0);
     epi_put<HC>(mine, c[0][1], 1);
     if constexpr (!UNIT) {
@@ -808,7 +852,7 @@ __global__ __launch_bounds__(512, 2) void scaled_wide(const ScaledArgs p) {
     if constexpr (!UNIT) {
         bool again = bring_down(c[0]);
         again |= bring_down(c[1]);
-        if (again) {
+        if (again && far_scales<SCALE, true, 256, 256, 32>(wm * 64, wn * 32)) {
             const TileArgs &q = arguments_again().t;
             const Part own(q, 0, 256 * 256);
             grouped_tile32<kGroupWide>(own.tile, q.tiles_m, q.tiles_n, tm, tn);
@@ -986,8 +1030,17 @@ __global__ __launch_bounds__(512) void scaled_few(const ScaledArgs p) {
         const bool again = bring_down(sum);
         c = sum[0][0][0];
         if (again) {
-            c = f32x4{};
-            run(std::true_type{});
+            float x = 0.0f, y = 0.0f;
+            for (int b = begin; b < end; ++b) {
+                const uint32_t word = MAKE ? made_scales[m * blocks + b]
+                                           : scale_at(sx_at + b * p.sx_block * SIZE);
+                x = larger(x, scale_value<SCALE>(word));
+                y = larger(y, scale_value<SCALE>(w_scale(l16, b)));
+            }
+            if (far_scales(x, y)) {
+                c = f32x4{};
+                run(std::true_type{});
+            }
         }
     }
 
