@@ -256,10 +256,10 @@ constexpr int kBlock = LANES < 256 ? 256 : LANES;
 
 // ---- forward ------------------------------------------------------------------------------
 
-// What hides the memory's latency is the number of waves: 8 a SIMD, where the VGPRs allow it.
-// 8192 x 4096 bf16, add_norm with one weight: 46 us in a row of calls, 52.6 with the inputs from
-// memory (5.1 TB/s); 1000 x 5461 f32, layer, with a gate: 23 (3.8 TB/s), two workgroups a
-// CU whose rows end inside a chunk.
+// What hides the memory's latency is the number of waves: 8 a SIMD, where the registers allow it.
+// RAGGED takes 106 SGPRs, which leave 7: one workgroup of 1024 lanes a CU, not two.
+// 8192 x 4096 bf16, add_norm with one weight: 48 us in a row of calls, 52 with the inputs from
+// memory (5.1 TB/s); 1000 x 5461 f32, layer, with a gate: 26 and 30 (2.9 TB/s).
 template <typename T, typename P, int LANES, int E, bool RAGGED>
 __global__ __launch_bounds__(kBlock<LANES>, RAGGED || E > 8 ? 4 : LANES < 256 ? 7 : 8)
 void norm_forward(const NormArgs p) {
@@ -503,7 +503,8 @@ __device__ __forceinline__ void normalize_gradient(float (&g)[E], const float (&
 
 // A workgroup takes a chunk of rows of one group, ROWS at a time, and keeps the sums of
 // the vectors' gradients in registers until its end.  There are as many chunks as
-// workgroups run at once, one or two a CU, since each costs a row of sums in memory.
+// workgroups run at once, one or two a CU, since each costs a row of sums in memory; but a
+// chunk for each group at least, where there are more of those.
 // 8192 x 4096 bf16, norms before and behind the block and a gate: 88 us (4.6 TB/s); 1000 x 5461
 // f32, layer, with biases: 38 (3.5 TB/s).
 // POST: there is a norm of H.
@@ -1001,9 +1002,12 @@ struct NormJoinArgs {
 constexpr int kJoin = 32;
 
 // The loads' latency bounds it: with many chunks there are more groups (512 chunks of three
-// sums of 4096 take 6.9 us with 8, 6.4 with 32; 63 of two sums 4 us less with 8), and a lane's loads go eight at a time, the last
-// of them at the last chunk again (one at a time for the rest, 63 chunks of three sums of
-// 5461 took 9.0 us, so 6.6).
+// sums of 4096 take 6.9 us with 8, 6.4 with 32; 63 of two sums 4 us less with 8), and a lane's
+// loads go eight at a time, the last of them at the last chunk again (one at a time for the rest,
+// 63 chunks of three sums of 5461 took 9.0 us, so 6.6).  Many are the chunks of a group of rows:
+// with a vector that several groups share, whose sum is over all chunks, beside vectors of
+// their own, 32 groups of lanes are too many for those (backward pass of 4096 x 1024 bf16, 4 groups
+// 28.7 us with 8, 26.8 with 32, but 16 groups 29.3 and 31.2, 256 40 and 87).
 template <typename P, int GROUPS>
 __global__ __launch_bounds__(kJoin * GROUPS) void norm_join(const NormJoinArgs p) {
     __shared__ float part[GROUPS][kJoin];

@@ -408,7 +408,7 @@ __device__ __forceinline__ void sums_again(char *lds, int row, int col) {
 // For products of few tiles, which latency bounds as much as the matrix units, and for
 // binary32 results, whose widening keeps the vector units as busy as those: 512 x 4096 x 4096
 // with e8m0 scales to bfloat16 17.0 us (1.01 PFLOP/s), to binary32 29.2 (0.59);
-// 4096 x 8192 x 4096 to binary32 237 (1.16 PFLOP/s).
+// 4096 x 8192 x 4096 to binary32 240 (1.15 PFLOP/s).
 template <int BM, int BN, int SCALE>
 struct ScaledShape {
     static constexpr int WAVES = 4, TI = BM / 32, TJ = BN / 64, HC = BN / 4;
@@ -422,7 +422,7 @@ struct ScaledShape {
 };
 
 // EACH: binary32 results and e8m0 scales, one for each row of W; else 128 rows share one, as
-// with binary32 scales (4096 x 8192 x 4096: 335 us with EACH in 64 x 128 tiles, 237 without in 128 x 128, whose
+// with binary32 scales (4096 x 8192 x 4096: 339 us with EACH in 64 x 128 tiles, 244 without in 128 x 128, whose
 // VGPRs EACH would leave one workgroup a CU).
 template <typename T, int FORMATS, int SCALE, bool EACH, int BM, int BN, int S>
 __global__ __launch_bounds__(256, (ScaledShape<BM, BN, SCALE>::per_cu(S))) void scaled_tile(
@@ -638,9 +638,10 @@ __global__ __launch_bounds__(256, (ScaledShape<BM, BN, SCALE>::per_cu(S))) void 
 // be read in one of them has to be in LDS, of both groups' loads, at the end of the second
 // one before it: behind R0, R1 and C1 a wave waits until its last 4 panels and scales, in
 // the order above, are all that is in flight.
-// 8192 x 12288 x 4096 with e8m0 scales takes 339 us (2.43 PFLOP/s), 1.34 us a K tile and 8 for a
-// tile's first loads and stores: the matrix units are busy 64 to 76% of the time, at clocks
-// that the power lowers (1.9 GHz).
+// 8192 x 12288 x 4096 with e8m0 scales, six rounds of tiles, takes 321 us with its operands in the
+// cache and 334 to 339 from memory (2.43 PFLOP/s).  Of the 53 us a tile 1.31 are each K tile's, and 12
+// go for its first loads and its stores, which are 7 at the memory's rate.  The matrix units are
+// busy 62 to 76% of the time, at clocks that the power lowers (1.9 GHz).
 // Binary32 scales: a row tile's sums are added while the next ones' MFMAs run, a step's last
 // behind the next step's reads, while the other group's do.
 template <typename T, int FORMATS, int SCALE>
@@ -891,7 +892,7 @@ __global__ __launch_bounds__(512, 2) void scaled_wide(const ScaledArgs p) {
 // MAKE: X is of type T and quantized here, by every workgroup for itself, into LDS, while
 // its first weights are on their way; for a few thousand elements that takes less than a
 // launch of its own.  The bits are those of tra_quantize.  EACH: as in scaled_tile.
-// 1 x 12288 x 4096 with binary32 scales: 12.4 us, 4.1 TB/s of weights read.
+// 1 x 12288 x 4096 with binary32 scales: 11.1 us, 4.5 TB/s of weights read.
 template <typename T, int FORMATS, int SCALE, bool EACH, bool MAKE>
 __global__ __launch_bounds__(512) void scaled_few(const ScaledArgs p) {
     constexpr int WAVES = 8, U = 4;    // U blocks in hand
