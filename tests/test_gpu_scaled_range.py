@@ -13,7 +13,7 @@ import pytest
 import torch
 
 import tiling_roofline_analysis_amd as tra
-from scaled_plans import describe
+from scaled_plans import CALLS, describe
 from scaled_reference import FP8, SCALES, Operand, product_bound, up
 from test_gpu_linear import half_step, within
 
@@ -177,3 +177,26 @@ def test_nan_stays_in_its_row(scale, block_rows, dtype):
             rows = torch.arange(M, device="cuda") != M // 2
             assert torch.equal(got[rows], want[rows]) and torch.isnan(got[M // 2]).all()
             assert torch.isfinite(want).all()
+
+
+@pytest.mark.parametrize("scale,block_rows,dtype", FORMS, ids=str)
+@pytest.mark.parametrize("call", CALLS, ids=str)
+def test_every_kernel_instance(call, scale, block_rows, dtype):
+    # whole and split, deep and shallow, all tile sizes: a block whose sum is 0 under scales of 2^140,
+    # a row whose values are small under large scales, a row of NaN
+    M, N, K = call
+    x, w, xs, ws = operands(M, N, K, block_rows)
+    x[:, :128], w[:, :128:2], w[:, 1:128:2] = 448.0, 448.0, -448.0
+    xs[:, 0], ws[:, 0] = 70, 70
+    for b in range(1, xs.shape[1]):
+        x[:, b * 128:b * 128 + 8], w[:, b * 128:b * 128 + 8] = 1.0, 1.0
+    want = torch.full((M, N), 8.0 * (xs.shape[1] - 1), device="cuda", dtype=dtype)
+    if M > 2:
+        # 2^-9 x 448 x 2^(30 + 70), which is 2^99.8, and exact
+        x[M // 2, :128], x[M // 2, 0], xs[M // 2, 0] = 0.0, 2.0 ** -9, 30
+        want[M // 2] = (2.0 ** -9 * 448.0 * 2.0 ** 100)
+        x[M // 3, 1] = float("nan")
+        want[M // 3] = float("nan")
+    y = product(x, w, xs, ws, scale, dtype)
+    assert torch.equal(y.isnan(), want.isnan())
+    assert torch.equal(y.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
