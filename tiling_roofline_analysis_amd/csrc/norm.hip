@@ -1317,7 +1317,7 @@ GradPlan plan_backward(const tra_norm_grad_args &a) {
     const int64_t per_group = a.M / a.groups;
     // as many workgroups as run at once where their sums are kept, or 8 a CU of those that
     // take sums alone (2048 x 16384 bf16: 100 us and 9 for the join of 256 chunks, 87 and 5
-    // of 64); without sums as many as there are rows, to 4096
+    // of 64); without sums as many as there are rounds of rows, to 4096
     int64_t most = 4096;
     if (g.vectors > 0)
         most = g.fits ? 256 * tra::backward_per_cu(bytes, a.D, bias)

@@ -23,7 +23,8 @@
 //   e8m0   16-bit results: the matrix unit multiplies by both scales; a lane passes its
 //          row's byte
 //   else   the block's sums start from zero and are added by v_fma_f32, times the product
-//          of the two scales: 4 instructions an MFMA, which run beside other MFMAs
+//          of the two scales, 2^32 times as large (kUp): 4 instructions an MFMA, which run
+//          beside other MFMAs
 #pragma once
 
 #include "linear_kernels.h"
@@ -96,9 +97,10 @@ __device__ __forceinline__ float scale_value(uint32_t word) {
 // 2^-150 at most, and t times it, brought down again, by no more: half of the least number.  Where
 // a sum comes out infinite or NaN and the scales are large enough for it (results past 2^96, products
 // of scales past it; else the operands are infinite or NaN themselves) the wave takes its sums once
-// more with add_scaled, whose steps leave the range only where their result does: 13 to 18 times the time of a tile.  Otherwise it costs
-// the look at the sums at a tile's end: 8192 x 12288 x 4096 with binary32 scales 380 us, 368 without;
-// with the extremes of the scales kept in the K loop instead, to find such products, 393.
+// more with add_scaled, whose steps leave the range only where their result does: 13 to 18 times
+// the time of a tile.  Otherwise it costs the look at the sums at a tile's end: 8192 x 12288 x 4096
+// with binary32 scales 380 us, 368 without; with the extremes of the scales kept in the K loop
+// instead, to find such products, 393.
 constexpr float kUp = 4294967296.0f, kDown = 1.0f / kUp;
 
 // d + t a b for two scales: t times their product where that is a normal number, else times the
